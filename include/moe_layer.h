@@ -58,7 +58,9 @@ enum {
     MOE_ERR_DEVICE_STATUS = -5  /* a kernel guard fired (see moe_check_status) */
 };
 
-enum { MOE_FP16 = 0 };
+/* Element types.  A layer's io_dtype is MOE_FP16; the layer-free calls say
+ * which ones they take. */
+enum { MOE_FP16 = 0, MOE_BF16 = 1, MOE_FP32 = 2 };
 
 /* Device status bits reported by moe_check_status (or'ed together). */
 enum {
@@ -386,6 +388,119 @@ int moe_ep_dispatch(const void *x, int n_tokens, int hidden, const int32_t *topk
 int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const float *topk_w,
                    const int32_t *pos_of_pair, const void *y_rows, const void *sh_gate_w,
                    const void *y_shared, int residual, void *out, void *stream);
+
+/*
+ * 4-bit linear product without a layer ("Strata" article, section 3.4: the
+ * hand-written INT4 GEMV; "Flash-MoE" article, section 3: dequant matvec): the
+ * dense projections and the vocabulary head around the MoE layers, in the
+ * experts' packed format.
+ *   y[t][r] = sum_k x[t][k] W[r][k] (+ bias[r]) (+ residual[t][r]),
+ *   W[r][k] = (q[r][k] - zero[r][k/G]) * scale[r][k/G]
+ * codes uint8 [rows][cols/2] (low nibble = even k), scales fp16 and zeros
+ * uint8 (values 0 .. 15) [rows][cols/G] with G = group_size: 32, 64 or 128.
+ * rows 1 .. 1048576; cols a multiple of G, at most 65536.  The matrix is read
+ * in place: no layer, no repacking, no allocation.
+ * x [n_tokens][cols], residual and y [n_tokens][rows], bias [rows] are fp16 or
+ * bf16 (dtype MOE_FP16 or MOE_BF16); ldx, ldr, ldy are their row strides in
+ * elements (at least the row's length; columns beyond it are neither read nor
+ * written).  bias and residual may be NULL; y may be residual itself, and must
+ * not overlap x.  n_tokens 1 .. 524288.
+ * Sums are fp32, with bias and residual added before the one rounding to the
+ * output type.  For groups of 128 and few tokens the group's fp32 sum of x *
+ * (q - zero) is scaled; otherwise each weight is rounded once to the
+ * activations' type before the product.  The same call gives the same bits
+ * every time.
+ * All pointers are DEVICE pointers of the current device: codes and the rows
+ * of x 16-byte aligned (ldx a multiple of 8), the others to their element.
+ * status (int32 [1], may be NULL) gets MOE_STATUS_TIMEOUT or'ed in when a
+ * pipeline wait gave up (the output of that call is incomplete); it is never
+ * cleared here.  Asynchronous on `stream`; calls on different streams are
+ * independent.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, strides,
+ * overlap), UNSUPPORTED (dtype, group_size), CUDA.
+ */
+int moe_linear(const void *codes, const void *scales, const void *zeros, int rows, int cols,
+               int group_size, const void *x, long long ldx, int n_tokens, int dtype,
+               const void *bias, const void *residual, long long ldr, void *y, long long ldy,
+               int *status, void *stream);
+
+/*
+ * Gradient of moe_linear's input through the frozen 4-bit matrix:
+ *   dx[t][k] = sum_r dy[t][r] W[r][k]
+ * dy [n_tokens][rows] and dx [n_tokens][cols] of type dtype with row strides
+ * lddy, lddx; each weight is rounded once to that type, sums are fp32.  (The
+ * gradient of bias is the sum of dy over the tokens, that of residual dy.)
+ * Pointers as for moe_linear; codes 16-byte aligned, dy and dx to their
+ * element (16-byte aligned rows of dy take the faster kernel when there are
+ * many tokens).  dx must not overlap dy.
+ * Errors: those of moe_linear.
+ */
+int moe_linear_input_grad(const void *codes, const void *scales, const void *zeros, int rows,
+                          int cols, int group_size, const void *dy, long long lddy, int n_tokens,
+                          int dtype, void *dx, long long lddx, int *status, void *stream);
+
+/*
+ * Routing losses of a batch of router logits (moe_router_logits) and their
+ * top-k experts (moe_route_topk).  The pages have no counterpart: their
+ * routers are given.  It serves whoever trains or tunes a router for the
+ * layer; counts is also what moe_residency_plan takes.
+ * The tokens come as n_segments sequences, seq_offsets int32 [n_segments + 1]
+ * (nondecreasing token offsets; NULL: one segment of all tokens).  A token
+ * whose mask byte is 0 (mask may be NULL), or that lies in no segment, takes
+ * no part.  With T_s the tokens of segment s that do, p = softmax(logits[t]):
+ *   counts[s][e] = pairs of the segment routed to e (an id outside [0, E) is
+ *                  not counted; an id twice in a token counts twice)
+ *   prob[s][e]   = 1/T_s sum_t p[t][e]                       (0 if T_s = 0)
+ *   loss[0]      = mean over the segments with T_s > 0 of
+ *                  sum_e E / (k T_s) counts[s][e] * prob[s][e]
+ *   loss[1]      = sum_t lse[t]^2 / sum_s T_s,  lse[t] = log sum_e exp(logits[t][e])
+ *                  (both 0 without tokens)
+ *   tokens[s]    = T_s; lse[t] = 0 for tokens that take no part
+ * A logit of -inf has probability 0; a row of nothing but -inf has p = 0,
+ * lse = -inf, adds 0 to the losses and counts in T_s.  Other non-finite values
+ * propagate.
+ * logits [n_tokens][n_experts] of type dtype (MOE_FP32, MOE_FP16, MOE_BF16)
+ * with row stride ld; topk_idx int32 [n][top_k]; loss fp32 [2]; counts int32
+ * [S][E]; tokens int32 [S]; prob fp32 [S][E]; lse fp32 [n].  n_experts 1 ..
+ * 1024, top_k 1 .. min(32, E), n_segments 1 .. 65535, n_tokens 1 .. 67108864.
+ * workspace: moe_balance_workspace(n, E, S) bytes, 256-byte aligned, any
+ * contents, used by one call at a time.  Sums are fp32 or wider in a fixed
+ * order: the same call gives the same bits every time.  All pointers are
+ * DEVICE pointers of the current device.  No allocation; asynchronous.
+ * moe_balance_workspace returns 0 for sizes out of range.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes),
+ * UNSUPPORTED (dtype), CUDA.
+ */
+size_t moe_balance_workspace(int n_tokens, int n_experts, int n_segments);
+int moe_balance_loss(const void *logits, int dtype, long long ld, int n_tokens, int n_experts,
+                     const int32_t *topk_idx, int top_k, const int32_t *seq_offsets,
+                     int n_segments, const uint8_t *mask, float *loss, int32_t *counts,
+                     int32_t *tokens, float *prob, float *lse, void *workspace,
+                     size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of the routing losses in the logits, from moe_balance_loss's lse,
+ * counts and tokens (counts do not move with the logits):
+ *   dlogits[t][e] = dloss[0] / (S' T_s) p_e (f_e - sum_j f_j p_j)
+ *                 + dloss[1] 2 lse[t] / T p_e
+ *                 + sum over j with topk_idx[t][j] = e of w_j (dw_j - sum_i w_i dw_i)
+ * with f_e = E / (k T_s) counts[s][e], S' the segments with tokens, T their
+ * sum.  The last term is the gradient through the renormalised top-k weights
+ * w (topk_w fp32 [n][k], as moe_route_topk gives them), with dw = dtopk_w
+ * (fp32 [n][k]) the gradient that arrives at them; it is left out when dtopk_w
+ * is NULL (topk_idx and topk_w may then be NULL).  An id outside [0, E) gets
+ * no gradient.  dloss fp32 [2] is device memory.  Tokens that take no part
+ * get 0 in their whole row.
+ * dlogits has the type of logits, row stride ldd, and may be logits itself.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes,
+ * overlap), UNSUPPORTED (dtype), CUDA.
+ */
+int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tokens,
+                          int n_experts, const int32_t *topk_idx, int top_k,
+                          const int32_t *seq_offsets, int n_segments, const uint8_t *mask,
+                          const float *lse, const int32_t *counts, const int32_t *tokens,
+                          const float *dloss, const float *topk_w, const float *dtopk_w,
+                          void *dlogits, long long ldd, void *stream);
 
 /* Facts about the layer (no device work). */
 int moe_layer_info(const moe_layer_t *layer, moe_layer_info_t *info);

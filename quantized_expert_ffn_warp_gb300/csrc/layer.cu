@@ -612,6 +612,16 @@ int norm_launch(const __half *r, const __half *g, float eps, int n, int H, __hal
 namespace qe {
 // Host helpers shared with the layer-free entry point.
 bool device_pointer(const void *p) { return is_device_ptr(p); }
+// Device memory of device `dev` (or managed memory).
+bool device_pointer_here(const void *p, int dev)
+{
+    cudaPointerAttributes a;
+    if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+        cudaGetLastError();
+        return false;
+    }
+    return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+}
 int router_k_slices(int H, int E, int n, int num_sms) { return choose_ks(H, E, n, num_sms); }
 }  // namespace qe
 

@@ -11,6 +11,8 @@ import os
 
 import numpy as np
 
+from .synth import GROUP
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmoe_layer.so")
 
@@ -25,6 +27,7 @@ MOE_STATUS_NONFINITE = 2
 MOE_STATUS_TIMEOUT = 4
 MOE_STATUS_TIER_OVERFLOW = 8
 MOE_NOALLOC_MAX_SCORES = 16384
+MOE_FP16, MOE_BF16, MOE_FP32 = 0, 1, 2
 PHASES = ("route", "group", "gate_up", "down", "combine")
 
 EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_route_topk", "moe_router_logits",
@@ -32,7 +35,9 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_route_topk", "moe_route
            "moe_profile_enable", "moe_profile_read", "moe_last_error",
            "moe_route_topk_noalloc", "moe_layer_set_gemm_min_tokens", "moe_rmsnorm",
            "moe_forward_prenorm", "moe_copy", "moe_layer_set_residency", "moe_residency_plan",
-           "moe_layer_tier_stats", "moe_layer_tier_slots", "moe_ep_dispatch", "moe_ep_combine")
+           "moe_layer_tier_stats", "moe_layer_tier_slots", "moe_ep_dispatch", "moe_ep_combine",
+           "moe_linear", "moe_linear_input_grad", "moe_balance_workspace", "moe_balance_loss",
+           "moe_balance_loss_grad")
 
 
 class MoeError(RuntimeError):
@@ -96,6 +101,13 @@ def load_library(path: str = LIB_PATH):
     lib.moe_layer_tier_slots.argtypes = [P, P, I]
     lib.moe_ep_dispatch.argtypes = [P, I, I, P, I, I, I, P, P, P, P, P, P]
     lib.moe_ep_combine.argtypes = [P, I, I, I, P, P, P, P, P, I, P, P]
+    L, Z = C.c_longlong, C.c_size_t
+    lib.moe_linear.argtypes = [P, P, P, I, I, I, P, L, I, I, P, P, L, P, L, P, P]
+    lib.moe_linear_input_grad.argtypes = [P, P, P, I, I, I, P, L, I, I, P, L, P, P]
+    lib.moe_balance_workspace.argtypes = [I, I, I]
+    lib.moe_balance_workspace.restype = Z
+    lib.moe_balance_loss.argtypes = [P, I, L, I, I, P, I, P, I, P, P, P, P, P, P, P, Z, P]
+    lib.moe_balance_loss_grad.argtypes = [P, I, L, I, I, P, I, P, I, P, P, P, P, P, P, P, P, L, P]
     lib.moe_last_error.restype = C.c_char_p
     lib.moe_last_error.argtypes = []
     _lib = lib
@@ -365,6 +377,176 @@ def copy(dst, src, stream=None):
     assert dst.numel() * dst.element_size() == nbytes
     _check(load_library().moe_copy(_ptr(dst), _ptr(src), nbytes, _stream(stream)))
     return dst
+
+
+def _bad(msg):
+    raise MoeError(MOE_ERR_INVALID_ARG, msg)
+
+
+def _need(t, name, dtypes, shape):
+    """t is a CUDA tensor of one of the types and of the shape, its rows
+    contiguous; returns (address, row stride in elements)."""
+    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_cuda:
+        _bad("%s: need a CUDA tensor %s of %s, got %s of %s on %s"
+             % (name, shape, " or ".join(map(str, dtypes)), tuple(t.shape), t.dtype, t.device))
+    w = shape[-1]
+    if (w > 1 and t.stride(-1) != 1) or (len(shape) == 2 and shape[0] > 1 and t.stride(0) < w):
+        _bad("%s: rows must be contiguous, got strides %s" % (name, t.stride()))
+    # the stride of a single row means nothing
+    return t.data_ptr(), (t.stride(0) if len(shape) == 2 and shape[0] > 1 else -(-w // 8) * 8)
+
+
+def _dense(t, name, dtypes, shape):
+    """As _need, for a contiguous tensor; its address."""
+    p, _ = _need(t, name, dtypes, shape)
+    if not t.is_contiguous():
+        _bad("%s: must be contiguous, got strides %s" % (name, t.stride()))
+    return p
+
+
+def _code_of(dtype):
+    import torch
+    code = {torch.float16: MOE_FP16, torch.bfloat16: MOE_BF16, torch.float32: MOE_FP32}.get(dtype)
+    if code is None:
+        raise MoeError(MOE_ERR_UNSUPPORTED, "dtype %s: need float16, bfloat16 or float32" % dtype)
+    return code
+
+
+def _w4(codes, scales, zeros, group_size):
+    """(rows, cols, addresses) of a 4-bit matrix in the canonical layout."""
+    import torch
+    if codes.dim() != 2 or group_size not in (32, 64, 128):
+        if codes.dim() == 2:
+            raise MoeError(MOE_ERR_UNSUPPORTED, "group_size must be 32, 64 or 128")
+        _bad("codes: need uint8 [rows, cols / 2], got shape %s" % (tuple(codes.shape),))
+    rows, cols = codes.shape[0], 2 * codes.shape[1]
+    meta = (rows, cols // group_size)
+    return rows, cols, (
+        _dense(codes, "codes", (torch.uint8,), (rows, codes.shape[1])),
+        _dense(scales, "scales", (torch.float16, torch.int16), meta),   # int16: fp16 bit patterns
+        _dense(zeros, "zeros", (torch.uint8,), meta))
+
+
+def linear(x, codes, scales, zeros, group_size=GROUP, bias=None, residual=None, out=None,
+           status=None, stream=None):
+    """y = x W^T (+ bias) (+ residual) with a 4-bit matrix in the canonical
+    layout (moe_linear): x fp16 or bf16 [n, cols] (rows may be strided), codes
+    uint8 [rows, cols / 2], scales fp16 and zeros uint8 [rows, cols /
+    group_size], bias [rows], residual and out [n, rows] of x's type.  out may
+    be residual itself."""
+    import torch
+    rows, cols, (pc, ps, pz) = _w4(codes, scales, zeros, group_size)
+    if x.dim() != 2:
+        _bad("x: need [n, cols], got shape %s" % (tuple(x.shape),))
+    n, dt = x.shape[0], (x.dtype,)
+    px, ldx = _need(x, "x", dt, (n, cols))
+    if out is None:
+        out = torch.empty((n, rows), dtype=x.dtype, device=x.device)
+    py, ldy = _need(out, "out", dt, (n, rows))
+    pb = None if bias is None else _dense(bias, "bias", dt, (rows,))
+    pr, ldr = (None, 0) if residual is None else _need(residual, "residual", dt, (n, rows))
+    pst = None if status is None else _dense(status, "status", (torch.int32,), (1,))
+    _check(load_library().moe_linear(pc, ps, pz, rows, cols, group_size, px, ldx, n,
+                                     _code_of(x.dtype), pb, pr, ldr, py, ldy, pst,
+                                     _stream(stream)))
+    return out
+
+
+def linear_input_grad(dy, codes, scales, zeros, group_size=GROUP, out=None, status=None,
+                      stream=None):
+    """dx = dy W, the gradient of linear's input through the frozen 4-bit
+    matrix (moe_linear_input_grad): dy fp16 or bf16 [n, rows] (rows may be
+    strided); dx [n, cols] of the same type."""
+    import torch
+    rows, cols, (pc, ps, pz) = _w4(codes, scales, zeros, group_size)
+    if dy.dim() != 2:
+        _bad("dy: need [n, rows], got shape %s" % (tuple(dy.shape),))
+    n, dt = dy.shape[0], (dy.dtype,)
+    pd, ldd = _need(dy, "dy", dt, (n, rows))
+    if out is None:
+        out = torch.empty((n, cols), dtype=dy.dtype, device=dy.device)
+    po, ldo = _need(out, "out", dt, (n, cols))
+    pst = None if status is None else _dense(status, "status", (torch.int32,), (1,))
+    _check(load_library().moe_linear_input_grad(pc, ps, pz, rows, cols, group_size, pd, ldd, n,
+                                                _code_of(dy.dtype), po, ldo, pst,
+                                                _stream(stream)))
+    return out
+
+
+def _batch(logits, topk_idx, seq_offsets, mask):
+    """Checked addresses and sizes of a routed batch."""
+    import torch
+    if logits.dim() != 2:
+        _bad("logits: need [n, E], got shape %s" % (tuple(logits.shape),))
+    n, E = logits.shape
+    code = _code_of(logits.dtype)
+    pl, ld = _need(logits, "logits", (logits.dtype,), (n, E))
+    pi, k = None, 1
+    if topk_idx is not None:
+        if topk_idx.dim() != 2:
+            _bad("topk_idx: need [n, k], got shape %s" % (tuple(topk_idx.shape),))
+        k = topk_idx.shape[1]
+        pi = _dense(topk_idx, "topk_idx", (torch.int32,), (n, k))
+    S, po = 1, None
+    if seq_offsets is not None:
+        S = seq_offsets.numel() - 1
+        po = _dense(seq_offsets, "seq_offsets", (torch.int32,), (S + 1,))
+    pm = None if mask is None else _dense(mask, "mask", (torch.uint8, torch.bool), (n,))
+    return n, E, k, S, code, pl, ld, pi, po, pm
+
+
+def balance_loss(logits, topk_idx, seq_offsets=None, mask=None, stream=None):
+    """Routing statistics and losses of a batch (moe_balance_loss): logits
+    fp32, fp16 or bf16 [n, E] (rows may be strided), topk_idx int32 [n, k],
+    seq_offsets int32 [S + 1] or None (one segment), mask uint8 or bool [n] or
+    None.  Returns dict(loss fp32 [2] = (balance, z), counts int32 [S, E],
+    tokens int32 [S], prob fp32 [S, E], lse fp32 [n]); balance_loss_grad takes
+    it, and counts.sum(0) is what residency_plan takes."""
+    import torch
+    if topk_idx is None:
+        _bad("topk_idx: need int32 [n, k]")
+    n, E, k, S, code, pl, ld, pi, po, pm = _batch(logits, topk_idx, seq_offsets, mask)
+    lib, dev = load_library(), logits.device
+    f32, i32 = torch.float32, torch.int32
+    r = dict(loss=torch.empty(2, dtype=f32, device=dev),
+             counts=torch.empty((S, E), dtype=i32, device=dev),
+             tokens=torch.empty(S, dtype=i32, device=dev),
+             prob=torch.empty((S, E), dtype=f32, device=dev),
+             lse=torch.empty(n, dtype=f32, device=dev))
+    size = lib.moe_balance_workspace(n, E, S)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    s = stream if stream is not None else torch.cuda.current_stream()
+    _check(lib.moe_balance_loss(pl, code, ld, n, E, pi, k, po, S, pm, r["loss"].data_ptr(),
+                                r["counts"].data_ptr(), r["tokens"].data_ptr(),
+                                r["prob"].data_ptr(), r["lse"].data_ptr(), ws.data_ptr(), size,
+                                s.cuda_stream))
+    if stream is not None:      # the workspace is freed to its own stream's pool on return
+        ws.record_stream(stream)
+    return r
+
+
+def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, seq_offsets=None,
+                      mask=None, out=None, stream=None):
+    """Gradient of balance_loss in the logits (moe_balance_loss_grad): fwd is
+    balance_loss's result (its lse, counts and tokens are read), dloss fp32 [2]
+    the gradients of the two losses on the device.  With dtopk_w fp32 [n, k],
+    the gradient of the renormalised top-k weights topk_w fp32 [n, k], the
+    gradient through them is added.  out may be logits itself."""
+    import torch
+    n, E, k, S, code, pl, ld, pi, po, pm = _batch(logits, topk_idx, seq_offsets, mask)
+    f32, i32 = (torch.float32,), (torch.int32,)
+    if dtopk_w is not None and (topk_idx is None or topk_w is None):
+        _bad("dtopk_w needs topk_idx and topk_w")
+    pw = None if dtopk_w is None else _dense(topk_w, "topk_w", f32, (n, k))
+    pdw = None if dtopk_w is None else _dense(dtopk_w, "dtopk_w", f32, (n, k))
+    if out is None:
+        out = torch.empty((n, E), dtype=logits.dtype, device=logits.device)
+    pout, ldo = _need(out, "out", (logits.dtype,), (n, E))
+    _check(load_library().moe_balance_loss_grad(
+        pl, code, ld, n, E, pi, k, po, S, pm, _dense(fwd["lse"], "lse", f32, (n,)),
+        _dense(fwd["counts"], "counts", i32, (S, E)), _dense(fwd["tokens"], "tokens", i32, (S,)),
+        _dense(dloss, "dloss", f32, (2,)), pw, pdw, pout, ldo, _stream(stream)))
+    return out
 
 
 def forward_host(layer: MoeLayer, x_host, out_host, stream=None, norm=None):

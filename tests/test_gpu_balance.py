@@ -1,0 +1,330 @@
+"""Routing losses and their gradient against a 64-bit evaluation.
+
+Tolerances (h = 2^-24, half an fp32 step): exp of a rounded difference d has a
+relative error of at most (|d| + 4) h, with |d| below 100 wherever the result
+matters; a sum of N terms in any order at most N h of the sum of magnitudes;
+16-bit outputs add half a step of their type.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+DT = {"fp32": torch.float32, "fp16": torch.float16, "bf16": torch.bfloat16}
+H = 2.0 ** -24
+INF = float("inf")
+
+
+def _moe():
+    from quantized_expert_ffn_warp_gb300 import moe
+    return moe
+
+
+def batch(n, E, k, seed, dtype=torch.float32, spread=2.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    logits = (spread * torch.randn((n, E), device="cuda", generator=g)).to(dtype)
+    idx = torch.topk(logits.float(), k, dim=1).indices.to(torch.int32).contiguous()
+    sel = torch.gather(logits.float(), 1, idx.long())
+    w = torch.softmax(sel, 1).contiguous()
+    return logits, idx, w
+
+
+def tensors(seq, mask, n):
+    s = None if seq is None else torch.tensor(seq, dtype=torch.int32, device="cuda")
+    m = None
+    if mask is not None:
+        g = torch.Generator(device="cuda").manual_seed(77)
+        m = (torch.rand(n, device="cuda", generator=g) < mask).to(torch.uint8)
+    return s, m
+
+
+def reference(logits, idx, seq, mask):
+    """dict as balance_loss gives it, in 64 bits, by the definition."""
+    n, E = logits.shape
+    k = idx.shape[1]
+    seq = [0, n] if seq is None else seq.tolist()
+    S = len(seq) - 1
+    live = torch.zeros(n, dtype=torch.bool, device="cuda")
+    for s in range(S):
+        live[seq[s]:seq[s + 1]] = True
+    if mask is not None:
+        live &= mask != 0
+    l = logits.double()
+    lse = torch.where(live, torch.logsumexp(l, 1), 0.0)
+    p = torch.where(live[:, None], torch.exp(l - lse[:, None]), 0.0)
+    empty = live & (l == -INF).all(1)
+    p[empty] = 0
+    counts = torch.zeros((S, E), dtype=torch.int64)
+    prob = torch.zeros((S, E), dtype=torch.float64, device="cuda")
+    tokens, bal, parts = [], 0.0, 0
+    for s in range(S):
+        r = slice(seq[s], seq[s + 1])
+        T = int(live[r].sum())
+        tokens.append(T)
+        ids = idx[r][live[r]].reshape(-1)
+        ids = ids[(ids >= 0) & (ids < E)].long().cpu()
+        counts[s] = torch.bincount(ids, minlength=E)
+        if T:
+            parts += 1
+            prob[s] = p[r].sum(0) / T
+            bal = bal + (counts[s].cuda().double() * E / (k * T) * prob[s]).sum()
+    ltot = torch.where(empty, 0.0, lse)
+    z = (ltot ** 2).sum() / max(sum(tokens), 1)
+    bal = torch.as_tensor(bal, dtype=torch.float64, device="cuda") / max(parts, 1)
+    return dict(loss=torch.stack((bal, z)), counts=counts.int().cuda(), prob=prob, lse=lse,
+                tokens=torch.tensor(tokens, dtype=torch.int32, device="cuda"), p=p, live=live,
+                parts=parts, empty=empty)
+
+
+def reference_grad(logits, idx, ref, dloss, w, dw, seq):
+    n, E = logits.shape
+    k = idx.shape[1]
+    seq = [0, n] if seq is None else seq.tolist()
+    f, gs = torch.zeros((n, E), device="cuda").double(), torch.zeros(n, device="cuda").double()
+    for s in range(len(seq) - 1):
+        T = int(ref["tokens"][s])
+        if T:
+            f[seq[s]:seq[s + 1]] = ref["counts"][s].double() * E / (k * T)
+            gs[seq[s]:seq[s + 1]] = dloss[0].double() / (ref["parts"] * T)
+    p, lse = ref["p"], torch.where(ref["empty"], 0.0, ref["lse"])
+    total = max(int(ref["tokens"].sum()), 1)
+    dot = (f * p).sum(1, keepdim=True)
+    zt = (2 * dloss[1].double() * lse / total)[:, None]
+    g = p * ((f - dot) * gs[:, None] + zt)
+    size = p * ((f + dot) * gs[:, None].abs() + zt.abs())
+    if dw is not None:
+        w, dw = w.double(), dw.double()
+        d = w * (dw - (w * dw).sum(1, keepdim=True))
+        dm = w * (dw.abs() + (w * dw.abs()).sum(1, keepdim=True))
+        ok = (idx >= 0) & (idx < E) & ref["live"][:, None]
+        at = torch.where(ok, idx, 0).long()
+        g = g.scatter_add(1, at, torch.where(ok, d, 0.0))
+        size = size.scatter_add(1, at, torch.where(ok, dm, 0.0))
+    return g, size
+
+
+def check_forward(got, ref, n, E):
+    assert torch.equal(got["counts"], ref["counts"]) and torch.equal(got["tokens"], ref["tokens"])
+    fin = torch.isfinite(ref["lse"])
+    assert torch.equal(got["lse"][~fin].double(), ref["lse"][~fin])
+    le, lg = ref["lse"][fin], got["lse"][fin].double()
+    assert ((lg - le).abs() <= (104 + E) * H + 2 * H * le.abs()).all()
+    terms = 104 + E + n
+    assert ((got["prob"].double() - ref["prob"]).abs() <= terms * H * ref["prob"] + 1e-38).all()
+    a, b = got["loss"].double(), ref["loss"]
+    # a loss is a sum of non-negative terms; lse^2 doubles lse's relative error,
+    # which cancellation near lse = 0 can raise: its absolute error enters
+    lm = torch.where(fin, ref["lse"], 0.0).abs().max()
+    assert (a[0] - b[0]).abs() <= (terms + 8) * H * b[0] + 1e-38
+    assert (a[1] - b[1]).abs() <= (n + 16) * H * b[1] + 3 * lm * (104 + E + 2 * lm) * H
+
+
+def check_grad(got, ref, size, E, dtype):
+    err = (got.double() - ref).abs()
+    tol = (2 * (104 + E) + 200) * H * size + 1e-38
+    if dtype != torch.float32:
+        tol = tol + torch.finfo(dtype).eps / 2 * ref.abs() + torch.finfo(dtype).smallest_normal * \
+            torch.finfo(dtype).eps
+    assert (err <= tol).all(), (err / tol).max()
+
+
+CASES = [
+    # n, E, k, offsets, share of tokens kept by the mask
+    (1, 1, 1, None, None), (1, 8, 2, None, None), (7, 33, 32, None, None), (64, 64, 2, None, None),
+    (5, 100, 3, [0, 0, 2, 2, 5, 5], None), (1000, 256, 8, [0, 999, 1000], 0.9),
+    (777, 500, 4, [3, 3, 10, 500, 700], 0.5), (300, 1024, 8, None, 0.97),
+    (130, 130, 5, [0, 130], 0.0), (3000, 16, 2, list(range(0, 3001, 30)), 0.8),
+    (20000, 64, 6, [0, 1, 15000, 15000, 20000], None), (9, 3, 1, [9, 9], None),
+]
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,E,k,seq,keep", CASES)
+def test_losses_and_gradient(n, E, k, seq, keep, dtype):
+    moe = _moe()
+    logits, idx, w = batch(n, E, k, n + E, DT[dtype])
+    s, m = tensors(seq, keep, n)
+    got = moe.balance_loss(logits, idx, s, m)
+    ref = reference(logits, idx, s, m)
+    check_forward(got, ref, n, E)
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dw = torch.randn((n, k), device="cuda", generator=g)
+    for d in (None, dw):
+        out = moe.balance_loss_grad(logits, idx, got, dloss, w, d, s, m)
+        rg, size = reference_grad(logits, idx, ref, dloss, w, d, s)
+        check_grad(out, rg, size, E, DT[dtype])
+        assert (out[~ref["live"]] == 0).all()
+    # strided rows, and the gradient in the logits' place
+    wide = torch.full((n, E + 3), float("nan"), dtype=DT[dtype], device="cuda")
+    wide[:, :E] = logits
+    again = moe.balance_loss(wide[:, :E], idx, s, m)
+    for key in got:
+        assert torch.equal(again[key], got[key]), key
+    inplace = moe.balance_loss_grad(wide[:, :E], idx, got, dloss, w, dw, s, m, out=wide[:, :E])
+    assert torch.equal(inplace, out) and torch.isnan(wide[:, E:]).all()
+
+
+def test_gradient_against_differences():
+    """Central differences of the 64-bit losses in single logits, counts held:
+    their error is the third-order term, below 1e-5 at a step of 1e-3."""
+    moe = _moe()
+    n, E, k = 12, 10, 2
+    logits, idx, w = batch(n, E, k, 3)
+    s, m = tensors([0, 5, 12], None, n)
+    got = moe.balance_loss(logits, idx, s, m)
+    dloss = torch.tensor([1.0, 0.5], device="cuda")
+    dw = torch.linspace(-1, 1, n * k, device="cuda").view(n, k)
+    grad = moe.balance_loss_grad(logits, idx, got, dloss, w, dw, s, m).double()
+
+    def total(l):
+        r = reference(l, idx, s, m)
+        ws = torch.softmax(torch.gather(l.double(), 1, idx.long()), 1)
+        return (r["loss"] * dloss.double()).sum() + (ws * dw.double()).sum()
+
+    for t, e in [(0, 0), (3, 7), (4, int(idx[4, 0])), (5, int(idx[5, 1])), (11, 9)]:
+        h = torch.zeros_like(logits, dtype=torch.float64)
+        h[t, e] = 1e-3
+        fd = (total(logits.double() + h) - total(logits.double() - h)) / 2e-3
+        assert (fd - grad[t, e]).abs() <= 1e-5
+
+
+def test_masked_experts_rows_and_ids():
+    """-inf and lowest-value logits, rows of nothing but -inf, NaN in tokens
+    that take no part, ids out of range and twice in a token."""
+    moe = _moe()
+    n, E, k = 40, 70, 4
+    logits, idx, w = batch(n, E, k, 8)
+    logits[:, 5] = -INF
+    logits[3, 10:] = -INF
+    logits[4] = -INF
+    logits[4, 69] = 1.0
+    logits[6] = -INF
+    logits[7, 1:] = torch.finfo(torch.float32).min
+    logits[20] = float("nan")
+    logits[39] = INF
+    idx[2] = 11
+    idx[9] = torch.tensor([-1, E, 2 ** 31 - 1, 0])
+    idx[10] = torch.tensor([69, 3, 69, 3])
+    mask = torch.ones(n, dtype=torch.bool, device="cuda")
+    mask[20] = False
+    seq = torch.tensor([0, 8, 39], dtype=torch.int32, device="cuda")
+    got = moe.balance_loss(logits, idx, seq, mask)
+    ref = reference(logits, idx, seq, mask)
+    check_forward(got, ref, n, E)
+    dloss = torch.tensor([1.0, 1.0], device="cuda")
+    dw = torch.linspace(-2, 1, n * k, device="cuda").view(n, k)
+    out = moe.balance_loss_grad(logits, idx, got, dloss, w, dw, seq, mask)
+    rg, size = reference_grad(logits, idx, ref, dloss, w, dw, seq)
+    check_grad(out, rg, size, E, torch.float32)
+    assert (out[20] == 0).all() and (out[39] == 0).all()
+    # all that row 6 has is the gradient of its weights
+    free = torch.ones(E, dtype=torch.bool, device="cuda")
+    free[idx[6].long()] = False
+    assert (out[6][free] == 0).all()
+
+
+def test_non_finite_logits_propagate():
+    logits, idx, w = batch(6, 40, 2, 1)
+    logits[2, 7] = float("nan")
+    logits[3] = float("nan")
+    logits[4, 1] = INF
+    got = _moe().balance_loss(logits, idx)
+    bad = torch.tensor([0, 0, 1, 1, 1, 0], dtype=torch.bool, device="cuda")
+    assert torch.equal(torch.isnan(got["lse"]) | torch.isinf(got["lse"]), bad)
+    assert torch.isnan(got["loss"]).all() and torch.isnan(got["prob"]).any()
+    dloss = torch.ones(2, device="cuda")
+    grad = _moe().balance_loss_grad(logits, idx, got, dloss)
+    assert torch.equal(torch.isnan(grad).any(1), bad)
+
+
+def test_same_bits_streams_and_graphs():
+    moe = _moe()
+    n, E, k = 5000, 256, 8
+    logits, idx, w = batch(n, E, k, 1)
+    s, m = tensors([0, 100, 2500, 5000], 0.9, n)
+    dloss = torch.tensor([0.01, 0.001], device="cuda")
+    dw = torch.ones((n, k), device="cuda")
+    first = moe.balance_loss(logits, idx, s, m)
+    grad = moe.balance_loss_grad(logits, idx, first, dloss, w, dw, s, m)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for st in streams * 2:
+        with torch.cuda.stream(st):
+            f = moe.balance_loss(logits, idx, s, m)
+            got.append((f, moe.balance_loss_grad(logits, idx, f, dloss, w, dw, s, m)))
+    torch.cuda.synchronize()
+    for f, g in got:
+        assert all(torch.equal(f[q], first[q]) for q in first) and torch.equal(g, grad)
+    sl, si = logits.clone(), idx.clone()
+    graphs = []
+    for _ in range(2):              # two graphs, each with its own workspace
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            f = moe.balance_loss(sl, si, s, m)
+            g = moe.balance_loss_grad(sl, si, f, dloss, w, dw, s, m)
+        graphs.append((gr, f, g))
+    l2, i2, _ = batch(n, E, k, 2)
+    sl.copy_(l2)
+    si.copy_(i2)
+    torch.cuda.synchronize()
+    for st, (gr, _, _) in zip(streams, graphs):
+        with torch.cuda.stream(st):
+            gr.replay()
+    torch.cuda.synchronize()
+    want = moe.balance_loss(l2, i2, s, m)
+    wg = moe.balance_loss_grad(l2, i2, want, dloss, w, dw, s, m)
+    for _, f, g in graphs:
+        assert all(torch.equal(f[q], want[q]) for q in want) and torch.equal(g, wg)
+
+
+def test_router_tuning_step():
+    """The operators together, as a router behind a frozen 4-bit projection is
+    tuned: project, route with the library's router, losses, the gradient back
+    through the router and the projection, and the counts into the placement
+    of the experts."""
+    import numpy as np
+    from quantized_expert_ffn_warp_gb300 import synth
+    moe = _moe()
+    H, E, k, n, K = 256, 16, 2, 24, 512
+    g = torch.Generator(device="cuda").manual_seed(11)
+    codes = torch.randint(0, 256, (H, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    scales = (torch.rand((H, K // 128), device="cuda", generator=g) * 0.01 + 0.005).half()
+    zeros = torch.randint(6, 10, (H, K // 128), dtype=torch.uint8, device="cuda", generator=g)
+    spec = synth.LayerSpec("step", hidden=H, inter=256, n_experts=E, top_k=k, max_tokens=64)
+    layer = moe.MoeLayer.from_packed(synth.make_layer(spec))
+    x = (0.2 * torch.randn((n, K), device="cuda", generator=g)).half()
+    h = moe.linear(x, codes, scales, zeros)
+    r = layer.route_topk(h)
+    logits = layer.router_logits(h)
+    f = moe.balance_loss(logits, r["idx"])
+    assert torch.equal(f["counts"][0], r["counts"])
+    assert layer.forward_routed(h, r["idx"], r["w"]).isfinite().all()
+    plan = moe.residency_plan(f["counts"].sum(0).cpu().numpy(), 4)
+    counts = f["counts"].sum(0).cpu().numpy()
+    assert sorted(counts[plan].tolist()) == sorted(np.sort(counts)[-4:].tolist())
+
+    dloss = torch.tensor([1.0, 0.1], device="cuda")
+    dw = torch.randn((n, k), device="cuda", generator=g)
+    dl = moe.balance_loss_grad(logits, r["idx"], f, dloss, r["w"], dw)
+    wr = torch.from_numpy(synth.make_layer(spec).router_w.view(np.float16).astype(np.float64)).cuda()
+    dh = (dl.double() @ wr).half()
+    dx = moe.linear_input_grad(dh, codes, scales, zeros)
+
+    # the whole step in 64 bits through autograd, counts and ids held
+    q = torch.stack((codes & 15, codes >> 4), 2).reshape(H, K).double()
+    W = (q - zeros.double().repeat_interleave(128, 1)) * scales.double().repeat_interleave(128, 1)
+    xr = x.double().requires_grad_()
+    lr = (xr @ W.t()) @ wr.t()
+    lse = torch.logsumexp(lr, 1)
+    p = torch.exp(lr - lse[:, None])
+    bal = (f["counts"][0].double() * E / (k * n) * p.mean(0)).sum()
+    ws = torch.softmax(torch.gather(lr, 1, r["idx"].long()), 1)
+    loss = dloss[0] * bal + dloss[1] * (lse ** 2).mean() + (ws * dw).sum()
+    loss.backward()
+    # three fp16 roundings (h, dh, dx) and that of the weights; h's moves the
+    # logits by about 2^-11 of |h| |wr|, the losses' gradient no more than that
+    rel = (dx.double() - xr.grad).norm() / xr.grad.norm()
+    assert rel <= 16 * 2.0 ** -11
+    layer.close()
