@@ -378,12 +378,15 @@ cudaError_t launch_group_size(const W4Call &c, int grad, int num_sms, cudaStream
 
 }  // namespace
 
+bool linear_gemm_fits(const W4Call &c);
+cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int num_sms, cudaStream_t st);
 bool device_pointer_here(const void *p, int dev);
 int record_failure(int code, const char *msg);
 int record_success();
 
 namespace {
 
+constexpr int kFewTokens = 16;
 constexpr int kMaxRows = 1 << 20, kMaxCols = 1 << 16, kMaxTokens = 1 << 19;
 
 // The byte range of n rows of `width` 2-byte elements, ld elements apart.
@@ -441,8 +444,11 @@ int run_linear(const W4Call &c, int dtype, int grad, void *stream)
             return record_failure(MOE_ERR_INVALID_ARG,
                                   "arguments must be device pointers of the current device");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == MOE_FP16
-                              ? launch_group_size<__half>(c, grad, sms, st)
+    cudaError_t e;
+    if (c.n > kFewTokens && linear_gemm_fits(c))
+        e = launch_linear_gemm(c, dtype == MOE_BF16, grad, sms, st);
+    else
+        e = dtype == MOE_FP16 ? launch_group_size<__half>(c, grad, sms, st)
                               : launch_group_size<__nv_bfloat16>(c, grad, sms, st);
     if (e != cudaSuccess) {
         cudaGetLastError();

@@ -1,0 +1,628 @@
+// 4-bit group-quantised products for many tokens, on the tcgen05 tensor cores:
+//   y[t][r]  = sum_k x[t][k] W[r][k] (+ bias) (+ residual)      (GRAD = false)
+//   dx[t][k] = sum_r dy[t][r] W[r][k]                            (GRAD = true)
+//
+// The matrix stays packed in its canonical layout; a 128 x 128 block of it (8 KB
+// of codes: 128 rows of 64 bytes) is one TMA box, dequantised once per token
+// tile, W = (q - z) * s rounded once to the activations' type, into the MMA's A
+// operand in tensor memory (M = 128: the outputs' features).  The tokens
+// (up to 256 of them) are the MMA's N, their rows the B operand in shared
+// memory, read by TMA as they lie.  The contraction index runs along K of the
+// MMA in memory order in both directions:
+//   forward: a thread owns one weight row (its tensor-memory lane) and
+//     unpacks 64 of its K into 32 columns;
+//   gradient: the contraction runs over the weight rows, so a thread unpacks
+//     four columns of the matrix over pairs of rows (one byte permutation
+//     pairs two rows' nibbles) and stores them in the 16-lane x 256-bit tensor
+//     memory layout, lane 8 j + g of a quarter holding column 4 g + j.
+// Roles of a persistent CTA (one per SM): a code producer and a B producer
+// (TMA), two groups of four dequant warps taking alternate blocks, one or two
+// MMA warps, four epilogue warps.  Tiles of more than 128 tokens need one MMA
+// warp; smaller MMAs take less time than one thread needs to issue the next,
+// so two warps then run alternate 64-steps into accumulators of their own,
+// summed at the end.
+// A matrix with too few tiles for the SMs is split along the contraction over a
+// cluster of 2 to 8 CTAs, whose partial tiles meet in distributed shared
+// memory, in rank order.
+// Every wait is bounded in time; on expiry the output is incomplete and the
+// caller's status word gets MOE_STATUS_TIMEOUT.
+#include <algorithm>
+
+#include "tcgen05.cuh"
+#include "w4.cuh"
+
+namespace qe {
+
+namespace {
+
+constexpr int kM = 128;             // output features per tile (MMA M)
+constexpr int kBlk = 128;           // contraction elements per code block
+constexpr int kBlkBytes = 128 * 64; // codes of a block
+constexpr int kDeq = 8, kEpi = 4;   // warps
+constexpr int kEpi0 = kDeq, kProd = kDeq + kEpi, kBProd = kProd + 1, kMma0 = kProd + 2;
+constexpr int kGemmThreads = (kMma0 + 2) * 32;
+
+template <int TOK>
+struct LGeo {
+    static constexpr int chains = TOK > 128 ? 1 : 2;
+    static constexpr int acc_cols = chains * TOK;       // accumulator columns
+    static constexpr int a_cols = 32;                   // 64 contraction elements, two per column
+    static constexpr int b_stage = TOK * 128;           // TOK rows of 64 elements
+    // A and B stages (64 contraction elements each), in lockstep
+    static constexpr int as = TOK > 128 ? 6 : TOK > 64 ? 8 : 12;
+    static constexpr int cs = TOK > 128 ? 4 : TOK > 64 ? 8 : 12;    // code blocks
+    static constexpr int b_off = 0, c_off = as * b_stage;
+    static constexpr int bar_off = c_off + cs * kBlkBytes;
+    static constexpr int nbars = 2 * cs + 3 * as + 4;
+    static constexpr int smem = bar_off + 8 * nbars + 16 + 1024;
+};
+static_assert(LGeo<256>::smem <= 227 * 1024 && LGeo<128>::smem <= 227 * 1024, "shared memory");
+static_assert(LGeo<256>::acc_cols + LGeo<256>::as * 32 <= 512 &&
+                  LGeo<128>::acc_cols + LGeo<128>::as * 32 <= 512 &&
+                  LGeo<64>::acc_cols + LGeo<64>::as * 32 <= 512,
+              "tensor memory");
+static_assert(128 * 128 * 4 <= LGeo<128>::c_off && 128 * 64 * 4 <= LGeo<64>::c_off,
+              "a partial tile fits in the B stages");
+
+struct GemmCall {
+    W4Call c;
+    int tok;            // tokens per tile: a multiple of 16, at most TOK
+    int mt, nt;         // tiles along the features and the tokens
+    int splits;         // CTAs of a cluster along the contraction
+};
+
+// 16 lanes x 32 columns from the warp's registers, 16x256b layout: of every 8
+// columns thread (g, t) writes lane g, columns 2 t and 2 t + 1, then lane g + 8.
+__device__ __forceinline__ void tmem_st_16x256(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+          "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+          "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync()
+{
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void store_out(const W4Call &c, float v, int tok, int f)
+{
+    using Q = W4<T>;
+    if (c.bias)
+        v += Q::to_float(static_cast<const T *>(c.bias)[f]);
+    if (c.residual)
+        v += Q::to_float(static_cast<const T *>(c.residual)[tok * c.ldr + f]);
+    static_cast<T *>(c.out)[tok * c.ldo + f] = Q::from_float(v);
+}
+
+// Feature of tensor-memory lane m of a tile.
+template <bool GRAD>
+__device__ __forceinline__ int lane_feature(int m)
+{
+    return GRAD ? (m & ~31) | ((m & 7) << 2) | ((m >> 3) & 3) : m;
+}
+
+template <typename T, bool GRAD, int TOK>
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    linear_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
+                       const __grid_constant__ CUtensorMap bmap, const GemmCall a)
+{
+    using G = LGeo<TOK>;
+    using Q = W4<T>;
+    constexpr bool kBf16 = sizeof(typename Q::Scale) == 8;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G::bar_off);
+    const uint32_t code_full = saddr(bars), code_empty = code_full + 8 * G::cs;
+    const uint32_t a_full = code_empty + 8 * G::cs, b_full = a_full + 8 * G::as;
+    const uint32_t stage_empty = b_full + 8 * G::as;    // the MMAs on A and B stage s are done
+    const uint32_t acc_full = stage_empty + 8 * G::as, acc_empty = acc_full + 8;
+    const uint32_t drain = acc_empty + 8;               // [2]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + G::nbars);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < G::cs; s++) {
+            bar_init(code_full + 8 * s, 1);
+            bar_init(code_empty + 8 * s, kDeq / 2);
+        }
+        for (int s = 0; s < G::as; s++) {
+            bar_init(a_full + 8 * s, kDeq / 2);
+            bar_init(b_full + 8 * s, 1);
+            bar_init(stage_empty + 8 * s, 1);
+        }
+        bar_init(acc_full, G::chains);
+        bar_init(acc_empty, kEpi);
+        bar_init(drain, 1);
+        bar_init(drain + 8, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMma0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                     ::"r"(saddr(tmem_slot)), "r"(512u)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_enter();
+
+    const W4Call &c = a.c;
+    const int C = GRAD ? c.w.rows : c.w.K;      // contraction length
+    const int F = GRAD ? c.w.K : c.w.rows;      // output features
+    const int blocks = (C + kBlk - 1) / kBlk;
+    const int rank = blockIdx.x % a.splits;
+    const int blk0 = (int)((long long)blocks * rank / a.splits);
+    const int blk1 = (int)((long long)blocks * (rank + 1) / a.splits);
+    // 64-steps of this CTA: two per block, one when the contraction ends in its first half
+    const int nsteps = 2 * (blk1 - blk0) - (blk1 == blocks && blk1 > blk0 && C - (blocks - 1) * kBlk <= 64);
+    const int tile0 = blockIdx.x / a.splits, tile_step = gridDim.x / a.splits;
+    const int tiles = a.mt * a.nt;
+    bool ok = true;
+
+    if (warp == kProd) {
+        // -------------------------------------------------------- code producer
+        if (lane == 0) {
+            unsigned cc = 0;
+            for (int t = tile0; t < tiles && ok; t += tile_step) {
+                const int m0 = t % a.mt * kM;
+                for (int b = blk0; b < blk1; b++, cc++) {
+                    const uint32_t s = cc % G::cs;
+                    if (!bar_wait(code_empty + 8 * s, ((cc / G::cs) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    bar_expect_tx(code_full + 8 * s, kBlkBytes);
+                    tma_load_2d(saddr(smem + G::c_off + s * kBlkBytes), &wmap,
+                                GRAD ? m0 / 2 : b * (kBlk / 2), GRAD ? b * kBlk : m0,
+                                code_full + 8 * s);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                for (unsigned i = cc > (unsigned)G::cs ? cc - G::cs : 0; i < cc; i++) {
+                    const unsigned long long t0 = now_ns();
+                    while (!bar_try(code_full + 8 * (i % G::cs), (i / G::cs) & 1) &&
+                           now_ns() - t0 < kGWaitNs) {
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp == kBProd) {
+        // -------------------------------------------------------- B producer
+        if (lane == 0) {
+            unsigned bc = 0;
+            for (int t = tile0; t < tiles && ok; t += tile_step) {
+                const int tok0 = t / a.mt * a.tok;
+                for (int j = 0; j < nsteps; j++, bc++) {
+                    const uint32_t s = bc % G::as;
+                    if (!bar_wait(stage_empty + 8 * s, ((bc / G::as) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    bar_expect_tx(b_full + 8 * s, a.tok * 128);
+                    tma_load_2d(saddr(smem + G::b_off + s * G::b_stage), &bmap,
+                                blk0 * kBlk + j * 64, tok0, b_full + 8 * s);
+                }
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                for (unsigned i = bc > (unsigned)G::as ? bc - G::as : 0; i < bc; i++) {
+                    const unsigned long long t0 = now_ns();
+                    while (!bar_try(b_full + 8 * (i % G::as), (i / G::as) & 1) &&
+                           now_ns() - t0 < kGWaitNs) {
+                    }
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kMma0) {
+        // -------------------------------------------------------- MMA issuers
+        // chain ch takes the steps of its parity into its own accumulator
+        const int ch = warp - kMma0;
+        if (lane == 0 && ch < G::chains) {
+            const uint32_t idesc = idesc_f16(a.tok, kBf16);
+            const uint32_t dacc = tmem + ch * TOK;
+            unsigned ac = 0, ti = 0;
+            bool issued = false;
+            for (int t = tile0; t < tiles && ok; t += tile_step, ti++) {
+                if (!bar_wait(acc_empty, (ti & 1) ^ 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                for (int j = 0; j < nsteps; j++, ac++) {
+                    if (G::chains == 2 && (j & 1) != ch)
+                        continue;
+                    const uint32_t s = ac % G::as, par = (ac / G::as) & 1;
+                    if (!bar_wait(a_full + 8 * s, par, abort_flag) ||
+                        !bar_wait(b_full + 8 * s, par, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t abase = tmem + G::acc_cols + s * G::a_cols;
+                    const uint32_t bbase = saddr(smem + G::b_off + s * G::b_stage);
+#pragma unroll
+                    for (int kk = 0; kk < 4; kk++)      // 16 each: A 8 columns, B 32 bytes
+                        umma_ta(dacc, abase + kk * 8, sw128_desc(bbase + kk * 32), idesc,
+                                j >= G::chains || kk ? 1u : 0u);
+                    issued = true;
+                    umma_commit(stage_empty + 8 * s);
+                }
+                if (ok)
+                    umma_commit(acc_full);
+            }
+            if (!ok)
+                *abort_flag = 1;
+            if (issued) {   // every MMA issued has completed before the memory is freed
+                umma_commit(drain + 8 * ch);
+                const unsigned long long t0 = now_ns();
+                while (!bar_try(drain + 8 * ch, 0) && now_ns() - t0 < kGWaitNs) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp >= kEpi0) {
+        // -------------------------------------------------------- epilogue
+        const int q = warp & 3;
+        unsigned ti = 0;
+        for (int t = tile0; t < tiles && ok; t += tile_step, ti++) {
+            if (!bar_wait(acc_full, ti & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            const int f = t % a.mt * kM + lane_feature<GRAD>(32 * q + lane);
+            const int tok0 = t / a.mt * a.tok;
+            const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
+            const bool two = G::chains == 2 && nsteps > 1;
+            float *part = reinterpret_cast<float *>(smem + G::b_off);
+            for (int c0 = 0; c0 < a.tok && tok0 + c0 < c.n; c0 += 16) {
+                float d[16], e[16];
+                tmem_ld16(taddr + c0, d);
+                if (two) {
+                    tmem_ld16(taddr + TOK + c0, e);
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        d[i] += e[i];
+                }
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    if (a.splits > 1)
+                        part[(c0 + i) * kM + 32 * q + lane] = d[i];
+                    else if (f < F && tok0 + c0 + i < c.n)
+                        store_out<T>(c, d[i], tok0 + c0 + i, f);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(acc_empty);
+        }
+        if (!ok && lane == 0)
+            *abort_flag = 1;
+        __syncwarp();
+    } else {
+        // -------------------------------------------------------- dequant
+        const int q = warp & 3, wg = warp >> 2, g = lane >> 2, tq = lane & 3;
+        const uint32_t tlane = (uint32_t)(32 * q) << 16;
+        const int ng = c.w.K / c.w.group, gsh = c.w.group == 128 ? 7 : c.w.group == 64 ? 6 : 5;
+        unsigned cc = 0, ac = 0;
+        for (int t = tile0; t < tiles && ok; t += tile_step) {
+            const int m0 = t % a.mt * kM;
+            for (int b = blk0; b < blk1 && ok; b++, cc++) {
+                const int steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
+                if ((cc & 1) != (unsigned)wg) {
+                    ac += steps;
+                    continue;
+                }
+                // scale << 16 | zero point, 0 outside the matrix: forward, of this
+                // thread's row for each 32 K of the block; gradient, of the rows
+                // lane + 32 i for this quarter's columns
+                uint32_t meta[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int row = GRAD ? b * kBlk + 32 * i + lane : m0 + 32 * q + lane;
+                    const int k = GRAD ? m0 + 32 * q : b * kBlk + 32 * i;
+                    if (!GRAD && i > 0 && (k & (c.w.group - 1))) {
+                        meta[i] = meta[i - 1];
+                    } else {
+                        const long long at = (long long)row * ng + (k >> gsh);
+                        meta[i] = row < c.w.rows && k < c.w.K
+                                      ? (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at]
+                                      : 0;
+                    }
+                }
+                const uint32_t s = cc % G::cs;
+                if (!bar_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
+                    ok = false;
+                    break;
+                }
+                const uint8_t *blk = smem + G::c_off + s * kBlkBytes;
+                uint4 cw[4];
+                if (!GRAD) {
+                    // row r's 16-byte chunk i sits at i ^ (r / 2 % 4) (64-byte swizzle)
+                    const int r = 32 * q + lane;
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
+                                                                 ((i ^ ((r >> 1) & 3)) << 4));
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(code_empty + 8 * s);
+                }
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    if (h >= steps)
+                        break;
+                    const uint32_t as = ac % G::as;
+                    uint32_t col[32];
+                    if (!GRAD) {
+#pragma unroll
+                        for (int i = 0; i < 2; i++) {
+                            const uint32_t m = meta[2 * h + i];
+                            const typename Q::Zero z = Q::zero(m & 0xff, m & 0xff);
+                            const typename Q::Scale sc = Q::scale(m >> 16, m >> 16);
+                            const uint4 v = cw[2 * h + i];
+                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                            for (int u = 0; u < 4; u++) {
+                                uint32_t p[4];
+                                Q::unpack(w[u], z, p);
+#pragma unroll
+                                for (int n = 0; n < 4; n++)
+                                    p[n] = Q::mul(p[n], sc);
+                                // fields (i, i + 4) into memory order
+                                col[16 * i + 4 * u] = __byte_perm(p[0], p[1], 0x5410);
+                                col[16 * i + 4 * u + 1] = __byte_perm(p[2], p[3], 0x5410);
+                                col[16 * i + 4 * u + 2] = __byte_perm(p[0], p[1], 0x7632);
+                                col[16 * i + 4 * u + 3] = __byte_perm(p[2], p[3], 0x7632);
+                            }
+                        }
+                    } else {
+                        const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+                        for (int ss = 0; ss < 4; ss++) {        // 16 rows each
+                            uint32_t w[4], m[4];
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int r = 64 * h + 16 * ss + 4 * tq + i;
+                                w[i] = *reinterpret_cast<const uint32_t *>(
+                                    blk + r * 64 + ((q ^ ((r >> 1) & 3)) << 4) + 4 * (g >> 1));
+                                m[i] = __shfl_sync(0xffffffffu, meta[2 * h + (ss >> 1)],
+                                                   16 * (ss & 1) + 4 * tq + i);
+                            }
+                            const typename Q::Zero z01 = Q::zero(m[0] & 0xff, m[1] & 0xff);
+                            const typename Q::Zero z23 = Q::zero(m[2] & 0xff, m[3] & 0xff);
+                            const typename Q::Scale s01 = Q::scale(m[0] >> 16, m[1] >> 16);
+                            const typename Q::Scale s23 = Q::scale(m[2] >> 16, m[3] >> 16);
+                            uint32_t p[4], r[4];
+                            Q::unpack(__byte_perm(w[0], w[1], sel), z01, p);
+                            Q::unpack(__byte_perm(w[2], w[3], sel), z23, r);
+                            // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
+#pragma unroll
+                            for (int u = 0; u < 4; u++) {
+                                const int at = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
+                                col[at] = Q::mul(p[u], s01);
+                                col[at + 1] = Q::mul(r[u], s23);
+                            }
+                        }
+                        if (h + 1 == steps) {
+                            __syncwarp();
+                            if (lane == 0)
+                                bar_arrive(code_empty + 8 * s);
+                        }
+                    }
+                    if (!bar_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t at = tmem + tlane + G::acc_cols + as * G::a_cols;
+                    if (!GRAD) {
+                        tmem_st32(at, col);
+                    } else {
+                        uint32_t lo[16], hi[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            lo[i] = col[i];
+                            hi[i] = col[16 + i];
+                        }
+                        tmem_st_16x256(at, lo);
+                        tmem_st_16x256(at + (16u << 16), hi);
+                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        bar_arrive(a_full + 8 * as);
+                    ac++;
+                }
+            }
+        }
+        if (!ok && lane == 0)
+            *abort_flag = 1;
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMma0)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
+                     : "memory");
+    if (threadIdx.x == 0 && *abort_flag && c.status)
+        atomicOr(c.status, MOE_STATUS_TIMEOUT);
+    if (a.splits > 1) {
+        // the one tile of this cluster: rank r adds its share of the tokens
+        cluster_sync();
+        const int m0 = tile0 % a.mt * kM, tok0 = tile0 / a.mt * a.tok;
+        const int lo = a.tok * rank / a.splits, hi = a.tok * (rank + 1) / a.splits;
+        const uint32_t base = saddr(smem + G::b_off);
+        for (int i = lo * kM + threadIdx.x; i < hi * kM; i += kGemmThreads) {
+            const int tok = tok0 + i / kM, f = m0 + lane_feature<GRAD>(i % kM);
+            if (tok >= c.n || f >= F)
+                continue;
+            float v = 0.f;
+            for (int r = 0; r < a.splits; r++) {
+                uint32_t remote;
+                float p;
+                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + 4 * i), "r"(r));
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(remote));
+                v += p;
+            }
+            store_out<T>(c, v, tok, f);
+        }
+        cluster_sync();     // a CTA's shared memory stays until its peers have read it
+    }
+}
+
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encoder()
+{
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
+}
+
+bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+            uint64_t rows, uint64_t pitch, uint32_t box_cols, uint32_t box_rows,
+            CUtensorMapSwizzle swizzle)
+{
+    const EncodeFn fn = encoder();
+    if (!fn)
+        return false;
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {pitch};
+    const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+    return fn(map, type, 2, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Plan {
+    int tok, nt, splits;
+};
+
+// Tokens per tile and splits along the contraction: the smallest estimated time,
+// in SM cycles, of the busiest SM.  A 64-step of a tile of N tokens takes 2 N
+// cycles on the tensor core and, on the weights' side, at least about 220
+// (dequantisation, and the packed block's share of the HBM rate); a tile costs
+// its epilogue and a cluster the exchange of its partial tiles.
+Plan plan(int C, int F, int n, int num_sms)
+{
+    const int mt = (F + kM - 1) / kM, steps = (C + 63) / 64;
+    Plan best{};
+    double least = 0;
+    for (int nt = (n + 255) / 256; nt <= (n + 15) / 16; nt++) {
+        const int tok = ((n + nt - 1) / nt + 15) / 16 * 16;
+        if ((n + tok - 1) / tok != nt)
+            continue;
+        for (int s = 1; s == 1 || (s <= (tok <= 128 ? 8 : 1) && 4 * s <= steps); s *= 2) {
+            const long long ctas = (long long)mt * nt * s;
+            if (s > 1 && ctas > num_sms)
+                break;
+            const double waves = (double)((ctas + num_sms - 1) / num_sms);
+            const double step = std::max(2.0 * tok, 220.0);
+            const double cost = waves * ((double)(steps + s - 1) / s * step + 12.0 * tok + 1500) +
+                                (s > 1 ? 1500 + 6.0 * tok : 0);
+            if (!best.tok || cost < least) {
+                best = {tok, nt, s};
+                least = cost;
+            }
+        }
+        if (tok <= 32)
+            break;
+    }
+    return best;
+}
+
+template <typename T, bool GRAD, int TOK>
+cudaError_t launch(const GemmCall &a, const CUtensorMap &wmap, const CUtensorMap &bmap, int num_sms,
+                   cudaStream_t st)
+{
+    auto kernel = linear_gemm_kernel<T, GRAD, TOK>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LGeo<TOK>::smem);
+    if (e != cudaSuccess)
+        return e;
+    const long long tiles = (long long)a.mt * a.nt;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.splits > 1 ? tiles * a.splits : std::min<long long>(tiles, num_sms)));
+    cfg.blockDim = dim3(kGemmThreads);
+    cfg.dynamicSmemBytes = LGeo<TOK>::smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, wmap, bmap, a);
+}
+
+template <typename T, bool GRAD>
+cudaError_t launch_tok(const GemmCall &a, const CUtensorMap &wmap, const CUtensorMap &bmap,
+                       int num_sms, cudaStream_t st)
+{
+    if (a.tok > 128)
+        return launch<T, GRAD, 256>(a, wmap, bmap, num_sms, st);
+    if (a.tok > 64)
+        return launch<T, GRAD, 128>(a, wmap, bmap, num_sms, st);
+    return launch<T, GRAD, 64>(a, wmap, bmap, num_sms, st);
+}
+
+}  // namespace
+
+// Whether the activations can be read by TMA (rows on 16-byte boundaries).
+bool linear_gemm_fits(const W4Call &c)
+{
+    return reinterpret_cast<uintptr_t>(c.in) % 16 == 0 && c.ldi % 8 == 0;
+}
+
+cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int num_sms, cudaStream_t st)
+{
+    const int C = grad ? c.w.rows : c.w.K, F = grad ? c.w.K : c.w.rows;
+    const Plan p = plan(C, F, c.n, num_sms);
+    GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits};
+    CUtensorMap wmap, bmap;
+    if (!encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
+                128, CU_TENSOR_MAP_SWIZZLE_64B) ||
+        !encode(&bmap, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                c.in, C, c.n, 2 * c.ldi, 64, p.tok, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    if (bf16)
+        return grad ? launch_tok<__nv_bfloat16, true>(a, wmap, bmap, num_sms, st)
+                    : launch_tok<__nv_bfloat16, false>(a, wmap, bmap, num_sms, st);
+    return grad ? launch_tok<__half, true>(a, wmap, bmap, num_sms, st)
+                : launch_tok<__half, false>(a, wmap, bmap, num_sms, st);
+}
+
+}  // namespace qe
