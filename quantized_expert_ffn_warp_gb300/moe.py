@@ -67,6 +67,7 @@ class LayerInfo(C.Structure):
 
 
 _lib = None
+_torch = None
 
 
 def load_library(path: str = LIB_PATH):
@@ -383,48 +384,70 @@ def _bad(msg):
     raise MoeError(MOE_ERR_INVALID_ARG, msg)
 
 
-def _need(t, name, dtypes, shape):
-    """t is a CUDA tensor of one of the types and of the shape, its rows
-    contiguous; returns (address, row stride in elements)."""
-    if t.dtype not in dtypes or tuple(t.shape) != shape or not t.is_cuda:
-        _bad("%s: need a CUDA tensor %s of %s, got %s of %s on %s"
-             % (name, shape, " or ".join(map(str, dtypes)), tuple(t.shape), t.dtype, t.device))
-    w = shape[-1]
-    if (w > 1 and t.stride(-1) != 1) or (len(shape) == 2 and shape[0] > 1 and t.stride(0) < w):
-        _bad("%s: rows must be contiguous, got strides %s" % (name, t.stride()))
-    # the stride of a single row means nothing
-    return t.data_ptr(), (t.stride(0) if len(shape) == 2 and shape[0] > 1 else -(-w // 8) * 8)
+def _refuse(t, name, dtype, shape):
+    _bad("%s: need %s of %s with contiguous rows, got %s of %s, strides %s"
+         % (name, tuple(shape), dtype, tuple(t.shape), t.dtype, t.stride()))
 
 
-def _dense(t, name, dtypes, shape):
-    """As _need, for a contiguous tensor; its address."""
-    p, _ = _need(t, name, dtypes, shape)
-    if not t.is_contiguous():
-        _bad("%s: must be contiguous, got strides %s" % (name, t.stride()))
-    return p
+def _rows(t, name, dtype, n, w):
+    """Address and row stride (elements) of t, [n, w] of dtype with contiguous
+    rows.  Devices are checked by the library."""
+    if t.shape != (n, w) or t.dtype is not dtype:
+        _refuse(t, name, dtype, (n, w))
+    ld, one = t.stride()
+    if one != 1 and w > 1:
+        _refuse(t, name, dtype, (n, w))
+    if n == 1:
+        ld = (w + 7) & -8       # the stride of a single row means nothing
+    return t.data_ptr(), ld
 
 
-def _code_of(dtype):
-    import torch
-    code = {torch.float16: MOE_FP16, torch.bfloat16: MOE_BF16, torch.float32: MOE_FP32}.get(dtype)
+def _dense(t, name, dtype, shape):
+    """Address of t, contiguous, of the type and the shape."""
+    if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, name, dtype, shape)
+    return t.data_ptr()
+
+
+def _raw_stream(t, stream):
+    """Stream handle: the given stream, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    index = t.device.index
+    if index is None:
+        _bad("need CUDA tensors, got one on %s" % t.device)
+    return _types()[0]._C._cuda_getCurrentRawStream(index)
+
+
+def _types():
+    """(torch, its types' codes), looked up once."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = (torch, {torch.float16: MOE_FP16, torch.bfloat16: MOE_BF16,
+                          torch.float32: MOE_FP32})
+    return _torch
+
+
+def _code_of(dtype, codes):
+    code = codes.get(dtype)
     if code is None:
         raise MoeError(MOE_ERR_UNSUPPORTED, "dtype %s: need float16, bfloat16 or float32" % dtype)
     return code
 
 
-def _w4(codes, scales, zeros, group_size):
-    """(rows, cols, addresses) of a 4-bit matrix in the canonical layout."""
-    import torch
-    if codes.dim() != 2 or group_size not in (32, 64, 128):
-        if codes.dim() == 2:
-            raise MoeError(MOE_ERR_UNSUPPORTED, "group_size must be 32, 64 or 128")
+def _w4(torch, codes, scales, zeros, group_size):
+    """rows, cols and addresses of a 4-bit matrix in the canonical layout."""
+    if group_size not in (32, 64, 128):
+        raise MoeError(MOE_ERR_UNSUPPORTED, "group_size must be 32, 64 or 128")
+    if codes.dim() != 2:
         _bad("codes: need uint8 [rows, cols / 2], got shape %s" % (tuple(codes.shape),))
-    rows, cols = codes.shape[0], 2 * codes.shape[1]
-    meta = (rows, cols // group_size)
-    return rows, cols, (
-        _dense(codes, "codes", (torch.uint8,), (rows, codes.shape[1])),
-        _dense(scales, "scales", (torch.float16, torch.int16), meta),   # int16: fp16 bit patterns
-        _dense(zeros, "zeros", (torch.uint8,), meta))
+    rows, half = codes.shape
+    meta = (rows, 2 * half // group_size)
+    # scales may be fp16 or their bit patterns, as upload() lays them out
+    sdt = torch.int16 if scales.dtype is torch.int16 else torch.float16
+    return (rows, 2 * half, _dense(codes, "codes", torch.uint8, (rows, half)),
+            _dense(scales, "scales", sdt, meta), _dense(zeros, "zeros", torch.uint8, meta))
 
 
 def linear(x, codes, scales, zeros, group_size=GROUP, bias=None, residual=None, out=None,
@@ -434,21 +457,25 @@ def linear(x, codes, scales, zeros, group_size=GROUP, bias=None, residual=None, 
     uint8 [rows, cols / 2], scales fp16 and zeros uint8 [rows, cols /
     group_size], bias [rows], residual and out [n, rows] of x's type.  out may
     be residual itself."""
-    import torch
-    rows, cols, (pc, ps, pz) = _w4(codes, scales, zeros, group_size)
+    torch, types = _types()
+    rows, cols, pc, ps, pz = _w4(torch, codes, scales, zeros, group_size)
     if x.dim() != 2:
         _bad("x: need [n, cols], got shape %s" % (tuple(x.shape),))
-    n, dt = x.shape[0], (x.dtype,)
-    px, ldx = _need(x, "x", dt, (n, cols))
+    n, dt = x.shape[0], x.dtype
+    px, ldx = _rows(x, "x", dt, n, cols)
     if out is None:
-        out = torch.empty((n, rows), dtype=x.dtype, device=x.device)
-    py, ldy = _need(out, "out", dt, (n, rows))
+        out, ldy = torch.empty((n, rows), dtype=dt, device=x.device), rows
+        py = out.data_ptr()
+    else:
+        py, ldy = _rows(out, "out", dt, n, rows)
     pb = None if bias is None else _dense(bias, "bias", dt, (rows,))
-    pr, ldr = (None, 0) if residual is None else _need(residual, "residual", dt, (n, rows))
-    pst = None if status is None else _dense(status, "status", (torch.int32,), (1,))
-    _check(load_library().moe_linear(pc, ps, pz, rows, cols, group_size, px, ldx, n,
-                                     _code_of(x.dtype), pb, pr, ldr, py, ldy, pst,
-                                     _stream(stream)))
+    pr, ldr = (None, 0) if residual is None else _rows(residual, "residual", dt, n, rows)
+    pst = None if status is None else _dense(status, "status", torch.int32, (1,))
+    rc = load_library().moe_linear(pc, ps, pz, rows, cols, group_size, px, ldx, n,
+                                   _code_of(dt, types), pb, pr, ldr, py, ldy, pst,
+                                   _raw_stream(x, stream))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -457,42 +484,45 @@ def linear_input_grad(dy, codes, scales, zeros, group_size=GROUP, out=None, stat
     """dx = dy W, the gradient of linear's input through the frozen 4-bit
     matrix (moe_linear_input_grad): dy fp16 or bf16 [n, rows] (rows may be
     strided); dx [n, cols] of the same type."""
-    import torch
-    rows, cols, (pc, ps, pz) = _w4(codes, scales, zeros, group_size)
+    torch, types = _types()
+    rows, cols, pc, ps, pz = _w4(torch, codes, scales, zeros, group_size)
     if dy.dim() != 2:
         _bad("dy: need [n, rows], got shape %s" % (tuple(dy.shape),))
-    n, dt = dy.shape[0], (dy.dtype,)
-    pd, ldd = _need(dy, "dy", dt, (n, rows))
+    n, dt = dy.shape[0], dy.dtype
+    pd, ldd = _rows(dy, "dy", dt, n, rows)
     if out is None:
-        out = torch.empty((n, cols), dtype=dy.dtype, device=dy.device)
-    po, ldo = _need(out, "out", dt, (n, cols))
-    pst = None if status is None else _dense(status, "status", (torch.int32,), (1,))
-    _check(load_library().moe_linear_input_grad(pc, ps, pz, rows, cols, group_size, pd, ldd, n,
-                                                _code_of(dy.dtype), po, ldo, pst,
-                                                _stream(stream)))
+        out, ldo = torch.empty((n, cols), dtype=dt, device=dy.device), cols
+        po = out.data_ptr()
+    else:
+        po, ldo = _rows(out, "out", dt, n, cols)
+    pst = None if status is None else _dense(status, "status", torch.int32, (1,))
+    rc = load_library().moe_linear_input_grad(pc, ps, pz, rows, cols, group_size, pd, ldd, n,
+                                              _code_of(dt, types), po, ldo, pst,
+                                              _raw_stream(dy, stream))
+    if rc:
+        _check(rc)
     return out
 
 
-def _batch(logits, topk_idx, seq_offsets, mask):
+def _batch(torch, types, logits, topk_idx, seq_offsets, mask):
     """Checked addresses and sizes of a routed batch."""
-    import torch
     if logits.dim() != 2:
         _bad("logits: need [n, E], got shape %s" % (tuple(logits.shape),))
     n, E = logits.shape
-    code = _code_of(logits.dtype)
-    pl, ld = _need(logits, "logits", (logits.dtype,), (n, E))
-    pi, k = None, 1
+    dt = logits.dtype
+    pl, ld = _rows(logits, "logits", dt, n, E)
+    pi, k, S, po, pm = None, 1, 1, None, None
     if topk_idx is not None:
         if topk_idx.dim() != 2:
             _bad("topk_idx: need [n, k], got shape %s" % (tuple(topk_idx.shape),))
         k = topk_idx.shape[1]
-        pi = _dense(topk_idx, "topk_idx", (torch.int32,), (n, k))
-    S, po = 1, None
+        pi = _dense(topk_idx, "topk_idx", torch.int32, (n, k))
     if seq_offsets is not None:
         S = seq_offsets.numel() - 1
-        po = _dense(seq_offsets, "seq_offsets", (torch.int32,), (S + 1,))
-    pm = None if mask is None else _dense(mask, "mask", (torch.uint8, torch.bool), (n,))
-    return n, E, k, S, code, pl, ld, pi, po, pm
+        po = _dense(seq_offsets, "seq_offsets", torch.int32, (S + 1,))
+    if mask is not None:
+        pm = _dense(mask, "mask", torch.bool if mask.dtype is torch.bool else torch.uint8, (n,))
+    return n, E, k, S, _code_of(dt, types), pl, ld, pi, po, pm
 
 
 def balance_loss(logits, topk_idx, seq_offsets=None, mask=None, stream=None):
@@ -502,27 +532,25 @@ def balance_loss(logits, topk_idx, seq_offsets=None, mask=None, stream=None):
     None.  Returns dict(loss fp32 [2] = (balance, z), counts int32 [S, E],
     tokens int32 [S], prob fp32 [S, E], lse fp32 [n]); balance_loss_grad takes
     it, and counts.sum(0) is what residency_plan takes."""
-    import torch
+    torch, types = _types()
     if topk_idx is None:
         _bad("topk_idx: need int32 [n, k]")
-    n, E, k, S, code, pl, ld, pi, po, pm = _batch(logits, topk_idx, seq_offsets, mask)
-    lib, dev = load_library(), logits.device
+    n, E, k, S, code, pl, ld, pi, po, pm = _batch(torch, types, logits, topk_idx, seq_offsets, mask)
+    lib, dev, empty = load_library(), logits.device, torch.empty
     f32, i32 = torch.float32, torch.int32
-    r = dict(loss=torch.empty(2, dtype=f32, device=dev),
-             counts=torch.empty((S, E), dtype=i32, device=dev),
-             tokens=torch.empty(S, dtype=i32, device=dev),
-             prob=torch.empty((S, E), dtype=f32, device=dev),
-             lse=torch.empty(n, dtype=f32, device=dev))
+    loss, lse = empty(2, dtype=f32, device=dev), empty(n, dtype=f32, device=dev)
+    prob = empty((S, E), dtype=f32, device=dev)
+    counts, tokens = empty((S, E), dtype=i32, device=dev), empty(S, dtype=i32, device=dev)
     size = lib.moe_balance_workspace(n, E, S)
-    ws = torch.empty(size, dtype=torch.uint8, device=dev)
-    s = stream if stream is not None else torch.cuda.current_stream()
-    _check(lib.moe_balance_loss(pl, code, ld, n, E, pi, k, po, S, pm, r["loss"].data_ptr(),
-                                r["counts"].data_ptr(), r["tokens"].data_ptr(),
-                                r["prob"].data_ptr(), r["lse"].data_ptr(), ws.data_ptr(), size,
-                                s.cuda_stream))
+    ws = empty(size, dtype=torch.uint8, device=dev)
+    rc = lib.moe_balance_loss(pl, code, ld, n, E, pi, k, po, S, pm, loss.data_ptr(),
+                              counts.data_ptr(), tokens.data_ptr(), prob.data_ptr(),
+                              lse.data_ptr(), ws.data_ptr(), size, _raw_stream(logits, stream))
+    if rc:
+        _check(rc)
     if stream is not None:      # the workspace is freed to its own stream's pool on return
         ws.record_stream(stream)
-    return r
+    return dict(loss=loss, counts=counts, tokens=tokens, prob=prob, lse=lse)
 
 
 def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, seq_offsets=None,
@@ -532,20 +560,26 @@ def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, s
     the gradients of the two losses on the device.  With dtopk_w fp32 [n, k],
     the gradient of the renormalised top-k weights topk_w fp32 [n, k], the
     gradient through them is added.  out may be logits itself."""
-    import torch
-    n, E, k, S, code, pl, ld, pi, po, pm = _batch(logits, topk_idx, seq_offsets, mask)
-    f32, i32 = (torch.float32,), (torch.int32,)
-    if dtopk_w is not None and (topk_idx is None or topk_w is None):
-        _bad("dtopk_w needs topk_idx and topk_w")
-    pw = None if dtopk_w is None else _dense(topk_w, "topk_w", f32, (n, k))
-    pdw = None if dtopk_w is None else _dense(dtopk_w, "dtopk_w", f32, (n, k))
+    torch, types = _types()
+    n, E, k, S, code, pl, ld, pi, po, pm = _batch(torch, types, logits, topk_idx, seq_offsets, mask)
+    f32, i32 = torch.float32, torch.int32
+    pw = pdw = None
+    if dtopk_w is not None:
+        if topk_idx is None or topk_w is None:
+            _bad("dtopk_w needs topk_idx and topk_w")
+        pw = _dense(topk_w, "topk_w", f32, (n, k))
+        pdw = _dense(dtopk_w, "dtopk_w", f32, (n, k))
     if out is None:
-        out = torch.empty((n, E), dtype=logits.dtype, device=logits.device)
-    pout, ldo = _need(out, "out", (logits.dtype,), (n, E))
-    _check(load_library().moe_balance_loss_grad(
+        out, ldo = torch.empty((n, E), dtype=logits.dtype, device=logits.device), E
+        pout = out.data_ptr()
+    else:
+        pout, ldo = _rows(out, "out", logits.dtype, n, E)
+    rc = load_library().moe_balance_loss_grad(
         pl, code, ld, n, E, pi, k, po, S, pm, _dense(fwd["lse"], "lse", f32, (n,)),
         _dense(fwd["counts"], "counts", i32, (S, E)), _dense(fwd["tokens"], "tokens", i32, (S,)),
-        _dense(dloss, "dloss", f32, (2,)), pw, pdw, pout, ldo, _stream(stream)))
+        _dense(dloss, "dloss", f32, (2,)), pw, pdw, pout, ldo, _raw_stream(logits, stream))
+    if rc:
+        _check(rc)
     return out
 
 
