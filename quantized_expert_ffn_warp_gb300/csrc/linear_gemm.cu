@@ -288,8 +288,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int tok0 = t / a.mt * a.tok;
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
             const bool two = G::chains == 2 && nsteps > 1;
-            float *part = reinterpret_cast<float *>(smem + G::b_off);
-            for (int c0 = 0; c0 < a.tok && tok0 + c0 < c.n; c0 += 16) {
+            const int cols = min(a.tok, c.n - tok0);
+            float *part = reinterpret_cast<float *>(smem + G::b_off) + 32 * q + lane;
+            const bool in = f < F;
+            const float bias = c.bias && in ? Q::to_float(static_cast<const T *>(c.bias)[f]) : 0.f;
+            T *out = static_cast<T *>(c.out) + tok0 * c.ldo + f;
+            const T *res = static_cast<const T *>(c.residual) + (c.residual ? tok0 * c.ldr + f : 0);
+            for (int c0 = 0; c0 < cols; c0 += 16) {
                 float d[16], e[16];
                 tmem_ld16(taddr + c0, d);
                 if (two) {
@@ -298,13 +303,30 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int i = 0; i < 16; i++)
                         d[i] += e[i];
                 }
+                if (a.splits > 1) {
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    if (a.splits > 1)
-                        part[(c0 + i) * kM + 32 * q + lane] = d[i];
-                    else if (f < F && tok0 + c0 + i < c.n)
-                        store_out<T>(c, d[i], tok0 + c0 + i, f);
+                    for (int i = 0; i < 16; i++)
+                        part[(c0 + i) * kM] = d[i];
+                    continue;       // uniform over the grid
                 }
+                const int left = in ? cols - c0 : 0;
+                if (c.residual) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++, res += c.ldr)
+                        if (i < left)
+                            d[i] += Q::to_float(*res);
+                }
+                if (left >= 16) {
+#pragma unroll
+                    for (int i = 0; i < 16; i++, out += c.ldo)
+                        *out = Q::from_float(d[i] + bias);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; i++, out += c.ldo)
+                        if (i < left)
+                            *out = Q::from_float(d[i] + bias);
+                }
+                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -319,137 +341,144 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int q = warp & 3, wg = warp >> 2, g = lane >> 2, tq = lane & 3;
         const uint32_t tlane = (uint32_t)(32 * q) << 16;
         const int ng = c.w.K / c.w.group, gsh = c.w.group == 128 ? 7 : c.w.group == 64 ? 6 : 5;
-        unsigned cc = 0, ac = 0;
-        for (int t = tile0; t < tiles && ok; t += tile_step) {
-            const int m0 = t % a.mt * kM;
-            for (int b = blk0; b < blk1 && ok; b++, cc++) {
-                const int steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
-                if ((cc & 1) != (unsigned)wg) {
-                    ac += steps;
-                    continue;
-                }
-                // scale << 16 | zero point, 0 outside the matrix: forward, of this
-                // thread's row for each 32 K of the block; gradient, of the rows
-                // lane + 32 i for this quarter's columns
-                uint32_t meta[4];
+        const int nb = blk1 - blk0;
+        const unsigned total = tile0 < tiles ? ((tiles - 1 - tile0) / tile_step + 1) * nb : 0;
+        // scale << 16 | zero point of this CTA's code block i, 0 outside the
+        // matrix: forward, of this thread's row for each 32 K of the block;
+        // gradient, of the rows lane + 32 j for this quarter's columns
+        const auto load_meta = [&](unsigned i, uint32_t (&m)[4]) {
+            const int m0 = (tile0 + (int)(i / nb) * tile_step) % a.mt * kM;
+            const int b = blk0 + (int)(i % nb);
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int row = GRAD ? b * kBlk + 32 * i + lane : m0 + 32 * q + lane;
-                    const int k = GRAD ? m0 + 32 * q : b * kBlk + 32 * i;
-                    if (!GRAD && i > 0 && (k & (c.w.group - 1))) {
-                        meta[i] = meta[i - 1];
-                    } else {
-                        const long long at = (long long)row * ng + (k >> gsh);
-                        meta[i] = row < c.w.rows && k < c.w.K
-                                      ? (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at]
-                                      : 0;
+            for (int j = 0; j < 4; j++) {
+                const int row = GRAD ? b * kBlk + 32 * j + lane : m0 + 32 * q + lane;
+                const int k = GRAD ? m0 + 32 * q : b * kBlk + 32 * j;
+                if (!GRAD && j > 0 && (k & (c.w.group - 1))) {
+                    m[j] = m[j - 1];
+                } else {
+                    const long long at = (long long)row * ng + (k >> gsh);
+                    m[j] = row < c.w.rows && k < c.w.K
+                               ? (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at]
+                               : 0;
+                }
+            }
+        };
+        uint32_t meta[4] = {}, next[4] = {};
+        if ((unsigned)wg < total)
+            load_meta(wg, next);
+        for (unsigned cc = wg; cc < total && ok; cc += 2) {
+            const int b = blk0 + (int)(cc % nb);
+            const int steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
+            unsigned ac = cc / nb * nsteps + 2 * (cc % nb);
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                meta[j] = next[j];
+            if (cc + 2 < total)     // the next block's arrive while this one is unpacked
+                load_meta(cc + 2, next);
+            const uint32_t s = cc % G::cs;
+            if (!bar_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            const uint8_t *blk = smem + G::c_off + s * kBlkBytes;
+            uint4 cw[4];
+            if (!GRAD) {
+                // row r's 16-byte chunk i sits at i ^ (r / 2 % 4) (64-byte swizzle)
+                const int r = 32 * q + lane;
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
+                                                             ((i ^ ((r >> 1) & 3)) << 4));
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(code_empty + 8 * s);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                if (h >= steps)
+                    break;
+                const uint32_t as = ac % G::as;
+                uint32_t col[32];
+                if (!GRAD) {
+#pragma unroll
+                    for (int i = 0; i < 2; i++) {
+                        const uint32_t m = meta[2 * h + i];
+                        const typename Q::Zero z = Q::zero(m & 0xff, m & 0xff);
+                        const typename Q::Scale sc = Q::scale(m >> 16, m >> 16);
+                        const uint4 v = cw[2 * h + i];
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            uint32_t p[4];
+                            Q::unpack(w[u], z, p);
+#pragma unroll
+                            for (int n = 0; n < 4; n++)
+                                p[n] = Q::mul(p[n], sc);
+                            // fields (i, i + 4) into memory order
+                            col[16 * i + 4 * u] = __byte_perm(p[0], p[1], 0x5410);
+                            col[16 * i + 4 * u + 1] = __byte_perm(p[2], p[3], 0x5410);
+                            col[16 * i + 4 * u + 2] = __byte_perm(p[0], p[1], 0x7632);
+                            col[16 * i + 4 * u + 3] = __byte_perm(p[2], p[3], 0x7632);
+                        }
+                    }
+                } else {
+                    const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+#pragma unroll
+                    for (int ss = 0; ss < 4; ss++) {        // 16 rows each
+                        uint32_t w[4], m[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const int r = 64 * h + 16 * ss + 4 * tq + i;
+                            w[i] = *reinterpret_cast<const uint32_t *>(
+                                blk + r * 64 + ((q ^ ((r >> 1) & 3)) << 4) + 4 * (g >> 1));
+                            m[i] = __shfl_sync(0xffffffffu, meta[2 * h + (ss >> 1)],
+                                               16 * (ss & 1) + 4 * tq + i);
+                        }
+                        const typename Q::Zero z01 = Q::zero(m[0] & 0xff, m[1] & 0xff);
+                        const typename Q::Zero z23 = Q::zero(m[2] & 0xff, m[3] & 0xff);
+                        const typename Q::Scale s01 = Q::scale(m[0] >> 16, m[1] >> 16);
+                        const typename Q::Scale s23 = Q::scale(m[2] >> 16, m[3] >> 16);
+                        uint32_t p[4], r[4];
+                        Q::unpack(__byte_perm(w[0], w[1], sel), z01, p);
+                        Q::unpack(__byte_perm(w[2], w[3], sel), z23, r);
+                        // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
+#pragma unroll
+                        for (int u = 0; u < 4; u++) {
+                            const int at = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
+                            col[at] = Q::mul(p[u], s01);
+                            col[at + 1] = Q::mul(r[u], s23);
+                        }
+                    }
+                    if (h + 1 == steps) {
+                        __syncwarp();
+                        if (lane == 0)
+                            bar_arrive(code_empty + 8 * s);
                     }
                 }
-                const uint32_t s = cc % G::cs;
-                if (!bar_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
+                if (!bar_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                const uint8_t *blk = smem + G::c_off + s * kBlkBytes;
-                uint4 cw[4];
+                tc_fence_after();
+                const uint32_t at = tmem + tlane + G::acc_cols + as * G::a_cols;
                 if (!GRAD) {
-                    // row r's 16-byte chunk i sits at i ^ (r / 2 % 4) (64-byte swizzle)
-                    const int r = 32 * q + lane;
+                    tmem_st32(at, col);
+                } else {
+                    uint32_t lo[16], hi[16];
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
-                                                                 ((i ^ ((r >> 1) & 3)) << 4));
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_arrive(code_empty + 8 * s);
+                    for (int i = 0; i < 16; i++) {
+                        lo[i] = col[i];
+                        hi[i] = col[16 + i];
+                    }
+                    tmem_st_16x256(at, lo);
+                    tmem_st_16x256(at + (16u << 16), hi);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    if (h >= steps)
-                        break;
-                    const uint32_t as = ac % G::as;
-                    uint32_t col[32];
-                    if (!GRAD) {
-#pragma unroll
-                        for (int i = 0; i < 2; i++) {
-                            const uint32_t m = meta[2 * h + i];
-                            const typename Q::Zero z = Q::zero(m & 0xff, m & 0xff);
-                            const typename Q::Scale sc = Q::scale(m >> 16, m >> 16);
-                            const uint4 v = cw[2 * h + i];
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                            for (int u = 0; u < 4; u++) {
-                                uint32_t p[4];
-                                Q::unpack(w[u], z, p);
-#pragma unroll
-                                for (int n = 0; n < 4; n++)
-                                    p[n] = Q::mul(p[n], sc);
-                                // fields (i, i + 4) into memory order
-                                col[16 * i + 4 * u] = __byte_perm(p[0], p[1], 0x5410);
-                                col[16 * i + 4 * u + 1] = __byte_perm(p[2], p[3], 0x5410);
-                                col[16 * i + 4 * u + 2] = __byte_perm(p[0], p[1], 0x7632);
-                                col[16 * i + 4 * u + 3] = __byte_perm(p[2], p[3], 0x7632);
-                            }
-                        }
-                    } else {
-                        const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
-#pragma unroll
-                        for (int ss = 0; ss < 4; ss++) {        // 16 rows each
-                            uint32_t w[4], m[4];
-#pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const int r = 64 * h + 16 * ss + 4 * tq + i;
-                                w[i] = *reinterpret_cast<const uint32_t *>(
-                                    blk + r * 64 + ((q ^ ((r >> 1) & 3)) << 4) + 4 * (g >> 1));
-                                m[i] = __shfl_sync(0xffffffffu, meta[2 * h + (ss >> 1)],
-                                                   16 * (ss & 1) + 4 * tq + i);
-                            }
-                            const typename Q::Zero z01 = Q::zero(m[0] & 0xff, m[1] & 0xff);
-                            const typename Q::Zero z23 = Q::zero(m[2] & 0xff, m[3] & 0xff);
-                            const typename Q::Scale s01 = Q::scale(m[0] >> 16, m[1] >> 16);
-                            const typename Q::Scale s23 = Q::scale(m[2] >> 16, m[3] >> 16);
-                            uint32_t p[4], r[4];
-                            Q::unpack(__byte_perm(w[0], w[1], sel), z01, p);
-                            Q::unpack(__byte_perm(w[2], w[3], sel), z23, r);
-                            // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
-#pragma unroll
-                            for (int u = 0; u < 4; u++) {
-                                const int at = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
-                                col[at] = Q::mul(p[u], s01);
-                                col[at + 1] = Q::mul(r[u], s23);
-                            }
-                        }
-                        if (h + 1 == steps) {
-                            __syncwarp();
-                            if (lane == 0)
-                                bar_arrive(code_empty + 8 * s);
-                        }
-                    }
-                    if (!bar_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t at = tmem + tlane + G::acc_cols + as * G::a_cols;
-                    if (!GRAD) {
-                        tmem_st32(at, col);
-                    } else {
-                        uint32_t lo[16], hi[16];
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            lo[i] = col[i];
-                            hi[i] = col[16 + i];
-                        }
-                        tmem_st_16x256(at, lo);
-                        tmem_st_16x256(at + (16u << 16), hi);
-                        asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0)
-                        bar_arrive(a_full + 8 * as);
-                    ac++;
-                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(a_full + 8 * as);
+                ac++;
             }
         }
         if (!ok && lane == 0)
@@ -475,14 +504,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const int tok = tok0 + i / kM, f = m0 + lane_feature<GRAD>(i % kM);
             if (tok >= c.n || f >= F)
                 continue;
-            float v = 0.f;
-            for (int r = 0; r < a.splits; r++) {
+            float v = 0.f, p[8];
+#pragma unroll
+            for (int r = 0; r < 8; r++) {
                 uint32_t remote;
-                float p;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + 4 * i), "r"(r));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p) : "r"(remote));
-                v += p;
+                p[r] = 0.f;
+                if (r < a.splits) {
+                    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+                        : "=r"(remote)
+                        : "r"(base + 4 * i), "r"(r));
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[r]) : "r"(remote));
+                }
             }
+#pragma unroll
+            for (int r = 0; r < 8; r++)
+                v += p[r];
             store_out<T>(c, v, tok, f);
         }
         cluster_sync();     // a CTA's shared memory stays until its peers have read it
