@@ -27,6 +27,7 @@
 // Every wait is bounded in time; on expiry the output is incomplete and the
 // caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
+#include <cstring>
 
 #include "tcgen05.cuh"
 #include "w4.cuh"
@@ -82,6 +83,28 @@ __device__ __forceinline__ void tmem_st_16x256(uint32_t taddr, const uint32_t (&
           "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
           "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// bar_wait by a whole warp with one answer for all its lanes, so that a wait
+// that gives up never splits the warp in front of a collective instruction.
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int *abort_flag)
+{
+    return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag));
+}
+
+// A lane's word(s) read from lane `src`.
+template <typename S>
+__device__ __forceinline__ S shfl_of(const S &v, int src)
+{
+    constexpr int N = sizeof(S) / 4;
+    uint32_t u[N];
+    memcpy(u, &v, sizeof(S));
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        u[i] = __shfl_sync(0xffffffffu, u[i], src);
+    S r;
+    memcpy(&r, u, sizeof(S));
+    return r;
 }
 
 __device__ __forceinline__ void cluster_sync()
@@ -230,43 +253,52 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     } else if (warp >= kMma0) {
         // -------------------------------------------------------- MMA issuers
         // chain ch takes the steps of its parity into its own accumulator
-        const int ch = warp - kMma0;
-        if (lane == 0 && ch < G::chains) {
+        // Every lane walks the loop and one elected lane issues, so that the
+        // descriptors stay in uniform registers: an issue from a branch of one
+        // lane costs several times as much.
+        const int ch = __shfl_sync(0xffffffffu, warp - kMma0, 0);
+        if (ch < G::chains) {
             const uint32_t idesc = idesc_f16(a.tok, kBf16);
             const uint32_t dacc = tmem + ch * TOK;
-            unsigned ac = 0, ti = 0;
+            unsigned slot = 0, par = 0, ti = 0;
             bool issued = false;
             for (int t = tile0; t < tiles && ok; t += tile_step, ti++) {
-                if (!bar_wait(acc_empty, (ti & 1) ^ 1, abort_flag)) {
+                if (!warp_wait(acc_empty, (ti & 1) ^ 1, abort_flag)) {
                     ok = false;
                     break;
                 }
-                tc_fence_after();
-                for (int j = 0; j < nsteps; j++, ac++) {
-                    if (G::chains == 2 && (j & 1) != ch)
-                        continue;
-                    const uint32_t s = ac % G::as, par = (ac / G::as) & 1;
-                    if (!bar_wait(a_full + 8 * s, par, abort_flag) ||
-                        !bar_wait(b_full + 8 * s, par, abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t abase = tmem + G::acc_cols + s * G::a_cols;
-                    const uint32_t bbase = saddr(smem + G::b_off + s * G::b_stage);
+                for (int j = 0; j < nsteps; j++) {
+                    if (G::chains == 1 || (j & 1) == ch) {
+                        if (!warp_wait(a_full + 8 * slot, par, abort_flag) ||
+                            !warp_wait(b_full + 8 * slot, par, abort_flag)) {
+                            ok = false;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint32_t abase = tmem + G::acc_cols + slot * G::a_cols;
+                        const uint64_t bdesc = sw128_desc(saddr(smem + G::b_off) + slot * G::b_stage);
+                        if (elect_one()) {
 #pragma unroll
-                    for (int kk = 0; kk < 4; kk++)      // 16 each: A 8 columns, B 32 bytes
-                        umma_ta(dacc, abase + kk * 8, sw128_desc(bbase + kk * 32), idesc,
-                                j >= G::chains || kk ? 1u : 0u);
-                    issued = true;
-                    umma_commit(stage_empty + 8 * s);
+                            for (int kk = 0; kk < 4; kk++)      // 16 each: A 8 columns, B 32 bytes
+                                umma_ta(dacc, abase + kk * 8, bdesc + 2 * kk, idesc,
+                                        j >= G::chains || kk ? 1u : 0u);
+                            umma_commit(stage_empty + 8 * slot);
+                        }
+                        __syncwarp();
+                        issued = true;
+                    }
+                    if (++slot == (unsigned)G::as) {
+                        slot = 0;
+                        par ^= 1;
+                    }
                 }
-                if (ok)
+                if (ok && elect_one())
                     umma_commit(acc_full);
+                __syncwarp();
             }
-            if (!ok)
+            if (!ok && lane == 0)
                 *abort_flag = 1;
-            if (issued) {   // every MMA issued has completed before the memory is freed
+            if (issued && elect_one()) {    // every MMA issued has completed before the memory is freed
                 umma_commit(drain + 8 * ch);
                 const unsigned long long t0 = now_ns();
                 while (!bar_try(drain + 8 * ch, 0) && now_ns() - t0 < kGWaitNs) {
@@ -279,7 +311,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int q = warp & 3;
         unsigned ti = 0;
         for (int t = tile0; t < tiles && ok; t += tile_step, ti++) {
-            if (!bar_wait(acc_full, ti & 1, abort_flag)) {
+            if (!warp_wait(acc_full, ti & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -341,17 +373,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int q = warp & 3, wg = warp >> 2, g = lane >> 2, tq = lane & 3;
         const uint32_t tlane = (uint32_t)(32 * q) << 16;
         const int ng = c.w.K / c.w.group, gsh = c.w.group == 128 ? 7 : c.w.group == 64 ? 6 : 5;
-        const int nb = blk1 - blk0;
-        const unsigned total = tile0 < tiles ? ((tiles - 1 - tile0) / tile_step + 1) * nb : 0;
-        // scale << 16 | zero point of this CTA's code block i, 0 outside the
-        // matrix: forward, of this thread's row for each 32 K of the block;
-        // gradient, of the rows lane + 32 j for this quarter's columns
-        const auto load_meta = [&](unsigned i, uint32_t (&m)[4]) {
-            const int m0 = (tile0 + (int)(i / nb) * tile_step) % a.mt * kM;
-            const int b = blk0 + (int)(i % nb);
+        // scale << 16 | zero point, 0 outside the matrix.  Forward: of this
+        // thread's row for each 32 K of the block.  Gradient: of the rows 2 lane,
+        // 2 lane + 1 of the block's first and second half, for this quarter's columns.
+        const auto load_meta = [&](int m0, int b, uint32_t (&m)[4]) {
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const int row = GRAD ? b * kBlk + 32 * j + lane : m0 + 32 * q + lane;
+                const int row = GRAD ? b * kBlk + 64 * (j >> 1) + 2 * lane + (j & 1)
+                                     : m0 + 32 * q + lane;
                 const int k = GRAD ? m0 + 32 * q : b * kBlk + 32 * j;
                 if (!GRAD && j > 0 && (k & (c.w.group - 1))) {
                     m[j] = m[j - 1];
@@ -363,20 +392,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
         };
+        // this group's place in the CTA's blocks: every second one of them
+        struct Place {
+            int t, m0, b;
+            unsigned cc, ac0;       // blocks before this one; 64-steps before this tile
+        };
+        const int nb = blk1 - blk0;
+        const auto settle = [&](Place &p) {
+            if (p.b >= blk1) {
+                do {
+                    p.b -= nb;
+                    p.t += tile_step;
+                    p.ac0 += nsteps;
+                } while (p.b >= blk1);
+                p.m0 = p.t % a.mt * kM;
+            }
+        };
+        Place at{tile0, tile0 % a.mt * kM, blk0 + wg, (unsigned)wg, 0u};
+        settle(at);
         uint32_t meta[4] = {}, next[4] = {};
-        if ((unsigned)wg < total)
-            load_meta(wg, next);
-        for (unsigned cc = wg; cc < total && ok; cc += 2) {
-            const int b = blk0 + (int)(cc % nb);
-            const int steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
-            unsigned ac = cc / nb * nsteps + 2 * (cc % nb);
+        if (at.t < tiles)
+            load_meta(at.m0, at.b, next);
+        while (at.t < tiles && ok) {
+            const int b = at.b, steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
+            const unsigned cc = at.cc;
+            unsigned ac = at.ac0 + 2 * (b - blk0);
 #pragma unroll
             for (int j = 0; j < 4; j++)
                 meta[j] = next[j];
-            if (cc + 2 < total)     // the next block's arrive while this one is unpacked
-                load_meta(cc + 2, next);
+            at.b += 2;
+            at.cc += 2;
+            settle(at);
+            if (at.t < tiles)       // the next block's arrive while this one is unpacked
+                load_meta(at.m0, at.b, next);
             const uint32_t s = cc % G::cs;
-            if (!bar_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
+            if (!warp_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
                 ok = false;
                 break;
             }
@@ -422,31 +472,39 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                     }
                 } else {
+                    // this lane's row pair of the half, as the fields' operands
+                    const uint32_t m0 = meta[2 * h], m1 = meta[2 * h + 1];
+                    const typename Q::Zero zp = Q::zero(m0 & 0xff, m1 & 0xff);
+                    const typename Q::Scale sp = Q::scale(m0 >> 16, m1 >> 16);
                     const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
+                    // row r's 16-byte chunk q sits at q ^ (r / 2 % 4) (64-byte
+                    // swizzle); r = 64 h + 16 ss + 4 tq + i
+                    const uint8_t *w01 = blk + h * 4096 + tq * 256 + 4 * (g >> 1) +
+                                         ((q ^ ((2 * tq) & 3)) << 4);
+                    const uint8_t *w23 = blk + h * 4096 + tq * 256 + 4 * (g >> 1) +
+                                         ((q ^ ((2 * tq + 1) & 3)) << 4);
+                    uint32_t w[4][4];
 #pragma unroll
-                    for (int ss = 0; ss < 4; ss++) {        // 16 rows each
-                        uint32_t w[4], m[4];
+                    for (int ss = 0; ss < 4; ss++)
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            const int r = 64 * h + 16 * ss + 4 * tq + i;
-                            w[i] = *reinterpret_cast<const uint32_t *>(
-                                blk + r * 64 + ((q ^ ((r >> 1) & 3)) << 4) + 4 * (g >> 1));
-                            m[i] = __shfl_sync(0xffffffffu, meta[2 * h + (ss >> 1)],
-                                               16 * (ss & 1) + 4 * tq + i);
-                        }
-                        const typename Q::Zero z01 = Q::zero(m[0] & 0xff, m[1] & 0xff);
-                        const typename Q::Zero z23 = Q::zero(m[2] & 0xff, m[3] & 0xff);
-                        const typename Q::Scale s01 = Q::scale(m[0] >> 16, m[1] >> 16);
-                        const typename Q::Scale s23 = Q::scale(m[2] >> 16, m[3] >> 16);
+                        for (int i = 0; i < 4; i++)
+                            w[ss][i] = *reinterpret_cast<const uint32_t *>(
+                                (i < 2 ? w01 : w23) + ss * 1024 + i * 64);
+#pragma unroll
+                    for (int ss = 0; ss < 4; ss++) {        // 16 rows: pairs 8 ss + 2 tq, + 1
+                        const typename Q::Zero z01 = shfl_of(zp, 8 * ss + 2 * tq);
+                        const typename Q::Zero z23 = shfl_of(zp, 8 * ss + 2 * tq + 1);
+                        const typename Q::Scale s01 = shfl_of(sp, 8 * ss + 2 * tq);
+                        const typename Q::Scale s23 = shfl_of(sp, 8 * ss + 2 * tq + 1);
                         uint32_t p[4], r[4];
-                        Q::unpack(__byte_perm(w[0], w[1], sel), z01, p);
-                        Q::unpack(__byte_perm(w[2], w[3], sel), z23, r);
+                        Q::unpack(__byte_perm(w[ss][0], w[ss][1], sel), z01, p);
+                        Q::unpack(__byte_perm(w[ss][2], w[ss][3], sel), z23, r);
                         // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
-                            const int at = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
-                            col[at] = Q::mul(p[u], s01);
-                            col[at + 1] = Q::mul(r[u], s23);
+                            const int to = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
+                            col[to] = Q::mul(p[u], s01);
+                            col[to + 1] = Q::mul(r[u], s23);
                         }
                     }
                     if (h + 1 == steps) {
@@ -455,14 +513,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             bar_arrive(code_empty + 8 * s);
                     }
                 }
-                if (!bar_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
+                if (!warp_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const uint32_t at = tmem + tlane + G::acc_cols + as * G::a_cols;
+                const uint32_t dst = tmem + tlane + G::acc_cols + as * G::a_cols;
                 if (!GRAD) {
-                    tmem_st32(at, col);
+                    tmem_st32(dst, col);
                 } else {
                     uint32_t lo[16], hi[16];
 #pragma unroll
@@ -470,8 +528,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         lo[i] = col[i];
                         hi[i] = col[16 + i];
                     }
-                    tmem_st_16x256(at, lo);
-                    tmem_st_16x256(at + (16u << 16), hi);
+                    tmem_st_16x256(dst, lo);
+                    tmem_st_16x256(dst + (16u << 16), hi);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 }
                 tc_fence_before();

@@ -63,6 +63,15 @@ __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile i
     }
 }
 
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t p;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}"
+                 : "=r"(p));
+    return p != 0;
+}
+
 // Copy with an L2 evict-first policy: streamed data that no one reads again.
 __device__ __forceinline__ void bulk_copy_ef(uint32_t dst, const void *src, uint32_t bytes,
                                              uint32_t b, uint64_t policy)
