@@ -27,7 +27,6 @@
 // Every wait is bounded in time; on expiry the output is incomplete and the
 // caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
-#include <cstring>
 
 #include "tcgen05.cuh"
 #include "w4.cuh"
@@ -43,27 +42,34 @@ constexpr int kDeq = 8, kEpi = 4;   // warps
 constexpr int kEpi0 = kDeq, kProd = kDeq + kEpi, kBProd = kProd + 1, kMma0 = kProd + 2;
 constexpr int kGemmThreads = (kMma0 + 2) * 32;
 
-template <int TOK>
+template <int TOK, bool GRAD>
 struct LGeo {
     static constexpr int chains = TOK > 128 ? 1 : 2;
     static constexpr int acc_cols = chains * TOK;       // accumulator columns
     static constexpr int a_cols = 32;                   // 64 contraction elements, two per column
     static constexpr int b_stage = TOK * 128;           // TOK rows of 64 elements
     // A and B stages (64 contraction elements each), in lockstep
-    static constexpr int as = TOK > 128 ? 6 : TOK > 64 ? 8 : 12;
+    static constexpr int as = TOK > 128 ? (GRAD ? 5 : 6) : TOK > 64 ? 8 : 12;
     static constexpr int cs = TOK > 128 ? 4 : TOK > 64 ? 8 : 12;    // code blocks
     static constexpr int b_off = 0, c_off = as * b_stage;
-    static constexpr int bar_off = c_off + cs * kBlkBytes;
+    // gradient: per dequant group two buffers of a block's zero points and
+    // scales, as the unpacking's operand words: [4 column quarters][64 row pairs]
+    static constexpr int meta_off = c_off + cs * kBlkBytes;
+    static constexpr int meta_buf = 4 * 64 * 12;
+    static constexpr int bar_off = meta_off + (GRAD ? 4 * meta_buf : 0);
     static constexpr int nbars = 2 * cs + 3 * as + 4;
     static constexpr int smem = bar_off + 8 * nbars + 16 + 1024;
 };
-static_assert(LGeo<256>::smem <= 227 * 1024 && LGeo<128>::smem <= 227 * 1024, "shared memory");
-static_assert(LGeo<256>::acc_cols + LGeo<256>::as * 32 <= 512 &&
-                  LGeo<128>::acc_cols + LGeo<128>::as * 32 <= 512 &&
-                  LGeo<64>::acc_cols + LGeo<64>::as * 32 <= 512,
-              "tensor memory");
-static_assert(128 * 128 * 4 <= LGeo<128>::c_off && 128 * 64 * 4 <= LGeo<64>::c_off,
-              "a partial tile fits in the B stages");
+template <int TOK, bool GRAD>
+constexpr bool lgeo_ok()
+{
+    using G = LGeo<TOK, GRAD>;
+    return G::smem <= 227 * 1024 && G::acc_cols + G::as * G::a_cols <= 512 && G::cs % 2 == 0 &&
+           (TOK > 128 || 128 * TOK * 4 <= G::c_off);    // a partial tile fits in the B stages
+}
+static_assert(lgeo_ok<256, false>() && lgeo_ok<128, false>() && lgeo_ok<64, false>() &&
+                  lgeo_ok<256, true>() && lgeo_ok<128, true>() && lgeo_ok<64, true>(),
+              "stages fit shared and tensor memory");
 
 struct GemmCall {
     W4Call c;
@@ -92,20 +98,23 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
     return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag));
 }
 
-// A lane's word(s) read from lane `src`.
-template <typename S>
-__device__ __forceinline__ S shfl_of(const S &v, int src)
+// One answer for the four warps of a dequant group, which also orders their
+// shared-memory writes before it against the reads after it.
+__device__ __forceinline__ bool group_and(int id, bool v)
 {
-    constexpr int N = sizeof(S) / 4;
-    uint32_t u[N];
-    memcpy(u, &v, sizeof(S));
-#pragma unroll
-    for (int i = 0; i < N; i++)
-        u[i] = __shfl_sync(0xffffffffu, u[i], src);
-    S r;
-    memcpy(&r, u, sizeof(S));
-    return r;
+    uint32_t r;
+    asm volatile("{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n"
+                 " barrier.cta.red.and.pred q, %2, 128, p;\n selp.u32 %0, 1, 0, q;\n}"
+                 : "=r"(r)
+                 : "r"((uint32_t)v), "r"(id)
+                 : "memory");
+    return r != 0;
 }
+
+template <typename S>
+struct alignas(2 * sizeof(S)) ScalePair {
+    S a, b;
+};
 
 __device__ __forceinline__ void cluster_sync()
 {
@@ -135,7 +144,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     linear_gemm_kernel(const __grid_constant__ CUtensorMap wmap,
                        const __grid_constant__ CUtensorMap bmap, const GemmCall a)
 {
-    using G = LGeo<TOK>;
+    using G = LGeo<TOK, GRAD>;
     using Q = W4<T>;
     constexpr bool kBf16 = sizeof(typename Q::Scale) == 8;
     extern __shared__ uint8_t smem_raw[];
@@ -373,22 +382,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int q = warp & 3, wg = warp >> 2, g = lane >> 2, tq = lane & 3;
         const uint32_t tlane = (uint32_t)(32 * q) << 16;
         const int ng = c.w.K / c.w.group, gsh = c.w.group == 128 ? 7 : c.w.group == 64 ? 6 : 5;
-        // scale << 16 | zero point, 0 outside the matrix.  Forward: of this
-        // thread's row for each 32 K of the block.  Gradient: of the rows 2 lane,
-        // 2 lane + 1 of the block's first and second half, for this quarter's columns.
-        const auto load_meta = [&](int m0, int b, uint32_t (&m)[4]) {
+        const int per_blk = kBlk / c.w.group;       // groups along 128 K
+        const int r = 32 * q + lane;
+        // Scales and zero points (0 outside the matrix) of one matrix row over 128
+        // K: forward, this thread's row of the tile over the block; gradient,
+        // row r of the block over the tile.  They are loaded one block ahead and
+        // first touched a block later: a warp stalls on a loaded value where it
+        // is used.
+        struct Meta {
+            uint32_t s[4], z[4];
+        };
+        const auto load_meta = [&](int m0, int b, Meta &m) {
+            const int row = (GRAD ? b * kBlk : m0) + r;
+            const int g0 = (GRAD ? m0 : b * kBlk) >> gsh;
+            const long long at = (long long)row * ng + g0;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const int row = GRAD ? b * kBlk + 64 * (j >> 1) + 2 * lane + (j & 1)
-                                     : m0 + 32 * q + lane;
-                const int k = GRAD ? m0 + 32 * q : b * kBlk + 32 * j;
-                if (!GRAD && j > 0 && (k & (c.w.group - 1))) {
-                    m[j] = m[j - 1];
-                } else {
-                    const long long at = (long long)row * ng + (k >> gsh);
-                    m[j] = row < c.w.rows && k < c.w.K
-                               ? (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at]
-                               : 0;
+                m.s[j] = m.z[j] = 0;
+                if (j < per_blk && g0 + j < ng && row < c.w.rows) {
+                    m.s[j] = c.w.scales[at + j];
+                    m.z[j] = c.w.zeros[at + j];
                 }
             }
         };
@@ -410,23 +423,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         };
         Place at{tile0, tile0 % a.mt * kM, blk0 + wg, (unsigned)wg, 0u};
         settle(at);
-        uint32_t meta[4] = {}, next[4] = {};
+        Meta meta{}, next{};
         if (at.t < tiles)
             load_meta(at.m0, at.b, next);
-        while (at.t < tiles && ok) {
+        for (unsigned buf = 0; at.t < tiles && (GRAD || ok); buf ^= 1) {
             const int b = at.b, steps = b + 1 == blocks && C - b * kBlk <= 64 ? 1 : 2;
             const unsigned cc = at.cc;
             unsigned ac = at.ac0 + 2 * (b - blk0);
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                meta[j] = next[j];
+            meta = next;
             at.b += 2;
             at.cc += 2;
             settle(at);
             if (at.t < tiles)       // the next block's arrive while this one is unpacked
                 load_meta(at.m0, at.b, next);
             const uint32_t s = cc % G::cs;
-            if (!warp_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag)) {
+            // gradient: this group's words of the block (zero points, then scales)
+            uint32_t *zw = reinterpret_cast<uint32_t *>(smem + G::meta_off +
+                                                        (2 * wg + buf) * G::meta_buf);
+            typename Q::Scale *sw = reinterpret_cast<typename Q::Scale *>(zw + 4 * 64);
+            if (GRAD) {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (j < per_blk) {      // a row pair's two words, one by each of its lanes
+                        const uint32_t s2 = __shfl_xor_sync(0xffffffffu, meta.s[j], 1);
+                        const uint32_t z2 = __shfl_xor_sync(0xffffffffu, meta.z[j], 1);
+                        if (lane & 1)
+                            sw[64 * j + (r >> 1)] = Q::scale(s2, meta.s[j]);
+                        else
+                            zw[64 * j + (r >> 1)] = Q::zero(meta.z[j], z2).lo;
+                    }
+            }
+            bool have = ok && warp_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag);
+            if (GRAD)       // the group's words are written; its warps go on, or leave, together
+                have = group_and(1 + wg, have);
+            if (!have) {
                 ok = false;
                 break;
             }
@@ -434,11 +464,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             uint4 cw[4];
             if (!GRAD) {
                 // row r's 16-byte chunk i sits at i ^ (r / 2 % 4) (64-byte swizzle)
-                const int r = 32 * q + lane;
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
                                                              ((i ^ ((r >> 1) & 3)) << 4));
+                // every quarter of the block its group's
+#pragma unroll
+                for (int j = 3; j > 0; j--) {
+                    const int from = c.w.group == 128 ? 0 : c.w.group == 64 ? j / 2 : j;
+                    meta.s[j] = from == 0 ? meta.s[0] : from == 1 ? meta.s[1] : meta.s[j];
+                    meta.z[j] = from == 0 ? meta.z[0] : from == 1 ? meta.z[1] : meta.z[j];
+                }
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(code_empty + 8 * s);
@@ -452,9 +488,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (!GRAD) {
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const uint32_t m = meta[2 * h + i];
-                        const typename Q::Zero z = Q::zero(m & 0xff, m & 0xff);
-                        const typename Q::Scale sc = Q::scale(m >> 16, m >> 16);
+                        const uint32_t zb = meta.z[2 * h + i], sb = meta.s[2 * h + i];
+                        const typename Q::Zero z = Q::zero(zb, zb);
+                        const typename Q::Scale sc = Q::scale(sb, sb);
                         const uint4 v = cw[2 * h + i];
                         const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
@@ -472,10 +508,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                     }
                 } else {
-                    // this lane's row pair of the half, as the fields' operands
-                    const uint32_t m0 = meta[2 * h], m1 = meta[2 * h + 1];
-                    const typename Q::Zero zp = Q::zero(m0 & 0xff, m1 & 0xff);
-                    const typename Q::Scale sp = Q::scale(m0 >> 16, m1 >> 16);
+                    const int slot = 64 * ((32 * q) >> gsh) + 32 * h + 2 * tq;
                     const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
                     // row r's 16-byte chunk q sits at q ^ (r / 2 % 4) (64-byte
                     // swizzle); r = 64 h + 16 ss + 4 tq + i
@@ -492,19 +525,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                                 (i < 2 ? w01 : w23) + ss * 1024 + i * 64);
 #pragma unroll
                     for (int ss = 0; ss < 4; ss++) {        // 16 rows: pairs 8 ss + 2 tq, + 1
-                        const typename Q::Zero z01 = shfl_of(zp, 8 * ss + 2 * tq);
-                        const typename Q::Zero z23 = shfl_of(zp, 8 * ss + 2 * tq + 1);
-                        const typename Q::Scale s01 = shfl_of(sp, 8 * ss + 2 * tq);
-                        const typename Q::Scale s23 = shfl_of(sp, 8 * ss + 2 * tq + 1);
-                        uint32_t p[4], r[4];
+                        const uint2 zz = *reinterpret_cast<const uint2 *>(zw + slot + 8 * ss);
+                        const typename Q::Zero z01 = Q::zero_of(zz.x), z23 = Q::zero_of(zz.y);
+                        const ScalePair<typename Q::Scale> sc =
+                            *reinterpret_cast<const ScalePair<typename Q::Scale> *>(sw + slot + 8 * ss);
+                        uint32_t p[4], p2[4];
                         Q::unpack(__byte_perm(w[ss][0], w[ss][1], sel), z01, p);
-                        Q::unpack(__byte_perm(w[ss][2], w[ss][3], sel), z23, r);
+                        Q::unpack(__byte_perm(w[ss][2], w[ss][3], sel), z23, p2);
                         // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
 #pragma unroll
                         for (int u = 0; u < 4; u++) {
                             const int to = 16 * (u >> 1) + 4 * ss + 2 * (u & 1);
-                            col[to] = Q::mul(p[u], s01);
-                            col[to + 1] = Q::mul(r[u], s23);
+                            col[to] = Q::mul(p[u], sc.a);
+                            col[to + 1] = Q::mul(p2[u], sc.b);
                         }
                     }
                     if (h + 1 == steps) {
@@ -661,14 +694,14 @@ cudaError_t launch(const GemmCall &a, const CUtensorMap &wmap, const CUtensorMap
 {
     auto kernel = linear_gemm_kernel<T, GRAD, TOK>;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LGeo<TOK>::smem);
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, LGeo<TOK, GRAD>::smem);
     if (e != cudaSuccess)
         return e;
     const long long tiles = (long long)a.mt * a.nt;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.splits > 1 ? tiles * a.splits : std::min<long long>(tiles, num_sms)));
     cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = LGeo<TOK>::smem;
+    cfg.dynamicSmemBytes = LGeo<TOK, GRAD>::smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -36,7 +36,12 @@ struct W4<__half> {
     static __device__ __forceinline__ Zero zero(uint32_t z0, uint32_t z1)
     {
         const uint32_t z = z0 | (z1 << 16);
-        return {0x64006400u + z, 0xD400D400u + (z << 4)};
+        return zero_of(0x64006400u + z);
+    }
+    // from its `lo` word: the two words' 16 z differ by a constant
+    static __device__ __forceinline__ Zero zero_of(uint32_t lo)
+    {
+        return {lo, (lo << 4) + (0xD400D400u - (0x64006400u << 4))};
     }
     // the four fields' q - z
     static __device__ __forceinline__ void unpack(uint32_t w, const Zero &z, uint32_t (&p)[4])
@@ -77,6 +82,7 @@ struct W4<__nv_bfloat16> {
     {
         return {0x43004300u + (z0 | (z1 << 16))};
     }
+    static __device__ __forceinline__ Zero zero_of(uint32_t lo) { return {lo}; }
     static __device__ __forceinline__ void unpack(uint32_t w, const Zero &z, uint32_t (&p)[4])
     {
 #pragma unroll
