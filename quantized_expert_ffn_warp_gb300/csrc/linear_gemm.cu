@@ -16,7 +16,7 @@
 //     pairs two rows' nibbles) and stores them in the 16-lane x 256-bit tensor
 //     memory layout, lane 8 j + g of a quarter holding column 4 g + j.
 // Roles of a persistent CTA (one per SM): a code producer and a B producer
-// (TMA), two groups of four dequant warps taking alternate blocks, one or two
+// (TMA), three groups of four dequant warps taking blocks in turn, one or two
 // MMA warps, four epilogue warps.  Tiles of more than 128 tokens need one MMA
 // warp; smaller MMAs take less time than one thread needs to issue the next,
 // so two warps then run alternate 64-steps into accumulators of their own,
@@ -38,7 +38,8 @@ namespace {
 constexpr int kM = 128;             // output features per tile (MMA M)
 constexpr int kBlk = 128;           // contraction elements per code block
 constexpr int kBlkBytes = 128 * 64; // codes of a block
-constexpr int kDeq = 8, kEpi = 4;   // warps
+constexpr int kGroups = 3;          // dequant groups of four warps
+constexpr int kDeq = 4 * kGroups, kEpi = 4;   // warps
 constexpr int kEpi0 = kDeq, kProd = kDeq + kEpi, kBProd = kProd + 1, kMma0 = kProd + 2;
 constexpr int kGemmThreads = (kMma0 + 2) * 32;
 
@@ -49,22 +50,23 @@ struct LGeo {
     static constexpr int a_cols = 32;                   // 64 contraction elements, two per column
     static constexpr int b_stage = TOK * 128;           // TOK rows of 64 elements
     // A and B stages (64 contraction elements each), in lockstep
-    static constexpr int as = TOK > 128 ? (GRAD ? 5 : 6) : TOK > 64 ? 8 : 12;
-    static constexpr int cs = TOK > 128 ? 4 : TOK > 64 ? 8 : 12;    // code blocks
+    static constexpr int as = TOK > 128 ? 5 : TOK > 64 ? 8 : 12;
+    // code blocks: a multiple of the groups, so that a group always reads the same ones
+    static constexpr int cs = TOK > 64 ? 6 : 12;
     static constexpr int b_off = 0, c_off = as * b_stage;
     // gradient: per dequant group two buffers of a block's zero points and
     // scales, as the unpacking's operand words: [4 column quarters][64 row pairs]
     static constexpr int meta_off = c_off + cs * kBlkBytes;
     static constexpr int meta_buf = 4 * 64 * 12;
-    static constexpr int bar_off = meta_off + (GRAD ? 4 * meta_buf : 0);
+    static constexpr int bar_off = meta_off + (GRAD ? 2 * kGroups * meta_buf : 0);
     static constexpr int nbars = 2 * cs + 3 * as + 4;
-    static constexpr int smem = bar_off + 8 * nbars + 16 + 1024;
+    static constexpr int smem = bar_off + 8 * nbars + 16;
 };
 template <int TOK, bool GRAD>
 constexpr bool lgeo_ok()
 {
     using G = LGeo<TOK, GRAD>;
-    return G::smem <= 227 * 1024 && G::acc_cols + G::as * G::a_cols <= 512 && G::cs % 2 == 0 &&
+    return G::smem <= 227 * 1024 && G::acc_cols + G::as * G::a_cols <= 512 && G::cs % kGroups == 0 && G::as >= 5 &&
            (TOK > 128 || 128 * TOK * 4 <= G::c_off);    // a partial tile fits in the B stages
 }
 static_assert(lgeo_ok<256, false>() && lgeo_ok<128, false>() && lgeo_ok<64, false>() &&
@@ -147,10 +149,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     using G = LGeo<TOK, GRAD>;
     using Q = W4<T>;
     constexpr bool kBf16 = sizeof(typename Q::Scale) == 8;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024u - (saddr(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+    if (saddr(smem) & 1023) {       // the swizzled stages need it; never seen otherwise
+        if (threadIdx.x == 0 && a.c.status)
+            atomicOr(a.c.status, MOE_STATUS_TIMEOUT);
+        return;
+    }
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G::bar_off);
     const uint32_t code_full = saddr(bars), code_empty = code_full + 8 * G::cs;
     const uint32_t a_full = code_empty + 8 * G::cs, b_full = a_full + 8 * G::as;
@@ -163,12 +169,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::cs; s++) {
             bar_init(code_full + 8 * s, 1);
-            bar_init(code_empty + 8 * s, kDeq / 2);
+            bar_init(code_empty + 8 * s, 4);
         }
         for (int s = 0; s < G::as; s++) {
-            bar_init(a_full + 8 * s, kDeq / 2);
+            bar_init(a_full + 8 * s, 4);
             bar_init(b_full + 8 * s, 1);
-            bar_init(stage_empty + 8 * s, 1);
+            bar_init(stage_empty + 8 * s, G::chains);
         }
         bar_init(acc_full, G::chains);
         bar_init(acc_empty, kEpi);
@@ -277,25 +283,29 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     break;
                 }
                 for (int j = 0; j < nsteps; j++) {
-                    if (G::chains == 1 || (j & 1) == ch) {
-                        if (!warp_wait(a_full + 8 * slot, par, abort_flag) ||
-                            !warp_wait(b_full + 8 * slot, par, abort_flag)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
-                        const uint32_t abase = tmem + G::acc_cols + slot * G::a_cols;
-                        const uint64_t bdesc = sw128_desc(saddr(smem + G::b_off) + slot * G::b_stage);
-                        if (elect_one()) {
+                    // Both chains wait for every step's A and release its stage, so
+                    // that stages are released in step order; one of them
+                    // multiplies.
+                    const bool own = G::chains == 1 || (j & 1) == ch;
+                    if (!warp_wait(a_full + 8 * slot, par, abort_flag) ||
+                        (own && !warp_wait(b_full + 8 * slot, par, abort_flag))) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t abase = tmem + G::acc_cols + slot * G::a_cols;
+                    const uint64_t bdesc = sw128_desc(saddr(smem + G::b_off) + slot * G::b_stage);
+                    if (elect_one()) {
+                        if (own) {
 #pragma unroll
                             for (int kk = 0; kk < 4; kk++)      // 16 each: A 8 columns, B 32 bytes
                                 umma_ta(dacc, abase + kk * 8, bdesc + 2 * kk, idesc,
                                         j >= G::chains || kk ? 1u : 0u);
-                            umma_commit(stage_empty + 8 * slot);
                         }
-                        __syncwarp();
-                        issued = true;
+                        umma_commit(stage_empty + 8 * slot);
                     }
+                    __syncwarp();
+                    issued = true;
                     if (++slot == (unsigned)G::as) {
                         slot = 0;
                         par ^= 1;
@@ -405,7 +415,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
         };
-        // this group's place in the CTA's blocks: every second one of them
+        // this group's place in the CTA's blocks: every kGroups-th one of them
         struct Place {
             int t, m0, b;
             unsigned cc, ac0;       // blocks before this one; 64-steps before this tile
@@ -431,8 +441,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const unsigned cc = at.cc;
             unsigned ac = at.ac0 + 2 * (b - blk0);
             meta = next;
-            at.b += 2;
-            at.cc += 2;
+            at.b += kGroups;
+            at.cc += kGroups;
             settle(at);
             if (at.t < tiles)       // the next block's arrive while this one is unpacked
                 load_meta(at.m0, at.b, next);
@@ -546,6 +556,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             bar_arrive(code_empty + 8 * s);
                     }
                 }
+                // A parity wait cannot tell a phase from the one two before it.
+                // Stages are released in step order, and this group last waited for
+                // a step at most 5 before this one, so the use before the one
+                // waited for has ended (as >= 5).
                 if (!warp_wait(stage_empty + 8 * as, ((ac / G::as) & 1) ^ 1, abort_flag)) {
                     ok = false;
                     break;
