@@ -379,7 +379,8 @@ cudaError_t launch_group_size(const W4Call &c, int grad, int num_sms, cudaStream
 }  // namespace
 
 bool linear_gemm_fits(const W4Call &c);
-cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int num_sms, cudaStream_t st);
+cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int num_sms,
+                               cudaStream_t st);
 bool device_pointer_here(const void *p, int dev);
 int record_failure(int code, const char *msg);
 int record_success();
@@ -446,7 +447,7 @@ int run_linear(const W4Call &c, int dtype, int grad, void *stream)
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     if (c.n > kFewTokens && linear_gemm_fits(c))
-        e = launch_linear_gemm(c, dtype == MOE_BF16, grad, sms, st);
+        e = launch_linear_gemm(c, dtype == MOE_BF16, grad, dev, sms, st);
     else
         e = dtype == MOE_FP16 ? launch_group_size<__half>(c, grad, sms, st)
                               : launch_group_size<__nv_bfloat16>(c, grad, sms, st);

@@ -27,6 +27,7 @@
 // Every wait is bounded in time; on expiry the output is incomplete and the
 // caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
+#include <mutex>
 
 #include "tcgen05.cuh"
 #include "w4.cuh"
@@ -118,6 +119,11 @@ struct alignas(2 * sizeof(S)) ScalePair {
     S a, b;
 };
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
@@ -166,6 +172,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + G::nbars);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    if (warp == kProd && lane == 0)
+        prefetch_map(&wmap);
+    if (warp == kBProd && lane == 0)
+        prefetch_map(&bmap);
     if (threadIdx.x == 0) {
         for (int s = 0; s < G::cs; s++) {
             bar_init(code_full + 8 * s, 1);
@@ -340,7 +350,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
             const bool two = G::chains == 2 && nsteps > 1;
             const int cols = min(a.tok, c.n - tok0);
-            float *part = reinterpret_cast<float *>(smem + G::b_off) + 32 * q + lane;
+            float *part = reinterpret_cast<float *>(smem + G::b_off) +
+                          lane_feature<GRAD>(32 * q + lane);    // in feature order
             const bool in = f < F;
             const float bias = c.bias && in ? Q::to_float(static_cast<const T *>(c.bias)[f]) : 0.f;
             T *out = static_cast<T *>(c.out) + tok0 * c.ldo + f;
@@ -605,26 +616,36 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int m0 = tile0 % a.mt * kM, tok0 = tile0 / a.mt * a.tok;
         const int lo = a.tok * rank / a.splits, hi = a.tok * (rank + 1) / a.splits;
         const uint32_t base = saddr(smem + G::b_off);
-        for (int i = lo * kM + threadIdx.x; i < hi * kM; i += kGemmThreads) {
-            const int tok = tok0 + i / kM, f = m0 + lane_feature<GRAD>(i % kM);
+        for (int i = lo * kM + 4 * threadIdx.x; i < hi * kM; i += 4 * kGemmThreads) {
+            const int tok = tok0 + i / kM, f = m0 + i % kM;
             if (tok >= c.n || f >= F)
                 continue;
-            float v = 0.f, p[8];
+            float4 p[8];
 #pragma unroll
             for (int r = 0; r < 8; r++) {
                 uint32_t remote;
-                p[r] = 0.f;
+                p[r] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (r < a.splits) {
                     asm("mapa.shared::cluster.u32 %0, %1, %2;"
                         : "=r"(remote)
                         : "r"(base + 4 * i), "r"(r));
-                    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(p[r]) : "r"(remote));
+                    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                                 : "=f"(p[r].x), "=f"(p[r].y), "=f"(p[r].z), "=f"(p[r].w)
+                                 : "r"(remote));
                 }
             }
+            float v[4] = {};
 #pragma unroll
-            for (int r = 0; r < 8; r++)
-                v += p[r];
-            store_out<T>(c, v, tok, f);
+            for (int r = 0; r < 8; r++) {
+                v[0] += p[r].x;
+                v[1] += p[r].y;
+                v[2] += p[r].z;
+                v[3] += p[r].w;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                if (f + u < F)
+                    store_out<T>(c, v[u], tok, f + u);
         }
         cluster_sync();     // a CTA's shared memory stays until its peers have read it
     }
@@ -669,12 +690,57 @@ struct Plan {
     int tok, nt, splits;
 };
 
+// Clusters of each size that run at once (they cannot use every SM: a GPC
+// holds a whole number of them), looked up once per device.
+constexpr int kMaxSplits = 8;
+struct Clusters {
+    std::once_flag once;
+    int n[kMaxSplits + 1] = {};
+};
+
+const int *cluster_table(int dev)
+{
+    constexpr int kMaxDevices = 64;
+    static Clusters table[kMaxDevices];
+    static const int none[kMaxSplits + 1] = {};
+    if (dev < 0 || dev >= kMaxDevices)
+        return none;        // no splits
+    Clusters &t = table[dev];
+    std::call_once(t.once, [&t] {
+        auto kernel = linear_gemm_kernel<__half, false, 128>;
+        constexpr int smem = LGeo<128, false>::smem;
+        if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess) {
+            cudaGetLastError();
+            return;
+        }
+        for (int s = 2; s <= kMaxSplits; s++) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(s);
+            cfg.blockDim = dim3(kGemmThreads);
+            cfg.dynamicSmemBytes = smem;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = s;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&t.n[s], kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                t.n[s] = 0;
+            }
+        }
+    });
+    return t.n;
+}
+
 // Tokens per tile and splits along the contraction: the smallest estimated time,
 // in SM cycles, of the busiest SM.  A 64-step of a tile of N tokens takes 2 N
 // cycles on the tensor core and, on the weights' side, at least about 220
 // (dequantisation, and the packed block's share of the HBM rate); a tile costs
 // its epilogue and a cluster the exchange of its partial tiles.
-Plan plan(int C, int F, int n, int num_sms)
+Plan plan(int C, int F, int n, int num_sms, const int *clusters)
 {
     const int mt = (F + kM - 1) / kM, steps = (C + 63) / 64;
     Plan best{};
@@ -683,10 +749,10 @@ Plan plan(int C, int F, int n, int num_sms)
         const int tok = ((n + nt - 1) / nt + 15) / 16 * 16;
         if ((n + tok - 1) / tok != nt)
             continue;
-        for (int s = 1; s == 1 || (s <= (tok <= 128 ? 8 : 1) && 4 * s <= steps); s *= 2) {
+        for (int s = 1; s == 1 || (s <= kMaxSplits && tok <= 128 && 4 * s <= steps); s++) {
             const long long ctas = (long long)mt * nt * s;
-            if (s > 1 && ctas > num_sms)
-                break;
+            if (s > 1 && (long long)mt * nt > clusters[s])
+                continue;       // a cluster would wait for another one's SMs
             const double waves = (double)((ctas + num_sms - 1) / num_sms);
             const double step = std::max(2.0 * tok, 220.0);
             const double cost = waves * ((double)(steps + s - 1) / s * step + 12.0 * tok + 1500) +
@@ -748,10 +814,11 @@ bool linear_gemm_fits(const W4Call &c)
     return reinterpret_cast<uintptr_t>(c.in) % 16 == 0 && c.ldi % 8 == 0;
 }
 
-cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int num_sms, cudaStream_t st)
+cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int num_sms,
+                               cudaStream_t st)
 {
     const int C = grad ? c.w.rows : c.w.K, F = grad ? c.w.K : c.w.rows;
-    const Plan p = plan(C, F, c.n, num_sms);
+    const Plan p = plan(C, F, c.n, num_sms, cluster_table(dev));
     GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits};
     CUtensorMap wmap, bmap;
     if (!encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
