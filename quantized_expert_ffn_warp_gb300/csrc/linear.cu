@@ -5,11 +5,15 @@
 // one scale and one zero point per group along K; section 3.4: hand-written
 // INT4 GEMV; "Flash-MoE", section 3: dequant matvec).
 //
-// Both read every packed byte once per block of tokens and are bound by that
-// stream while the tokens are few.  The weights are the MMA's A operand
-// (M = 16), the tokens its N = 8 columns.  The MMA's K order is free as long as
-// A and B agree, so a lane's MMA elements are the nibbles of words it loads
-// contiguously, and no lane exchanges weights with another.
+// Both are bound by the stream of packed bytes.  The weights are the MMA's A
+// operand (M = 16), the tokens its N = 8 columns.  The MMA's K order is free as
+// long as A and B agree, so a lane's MMA elements are the nibbles of whole
+// words, and no lane exchanges weights with another.
+//
+// One CTA per SM.  Each of its (up to 16) warps has its own slice of the matrix
+// and its own ring in shared memory, which TMA fills ahead; the warp refills a
+// stage itself as soon as it has read it, so that about 128 KB per SM are under
+// way whatever the arithmetic does, and no warp waits for another.
 #include <algorithm>
 
 #include "w4.cuh"
@@ -18,263 +22,588 @@ namespace qe {
 
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kWarps = 16;              // multiplying warps
+constexpr int kRing = 8 * 1024;         // bytes per warp
 
 // ---- y = x W^T -------------------------------------------------------------
-// A warp's unit is 16 rows x 512 K: lane (g = lane / 4, t = lane % 4) loads, of
-// rows g and g + 8, the 16 bytes at K = 128 j + 32 t for j = 0..3, i.e. the
-// warp reads 256 contiguous bytes of each row.  Each 16-byte word is four
-// MMA K-steps' worth of half of the lane's A elements: its fields (i, i + 4)
-// pair with the activations (i, i + 4) of the same 8 elements.
-// Groups of 128: the products with the exact integers q - z are summed per
-// group and the fp32 sum is scaled (no rounding of weights).  Smaller groups
-// lie inside one MMA: the scale is folded into the weights, one rounding.
-template <typename T, int GS, int NT, int RT>
-__global__ void __launch_bounds__(kThreads) linear_kernel(W4Call c, int kw_n)
+// A stage is 16 RT rows x a slice of 256 K, i.e. 128 bytes of each row (128-byte
+// swizzle).  The warps of a row tile (16 RT rows) take its slices in turn; up
+// to 4096 K a warp has one slice for the whole call, and that slice's
+// activations stay in its registers as MMA operands.  Of 128 K, lane (g, t)
+// holds word t of each of the four 16-byte pieces v of rows g and g + 8, i.e. K =
+// 32 v + 8 t .. + 7, whose fields (i, i + 4) pair with the activations (i, i
+// + 4) of the same 8.  So two MMAs cover 32 consecutive K: the products with
+// the exact integers q - z are summed over one group and the fp32 sum is
+// scaled; no weight is rounded, for any group size.
+// A tile's partial sums go to one more warp through shared memory, which adds
+// them in order and stores the results while the others go on.
+struct FwdArgs {
+    W4Call c;
+    int kw_n, rw_n;     // warps along K, and row tiles at a time, of a CTA
+    int vec_meta;       // rows of scales and zero points allow vector loads
+};
+
+template <int RT>
+struct FwdGeo {
+    static constexpr int stage = RT * 16 * 128, stages = kRing / stage;
+    static constexpr int out = 16 * RT * 8;                // results of a row tile
+    static constexpr int red_off = kWarps * kRing;              // [2][kWarps][out] sums
+    static constexpr int bar_off = red_off + 2 * 4 * kWarps * out;
+    static constexpr int nbars = kWarps * stages + 4;   // full stages; sums full, empty
+    static constexpr int smem = bar_off + 8 * nbars + 16;
+};
+static_assert(FwdGeo<1>::smem <= 227 * 1024 && FwdGeo<2>::smem <= 227 * 1024, "shared memory");
+
+// A row's scales and zero points over 256 K, as loaded.
+template <int GS>
+struct RowMeta;
+template <>
+struct RowMeta<128> {
+    uint32_t s, z;
+    __device__ __forceinline__ void load(const uint16_t *sp, const uint8_t *zp)
+    {
+        s = *reinterpret_cast<const uint32_t *>(sp);
+        z = *reinterpret_cast<const uint16_t *>(zp);
+    }
+};
+template <>
+struct RowMeta<64> {
+    uint2 s;
+    uint32_t z;
+    __device__ __forceinline__ void load(const uint16_t *sp, const uint8_t *zp)
+    {
+        s = *reinterpret_cast<const uint2 *>(sp);
+        z = *reinterpret_cast<const uint32_t *>(zp);
+    }
+};
+template <>
+struct RowMeta<32> {
+    uint4 s;
+    uint2 z;
+    __device__ __forceinline__ void load(const uint16_t *sp, const uint8_t *zp)
+    {
+        s = *reinterpret_cast<const uint4 *>(sp);
+        z = *reinterpret_cast<const uint2 *>(zp);
+    }
+};
+
+// The same by single loads, the last group repeated past the row's end.
+template <int GS>
+__device__ __forceinline__ void load_each(RowMeta<GS> &m, const uint16_t *sp, const uint8_t *zp,
+                                          int left)
+{
+    constexpr int N = 256 / GS;
+    uint32_t s[(N + 1) / 2] = {}, z[(N + 3) / 4] = {};
+#pragma unroll
+    for (int i = 0; i < N; i++) {
+        const int at = min(i, left - 1);
+        s[i / 2] |= (uint32_t)sp[at] << (16 * (i & 1));
+        z[i / 4] |= (uint32_t)zp[at] << (8 * (i & 3));
+    }
+    memcpy(&m.s, s, sizeof(m.s));
+    memcpy(&m.z, z, sizeof(m.z));
+}
+
+// Group i's zero point and scale out of a row's.
+__device__ __forceinline__ uint32_t word_of(uint32_t v, int) { return v; }
+__device__ __forceinline__ uint32_t word_of(const uint2 &v, int i) { return i ? v.y : v.x; }
+__device__ __forceinline__ uint32_t word_of(const uint4 &v, int i)
+{
+    return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+template <typename Q, typename M>
+__device__ __forceinline__ typename Q::Zero group_zero(const M &m, int i)
+{
+    const uint32_t z = word_of(m.z, i / 4) >> (8 * (i & 3)) & 0xff;
+    return Q::zero(z, z);
+}
+template <typename M>
+__device__ __forceinline__ float group_scale(const M &m, int i)
+{
+    return __half2float(__ushort_as_half((unsigned short)(word_of(m.s, i / 2) >> (16 * (i & 1)))));
+}
+
+template <typename T, int GS, int RT>
+__global__ void __launch_bounds__(32 * (kWarps + 1), 1)
+    linear_kernel(const __grid_constant__ CUtensorMap wmap, const FwdArgs a)
 {
     using Q = W4<T>;
-    extern __shared__ float red[];      // [kWarps][RT][NT][4][32]
-    pdl_enter();
+    using G = FwdGeo<RT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G::bar_off);
+    const uint32_t red_full = saddr(bars + kWarps * G::stages), red_empty = red_full + 16;
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + G::nbars);
+    const W4Call &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int kw = warp % kw_n, rw = warp / kw_n;
-    const int rows = c.w.rows, K = c.w.K, tok0 = blockIdx.y * 8 * NT;
-    const int row0 = (blockIdx.x * (kWarps / kw_n) + rw) * 16 * RT;
-    const int ng = K / GS;
-    const T *x = static_cast<const T *>(c.in);
-
-    float acc[RT][NT][4];
-#pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int m = 0; m < NT; m++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                acc[r][m][i] = 0.f;
-
-    for (int k0 = kw * 512; k0 < K; k0 += kw_n * 512) {
-        uint4 wq[RT][4][2];
-        uint32_t sz[RT][GS == 128 ? 1 : 4][2];   // scale bits << 16 | zero point
-#pragma unroll
-        for (int r = 0; r < RT; r++)
-#pragma unroll
-            for (int h = 0; h < 2; h++) {
-                // rows past the matrix repeat its last row; their sums are not stored
-                const long long row = min(row0 + r * 16 + g + 8 * h, rows - 1);
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int k = k0 + 128 * j + 32 * t;
-                    wq[r][j][h] = k < K ? ld_codes16(c.w.codes + row * (K / 2) + k / 2)
-                                        : make_uint4(0, 0, 0, 0);
-                }
-                if (GS == 128) {
-                    const long long at = row * ng + min(k0 / 128 + t, ng - 1);
-                    sz[r][0][h] = (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const long long at = row * ng + min((k0 + 128 * j + 32 * t) / GS, ng - 1);
-                        sz[r][j][h] = (uint32_t)c.w.scales[at] << 16 | c.w.zeros[at];
-                    }
-                }
+    const int warps = a.kw_n * a.rw_n;      // multiplying warps; the next one adds
+    const int kw = warp % a.kw_n, rw = warp / a.kw_n;
+    const uint32_t full = saddr(bars + warp * G::stages);
+    const uint32_t ring = saddr(smem) + warp * kRing;
+    if (saddr(smem) & 1023) {       // the swizzled stages need it; never seen otherwise
+        if (threadIdx.x == 0 && c.status)
+            atomicOr(c.status, MOE_STATUS_TIMEOUT);
+        return;
+    }
+    if (lane == 0) {
+        if (warp < warps) {
+            prefetch_map(&wmap);
+            for (int i = 0; i < G::stages; i++)
+                bar_init(full + 8 * i, 1);
+        } else {
+            for (int i = 0; i < 2; i++) {
+                bar_init(red_full + 8 * i, warps);
+                bar_init(red_empty + 8 * i, 1);
             }
-#pragma unroll
-        for (int j = 0; j < 4; j++) {
-            const int k = k0 + 128 * j + 32 * t;
-            uint4 xv[NT][4];
-#pragma unroll
-            for (int m = 0; m < NT; m++) {
-                const int tok = tok0 + 8 * m + g;
-#pragma unroll
-                for (int v = 0; v < 4; v++)
-                    xv[m][v] = tok < c.n && k < K
-                                   ? *reinterpret_cast<const uint4 *>(x + tok * c.ldi + k + 8 * v)
-                                   : make_uint4(0, 0, 0, 0);
+            *abort_flag = 0;
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    pdl_enter();
+
+    const int rows = c.w.rows, K = c.w.K, tok0 = blockIdx.y * 8, ng = K / GS;
+    const int tiles = (rows + 16 * RT - 1) / (16 * RT), sets = (tiles + a.rw_n - 1) / a.rw_n;
+    const int slices = (K + 255) / 256;
+    bool ok = true;
+
+    if (warp < warps) {
+        // ------------------------------------------------------ multiply
+        // a stage's place: set of row tiles, and slice of K
+        struct Place {
+            int set, slice;
+        };
+        const auto advance = [&](Place &p) {
+            p.slice += a.kw_n;
+            if (p.slice >= slices) {
+                p.slice = kw;
+                p.set += gridDim.x;
             }
+        };
+        const auto fetch = [&](const Place &p, int slot) {
+            if (lane == 0) {
+                bar_expect_tx(full + 8 * slot, G::stage);
+                tma_load_2d(ring + slot * G::stage, &wmap, p.slice * 128,
+                            (p.set * a.rw_n + rw) * 16 * RT, full + 8 * slot);
+            }
+        };
+        Place first{(int)blockIdx.x, kw}, filled = first, loaded = first;
+        for (int i = 0; i < G::stages; i++)
+            if (filled.set < sets) {
+                fetch(filled, i);
+                advance(filled);
+            }
+
+        // Scales and zero points of a stage: lane l those of row l.  They are
+        // loaded two stages ahead, about as far as the codes: with that much
+        // under way a load takes several microseconds.
+        const auto load_meta = [&](const Place &p, RowMeta<GS> &m) {
+            // rows past the matrix repeat its last row; their sums are not stored
+            const int row = min((p.set * a.rw_n + rw) * 16 * RT + (lane & (16 * RT - 1)), rows - 1);
+            const int at = p.slice * (256 / GS);
+            const uint16_t *sp = c.w.scales + (long long)row * ng + at;
+            const uint8_t *zp = c.w.zeros + (long long)row * ng + at;
+            if (a.vec_meta)
+                m.load(sp, zp);
+            else
+                load_each<GS>(m, sp, zp, ng - at);
+        };
+        RowMeta<GS> ahead[2] = {};
 #pragma unroll
-            for (int r = 0; r < RT; r++) {
-                uint32_t a0, a1;
-                if (GS == 128) {
-                    a0 = __shfl_sync(0xffffffffu, sz[r][0][0], (lane & ~3) | j);
-                    a1 = __shfl_sync(0xffffffffu, sz[r][0][1], (lane & ~3) | j);
-                } else {
-                    a0 = sz[r][j][0];
-                    a1 = sz[r][j][1];
-                }
-                const typename Q::Zero z0 = Q::zero(a0 & 0xff, a0 & 0xff);
-                const typename Q::Zero z1 = Q::zero(a1 & 0xff, a1 & 0xff);
-                const uint32_t w0[4] = {wq[r][j][0].x, wq[r][j][0].y, wq[r][j][0].z, wq[r][j][0].w};
-                const uint32_t w1[4] = {wq[r][j][1].x, wq[r][j][1].y, wq[r][j][1].z, wq[r][j][1].w};
-                float part[NT][4];
+        for (int i = 0; i < 2; i++)
+            if (loaded.set < sets) {
+                load_meta(loaded, ahead[i]);
+                advance(loaded);
+            }
+
+        // a slice's activations as B operands: fields (i, i + 4) of each 8
+        uint32_t xb[2][4][4];
+        const auto load_x = [&](int slice) {
 #pragma unroll
-                for (int m = 0; m < NT; m++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        part[m][i] = GS == 128 ? 0.f : acc[r][m][i];
+            for (int j = 0; j < 2; j++)
 #pragma unroll
                 for (int v = 0; v < 4; v++) {
-                    uint32_t p[4], q[4];
-                    Q::unpack(w0[v], z0, p);
-                    Q::unpack(w1[v], z1, q);
-                    if (GS != 128) {
-                        const typename Q::Scale s0 = Q::scale(a0 >> 16, a0 >> 16);
-                        const typename Q::Scale s1 = Q::scale(a1 >> 16, a1 >> 16);
+                    const int tok = tok0 + g, k = slice * 256 + 128 * j + 32 * v + 8 * t;
+                    uint4 b = make_uint4(0, 0, 0, 0);
+                    if (tok < c.n && k < K)
+                        b = *reinterpret_cast<const uint4 *>(static_cast<const T *>(c.in) +
+                                                             tok * c.ldi + k);
+                    xb[j][v][0] = __byte_perm(b.x, b.z, 0x5410);
+                    xb[j][v][1] = __byte_perm(b.x, b.z, 0x7632);
+                    xb[j][v][2] = __byte_perm(b.y, b.w, 0x5410);
+                    xb[j][v][3] = __byte_perm(b.y, b.w, 0x7632);
+                }
+        };
+        if (slices <= a.kw_n)
+            load_x(kw);
+
+        int slot = 0;
+        uint32_t parity = 0, buf = 0, red_parity = 1;
+        for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+            float acc[RT][4];
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            p[i] = Q::mul(p[i], s0);
-                            q[i] = Q::mul(q[i], s1);
+            for (int r = 0; r < RT; r++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    acc[r][i] = 0.f;
+            for (int slice = kw; slice < slices; slice += a.kw_n) {
+                if (slices > a.kw_n)
+                    load_x(slice);
+                const RowMeta<GS> meta = ahead[0];
+                ahead[0] = ahead[1];
+                if (loaded.set < sets) {
+                    load_meta(loaded, ahead[1]);
+                    advance(loaded);
+                }
+                if (ok && !warp_wait(full + 8 * slot, parity, abort_flag)) {
+                    ok = false;
+                    *abort_flag = 1;
+                }
+                const uint32_t stage = ring + slot * G::stage;
+#pragma unroll
+                for (int r = 0; r < RT; r++) {
+                    // of rows g and g + 8 of this 16-row tile
+                    const RowMeta<GS> m0 = shfl_of(meta, 16 * r + g), m1 = shfl_of(meta, 16 * r + g + 8);
+#pragma unroll
+                    for (int j = 0; j < 2; j++) {
+                        uint32_t w0[4], w1[4];
+                        // 16-byte piece p of row r sits at p ^ (r % 8)
+                        const uint32_t row = stage + (r * 16 + (lane & 7)) * 128 +
+                                             (((4 * j + (lane >> 3)) ^ (lane & 7)) << 4);
+                        ldmatrix4(w0, row);
+                        ldmatrix4(w1, row + 8 * 128);
+                        float part[4];
+                        typename Q::Zero z0, z1;
+                        float f0 = 0.f, f1 = 0.f;
+#pragma unroll
+                        for (int v = 0; v < 4; v++) {
+                            if ((32 * v) % GS == 0) {       // a group begins
+                                const int i = (128 * j + 32 * v) / GS;
+                                z0 = group_zero<Q>(m0, i);
+                                z1 = group_zero<Q>(m1, i);
+                                f0 = group_scale(m0, i);
+                                f1 = group_scale(m1, i);
+                            }
+                            uint32_t p[4], q[4];
+                            Q::unpack(w0[v], z0, p);
+                            Q::unpack(w1[v], z1, q);
+                            const uint32_t *b = xb[j][v];
+                            if ((32 * v) % GS == 0)
+                                mma16816c<T>(part, p[0], q[0], p[1], q[1], b[0], b[1], 0.f, 0.f, 0.f,
+                                             0.f);
+                            else
+                                mma16816<T>(part, p[0], q[0], p[1], q[1], b[0], b[1]);
+                            mma16816<T>(part, p[2], q[2], p[3], q[3], b[2], b[3]);
+                            if ((32 * v + 32) % GS == 0) {  // and ends
+#pragma unroll
+                                for (int i = 0; i < 4; i++)
+                                    acc[r][i] = fmaf(i < 2 ? f0 : f1, part[i], acc[r][i]);
+                            }
                         }
                     }
-#pragma unroll
-                    for (int m = 0; m < NT; m++) {
-                        const uint4 b = xv[m][v];
-                        mma16816<T>(part[m], p[0], q[0], p[1], q[1], __byte_perm(b.x, b.z, 0x5410),
-                                    __byte_perm(b.x, b.z, 0x7632));
-                        mma16816<T>(part[m], p[2], q[2], p[3], q[3], __byte_perm(b.y, b.w, 0x5410),
-                                    __byte_perm(b.y, b.w, 0x7632));
-                    }
                 }
-                const float f0 = __half2float(__ushort_as_half((unsigned short)(a0 >> 16)));
-                const float f1 = __half2float(__ushort_as_half((unsigned short)(a1 >> 16)));
-#pragma unroll
-                for (int m = 0; m < NT; m++)
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        acc[r][m][i] = GS == 128 ? fmaf(i < 2 ? f0 : f1, part[m][i], acc[r][m][i])
-                                                 : part[m][i];
+                // every lane's reads are done before the copy engine writes the stage
+                fence_async_shared();
+                __syncwarp();
+                if (filled.set < sets) {
+                    fetch(filled, slot);
+                    advance(filled);
+                }
+                if (++slot == G::stages) {
+                    slot = 0;
+                    parity ^= 1;
+                }
             }
+            // this warp's sums, element o of the tile at o (token major)
+            if (ok && !warp_wait(red_empty + 8 * buf, red_parity, abort_flag)) {
+                ok = false;
+                *abort_flag = 1;
+            }
+            float *red = reinterpret_cast<float *>(smem + G::red_off) + (buf * kWarps + warp) * G::out;
+#pragma unroll
+            for (int r = 0; r < RT; r++)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    red[(2 * t + (i & 1)) * 16 * RT + 16 * r + g + 8 * (i >> 1)] = acc[r][i];
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(red_full + 8 * buf);
+            buf ^= 1;
+            if (!buf)
+                red_parity ^= 1;
+        }
+    } else {
+        // ------------------------------------------------------ add and store
+        // results of a set, 4 at a time: rows 4 i .. 4 i + 3 of a token
+        constexpr int kVec = G::out / 4, kPer = (kVec + 31) / 32;
+        const auto store = [&](int set, int rb, int o, const float (&v)[4]) {
+            const int row0 = (set * a.rw_n + rb) * 16 * RT + 4 * o % (16 * RT);
+            const int tok = tok0 + 4 * o / (16 * RT);
+            if (tok >= c.n)
+                return;
+            T *y = static_cast<T *>(c.out) + tok * c.ldo + row0;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                if (row0 + i >= rows)
+                    break;
+                float s = v[i];
+                if (c.bias)
+                    s += Q::to_float(static_cast<const T *>(c.bias)[row0 + i]);
+                if (c.residual)
+                    s += Q::to_float(static_cast<const T *>(c.residual)[tok * c.ldr + row0 + i]);
+                y[i] = Q::from_float(s);
+            }
+        };
+        uint32_t buf = 0, parity = 0;
+        for (int set = blockIdx.x; set < sets; set += gridDim.x) {
+            if (ok && !warp_wait(red_full + 8 * buf, parity, abort_flag)) {
+                ok = false;
+                *abort_flag = 1;
+            }
+            const float4 *red = reinterpret_cast<const float4 *>(smem + G::red_off) + buf * kWarps * kVec;
+            for (int rb = 0; rb < a.rw_n; rb++)
+#pragma unroll
+                for (int n = 0; n < kPer; n++) {
+                    const int o = 32 * n + lane;
+                    if (o >= kVec)
+                        break;
+                    float v[4] = {};
+#pragma unroll 4
+                    for (int w = 0; w < a.kw_n; w++) {
+                        const float4 p = red[(rb * a.kw_n + w) * kVec + o];
+                        v[0] += p.x;
+                        v[1] += p.y;
+                        v[2] += p.z;
+                        v[3] += p.w;
+                    }
+                    store(set, rb, o, v);
+                }
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(red_empty + 8 * buf);
+            buf ^= 1;
+            if (!buf)
+                parity ^= 1;
         }
     }
-
-    // sums of the K slices, in slice order
-#pragma unroll
-    for (int r = 0; r < RT; r++)
-#pragma unroll
-        for (int m = 0; m < NT; m++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                red[(((warp * RT + r) * NT + m) * 4 + i) * 32 + lane] = acc[r][m][i];
-    __syncthreads();
-    constexpr int kOut = 16 * RT * 8 * NT;      // results of one row block
-    T *y = static_cast<T *>(c.out);
-    const T *bias = static_cast<const T *>(c.bias), *res = static_cast<const T *>(c.residual);
-    for (int o = threadIdx.x; o < kOut * (kWarps / kw_n); o += kThreads) {
-        const int rr = o % (16 * RT), tt = o / (16 * RT) % (8 * NT), rb = o / kOut;
-        const int row = (blockIdx.x * (kWarps / kw_n) + rb) * 16 * RT + rr, tok = tok0 + tt;
-        if (row >= rows || tok >= c.n)
-            continue;
-        const int r = rr / 16, gr = rr % 8, hi = rr % 16 / 8, m = tt / 8, tc = tt % 8;
-        const int at = ((r * NT + m) * 4 + 2 * hi + (tc & 1)) * 32 + gr * 4 + tc / 2;
-        float s = 0.f;
-        for (int w = 0; w < kw_n; w++)
-            s += red[(rb * kw_n + w) * RT * NT * 128 + at];
-        if (bias)
-            s += Q::to_float(bias[row]);
-        if (res)
-            s += Q::to_float(res[tok * c.ldr + row]);
-        y[tok * c.ldo + row] = Q::from_float(s);
-    }
+    if (!ok && lane == 0 && c.status)
+        atomicOr(c.status, MOE_STATUS_TIMEOUT);
 }
 
 // ---- dx = dy W -------------------------------------------------------------
-// A warp's step is 16 rows x 128 K: lane (g, t) loads, of rows 4 t .. 4 t + 3,
-// the 8 bytes at K = 16 g.  The rows are the MMA's K and the columns its M:
-// one byte permutation pairs the halves of two rows' words, so that a field
-// holds one column of two rows.  The scale differs along the MMA's K, so it is
-// folded into the weights (one rounding).  The warps of a CTA and the CTAs of
-// a cluster (1 to 8) split the rows; the partial sums meet in shared and
-// distributed shared memory, in a fixed order.
-template <typename T, int GS, int NT>
-__global__ void __launch_bounds__(kThreads) linear_grad_kernel(W4Call c, int vec_in)
+// A CTA owns 128 columns; a stage is 32 rows x 64 bytes (64-byte swizzle).  The
+// rows are the MMA's K and the columns its M: lane (g, t) holds, of rows 4 t ..
+// 4 t + 3 of 16, the 8 bytes g (16 columns), and one byte permutation pairs the
+// halves of two rows' words, so that a field holds one column of two rows.  The
+// scale differs along the MMA's K:
+//   bf16, groups of 128: one scale per row holds for all columns of the CTA, so
+//     it multiplies the gradients, dy * s rounded once to bf16 (fp32 range);
+//   otherwise it is folded into the weights, (q - z) * s rounded once (in fp16
+//     a product of gradient and scale could fall below the normal range).
+// The warps of a CTA and the CTAs of a cluster (1 to 8) split the rows; the
+// partial sums meet in shared and distributed shared memory, in a fixed order.
+constexpr int kThreads = 32 * kWarps;
+constexpr int kGradCols = 128, kGradStage = 32 * 64, kGradStages = kRing / kGradStage;
+constexpr int kGradSmem = kWarps * kRing + 8 * kWarps * kGradStages + 16;
+
+template <typename T, int GS>
+__global__ void __launch_bounds__(kThreads, 1)
+    linear_grad_kernel(const __grid_constant__ CUtensorMap wmap, const W4Call c, int vec_in)
 {
     using Q = W4<T>;
-    extern __shared__ float red[];      // [kWarps][8 * NT tokens][128 columns]
-    pdl_enter();
+    constexpr bool kScaleIn = GS == 128 && sizeof(typename Q::Scale) == 8;
+    constexpr int kMeta = kGradCols / GS;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    float *red = reinterpret_cast<float *>(smem);       // [kWarps][8 tokens][128 columns]
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + kWarps * kRing);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + kWarps * kGradStages);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int rows = c.w.rows, K = c.w.K, ng = K / GS;
-    const int col0 = blockIdx.x * 128, tok0 = blockIdx.z * 8 * NT;
-    const int splits = gridDim.y, rank = blockIdx.y;
-    // columns past the matrix read its first columns; their sums are not stored
-    const int col = col0 + 16 * g < K ? col0 + 16 * g : 0;
-    const T *dy = static_cast<const T *>(c.in);
+    const uint32_t full = saddr(bars + warp * kGradStages);
+    const uint32_t ring = saddr(smem) + warp * kRing;
+    if (saddr(smem) & 1023) {       // the swizzled stages need it; never seen otherwise
+        if (threadIdx.x == 0 && c.status)
+            atomicOr(c.status, MOE_STATUS_TIMEOUT);
+        return;
+    }
+    if (lane == 0) {
+        prefetch_map(&wmap);
+        for (int i = 0; i < kGradStages; i++)
+            bar_init(full + 8 * i, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x == 0)
+        *abort_flag = 0;
+    __syncthreads();
+    pdl_enter();
 
-    float acc[8][NT][4];
+    const int rows = c.w.rows, K = c.w.K, ng = K / GS;
+    const int splits = gridDim.x, rank = blockIdx.x, col0 = blockIdx.y * kGradCols;
+    const int tok0 = blockIdx.z * 8;
+    const T *dy = static_cast<const T *>(c.in);
+    const int first = (rank * kWarps + warp) * 32, r_step = splits * kWarps * 32;
+
+    const auto fetch = [&](int r0, int slot) {      // one lane
+        bar_expect_tx(full + 8 * slot, kGradStage);
+        tma_load_2d(ring + slot * kGradStage, &wmap, col0 / 2, r0, full + 8 * slot);
+    };
+    if (lane == 0)
+        for (int i = 0; i < kGradStages; i++)
+            if (first + i * r_step < rows)
+                fetch(first + i * r_step, i);
+
+    // scales and zero points of a stage: lane l those of row l
+    struct Meta {
+        uint32_t s[kMeta], z[kMeta];
+    };
+    const auto load_meta = [&](int r0, Meta &m) {
+        // rows past the matrix repeat its last row, against gradients of zero
+        const long long at = (long long)min(r0 + lane, rows - 1) * ng;
+#pragma unroll
+        for (int i = 0; i < kMeta; i++) {
+            const int grp = min(col0 / GS + i, ng - 1);
+            m.s[i] = c.w.scales[at + grp];
+            m.z[i] = c.w.zeros[at + grp];
+        }
+    };
+
+    float acc[8][4];
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                acc[m][j][i] = 0.f;
+        for (int i = 0; i < 4; i++)
+            acc[m][i] = 0.f;
 
-#pragma unroll 4
-    for (int r0 = (rank * kWarps + warp) * 16; r0 < rows; r0 += splits * kWarps * 16) {
-        uint2 wq[4];
-        uint32_t sc[4], zz[4];
+    // loaded about as far ahead as the codes: with that much under way a load
+    // takes several microseconds
+    constexpr int kAhead = GS == 128 ? 4 : 2;
+    Meta ahead[kAhead] = {};
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            // rows past the matrix repeat its last row, against gradients of zero
-            const long long row = min(r0 + 4 * t + i, rows - 1);
-            wq[i] = ld_codes8(c.w.codes + row * (K / 2) + col / 2);
-            const long long at = row * ng + col / GS;
-            sc[i] = c.w.scales[at];
-            zz[i] = c.w.zeros[at];
-        }
-        uint2 b[NT];
+    for (int i = 0; i < kAhead; i++)
+        if (first + i * r_step < rows)
+            load_meta(first + i * r_step, ahead[i]);
+    bool ok = true;
+    unsigned it = 0;
+    for (int r0 = first; r0 < rows; r0 += r_step, it++) {
+        const Meta meta = ahead[0];
 #pragma unroll
-        for (int j = 0; j < NT; j++) {
-            const int tok = tok0 + 8 * j + g, r = r0 + 4 * t;
-            b[j] = make_uint2(0, 0);
+        for (int i = 0; i + 1 < kAhead; i++)
+            ahead[i] = ahead[i + 1];
+        if (r0 + kAhead * r_step < rows)
+            load_meta(r0 + kAhead * r_step, ahead[kAhead - 1]);
+        uint2 b[2];
+#pragma unroll
+        for (int ss = 0; ss < 2; ss++) {
+            const int tok = tok0 + g, r = r0 + 16 * ss + 4 * t;
+            b[ss] = make_uint2(0, 0);
             if (tok < c.n) {
                 const T *p = dy + tok * c.ldi + r;
                 if (vec_in && r + 3 < rows) {
-                    b[j] = *reinterpret_cast<const uint2 *>(p);
+                    b[ss] = *reinterpret_cast<const uint2 *>(p);
                 } else {
                     const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
                     if (r < rows)
-                        b[j].x = u[0];
+                        b[ss].x = u[0];
                     if (r + 1 < rows)
-                        b[j].x |= (uint32_t)u[1] << 16;
+                        b[ss].x |= (uint32_t)u[1] << 16;
                     if (r + 2 < rows)
-                        b[j].y = u[2];
+                        b[ss].y = u[2];
                     if (r + 3 < rows)
-                        b[j].y |= (uint32_t)u[3] << 16;
+                        b[ss].y |= (uint32_t)u[3] << 16;
                 }
             }
         }
-        const typename Q::Zero z01 = Q::zero(zz[0], zz[1]), z23 = Q::zero(zz[2], zz[3]);
-        const typename Q::Scale s01 = Q::scale(sc[0], sc[1]), s23 = Q::scale(sc[2], sc[3]);
+        // this lane's row pair (lane & ~1, + 1) as the unpacking's operand words
+        typename Q::Zero zp[kMeta];
+        typename Q::Scale sp[kMeta];
+        uint32_t raw[kMeta];
 #pragma unroll
-        for (int q4 = 0; q4 < 4; q4++) {        // four columns: half of one of the two words
-            const uint32_t sel = q4 & 1 ? 0x7632 : 0x5410;
-            const uint32_t u01 = q4 < 2 ? __byte_perm(wq[0].x, wq[1].x, sel)
-                                        : __byte_perm(wq[0].y, wq[1].y, sel);
-            const uint32_t u23 = q4 < 2 ? __byte_perm(wq[2].x, wq[3].x, sel)
-                                        : __byte_perm(wq[2].y, wq[3].y, sel);
-            uint32_t p[4], q[4];
-            Q::unpack(u01, z01, p);
-            Q::unpack(u23, z23, q);
+        for (int i = 0; i < kMeta; i++) {
+            const uint32_t s2 = __shfl_xor_sync(0xffffffffu, meta.s[i], 1);
+            const uint32_t z2 = __shfl_xor_sync(0xffffffffu, meta.z[i], 1);
+            const bool odd = lane & 1;
+            zp[i] = Q::zero(odd ? z2 : meta.z[i], odd ? meta.z[i] : z2);
+            raw[i] = odd ? s2 | meta.s[i] << 16 : meta.s[i] | s2 << 16;
+            if (!kScaleIn)
+                sp[i] = Q::scale(raw[i] & 0xffff, raw[i] >> 16);
+        }
+        const int slot = it % kGradStages;
+        if (ok && !warp_wait(full + 8 * slot, (it / kGradStages) & 1, abort_flag)) {
+            ok = false;
+            *abort_flag = 1;
+        }
+        // row r's 16-byte piece p sits at p ^ (r / 2 % 4); r = 16 ss + 4 t + i
+        const uint8_t *stage = smem + warp * kRing + slot * kGradStage + t * 256 + 8 * (g & 1);
+        const uint8_t *w01 = stage + (((g >> 1) ^ (2 * t & 3)) << 4);
+        const uint8_t *w23 = stage + (((g >> 1) ^ ((2 * t + 1) & 3)) << 4);
+        uint2 w[2][4];
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                p[i] = Q::mul(p[i], s01);
-                q[i] = Q::mul(q[i], s23);
+        for (int ss = 0; ss < 2; ss++)
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                w[ss][i] = *reinterpret_cast<const uint2 *>((i < 2 ? w01 : w23) + ss * 1024 + i * 64);
+        // every lane's reads are done before the copy engine writes the stage
+        fence_async_shared();
+        __syncwarp();
+        if (lane == 0 && r0 + kGradStages * r_step < rows)
+            fetch(r0 + kGradStages * r_step, slot);
+#pragma unroll
+        for (int ss = 0; ss < 2; ss++) {
+            const int from = 16 * ss + 4 * t;
+            uint32_t z[2], sr[2];
+            typename Q::Scale s[2];
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                // of this lane's group (16 g of the CTA's columns)
+                z[h] = 0;
+                sr[h] = 0;
+#pragma unroll
+                for (int i = 0; i < kMeta; i++) {
+                    const uint32_t zi = __shfl_sync(0xffffffffu, zp[i].lo, from + 2 * h);
+                    if (kMeta == 1 || 16 * g / GS == i)
+                        z[h] = zi;
+                    if (kScaleIn) {
+                        sr[h] = __shfl_sync(0xffffffffu, raw[i], from + 2 * h);
+                    } else {
+                        const typename Q::Scale si = shfl_of(sp[i], from + 2 * h);
+                        if (kMeta == 1 || 16 * g / GS == i)
+                            s[h] = si;
+                    }
+                }
+            }
+            const typename Q::Zero z01 = Q::zero_of(z[0]), z23 = Q::zero_of(z[1]);
+            uint2 bb = b[ss];
+            if (kScaleIn) {
+                bb.x = Q::times(bb.x, sr[0] & 0xffff, sr[0] >> 16);
+                bb.y = Q::times(bb.y, sr[1] & 0xffff, sr[1] >> 16);
             }
 #pragma unroll
-            for (int j = 0; j < NT; j++) {
-                mma16816<T>(acc[2 * q4][j], p[0], p[1], q[0], q[1], b[j].x, b[j].y);
-                mma16816<T>(acc[2 * q4 + 1][j], p[2], p[3], q[2], q[3], b[j].x, b[j].y);
+            for (int q4 = 0; q4 < 4; q4++) {        // four columns: half of one of the two words
+                const uint32_t sel = q4 & 1 ? 0x7632 : 0x5410;
+                uint32_t p[4], q[4];
+                Q::unpack(q4 < 2 ? __byte_perm(w[ss][0].x, w[ss][1].x, sel)
+                                 : __byte_perm(w[ss][0].y, w[ss][1].y, sel), z01, p);
+                Q::unpack(q4 < 2 ? __byte_perm(w[ss][2].x, w[ss][3].x, sel)
+                                 : __byte_perm(w[ss][2].y, w[ss][3].y, sel), z23, q);
+                if (!kScaleIn) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        p[i] = Q::mul(p[i], s[0]);
+                        q[i] = Q::mul(q[i], s[1]);
+                    }
+                }
+                mma16816<T>(acc[2 * q4], p[0], p[1], q[0], q[1], bb.x, bb.y);
+                mma16816<T>(acc[2 * q4 + 1], p[2], p[3], q[2], q[3], bb.x, bb.y);
             }
         }
     }
+    __syncthreads();        // the rings become the sums' buffer
 
-    constexpr int kOut = 8 * NT * 128;
+    constexpr int kOut = 8 * kGradCols;
+    static_assert(4 * kWarps * kOut <= kWarps * kRing, "the sums fit in the rings");
 #pragma unroll
     for (int m = 0; m < 8; m++)
 #pragma unroll
-        for (int j = 0; j < NT; j++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                red[warp * kOut + (8 * j + 2 * t + (i & 1)) * 128 + 16 * g + 2 * m + (i >> 1)] =
-                    acc[m][j][i];
+        for (int i = 0; i < 4; i++)
+            red[warp * kOut + (2 * t + (i & 1)) * kGradCols + 16 * g + 2 * m + (i >> 1)] = acc[m][i];
     __syncthreads();
     for (int o = threadIdx.x; o < kOut; o += kThreads) {
         float s = red[o];
@@ -284,95 +613,136 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(W4Call c, int vec
         red[o] = s;
     }
     if (splits > 1) {
-        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+        cluster_arrive();
+        cluster_wait();
     } else {
         __syncthreads();
     }
     T *dx = static_cast<T *>(c.out);
-    const uint32_t base = (uint32_t)__cvta_generic_to_shared(red);
     for (int o = rank * kThreads + threadIdx.x; o < kOut; o += splits * kThreads) {
-        const int cc = col0 + o % 128, tok = tok0 + o / 128;
+        const int cc = col0 + o % kGradCols, tok = tok0 + o / kGradCols;
         if (cc >= K || tok >= c.n)
             continue;
         float s = 0.f;
         if (splits > 1) {
-            for (int p = 0; p < splits; p++) {
-                uint32_t remote;
-                float v;
-                asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(base + 4 * o), "r"(p));
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote));
-                s += v;
+            float v[8];
+#pragma unroll
+            for (int p = 0; p < 8; p++) {
+                v[p] = 0.f;
+                if (p < splits)
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v[p])
+                                 : "r"(cluster_addr(saddr(red + o), p)));
             }
+#pragma unroll
+            for (int p = 0; p < 8; p++)
+                s += v[p];
         } else {
             s = red[o];
         }
         dx[tok * c.ldo + cc] = Q::from_float(s);
     }
-    if (splits > 1)     // a CTA's shared memory stays until its peers have read it
-        asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
-
-template <typename T, int GS, int NT>
-cudaError_t launch_fwd(const W4Call &c, cudaStream_t st)
-{
-    constexpr int RT = 1;
-    const int units = (c.w.K + 511) / 512;
-    const int kw = units >= 8 ? 8 : units >= 4 ? 4 : units >= 2 ? 2 : 1;
-    const int rows_cta = 16 * RT * (kWarps / kw);
-    const dim3 grid((c.w.rows + rows_cta - 1) / rows_cta, (c.n + 8 * NT - 1) / (8 * NT));
-    return launch_pdl(linear_kernel<T, GS, NT, RT>, grid, dim3(kThreads),
-                      sizeof(float) * kWarps * RT * NT * 128, st, c, kw);
-}
-
-template <typename T, int GS, int NT>
-cudaError_t launch_bwd(const W4Call &c, int num_sms, cudaStream_t st)
-{
-    const size_t smem = sizeof(float) * kWarps * 8 * NT * 128;
-    auto kernel = linear_grad_kernel<T, GS, NT>;
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess)
-            return e;
+    if (splits > 1) {   // a CTA's shared memory stays until its peers have read it
+        cluster_arrive();
+        cluster_wait();
     }
-    const int strips = (c.w.K + 127) / 128, blocks = (c.n + 8 * NT - 1) / (8 * NT);
-    const int steps = (c.w.rows + 16 * kWarps - 1) / (16 * kWarps);
-    int splits = 1;
-    while (splits < 8 && (long long)strips * blocks * splits < 2LL * num_sms && 2 * splits <= steps)
-        splits *= 2;
-    const int vec = reinterpret_cast<uintptr_t>(c.in) % 8 == 0 && c.ldi % 4 == 0;
+    if (!ok && lane == 0 && c.status)
+        atomicOr(c.status, MOE_STATUS_TIMEOUT);
+}
+
+// Launch of clusters along x, chained like the library's other kernels.
+template <typename... P, typename... A>
+cudaError_t launch_cluster(void (*kernel)(P...), dim3 grid, int threads, int smem, int cluster,
+                           cudaStream_t st, A... args)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess)
+        return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(strips, splits, blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = 1;
-    attr[1].val.clusterDim.y = splits;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, c, vec);
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename T, int GS, int RT>
+cudaError_t launch_fwd_rt(const W4Call &c, int num_sms, cudaStream_t st)
+{
+    FwdArgs a{c, 0, 1, 0};
+    const int slices = (c.w.K + 255) / 256, tiles = (c.w.rows + 16 * RT - 1) / (16 * RT);
+    const int rounds = (slices + kWarps - 1) / kWarps;
+    a.kw_n = (slices + rounds - 1) / rounds;
+    // several row tiles at a time only when there are enough for every SM
+    a.rw_n = std::max(1, std::min(kWarps / a.kw_n, tiles / num_sms));
+    a.vec_meta = c.w.K % 256 == 0 && reinterpret_cast<uintptr_t>(c.w.scales) % 16 == 0 &&
+                 reinterpret_cast<uintptr_t>(c.w.zeros) % 8 == 0;
+    const int sets = (tiles + a.rw_n - 1) / a.rw_n;
+    CUtensorMap wmap;
+    if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2,
+                    128, 16 * RT, CU_TENSOR_MAP_SWIZZLE_128B))
+        return cudaErrorInvalidValue;
+    auto kernel = linear_kernel<T, GS, RT>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               FwdGeo<RT>::smem);
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(kernel, dim3(std::min(sets, num_sms), (c.n + 7) / 8),
+                      dim3(32 * (a.kw_n * a.rw_n + 1)), FwdGeo<RT>::smem, st, wmap, a);
 }
 
 template <typename T, int GS>
-cudaError_t launch_few(const W4Call &c, int grad, int num_sms, cudaStream_t st)
+cudaError_t launch_fwd(const W4Call &c, int num_sms, cudaStream_t st)
 {
-    if (grad)
-        return c.n <= 8 ? launch_bwd<T, GS, 1>(c, num_sms, st) : launch_bwd<T, GS, 2>(c, num_sms, st);
-    return c.n <= 8 ? launch_fwd<T, GS, 1>(c, st) : launch_fwd<T, GS, 2>(c, st);
+    // 32-row tiles join sums, and read activations, half as often; 16-row tiles
+    // spread a small matrix over the SMs
+    return c.w.rows >= 24 * num_sms ? launch_fwd_rt<T, GS, 2>(c, num_sms, st)
+                                    : launch_fwd_rt<T, GS, 1>(c, num_sms, st);
+}
+
+template <typename T, int GS>
+cudaError_t launch_bwd(const W4Call &c, int dev, int num_sms, cudaStream_t st)
+{
+    const int strips = (c.w.K + kGradCols - 1) / kGradCols, blocks = (c.n + 7) / 8;
+    // every warp of a cluster has a stage, and all clusters run at once
+    const int steps = (c.w.rows + 32 * kWarps - 1) / (32 * kWarps);
+    const int *clusters = cluster_table(dev);
+    int splits = 1;
+    for (int s = 2; s <= std::min(8, steps); s++)
+        if ((long long)strips * blocks <= clusters[s])
+            splits = s;
+    const int vec = reinterpret_cast<uintptr_t>(c.in) % 8 == 0 && c.ldi % 4 == 0;
+    CUtensorMap wmap;
+    if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2,
+                    64, 32, CU_TENSOR_MAP_SWIZZLE_64B))
+        return cudaErrorInvalidValue;
+    return launch_cluster(linear_grad_kernel<T, GS>, dim3(splits, strips, blocks), kThreads,
+                          kGradSmem, splits, st, wmap, c, vec);
+}
+
+template <typename T, int GS>
+cudaError_t launch_few(const W4Call &c, int grad, int dev, int num_sms, cudaStream_t st)
+{
+    return grad ? launch_bwd<T, GS>(c, dev, num_sms, st) : launch_fwd<T, GS>(c, num_sms, st);
 }
 
 template <typename T>
-cudaError_t launch_group_size(const W4Call &c, int grad, int num_sms, cudaStream_t st)
+cudaError_t launch_group_size(const W4Call &c, int grad, int dev, int num_sms, cudaStream_t st)
 {
     switch (c.w.group) {
-    case 32: return launch_few<T, 32>(c, grad, num_sms, st);
-    case 64: return launch_few<T, 64>(c, grad, num_sms, st);
-    default: return launch_few<T, 128>(c, grad, num_sms, st);
+    case 32: return launch_few<T, 32>(c, grad, dev, num_sms, st);
+    case 64: return launch_few<T, 64>(c, grad, dev, num_sms, st);
+    default: return launch_few<T, 128>(c, grad, dev, num_sms, st);
     }
 }
 
@@ -387,7 +757,7 @@ int record_success();
 
 namespace {
 
-constexpr int kFewTokens = 16;
+constexpr int kFewTokens = 8;
 constexpr int kMaxRows = 1 << 20, kMaxCols = 1 << 16, kMaxTokens = 1 << 19;
 
 // The byte range of n rows of `width` 2-byte elements, ld elements apart.
@@ -449,8 +819,8 @@ int run_linear(const W4Call &c, int dtype, int grad, void *stream)
     if (c.n > kFewTokens && linear_gemm_fits(c))
         e = launch_linear_gemm(c, dtype == MOE_BF16, grad, dev, sms, st);
     else
-        e = dtype == MOE_FP16 ? launch_group_size<__half>(c, grad, sms, st)
-                              : launch_group_size<__nv_bfloat16>(c, grad, sms, st);
+        e = dtype == MOE_FP16 ? launch_group_size<__half>(c, grad, dev, sms, st)
+                              : launch_group_size<__nv_bfloat16>(c, grad, dev, sms, st);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return record_failure(MOE_ERR_CUDA, cudaGetErrorString(e));

@@ -94,13 +94,6 @@ __device__ __forceinline__ void tmem_st_16x256(uint32_t taddr, const uint32_t (&
         : "memory");
 }
 
-// bar_wait by a whole warp with one answer for all its lanes, so that a wait
-// that gives up never splits the warp in front of a collective instruction.
-__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int *abort_flag)
-{
-    return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag));
-}
-
 // One answer for the four warps of a dequant group, which also orders their
 // shared-memory writes before it against the reads after it.
 __device__ __forceinline__ bool group_and(int id, bool v)
@@ -118,16 +111,6 @@ template <typename S>
 struct alignas(2 * sizeof(S)) ScalePair {
     S a, b;
 };
-
-__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
-{
-    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
-}
-
-__device__ __forceinline__ void cluster_sync()
-{
-    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
-}
 
 template <typename T>
 __device__ __forceinline__ void store_out(const W4Call &c, float v, int tok, int f)
@@ -612,7 +595,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         atomicOr(c.status, MOE_STATUS_TIMEOUT);
     if (a.splits > 1) {
         // the one tile of this cluster: rank r adds its share of the tokens
-        cluster_sync();
+        cluster_arrive();
+        cluster_wait();
         const int m0 = tile0 % a.mt * kM, tok0 = tile0 / a.mt * a.tok;
         const int lo = a.tok * rank / a.splits, hi = a.tok * (rank + 1) / a.splits;
         const uint32_t base = saddr(smem + G::b_off);
@@ -623,12 +607,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             float4 p[8];
 #pragma unroll
             for (int r = 0; r < 8; r++) {
-                uint32_t remote;
                 p[r] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (r < a.splits) {
-                    asm("mapa.shared::cluster.u32 %0, %1, %2;"
-                        : "=r"(remote)
-                        : "r"(base + 4 * i), "r"(r));
+                    const uint32_t remote = cluster_addr(base + 4 * i, r);
                     asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
                                  : "=f"(p[r].x), "=f"(p[r].y), "=f"(p[r].z), "=f"(p[r].w)
                                  : "r"(remote));
@@ -647,7 +628,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (f + u < F)
                     store_out<T>(c, v[u], tok, f + u);
         }
-        cluster_sync();     // a CTA's shared memory stays until its peers have read it
+        cluster_arrive();
+        cluster_wait();     // a CTA's shared memory stays until its peers have read it
     }
 }
 
@@ -672,7 +654,17 @@ EncodeFn encoder()
     return fn;
 }
 
-bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+// Clusters of each size that run at once (they cannot use every SM: a GPC
+// holds a whole number of them), looked up once per device.
+constexpr int kMaxSplits = 8;
+struct Clusters {
+    std::once_flag once;
+    int n[kMaxSplits + 1] = {};
+};
+
+}  // namespace
+
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
             uint64_t rows, uint64_t pitch, uint32_t box_cols, uint32_t box_rows,
             CUtensorMapSwizzle swizzle)
 {
@@ -685,18 +677,6 @@ bool encode(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64
               CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-
-struct Plan {
-    int tok, nt, splits;
-};
-
-// Clusters of each size that run at once (they cannot use every SM: a GPC
-// holds a whole number of them), looked up once per device.
-constexpr int kMaxSplits = 8;
-struct Clusters {
-    std::once_flag once;
-    int n[kMaxSplits + 1] = {};
-};
 
 const int *cluster_table(int dev)
 {
@@ -734,6 +714,12 @@ const int *cluster_table(int dev)
     });
     return t.n;
 }
+
+namespace {
+
+struct Plan {
+    int tok, nt, splits;
+};
 
 // Tokens per tile and splits along the contraction: the smallest estimated time,
 // in SM cycles, of the busiest SM.  A 64-step of a tile of N tokens takes 2 N
@@ -821,9 +807,9 @@ cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int
     const Plan p = plan(C, F, c.n, num_sms, cluster_table(dev));
     GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits};
     CUtensorMap wmap, bmap;
-    if (!encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
+    if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
                 128, CU_TENSOR_MAP_SWIZZLE_64B) ||
-        !encode(&bmap, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+        !encode_map(&bmap, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
                 c.in, C, c.n, 2 * c.ldi, 64, p.tok, CU_TENSOR_MAP_SWIZZLE_128B))
         return cudaErrorInvalidValue;
     if (bf16)

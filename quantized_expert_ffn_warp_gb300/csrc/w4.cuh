@@ -6,7 +6,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cstring>
+
 #include "internal.cuh"
+#include "tcgen05.cuh"
 
 namespace qe {
 
@@ -66,6 +69,10 @@ struct W4<__half> {
     {
         return u(__hmul2(h(p), h(s.s)));
     }
+    static __device__ __forceinline__ uint32_t times(uint32_t v, uint32_t s0, uint32_t s1)
+    {
+        return u(__hmul2(h(v), h(s0 | (s1 << 16))));
+    }
     static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
 };
@@ -108,53 +115,125 @@ struct W4<__nv_bfloat16> {
     {
         return u(__hfma2(h(p), h(s.hi), __hmul2(h(p), h(s.lo))));
     }
+    // A pair of bf16 values times two fp16 scales (as bits), each rounded once.
+    static __device__ __forceinline__ uint32_t times(uint32_t v, uint32_t s0, uint32_t s1)
+    {
+        const float2 f = __bfloat1622float2(h(v));
+        return u(__floats2bfloat162_rn(
+            f.x * __half2float(__ushort_as_half((unsigned short)s0)),
+            f.y * __half2float(__ushort_as_half((unsigned short)s1))));
+    }
     static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 };
 
-// D (fp32, 16 x 8) += A (16 x 16) B (16 x 8), one warp.
+// D (fp32, 16 x 8) = A (16 x 16) B (16 x 8) + C, one warp.
+template <typename T>
+__device__ __forceinline__ void mma16816c(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1, float c0, float c1,
+                                          float c2, float c3);
+
+template <>
+__device__ __forceinline__ void mma16816c<__half>(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                  uint32_t a2, uint32_t a3, uint32_t b0,
+                                                  uint32_t b1, float c0, float c1, float c2,
+                                                  float c3)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+template <>
+__device__ __forceinline__ void mma16816c<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1,
+                                                         uint32_t a2, uint32_t a3, uint32_t b0,
+                                                         uint32_t b1, float c0, float c1, float c2,
+                                                         float c3)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
+}
+
+// D += A B.
 template <typename T>
 __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1);
-
-template <>
-__device__ __forceinline__ void mma16816<__half>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                 uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+                                         uint32_t a3, uint32_t b0, uint32_t b1)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-                 "{%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    mma16816c<T>(d, a0, a1, a2, a3, b0, b1, d[0], d[1], d[2], d[3]);
 }
 
-template <>
-__device__ __forceinline__ void mma16816<__nv_bfloat16>(float (&d)[4], uint32_t a0, uint32_t a1,
-                                                        uint32_t a2, uint32_t a3, uint32_t b0,
-                                                        uint32_t b1)
+// Four 8 x 16-byte tiles: lane (g, t) receives word t of row g of each; lane i
+// gives the address of row i % 8 of tile i / 8.
+__device__ __forceinline__ void ldmatrix4(uint32_t (&d)[4], uint32_t addr)
 {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, "
-                 "{%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                 : "r"(addr)
+                 : "memory");
 }
 
-// Packed codes are read once per call: no L1 line is kept for them.
-__device__ __forceinline__ uint4 ld_codes16(const uint8_t *p)
+// 2-D TMA map (linear_gemm.cu): boxes of box_rows x box_cols elements of a
+// row-major matrix [rows][cols] with rows `pitch` bytes apart.
+bool encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
+                uint64_t rows, uint64_t pitch, uint32_t box_cols, uint32_t box_rows,
+                CUtensorMapSwizzle swizzle);
+// Clusters of s CTAs (s <= 8), one CTA per SM, that run at once on device
+// `dev` (linear_gemm.cu); [0] and [1] are unused.
+const int *cluster_table(int dev);
+
+// bar_wait by a whole warp with one answer for all its lanes, so that a wait
+// that gives up never splits the warp in front of a collective instruction.
+__device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile int *abort_flag)
 {
-    uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
-    return v;
+    return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag));
 }
 
-__device__ __forceinline__ uint2 ld_codes8(const uint8_t *p)
+// Orders this thread's accesses to shared memory before later ones of the copy
+// engine (TMA): a read still on its way is not overtaken by a refill.
+__device__ __forceinline__ void fence_async_shared()
 {
-    uint2 v;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
-                 : "=r"(v.x), "=r"(v.y)
-                 : "l"(p));
-    return v;
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// A lane's word(s) read from lane `src`.
+template <typename S>
+__device__ __forceinline__ S shfl_of(const S &v, int src)
+{
+    constexpr int N = sizeof(S) / 4;
+    uint32_t u[N];
+    memcpy(u, &v, sizeof(S));
+#pragma unroll
+    for (int i = 0; i < N; i++)
+        u[i] = __shfl_sync(0xffffffffu, u[i], src);
+    S r;
+    memcpy(&r, u, sizeof(S));
+    return r;
+}
+
+__device__ __forceinline__ void prefetch_map(const CUtensorMap *map)
+{
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+}
+
+// This CTA's shared address `addr` in the CTA `rank` of its cluster.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank)
+{
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
 }
 
 // A frozen 4-bit matrix in the canonical layout.
