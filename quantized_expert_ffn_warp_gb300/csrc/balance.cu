@@ -10,13 +10,17 @@
 //   dl[t][idx_j] += w_j (dw_j - sum_i w_i dw_i).
 //
 // Everything is a stream over the logits, one warp per token, its row in
-// registers.  The forward sums p over the tokens of a block in registers and
-// writes one partial row per (block of tokens, segment); a second kernel adds
-// the partial rows in block order, so a result never depends on timing.
+// registers, the next token's row already under way (a token's arithmetic is
+// shorter than a load).  The forward sums p over the tokens of a block in
+// registers and writes one partial row per (block of tokens, segment); a
+// second kernel adds the partial rows in block order, so a result never depends
+// on timing.  A batch that one CTA handles needs neither partial rows nor the
+// second kernel.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <cstring>
 
 #include "internal.cuh"
 
@@ -45,12 +49,120 @@ __device__ __forceinline__ float warp_max(float v)
     return v;
 }
 
-__device__ __forceinline__ float ldf(const float *p) { return *p; }
-__device__ __forceinline__ float ldf(const __half *p) { return __half2float(*p); }
-__device__ __forceinline__ float ldf(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void stf(float *p, float v) { *p = v; }
-__device__ __forceinline__ void stf(__half *p, float v) { *p = __float2half_rn(v); }
-__device__ __forceinline__ void stf(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+// A pair of values as one word (or two), so that it is loaded and stored whole.
+template <typename T>
+struct Pair {
+    uint32_t u;
+};
+template <>
+struct Pair<float> {
+    float2 u;
+};
+__device__ __forceinline__ float2 unpair(const Pair<float> &p) { return p.u; }
+__device__ __forceinline__ float2 unpair(const Pair<__half> &p)
+{
+    return __half22float2(*reinterpret_cast<const __half2 *>(&p.u));
+}
+__device__ __forceinline__ float2 unpair(const Pair<__nv_bfloat16> &p)
+{
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&p.u));
+}
+__device__ __forceinline__ void pair(Pair<float> &p, float a, float b) { p.u = make_float2(a, b); }
+__device__ __forceinline__ void pair(Pair<__half> &p, float a, float b)
+{
+    const __half2 h = __floats2half2_rn(a, b);
+    p.u = *reinterpret_cast<const uint32_t *>(&h);
+}
+__device__ __forceinline__ void pair(Pair<__nv_bfloat16> &p, float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    p.u = *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// exp(x) for x <= 0 by the hardware's 2^x: relative error below (|x| + 5) 2^-24.
+__device__ __forceinline__ float exp_neg(float x) { return __expf(x); }
+
+// The hardware's 2^x.
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A lane's part of a row of E values, as loaded: V of them, pairs side by side
+// (V = 1: one value, the pair's first).  The same values in the same lane
+// whether or not the rows allow pair loads (`wide`: E and the stride even, the
+// base on a pair), so that sums do not depend on the stride.
+template <typename T, int V>
+struct Row {
+    static constexpr int W = V > 1 ? 2 : 1, N = V / W;
+    Pair<T> q[N];
+    static __device__ __forceinline__ int at(int i, int lane)
+    {
+        return (i / W) * 32 * W + lane * W + i % W;
+    }
+    // values past the row read -inf
+    __device__ __forceinline__ void load(const T *row, int E, int lane, bool wide)
+    {
+        if (wide && E == 32 * V) {
+#pragma unroll
+            for (int n = 0; n < N; n++)
+                if (W == 2)
+                    q[n] = *reinterpret_cast<const Pair<T> *>(row + at(n * W, lane));
+            if (W == 2)
+                return;
+        }
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int e = at(n * W, lane);
+            pair(q[n], -INFINITY, -INFINITY);
+            if (W == 2 && wide) {
+                if (e < E)
+                    q[n] = *reinterpret_cast<const Pair<T> *>(row + e);
+            } else {
+                T v[2];
+                memcpy(v, &q[n], sizeof(v));
+                if (e < E)
+                    v[0] = row[e];
+                if (W == 2 && e + 1 < E)
+                    v[1] = row[e + 1];
+                memcpy(&q[n], v, sizeof(v));
+            }
+        }
+    }
+    __device__ __forceinline__ void get(float (&d)[V]) const
+    {
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const float2 f = unpair(q[n]);
+            d[n * W] = f.x;
+            if (W == 2)
+                d[n * W + W - 1] = f.y;
+        }
+    }
+    static __device__ __forceinline__ void store(T *row, const float (&d)[V], int E, int lane,
+                                                 bool wide)
+    {
+#pragma unroll
+        for (int n = 0; n < N; n++) {
+            const int e = at(n * W, lane);
+            Pair<T> p;
+            pair(p, d[n * W], d[n * W + W - 1]);
+            if (W == 2 && wide) {
+                if (e < E)
+                    *reinterpret_cast<Pair<T> *>(row + e) = p;
+            } else {
+                T v[2];
+                memcpy(v, &p, sizeof(p));
+                if (e < E)
+                    row[e] = v[0];
+                if (W == 2 && e + 1 < E)
+                    row[e + 1] = v[1];
+            }
+        }
+    }
+};
 
 // Segment bounds as the kernels use them: inside [0, n] whatever the array holds.
 struct Segs {
@@ -81,25 +193,33 @@ struct Segs {
     }
 };
 
-// Workspace: [ticket, 256 B][loss parts f64 [S][ceil(E/32)]][z sums f64 [slots]]
-// [valid tokens int [slots]][prob sums f32 [slots][E]][counts int [slots][E]]
+// Sums are fp32 trees of short chains (64-bit arithmetic is slow on this GPU).
+// Workspace: [ticket, 256 B][loss parts f32 [S][ceil(E/32)]][z sums f32 [slots]]
+// [z sums f32 [S]][valid tokens int [slots]][prob sums f32 [slots][E]][counts int [slots][E]]
 struct BalanceWs {
     unsigned *ticket;
-    double *part;
-    double *z;
+    float *part;
+    float *z;
+    float *zseg;
     int *valid;
     float *prob;
     int *counts;
     size_t bytes;
 };
 
-// Tokens of a block: enough blocks for two per SM of the largest parts, and
-// at least one token per warp.
+// Tokens of a block: about four blocks per SM of the largest parts, and at
+// least one token per warp.
 int block_tokens(int n)
 {
-    const int per = (n + 303) / 304;
+    const int per = (n + 607) / 608;
     return (std::max(per, 1) + kWarps - 1) / kWarps * kWarps;
 }
+
+// Whether one CTA of kOneWarps warps handles the whole batch: it takes about a
+// microsecond per 64 tokens and per segment, two dependent kernels about five
+// more than that.
+constexpr int kOneWarps = 32;
+bool one_block(int n, int E, int S) { return n <= 8 * kOneWarps && E <= 512 && S <= 4; }
 
 BalanceWs balance_ws(void *base, int n, int E, int S)
 {
@@ -114,8 +234,9 @@ BalanceWs balance_ws(void *base, int n, int E, int S)
         return p;
     };
     w.ticket = reinterpret_cast<unsigned *>(take(4));
-    w.part = reinterpret_cast<double *>(take(8 * (size_t)S * ((E + 31) / 32)));
-    w.z = reinterpret_cast<double *>(take(8 * slots));
+    w.part = reinterpret_cast<float *>(take(4 * (size_t)S * ((E + 31) / 32)));
+    w.z = reinterpret_cast<float *>(take(4 * slots));
+    w.zseg = reinterpret_cast<float *>(take(4 * (size_t)S));
     w.valid = reinterpret_cast<int *>(take(4 * slots));
     w.prob = reinterpret_cast<float *>(take(4 * slots * E));
     w.counts = reinterpret_cast<int *>(take(4 * slots * E));
@@ -130,6 +251,7 @@ struct FwdArgs {
     const uint8_t *mask;
     Segs segs;
     int n, E, k, C;
+    bool wide;              // rows allow pair loads
     BalanceWs ws;
     float *loss, *prob, *lse;
     int32_t *counts, *tokens;
@@ -137,31 +259,60 @@ struct FwdArgs {
 
 // Per block of C tokens: lse of every token, and per segment that the block
 // meets the partial sums at slot (block + segment): both only ever grow along
-// the tokens, so a slot belongs to one pair.
-template <typename T, int V>
-__global__ void __launch_bounds__(kThreads) balance_stats_kernel(FwdArgs a)
+// the tokens, so a slot belongs to one pair.  ONE: the block is the batch and
+// writes the results themselves.
+template <typename T, int V, bool ONE>
+__global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : 0)
+    balance_stats_kernel(FwdArgs a)
 {
-    extern __shared__ float sm[];       // prob [kWarps][E], then counts int [E]
-    __shared__ double zred[kWarps];
-    __shared__ int vred[kWarps];
+    constexpr int NW = ONE ? kOneWarps : kWarps, NT = 32 * NW;
+    using R = Row<T, V>;
+    extern __shared__ float sm[];       // prob [NW][E], then counts int [E]
+    __shared__ float zred[NW];
+    __shared__ int vred[NW];
+    __shared__ float lred[NW];
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int E = a.E, t_lo = blockIdx.x * a.C, t_hi = min(a.n, t_lo + a.C);
-    int *hist = reinterpret_cast<int *>(sm + kWarps * E);
+    int *hist = reinterpret_cast<int *>(sm + NW * E);
     const T *logits = static_cast<const T *>(a.logits);
-    if (blockIdx.x == 0 && threadIdx.x == 0)
+    if (!ONE && blockIdx.x == 0 && threadIdx.x == 0)
         *a.ws.ticket = 0;
+    float bal = 0.f, zall = 0.f;        // ONE: sums over the segments
+    int all = 0, segs = 0;
+
+    // U tokens at a time: one's reductions run in the other's shadow
+    constexpr int U = V <= 16 ? 2 : 1;
+    struct Token {
+        R row;
+        int id;
+        bool on;
+    };
+    const auto load = [&](int tok, int end, Token &k) {
+        k.on = false;
+        k.id = -1;
+        if (tok < end) {
+            k.row.load(logits + tok * a.ld, E, lane, a.wide);
+            k.on = !a.mask || a.mask[tok];
+            if (lane < a.k)
+                k.id = a.idx[(long long)tok * a.k + lane];
+        }
+    };
 
     int t = t_lo;       // next token without a segment
-    for (int s = a.segs.first_after(t_lo); s < a.segs.S && t < t_hi; s++) {
+    for (int s = a.segs.first_after(t_lo); s < a.segs.S && (t < t_hi || ONE); s++) {
         const int b = min(max(a.segs.begin(s), t), t_hi), e = min(a.segs.end(s), t_hi);
-        for (int i = t + threadIdx.x; i < b; i += kThreads)
+        for (int i = t + threadIdx.x; i < b; i += NT)
             a.lse[i] = 0.f;             // tokens in front of the first segment
         t = max(t, b);
-        if (e <= b)
+        if (e <= b && !ONE)
             continue;
-        t = e;
-        for (int i = threadIdx.x; i < E; i += kThreads)
+        t = max(t, e);
+        Token next[U];
+#pragma unroll
+        for (int i = 0; i < U; i++)
+            load(b + warp + i * NW, e, next[i]);
+        for (int i = threadIdx.x; i < E; i += NT)
             hist[i] = 0;
         __syncthreads();
         float psum[V];
@@ -170,81 +321,132 @@ __global__ void __launch_bounds__(kThreads) balance_stats_kernel(FwdArgs a)
             psum[i] = 0.f;
         float zsum = 0.f;
         int valid = 0;
-        for (int tok = b + warp; tok < e; tok += kWarps) {
-            if (a.mask && !a.mask[tok]) {
-                if (lane == 0)
-                    a.lse[tok] = 0.f;
-                continue;
-            }
-            valid++;
-            if (lane < a.k) {
-                const int id = a.idx[(long long)tok * a.k + lane];
-                if (id >= 0 && id < E)
-                    atomicAdd(hist + id, 1);
-            }
-            const T *row = logits + tok * a.ld;
-            float l[V];
-            float m = -INFINITY;
+        for (int tok = b + warp; tok < e; tok += U * NW) {
+            float l[U][V], m[U], sum[U];
+            bool on[U];
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                const int x = i * 32 + lane;
-                l[i] = x < E ? ldf(row + x) : -INFINITY;
+            for (int u = 0; u < U; u++) {
+                on[u] = next[u].on;
+                valid += on[u];
+                if (on[u] && next[u].id >= 0 && next[u].id < E)
+                    atomicAdd(hist + next[u].id, 1);
+                next[u].row.get(l[u]);
+                m[u] = -INFINITY;
+                if (!on[u]) {   // a row of -inf: p = 0
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        l[u][i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    m[u] = fmaxf(m[u], l[u][i]);
+                load(tok + (U + u) * NW, e, next[u]);
             }
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                m = fmaxf(m, l[i]);
-            m = warp_max(m);
-            const float base = m == -INFINITY ? 0.f : m;
-            float sum = 0.f;
+            for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-            for (int i = 0; i < V; i++) {
-                l[i] = expf(l[i] - base);
-                sum += l[i];
+                for (int u = 0; u < U; u++)
+                    m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], d));
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                // exp(l - m) = 2^(l log2 e - m log2 e): the rounding of m log2 e is a
+                // common factor of the row, which p does not see and lse, about m
+                // itself, holds to an fp32 step
+                constexpr float kLog2e = 1.4426950408889634f;
+                m[u] = m[u] == -INFINITY ? 0.f : m[u];
+                const float ml = -m[u] * kLog2e;
+                sum[u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; i++) {
+                    l[u][i] = exp2_fast(fmaf(l[u][i], kLog2e, ml));
+                    sum[u] += l[u][i];
+                }
             }
-            sum = warp_sum(sum);
-            // a row of -inf (every expert masked) has no distribution: p = 0
-            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
 #pragma unroll
-            for (int i = 0; i < V; i++)
-                psum[i] = fmaf(l[i], inv, psum[i]);
-            const float lse = base + logf(sum);
-            if (sum != 0.f)
-                zsum = fmaf(lse, lse, zsum);
-            if (lane == 0)
-                a.lse[tok] = lse;
+            for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                // a row of -inf (every expert masked) has no distribution: p = 0
+                const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.0f, sum[u]);
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    psum[i] = fmaf(l[u][i], inv, psum[i]);
+                const float lse = m[u] + __logf(sum[u]);
+                if (sum[u] != 0.f)
+                    zsum = fmaf(lse, lse, zsum);
+                if (lane == 0 && tok + u * NW < e)
+                    a.lse[tok + u * NW] = on[u] ? lse : 0.f;
+            }
         }
 #pragma unroll
         for (int i = 0; i < V; i++)
-            if (i * 32 + lane < E)
-                sm[warp * E + i * 32 + lane] = psum[i];
+            if (R::at(i, lane) < E)
+                sm[warp * E + R::at(i, lane)] = psum[i];
         if (lane == 0) {
             zred[warp] = zsum;
             vred[warp] = valid;
         }
         __syncthreads();
-        const long long slot = (long long)blockIdx.x + s;
-        for (int i = threadIdx.x; i < E; i += kThreads) {
-            float p = sm[i];
-#pragma unroll
-            for (int w = 1; w < kWarps; w++)
-                p += sm[w * E + i];
-            a.ws.prob[slot * E + i] = p;
-            a.ws.counts[slot * E + i] = hist[i];
-        }
-        if (threadIdx.x == 0) {
-            double z = 0;
-            int v = 0;
-            for (int w = 0; w < kWarps; w++) {
+        int v = 0;
+        float z = 0.f;
+        if (ONE || threadIdx.x == 0) {
+#pragma unroll 8
+            for (int w = 0; w < NW; w++) {
                 z += zred[w];
                 v += vred[w];
             }
+        }
+        float part = 0.f;
+        const long long slot = (long long)blockIdx.x + s;
+        for (int i = threadIdx.x; i < E; i += NT) {
+            float p = sm[i];
+#pragma unroll 8
+            for (int w = 1; w < NW; w++)
+                p += sm[w * E + i];
+            if (ONE) {
+                a.counts[(long long)s * E + i] = hist[i];
+                a.prob[(long long)s * E + i] = v > 0 ? p / (float)v : 0.f;
+                part += (float)hist[i] * p;
+            } else {
+                a.ws.prob[slot * E + i] = p;
+                a.ws.counts[slot * E + i] = hist[i];
+            }
+        }
+        if (ONE) {
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1)
+                part += __shfl_xor_sync(0xffffffffu, part, d);
+            if (lane == 0)
+                lred[warp] = part;
+            if (v > 0) {
+                zall += z;
+                all += v;
+                segs++;
+            }
+            if (threadIdx.x == 0)
+                a.tokens[s] = v;
+        } else if (threadIdx.x == 0) {
             a.ws.z[slot] = z;
             a.ws.valid[slot] = v;
         }
         __syncthreads();
+        if (ONE && v > 0) {
+            part = 0.f;
+#pragma unroll 8
+            for (int w = 0; w < NW; w++)
+                part += lred[w];
+            bal += part / (float)v * ((float)E / ((float)a.k * (float)v));
+        }
     }
-    for (int i = t + threadIdx.x; i < t_hi; i += kThreads)
+    for (int i = t + threadIdx.x; i < t_hi; i += NT)
         a.lse[i] = 0.f;                 // tokens behind the last segment
+    if (ONE && threadIdx.x == 0) {
+        a.loss[0] = segs ? bal / (float)segs : 0.f;
+        a.loss[1] = all ? zall / (float)all : 0.f;
+    }
 }
 
 // One CTA per (32 experts, segment): the partial rows in block order, counts,
@@ -256,53 +458,54 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(FwdArgs a)
     __shared__ float sp[W][32];
     __shared__ int sc[W][32];
     __shared__ int sv[W];
-    __shared__ double dred[W], zred[W];
-    __shared__ long long tred[W], lred[W];
+    __shared__ float sz[W], sb[W];
     __shared__ int last;
     pdl_enter();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
     const int s = blockIdx.y, e = blockIdx.x * 32 + lane, E = a.E;
     const int b = a.segs.begin(s), end = a.segs.end(s);
     const int b0 = b / a.C, b1 = end > b ? (end - 1) / a.C + 1 : b0;
-    float p = 0.f;
+    float p = 0.f, z = 0.f;
     int c = 0, v = 0;
-    for (int i = b0 + warp; i < b1; i += W) {
+#pragma unroll 4
+    for (int i = b0 + warp; i < b1; i += warps) {
         const long long slot = (long long)i + s;
         if (e < E) {
             p += a.ws.prob[slot * E + e];
             c += a.ws.counts[slot * E + e];
         }
         v += a.ws.valid[slot];
+        z += a.ws.z[slot];
     }
     sp[warp][lane] = p;
     sc[warp][lane] = c;
-    if (lane == 0)
+    if (lane == 0) {
         sv[warp] = v;
+        sz[warp] = z;
+    }
     __syncthreads();
     if (warp == 0) {
-        p = 0.f;
-        c = 0;
-        v = 0;
-        for (int w = 0; w < W; w++) {
+        p = z = 0.f;
+        c = v = 0;
+        for (int w = 0; w < warps; w++) {
             p += sp[w][lane];
             c += sc[w][lane];
             v += sv[w];
+            z += sz[w];
         }
-        double part = 0;
-        if (v > 0)
-            part = (double)c * (double)p * ((double)E / ((double)a.k * v * v));
+        float part = 0.f;
+        if (v > 0 && e < E)
+            part = (float)c * p / (float)v * ((float)E / ((float)a.k * (float)v));
         if (e < E) {
             a.counts[(long long)s * E + e] = c;
             a.prob[(long long)s * E + e] = v > 0 ? p / (float)v : 0.f;
-        } else {
-            part = 0;
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1)
-            part += __shfl_xor_sync(0xffffffffu, part, d);
+        part = warp_sum(part);
         if (lane == 0) {
-            if (blockIdx.x == 0)
+            if (blockIdx.x == 0) {
                 a.tokens[s] = v;
+                a.ws.zseg[s] = z;
+            }
             a.ws.part[(long long)s * gridDim.x + blockIdx.x] = part;
             __threadfence();
             last = atomicAdd(a.ws.ticket, 1u) + 1 == gridDim.x * gridDim.y;
@@ -312,25 +515,16 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(FwdArgs a)
     if (!last)
         return;
     __threadfence();
-    double bal = 0, z = 0;
-    long long tokens = 0, live = 0;
-    for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += kFinalThreads)
+    float bal = 0.f;
+    z = 0.f;
+    int tokens = 0, live = 0;
+    for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += blockDim.x)
         bal += __ldcg(a.ws.part + i);
-    // the z sums of the slots in use: walk the segments' block ranges
-    for (int q = threadIdx.x; q < a.segs.S; q += kFinalThreads) {
-        const int v = __ldcg(a.tokens + q);
-        tokens += v;
-        live += v > 0;
-    }
-    for (int q = a.segs.S > W ? warp : 0; q < a.segs.S; q += a.segs.S > W ? W : 1) {
-        const int qb = a.segs.begin(q), qe = a.segs.end(q);
-        if (qe <= qb)
-            continue;
-        const int i1 = (qe - 1) / a.C + 1;
-        // few segments: all threads share each one's blocks; many: a warp each
-        for (int i = qb / a.C + (a.segs.S > W ? lane : (int)threadIdx.x); i < i1;
-             i += a.segs.S > W ? 32 : kFinalThreads)
-            z += a.ws.z[(long long)i + q];
+    for (int q = threadIdx.x; q < a.segs.S; q += blockDim.x) {
+        const int t = __ldcg(a.tokens + q);
+        tokens += t;
+        live += t > 0;
+        z += __ldcg(a.ws.zseg + q);
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
@@ -340,23 +534,23 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(FwdArgs a)
         live += __shfl_xor_sync(0xffffffffu, live, d);
     }
     if (lane == 0) {
-        dred[warp] = bal;
-        zred[warp] = z;
-        tred[warp] = tokens;
-        lred[warp] = live;
+        sb[warp] = bal;
+        sz[warp] = z;
+        sv[warp] = tokens;
+        sc[warp][0] = live;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        bal = z = 0;
+        bal = z = 0.f;
         tokens = live = 0;
-        for (int w = 0; w < W; w++) {
-            bal += dred[w];
-            z += zred[w];
-            tokens += tred[w];
-            live += lred[w];
+        for (int w = 0; w < warps; w++) {
+            bal += sb[w];
+            z += sz[w];
+            tokens += sv[w];
+            live += sc[w][0];
         }
-        a.loss[0] = live ? (float)(bal / (double)live) : 0.f;
-        a.loss[1] = tokens ? (float)(z / (double)tokens) : 0.f;
+        a.loss[0] = live ? bal / (float)live : 0.f;
+        a.loss[1] = tokens ? z / (float)tokens : 0.f;
     }
 }
 
@@ -367,6 +561,8 @@ struct BwdArgs {
     const uint8_t *mask;
     Segs segs;
     int n, E, k, per_warp;
+    int half_k;             // k rounded up to a power of two, halved
+    bool wide;              // rows allow pair loads and stores
     const float *lse;
     const int32_t *counts, *tokens;
     const float *dloss, *w, *dw;
@@ -375,13 +571,22 @@ struct BwdArgs {
 };
 
 // One warp per run of `per_warp` tokens, so that the row f of its segment
-// mostly stays in registers.
+// mostly stays in registers.  The gradients of the top-k weights are computed
+// for as many tokens as fill a warp, and reach their experts' lanes through two
+// rows of shared memory in turn: a token writes one and clears what the token
+// before it wrote in the other, so that one warp barrier separates them.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
 {
+    using R = Row<T, V>;
+    extern __shared__ float sm[];       // with dw: [kWarps][2][32 V], zero between tokens
     __shared__ int red_t[kWarps], red_l[kWarps];
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, E = a.E;
+    float *add = sm + warp * 64 * V;
+    if (a.dw)
+        for (int i = lane; i < 64 * V; i += 32)
+            add[i] = 0.f;
     // valid tokens and segments with any, over the batch
     int tokens = 0, live = 0;
     for (int s = threadIdx.x; s < a.segs.S; s += kThreads) {
@@ -398,107 +603,214 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
         red_t[warp] = tokens;
         red_l[warp] = live;
     }
-    __syncthreads();
-    tokens = live = 0;
-    for (int w = 0; w < kWarps; w++) {
-        tokens += red_t[w];
-        live += red_l[w];
-    }
-    const float gb = live > 0 ? a.dloss[0] / (float)live : 0.f;
-    const float gz = tokens > 0 ? 2.0f * a.dloss[1] / (float)tokens : 0.f;
 
     const T *logits = static_cast<const T *>(a.logits);
     T *out = static_cast<T *>(a.out);
     const long long t_lo = ((long long)blockIdx.x * kWarps + warp) * a.per_warp;
     const int t_hi = (int)min((long long)a.n, t_lo + a.per_warp);
+    constexpr int U = V <= 8 ? 2 : 1;       // tokens at a time
+    struct Token {
+        R row;
+        float lse;
+        bool on;
+    };
+    const auto load = [&](int tok, int end, Token &k) {
+        k.on = false;
+        if (tok < end) {
+            k.row.load(logits + tok * a.ld, E, lane, a.wide);
+            k.lse = a.lse[tok];
+            k.on = !a.mask || a.mask[tok];
+        }
+    };
+    // the top-k weights of 32 / kp tokens at once, kp lanes each
+    const int kp = 2 * a.half_k > 0 ? 2 * a.half_k : 1, batch = 32 / kp;
+    float w = 0.f, dw = 0.f;
+    int id = -1;
+    const auto load_w = [&](int tok) {
+        const int tk = tok + lane / kp, j = lane % kp;
+        w = dw = 0.f;
+        id = -1;
+        if (tk < t_hi && j < a.k) {
+            const long long at = (long long)tk * a.k + j;
+            w = a.w[at];
+            dw = a.dw[at];
+            id = a.idx[at];
+        }
+    };
+    Token next[U];
+#pragma unroll
+    for (int u = 0; u < U; u++)
+        load((int)min((long long)a.n, t_lo) + u, t_hi, next[u]);
+    if (a.dw)
+        load_w((int)min((long long)a.n, t_lo));
+    __syncthreads();
+    tokens = live = 0;
+    for (int i = 0; i < kWarps; i++) {
+        tokens += red_t[i];
+        live += red_l[i];
+    }
+    const float gb = live > 0 ? a.dloss[0] / (float)live : 0.f;
+    const float gz = tokens > 0 ? 2.0f * a.dloss[1] / (float)tokens : 0.f;
     if (t_lo >= a.n)
         return;
-    int s = a.segs.first_after((int)t_lo), s_end = -1, s_begin = 0;
-    float f[V];
-    float gs = 0.f;
-    for (int tok = (int)t_lo; tok < t_hi; tok++) {
-        if (tok >= s_end) {             // the next segment that holds or follows tok
-            if (s_end >= 0)
-                s = max(s, a.segs.first_after(tok));
-            s_begin = s < a.segs.S ? a.segs.begin(s) : a.n;
-            s_end = s < a.segs.S ? a.segs.end(s) : a.n;
-            const int ts = s < a.segs.S ? a.tokens[s] : 0;
-            const float scale = ts > 0 ? (float)E / ((float)a.k * (float)ts) : 0.f;
-            gs = ts > 0 ? gb / (float)ts : 0.f;
-#pragma unroll
-            for (int i = 0; i < V; i++) {
-                const int x = i * 32 + lane;
-                f[i] = s < a.segs.S && x < E ? (float)a.counts[(long long)s * E + x] * scale : 0.f;
+
+    int batch0 = (int)t_lo - batch;     // first token of the batch in v, to
+    float v = 0.f;                      // gradient in this lane's selected logit
+    int to = -1, was = -1;              // its expert; the entry to clear
+    int row = 0;                        // the two shared rows take turns
+    // this token's contributions into shared row `row`; clears the other row
+    const auto scatter = [&](int tok) {
+        if (tok >= batch0 + batch) {
+            batch0 = tok;
+            float wd = w * dw;
+            for (int o = a.half_k; o > 0; o >>= 1)
+                wd += __shfl_xor_sync(0xffffffffu, wd, o);
+            v = w * (dw - wd);
+            const bool real = id >= 0 && id < E;
+            // an expert twice in a token: its first slot adds them all, in order
+            const int key = real ? id * 32 + lane / kp : -1 - lane;
+            const unsigned same = __match_any_sync(0xffffffffu, key);
+            if (__any_sync(0xffffffffu, same & (same - 1))) {
+                float total = 0.f;
+                for (int j = 0; j < 32; j++) {
+                    const float o = __shfl_sync(0xffffffffu, v, j);
+                    total += same >> j & 1 ? o : 0.f;
+                }
+                v = total;
             }
+            to = real && (same & ((1u << lane) - 1)) == 0 ? id : -1;
+            load_w(tok + batch);
         }
-        T *orow = out + tok * a.ldo;
-        const bool in = tok >= s_begin && s < a.segs.S && (!a.mask || a.mask[tok]);
-        float d[V];
-#pragma unroll
-        for (int i = 0; i < V; i++)
-            d[i] = 0.f;
-        if (in) {
-            const T *row = logits + tok * a.ld;
-            const float lse = a.lse[tok];
-            // a row of -inf has no distribution: no gradient through p
-            if (lse != -INFINITY) {
-                float dot = 0.f;
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    const int x = i * 32 + lane;
-                    d[i] = x < E ? ldf(row + x) : -INFINITY;
-                }
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    d[i] = expf(d[i] - lse);
-                    dot = fmaf(f[i], d[i], dot);
-                }
-                dot = warp_sum(dot);
-                const float cz = gz * lse;
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    d[i] *= fmaf(gs, f[i] - dot, cz);
-            }
-            if (a.dw) {
-                const long long at = (long long)tok * a.k + lane;
-                const float w = lane < a.k ? a.w[at] : 0.f, dw = lane < a.k ? a.dw[at] : 0.f;
-                const int id = lane < a.k ? a.idx[at] : -1;
-                const float dot = warp_sum(w * dw);
-                const float v = w * (dw - dot);
-                for (int j = 0; j < a.k; j++) {
-                    const int e = __shfl_sync(0xffffffffu, id, j);
-                    const float add = __shfl_sync(0xffffffffu, v, j);
-                    const int at_i = e >= 0 && (e & 31) == lane ? e >> 5 : -1;
-#pragma unroll
-                    for (int i = 0; i < V; i++)
-                        if (at_i == i)
-                            d[i] += add;
-                }
-            }
-        }
+        const int mine = lane / kp == tok - batch0 ? to : -1;
+        if (was >= 0)
+            add[(row ^ 1) * 32 * V + was] = 0.f;
+        if (mine >= 0)
+            add[row * 32 * V + mine] = v;
+        was = mine;
+        __syncwarp();
+    };
+
+    int s = a.segs.first_after((int)t_lo), tok = (int)t_lo;
+    while (tok < t_hi) {
+        // a run of tokens inside one segment, or between two
+        const bool seg = s < a.segs.S;
+        const int sb = seg ? a.segs.begin(s) : a.n, se = seg ? a.segs.end(s) : a.n;
+        const bool in = seg && tok >= sb;
+        const int stop = min(t_hi, in ? max(se, tok + 1) : max(sb, tok + 1));
+        const int ts = in ? a.tokens[s] : 0;
+        const float scale = ts > 0 ? (float)E / ((float)a.k * (float)ts) * (gb / (float)ts) : 0.f;
+        float f[V];         // g_b / (S' T_s) f_e of this lane's experts
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            const int x = i * 32 + lane;
-            if (x < E)
-                stf(orow + x, d[i]);
+            const int x = R::at(i, lane);
+            f[i] = in && x < E ? (float)a.counts[(long long)s * E + x] * scale : 0.f;
         }
+        while (tok < stop) {
+            float d[U][V], dot[U], lse[U];
+            bool on[U];
+            const int left = stop - tok;
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                on[u] = in && u < left && next[u].on;
+                // a row of -inf has no distribution, and a token that takes no part
+                // no gradient: exp(-inf) = 0
+                const bool none = !on[u] || next[u].lse == -INFINITY;
+                lse[u] = none ? 0.f : next[u].lse;
+                next[u].row.get(d[u]);
+                dot[u] = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; i++) {
+                    d[u][i] = none ? 0.f : exp_neg(d[u][i] - lse[u]);
+                    dot[u] = fmaf(f[i], d[u][i], dot[u]);
+                }
+            }
+            // the next tokens, across the run's end too
+            if (U == 2 && left == 1) {
+                next[0] = next[U - 1];
+                load(tok + 2, t_hi, next[U - 1]);
+            } else {
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    load(tok + U + u, t_hi, next[u]);
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
+#pragma unroll
+            for (int u = 0; u < U; u++) {
+                const float all = gz * lse[u] - dot[u];
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    d[u][i] *= f[i] + all;
+                if (u >= left)
+                    continue;
+                if (a.dw) {
+                    scatter(tok + u);
+                    if (on[u]) {
+#pragma unroll
+                        for (int i = 0; i < V; i += R::W) {
+                            const float *p = add + row * 32 * V + R::at(i, lane);
+                            if (R::W == 2) {
+                                const float2 v2 = *reinterpret_cast<const float2 *>(p);
+                                d[u][i] += v2.x;
+                                d[u][i + R::W - 1] += v2.y;
+                            } else {
+                                d[u][i] += *p;
+                            }
+                        }
+                    }
+                    row ^= 1;
+                }
+                R::store(out + (tok + u) * a.ldo, d[u], E, lane, a.wide);
+            }
+            tok += min(U, left);
+        }
+        if (in)
+            s = max(s + 1, a.segs.first_after(tok));
     }
 }
 
 template <typename T, int V>
 cudaError_t launch_stats(const FwdArgs &a, cudaStream_t st)
 {
-    const size_t smem = sizeof(float) * (kWarps + 1) * a.E;
-    return launch_pdl(balance_stats_kernel<T, V>, dim3((a.n + a.C - 1) / a.C), dim3(kThreads),
-                      smem, st, a);
+    if (V <= 16 && one_block(a.n, a.E, a.segs.S)) {
+        auto kernel = balance_stats_kernel<T, V <= 16 ? V : 16, true>;
+        const size_t smem = sizeof(float) * (kOneWarps + 1) * a.E;
+        if (smem > 48 * 1024) {
+            const cudaError_t e = cudaFuncSetAttribute(
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess)
+                return e;
+        }
+        return launch_pdl(kernel, dim3(1), dim3(32 * kOneWarps), smem, st, a);
+    }
+    const cudaError_t e =
+        launch_pdl(balance_stats_kernel<T, V, false>, dim3((a.n + a.C - 1) / a.C),
+                   dim3(kThreads), sizeof(float) * (kWarps + 1) * a.E, st, a);
+    if (e != cudaSuccess)
+        return e;
+    // a warp for each block that a segment meets on average, up to 32
+    const int per = (int)((a.n + a.C - 1) / a.C / a.segs.S) + 1;
+    const int warps = per >= 16 ? 32 : per >= 8 ? 16 : per >= 4 ? 8 : 4;
+    return launch_pdl(balance_final_kernel, dim3((a.E + 31) / 32, a.segs.S), dim3(32 * warps), 0, st,
+                      a);
 }
 
 template <typename T, int V>
 cudaError_t launch_grad(const BwdArgs &a, cudaStream_t st)
 {
     const long long warps = (a.n + a.per_warp - 1) / a.per_warp;
+    const size_t smem = a.dw ? sizeof(float) * kWarps * 64 * V : 0;
+    if (smem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            balance_grad_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess)
+            return e;
+    }
     return launch_pdl(balance_grad_kernel<T, V>, dim3((unsigned)((warps + kWarps - 1) / kWarps)),
-                      dim3(kThreads), 0, st, a);
+                      dim3(kThreads), smem, st, a);
 }
 
 // V = ceil(E / 32) rounded up to a power of two: a row's registers per lane.
@@ -522,6 +834,12 @@ cudaError_t grad(const BwdArgs &a, cudaStream_t st)
            : a.E <= 256 ? launch_grad<T, 8>(a, st)
            : a.E <= 512 ? launch_grad<T, 16>(a, st)
                         : launch_grad<T, 32>(a, st);
+}
+
+// Whether every row starts on a boundary of two values of `size` bytes.
+bool pairs(const void *p, long long ld, int E, size_t size)
+{
+    return E % 2 == 0 && ld % 2 == 0 && reinterpret_cast<uintptr_t>(p) % (2 * size) == 0;
 }
 
 }  // namespace
@@ -626,20 +944,17 @@ extern "C" int moe_balance_loss(const void *logits, int dtype, long long ld, int
     a.n = n_tokens;
     a.E = n_experts;
     a.k = top_k;
-    a.C = block_tokens(n_tokens);
+    a.C = one_block(n_tokens, n_experts, n_segments) ? n_tokens : block_tokens(n_tokens);
+    a.wide = pairs(logits, ld, n_experts, size_of(dtype));
     a.loss = loss;
     a.counts = counts;
     a.tokens = tokens;
     a.prob = prob;
     a.lse = lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e = dtype == MOE_FP32   ? stats<float>(a, st)
+    return launched(dtype == MOE_FP32   ? stats<float>(a, st)
                     : dtype == MOE_FP16 ? stats<__half>(a, st)
-                                        : stats<__nv_bfloat16>(a, st);
-    if (e == cudaSuccess)
-        e = launch_pdl(balance_final_kernel, dim3((n_experts + 31) / 32, n_segments),
-                       dim3(kFinalThreads), 0, st, a);
-    return launched(e);
+                                        : stats<__nv_bfloat16>(a, st));
 }
 
 extern "C" int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tokens,
@@ -701,7 +1016,13 @@ extern "C" int moe_balance_loss_grad(const void *logits, int dtype, long long ld
     a.dw = dtopk_w;
     a.out = dlogits;
     a.ldo = ldd;
-    a.per_warp = (int)std::max(1LL, (long long)n_tokens / ((long long)sms * 6 * kWarps));
+    while (2 * a.half_k < top_k)
+        a.half_k = std::max(1, 2 * a.half_k);
+    a.wide = pairs(logits, ld, n_experts, size_of(dtype)) &&
+             pairs(dlogits, ldd, n_experts, size_of(dtype));
+    // about four CTAs per SM
+    const long long warps = 4LL * sms * kWarps;
+    a.per_warp = (int)((n_tokens + warps - 1) / warps);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return launched(dtype == MOE_FP32   ? grad<float>(a, st)
                     : dtype == MOE_FP16 ? grad<__half>(a, st)
