@@ -608,7 +608,6 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
     T *out = static_cast<T *>(a.out);
     const long long t_lo = ((long long)blockIdx.x * kWarps + warp) * a.per_warp;
     const int t_hi = (int)min((long long)a.n, t_lo + a.per_warp);
-    constexpr int U = V <= 8 ? 2 : 1;       // tokens at a time
     struct Token {
         R row;
         float lse;
@@ -637,10 +636,8 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
             id = a.idx[at];
         }
     };
-    Token next[U];
-#pragma unroll
-    for (int u = 0; u < U; u++)
-        load((int)min((long long)a.n, t_lo) + u, t_hi, next[u]);
+    Token next;
+    load((int)min((long long)a.n, t_lo), t_hi, next);
     if (a.dw)
         load_w((int)min((long long)a.n, t_lo));
     __syncthreads();
@@ -705,67 +702,47 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
             const int x = R::at(i, lane);
             f[i] = in && x < E ? (float)a.counts[(long long)s * E + x] * scale : 0.f;
         }
-        while (tok < stop) {
-            float d[U][V], dot[U], lse[U];
-            bool on[U];
-            const int left = stop - tok;
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                on[u] = in && u < left && next[u].on;
-                // a row of -inf has no distribution, and a token that takes no part
-                // no gradient: exp(-inf) = 0
-                const bool none = !on[u] || next[u].lse == -INFINITY;
-                lse[u] = none ? 0.f : next[u].lse;
-                next[u].row.get(d[u]);
-                dot[u] = 0.f;
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    d[u][i] = none ? 0.f : exp_neg(d[u][i] - lse[u]);
-                    dot[u] = fmaf(f[i], d[u][i], dot[u]);
-                }
-            }
-            // the next tokens, across the run's end too
-            if (U == 2 && left == 1) {
-                next[0] = next[U - 1];
-                load(tok + 2, t_hi, next[U - 1]);
-            } else {
-#pragma unroll
-                for (int u = 0; u < U; u++)
-                    load(tok + U + u, t_hi, next[u]);
-            }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-                for (int u = 0; u < U; u++)
-                    dot[u] += __shfl_xor_sync(0xffffffffu, dot[u], o);
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                const float all = gz * lse[u] - dot[u];
+        for (; tok < stop; tok++) {
+            const bool on = in && next.on;
+            // a row of -inf has no distribution, and a token that takes no part no
+            // gradient
+            const bool none = !on || next.lse == -INFINITY;
+            const float lse = none ? 0.f : next.lse;
+            float d[V], dot = 0.f;
+            next.row.get(d);
+            load(tok + 1, t_hi, next);
+            if (none) {
 #pragma unroll
                 for (int i = 0; i < V; i++)
-                    d[u][i] *= f[i] + all;
-                if (u >= left)
-                    continue;
-                if (a.dw) {
-                    scatter(tok + u);
-                    if (on[u]) {
+                    d[i] = -INFINITY;
+            }
 #pragma unroll
-                        for (int i = 0; i < V; i += R::W) {
-                            const float *p = add + row * 32 * V + R::at(i, lane);
-                            if (R::W == 2) {
-                                const float2 v2 = *reinterpret_cast<const float2 *>(p);
-                                d[u][i] += v2.x;
-                                d[u][i + R::W - 1] += v2.y;
-                            } else {
-                                d[u][i] += *p;
-                            }
+            for (int i = 0; i < V; i++) {
+                d[i] = exp_neg(d[i] - lse);
+                dot = fmaf(f[i], d[i], dot);
+            }
+            const float all = gz * lse - warp_sum(dot);
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                d[i] *= f[i] + all;
+            if (a.dw) {
+                scatter(tok);
+                if (on) {
+#pragma unroll
+                    for (int i = 0; i < V; i += R::W) {
+                        const float *p = add + row * 32 * V + R::at(i, lane);
+                        if (R::W == 2) {
+                            const float2 v2 = *reinterpret_cast<const float2 *>(p);
+                            d[i] += v2.x;
+                            d[i + R::W - 1] += v2.y;
+                        } else {
+                            d[i] += *p;
                         }
                     }
-                    row ^= 1;
                 }
-                R::store(out + (tok + u) * a.ldo, d[u], E, lane, a.wide);
+                row ^= 1;
             }
-            tok += min(U, left);
+            R::store(out + tok * a.ldo, d, E, lane, a.wide);
         }
         if (in)
             s = max(s + 1, a.segs.first_after(tok));
@@ -1020,8 +997,8 @@ extern "C" int moe_balance_loss_grad(const void *logits, int dtype, long long ld
         a.half_k = std::max(1, 2 * a.half_k);
     a.wide = pairs(logits, ld, n_experts, size_of(dtype)) &&
              pairs(dlogits, ldd, n_experts, size_of(dtype));
-    // about four CTAs per SM
-    const long long warps = 4LL * sms * kWarps;
+    // as many CTAs as run at once: a row takes up to 32 registers a few times over
+    const long long warps = (n_experts > 256 ? 2LL : 4LL) * sms * kWarps;
     a.per_warp = (int)((n_tokens + warps - 1) / warps);
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return launched(dtype == MOE_FP32   ? grad<float>(a, st)
