@@ -391,9 +391,9 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
 
 // ---- dx = dy W -------------------------------------------------------------
 // A CTA owns 128 columns; a stage is 32 rows x 64 bytes (64-byte swizzle).  The
-// rows are the MMA's K and the columns its M: lane (g, t) holds, of rows 4 t ..
-// 4 t + 3 of 16, the 8 bytes g (16 columns), and one byte permutation pairs the
-// halves of two rows' words, so that a field holds one column of two rows.  The
+// rows are the MMA's K and the columns its M.  A transposing matrix load of 8
+// rows x 16 bytes gives lane (g, t) the 16-bit piece g (4 columns) of the rows 2 t
+// and 2 t + 1 in one word, so that a field holds one column of two rows.  The
 // scale differs along the MMA's K:
 //   bf16, groups of 128: one scale per row holds for all columns of the CTA, so
 //     it multiplies the gradients, dy * s rounded once to bf16 (fp32 range);
@@ -489,28 +489,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             ahead[i] = ahead[i + 1];
         if (r0 + kAhead * r_step < rows)
             load_meta(r0 + kAhead * r_step, ahead[kAhead - 1]);
-        uint2 b[2];
+        uint32_t b[2][2];       // gradients of the rows 2 t, + 1 of each 8
 #pragma unroll
-        for (int ss = 0; ss < 2; ss++) {
-            const int tok = tok0 + g, r = r0 + 16 * ss + 4 * t;
-            b[ss] = make_uint2(0, 0);
-            if (tok < c.n) {
-                const T *p = dy + tok * c.ldi + r;
-                if (vec_in && r + 3 < rows) {
-                    b[ss] = *reinterpret_cast<const uint2 *>(p);
-                } else {
-                    const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
-                    if (r < rows)
-                        b[ss].x = u[0];
-                    if (r + 1 < rows)
-                        b[ss].x |= (uint32_t)u[1] << 16;
-                    if (r + 2 < rows)
-                        b[ss].y = u[2];
-                    if (r + 3 < rows)
-                        b[ss].y |= (uint32_t)u[3] << 16;
+        for (int ss = 0; ss < 2; ss++)
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const int tok = tok0 + g, r = r0 + 16 * ss + 8 * h + 2 * t;
+                b[ss][h] = 0;
+                if (tok < c.n) {
+                    const T *p = dy + tok * c.ldi + r;
+                    if (vec_in && r + 1 < rows) {
+                        b[ss][h] = *reinterpret_cast<const uint32_t *>(p);
+                    } else {
+                        const uint16_t *u = reinterpret_cast<const uint16_t *>(p);
+                        if (r < rows)
+                            b[ss][h] = u[0];
+                        if (r + 1 < rows)
+                            b[ss][h] |= (uint32_t)u[1] << 16;
+                    }
                 }
             }
-        }
         // this lane's row pair (lane & ~1, + 1) as the unpacking's operand words
         typename Q::Zero zp[kMeta];
         typename Q::Scale sp[kMeta];
@@ -530,16 +528,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             *abort_flag = 1;
         }
-        // row r's 16-byte piece p sits at p ^ (r / 2 % 4); r = 16 ss + 4 t + i
-        const uint8_t *stage = smem + warp * kRing + slot * kGradStage + t * 256 + 8 * (g & 1);
-        const uint8_t *w01 = stage + (((g >> 1) ^ (2 * t & 3)) << 4);
-        const uint8_t *w23 = stage + (((g >> 1) ^ ((2 * t + 1) & 3)) << 4);
-        uint2 w[2][4];
+        // w[ss][chunk of 32 columns][half]; row r's chunk p sits at p ^ (r / 2 % 4)
+        const uint32_t stage = ring + slot * kGradStage;
+        uint32_t w[2][4][2];
 #pragma unroll
         for (int ss = 0; ss < 2; ss++)
 #pragma unroll
-            for (int i = 0; i < 4; i++)
-                w[ss][i] = *reinterpret_cast<const uint2 *>((i < 2 ? w01 : w23) + ss * 1024 + i * 64);
+            for (int p = 0; p < 4; p += 2) {
+                const int r = 16 * ss + (lane & 15), chunk = p + (lane >> 4);
+                uint32_t d[4];
+                ldmatrix4_trans(d, stage + r * 64 + ((chunk ^ (r >> 1 & 3)) << 4));
+                w[ss][p][0] = d[0];
+                w[ss][p][1] = d[1];
+                w[ss][p + 1][0] = d[2];
+                w[ss][p + 1][1] = d[3];
+            }
         // every lane's reads are done before the copy engine writes the stage
         fence_async_shared();
         __syncwarp();
@@ -547,51 +550,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             fetch(r0 + kGradStages * r_step, slot);
 #pragma unroll
         for (int ss = 0; ss < 2; ss++) {
-            const int from = 16 * ss + 4 * t;
-            uint32_t z[2], sr[2];
-            typename Q::Scale s[2];
+            const int from = 16 * ss + 2 * t;
+            typename Q::Zero z01, z23;
+            typename Q::Scale s01, s23;
+            uint32_t b0 = b[ss][0], b1 = b[ss][1];
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
-                // of this lane's group (16 g of the CTA's columns)
-                z[h] = 0;
-                sr[h] = 0;
-#pragma unroll
-                for (int i = 0; i < kMeta; i++) {
-                    const uint32_t zi = __shfl_sync(0xffffffffu, zp[i].lo, from + 2 * h);
-                    if (kMeta == 1 || 16 * g / GS == i)
-                        z[h] = zi;
+            for (int p = 0; p < 4; p++) {       // 32 columns: 32 p + 4 g + field
+                if (32 * p % GS == 0) {         // a group begins
+                    const int i = 32 * p / GS;
+                    z01 = Q::zero_of(__shfl_sync(0xffffffffu, zp[i].lo, from));
+                    z23 = Q::zero_of(__shfl_sync(0xffffffffu, zp[i].lo, from + 8));
                     if (kScaleIn) {
-                        sr[h] = __shfl_sync(0xffffffffu, raw[i], from + 2 * h);
+                        const uint32_t sa = __shfl_sync(0xffffffffu, raw[i], from);
+                        const uint32_t sb = __shfl_sync(0xffffffffu, raw[i], from + 8);
+                        b0 = Q::times(b0, sa & 0xffff, sa >> 16);
+                        b1 = Q::times(b1, sb & 0xffff, sb >> 16);
                     } else {
-                        const typename Q::Scale si = shfl_of(sp[i], from + 2 * h);
-                        if (kMeta == 1 || 16 * g / GS == i)
-                            s[h] = si;
+                        s01 = shfl_of(sp[i], from);
+                        s23 = shfl_of(sp[i], from + 8);
                     }
                 }
-            }
-            const typename Q::Zero z01 = Q::zero_of(z[0]), z23 = Q::zero_of(z[1]);
-            uint2 bb = b[ss];
-            if (kScaleIn) {
-                bb.x = Q::times(bb.x, sr[0] & 0xffff, sr[0] >> 16);
-                bb.y = Q::times(bb.y, sr[1] & 0xffff, sr[1] >> 16);
-            }
-#pragma unroll
-            for (int q4 = 0; q4 < 4; q4++) {        // four columns: half of one of the two words
-                const uint32_t sel = q4 & 1 ? 0x7632 : 0x5410;
-                uint32_t p[4], q[4];
-                Q::unpack(q4 < 2 ? __byte_perm(w[ss][0].x, w[ss][1].x, sel)
-                                 : __byte_perm(w[ss][0].y, w[ss][1].y, sel), z01, p);
-                Q::unpack(q4 < 2 ? __byte_perm(w[ss][2].x, w[ss][3].x, sel)
-                                 : __byte_perm(w[ss][2].y, w[ss][3].y, sel), z23, q);
+                uint32_t f[4], h[4];
+                Q::unpack(w[ss][p][0], z01, f);
+                Q::unpack(w[ss][p][1], z23, h);
                 if (!kScaleIn) {
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        p[i] = Q::mul(p[i], s[0]);
-                        q[i] = Q::mul(q[i], s[1]);
+                        f[i] = Q::mul(f[i], s01);
+                        h[i] = Q::mul(h[i], s23);
                     }
                 }
-                mma16816<T>(acc[2 * q4], p[0], p[1], q[0], q[1], bb.x, bb.y);
-                mma16816<T>(acc[2 * q4 + 1], p[2], p[3], q[2], q[3], bb.x, bb.y);
+                mma16816<T>(acc[2 * p], f[0], f[1], h[0], h[1], b0, b1);
+                mma16816<T>(acc[2 * p + 1], f[2], f[3], h[2], h[3], b0, b1);
             }
         }
     }
@@ -603,7 +593,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int m = 0; m < 8; m++)
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            red[warp * kOut + (2 * t + (i & 1)) * kGradCols + 16 * g + 2 * m + (i >> 1)] = acc[m][i];
+            red[warp * kOut + (2 * t + (i & 1)) * kGradCols + 32 * (m >> 1) + 4 * g + 2 * (m & 1) +
+                (i >> 1)] = acc[m][i];
     __syncthreads();
     for (int o = threadIdx.x; o < kOut; o += kThreads) {
         float s = red[o];
@@ -721,7 +712,7 @@ cudaError_t launch_bwd(const W4Call &c, int dev, int num_sms, cudaStream_t st)
     for (int s = 2; s <= std::min(8, steps); s++)
         if ((long long)strips * blocks <= clusters[s])
             splits = s;
-    const int vec = reinterpret_cast<uintptr_t>(c.in) % 8 == 0 && c.ldi % 4 == 0;
+    const int vec = reinterpret_cast<uintptr_t>(c.in) % 4 == 0 && c.ldi % 2 == 0;
     CUtensorMap wmap;
     if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2,
                     64, 32, CU_TENSOR_MAP_SWIZZLE_64B))

@@ -12,9 +12,10 @@
 //   forward: a thread owns one weight row (its tensor-memory lane) and
 //     unpacks 64 of its K into 32 columns;
 //   gradient: the contraction runs over the weight rows, so a thread unpacks
-//     four columns of the matrix over pairs of rows (one byte permutation
-//     pairs two rows' nibbles) and stores them in the 16-lane x 256-bit tensor
-//     memory layout, lane 8 j + g of a quarter holding column 4 g + j.
+//     four columns of the matrix over pairs of rows (a transposing matrix load
+//     puts two rows' nibbles into one word) and stores them in the 16-lane x
+//     256-bit tensor memory layout, lane 8 j + g of a quarter holding column
+//     4 g + j.
 // Roles of a persistent CTA (one per SM): a code producer and a B producer
 // (TMA), three groups of four dequant warps taking blocks in turn, one or two
 // MMA warps, four epilogue warps.  Tiles of more than 128 tokens need one MMA
@@ -513,20 +514,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 } else {
                     const int slot = 64 * ((32 * q) >> gsh) + 32 * h + 2 * tq;
-                    const uint32_t sel = g & 1 ? 0x7632 : 0x5410;
-                    // row r's 16-byte chunk q sits at q ^ (r / 2 % 4) (64-byte
-                    // swizzle); r = 64 h + 16 ss + 4 tq + i
-                    const uint8_t *w01 = blk + h * 4096 + tq * 256 + 4 * (g >> 1) +
-                                         ((q ^ ((2 * tq) & 3)) << 4);
-                    const uint8_t *w23 = blk + h * 4096 + tq * 256 + 4 * (g >> 1) +
-                                         ((q ^ ((2 * tq + 1) & 3)) << 4);
-                    uint32_t w[4][4];
+                    // Tiles of 8 rows x 16 bytes, transposed, for 16 rows of the
+                    // contraction in memory order: the rows 4 tq, + 1 and 4 tq + 2,
+                    // + 3 of each 16.  Row r's 16-byte chunk q sits at q ^ (r / 2 %
+                    // 4) (64-byte swizzle).
+                    uint32_t w[4][2];
 #pragma unroll
-                    for (int ss = 0; ss < 4; ss++)
-#pragma unroll
-                        for (int i = 0; i < 4; i++)
-                            w[ss][i] = *reinterpret_cast<const uint32_t *>(
-                                (i < 2 ? w01 : w23) + ss * 1024 + i * 64);
+                    for (int ss = 0; ss < 4; ss += 2) {
+                        const int rr = 64 * h + 16 * (ss + (lane >> 4)) + 4 * (lane >> 1 & 3) +
+                                       2 * (lane >> 3 & 1) + (lane & 1);
+                        uint32_t d[4];
+                        ldmatrix4_trans(d, saddr(blk) + rr * 64 + ((q ^ (rr >> 1 & 3)) << 4));
+                        w[ss][0] = d[0];
+                        w[ss][1] = d[1];
+                        w[ss + 1][0] = d[2];
+                        w[ss + 1][1] = d[3];
+                    }
 #pragma unroll
                     for (int ss = 0; ss < 4; ss++) {        // 16 rows: pairs 8 ss + 2 tq, + 1
                         const uint2 zz = *reinterpret_cast<const uint2 *>(zw + slot + 8 * ss);
@@ -534,8 +537,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         const ScalePair<typename Q::Scale> sc =
                             *reinterpret_cast<const ScalePair<typename Q::Scale> *>(sw + slot + 8 * ss);
                         uint32_t p[4], p2[4];
-                        Q::unpack(__byte_perm(w[ss][0], w[ss][1], sel), z01, p);
-                        Q::unpack(__byte_perm(w[ss][2], w[ss][3], sel), z23, p2);
+                        Q::unpack(w[ss][0], z01, p);
+                        Q::unpack(w[ss][1], z23, p2);
                         // columns 0, 1 of the quad to lanes 0..15, 2, 3 to 16..31
 #pragma unroll
                         for (int u = 0; u < 4; u++) {

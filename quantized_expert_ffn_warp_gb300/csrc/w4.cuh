@@ -175,6 +175,16 @@ __device__ __forceinline__ void ldmatrix4(uint32_t (&d)[4], uint32_t addr)
                  : "memory");
 }
 
+// The same tiles transposed: of each, lane (g, t) receives the 16-bit pieces g of
+// rows 2 t (low half) and 2 t + 1 (high half).
+__device__ __forceinline__ void ldmatrix4_trans(uint32_t (&d)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+                 : "r"(addr)
+                 : "memory");
+}
+
 // 2-D TMA map (linear_gemm.cu): boxes of box_rows x box_cols elements of a
 // row-major matrix [rows][cols] with rows `pitch` bytes apart.
 bool encode_map(CUtensorMap *map, CUtensorMapDataType type, const void *base, uint64_t cols,
