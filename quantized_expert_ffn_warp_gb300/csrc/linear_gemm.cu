@@ -725,11 +725,11 @@ struct Plan {
 };
 
 // Tokens per tile and splits along the contraction: the smallest estimated time,
-// in SM cycles, of the busiest SM.  A 64-step of a tile of N tokens takes 2 N
-// cycles on the tensor core and, on the weights' side, at least about 220
-// (dequantisation, and the packed block's share of the HBM rate); a tile costs
-// its epilogue and a cluster the exchange of its partial tiles.
-Plan plan(int C, int F, int n, int num_sms, const int *clusters)
+// in SM cycles, of the busiest SM.  Measured: a 64-step of a tile of N tokens
+// takes 2 N cycles on the tensor core, and whatever N at least about 480 for its
+// dequantisation (560 in the gradient); a tile's epilogue takes about 20 N and
+// the exchange of a cluster's partial tiles 2500 + 8 N.
+Plan plan(int C, int F, int n, int grad, int num_sms, const int *clusters)
 {
     const int mt = (F + kM - 1) / kM, steps = (C + 63) / 64;
     Plan best{};
@@ -743,9 +743,9 @@ Plan plan(int C, int F, int n, int num_sms, const int *clusters)
             if (s > 1 && (long long)mt * nt > clusters[s])
                 continue;       // a cluster would wait for another one's SMs
             const double waves = (double)((ctas + num_sms - 1) / num_sms);
-            const double step = std::max(2.0 * tok, 220.0);
-            const double cost = waves * ((double)(steps + s - 1) / s * step + 12.0 * tok + 1500) +
-                                (s > 1 ? 1500 + 6.0 * tok : 0);
+            const double step = std::max(2.0 * tok, grad ? 560.0 : 480.0);
+            const double cost = waves * ((steps + s - 1) / s * step + 20.0 * tok) +
+                                (s > 1 ? 2500 + 8.0 * tok : 0);
             if (!best.tok || cost < least) {
                 best = {tok, nt, s};
                 least = cost;
@@ -807,7 +807,7 @@ cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int
                                cudaStream_t st)
 {
     const int C = grad ? c.w.rows : c.w.K, F = grad ? c.w.K : c.w.rows;
-    const Plan p = plan(C, F, c.n, num_sms, cluster_table(dev));
+    const Plan p = plan(C, F, c.n, grad, num_sms, cluster_table(dev));
     GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits};
     CUtensorMap wmap, bmap;
     if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
