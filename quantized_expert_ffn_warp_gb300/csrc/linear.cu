@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kWarps = 16;              // multiplying warps
 constexpr int kRing = 8 * 1024;         // bytes per warp
+constexpr int kAdders = 4;              // warps that add: one per scheduler, as they cost issue slots
 
 // ---- y = x W^T -------------------------------------------------------------
 // A stage is 16 RT rows x a slice of 256 K, i.e. 128 bytes of each row (128-byte
@@ -35,8 +36,8 @@ constexpr int kRing = 8 * 1024;         // bytes per warp
 // + 4) of the same 8.  So two MMAs cover 32 consecutive K: the products with
 // the exact integers q - z are summed over one group and the fp32 sum is
 // scaled; no weight is rounded, for any group size.
-// A tile's partial sums go to one more warp through shared memory, which adds
-// them in order and stores the results while the others go on.
+// A tile's partial sums go to four more warps through shared memory, which add
+// them in order and store the results while the others go on.
 struct FwdArgs {
     W4Call c;
     int kw_n, rw_n;     // warps along K, and row tiles at a time, of a CTA
@@ -124,7 +125,7 @@ __device__ __forceinline__ float group_scale(const M &m, int i)
 }
 
 template <typename T, int GS, int RT>
-__global__ void __launch_bounds__(32 * (kWarps + 1), 1)
+__global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
     linear_kernel(const __grid_constant__ CUtensorMap wmap, const FwdArgs a)
 {
     using Q = W4<T>;
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
     volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + G::nbars);
     const W4Call &c = a.c;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int warps = a.kw_n * a.rw_n;      // multiplying warps; the next one adds
+    const int warps = a.kw_n * a.rw_n;      // multiplying warps; the next ones add
     const int kw = warp % a.kw_n, rw = warp / a.kw_n;
     const uint32_t full = saddr(bars + warp * G::stages);
     const uint32_t ring = saddr(smem) + warp * kRing;
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
             prefetch_map(&wmap);
             for (int i = 0; i < G::stages; i++)
                 bar_init(full + 8 * i, 1);
-        } else {
+        } else if (warp == warps) {
             for (int i = 0; i < 2; i++) {
                 bar_init(red_full + 8 * i, warps);
-                bar_init(red_empty + 8 * i, 1);
+                bar_init(red_empty + 8 * i, kAdders);
             }
             *abort_flag = 0;
         }
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
                     parity ^= 1;
                 }
             }
-            // this warp's sums, element o of the tile at o (token major)
+            // this warp's sums, as its lanes hold them
             if (ok && !warp_wait(red_empty + 8 * buf, red_parity, abort_flag)) {
                 ok = false;
                 *abort_flag = 1;
@@ -323,7 +324,7 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
             for (int r = 0; r < RT; r++)
 #pragma unroll
                 for (int i = 0; i < 4; i++)
-                    red[(2 * t + (i & 1)) * 16 * RT + 16 * r + g + 8 * (i >> 1)] = acc[r][i];
+                    red[(4 * r + i) * 32 + lane] = acc[r][i];
             __syncwarp();
             if (lane == 0)
                 bar_arrive(red_full + 8 * buf);
@@ -333,49 +334,43 @@ __global__ void __launch_bounds__(32 * (kWarps + 1), 1)
         }
     } else {
         // ------------------------------------------------------ add and store
-        // results of a set, 4 at a time: rows 4 i .. 4 i + 3 of a token
-        constexpr int kVec = G::out / 4, kPer = (kVec + 31) / 32;
-        const auto store = [&](int set, int rb, int o, const float (&v)[4]) {
-            const int row0 = (set * a.rw_n + rb) * 16 * RT + 4 * o % (16 * RT);
-            const int tok = tok0 + 4 * o / (16 * RT);
-            if (tok >= c.n)
-                return;
-            T *y = static_cast<T *>(c.out) + tok * c.ldo + row0;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if (row0 + i >= rows)
-                    break;
-                float s = v[i];
-                if (c.bias)
-                    s += Q::to_float(static_cast<const T *>(c.bias)[row0 + i]);
-                if (c.residual)
-                    s += Q::to_float(static_cast<const T *>(c.residual)[tok * c.ldr + row0 + i]);
-                y[i] = Q::from_float(s);
-            }
-        };
+        // Two neighbouring lanes' sums per thread: o = 16 (4 r + i) + lane / 2 is row
+        // 16 r + 8 (i / 2) + g and the tokens 4 (o % 2) + i % 2 and + 2.
+        constexpr int kPairs = G::out / 2;
+        static_assert(kPairs <= 32 * kAdders, "a pair per thread");
+        const int o = (warp - warps) * 32 + lane, i = o / 16 % 4;
+        const int tok = tok0 + 4 * (o & 1) + (i & 1);
+        const int in_tile = o / 64 * 16 + 8 * (i >> 1) + o / 2 % 8;
+        const float2 *red = reinterpret_cast<const float2 *>(smem + G::red_off) + o;
         uint32_t buf = 0, parity = 0;
         for (int set = blockIdx.x; set < sets; set += gridDim.x) {
             if (ok && !warp_wait(red_full + 8 * buf, parity, abort_flag)) {
                 ok = false;
                 *abort_flag = 1;
             }
-            const float4 *red = reinterpret_cast<const float4 *>(smem + G::red_off) + buf * kWarps * kVec;
-            for (int rb = 0; rb < a.rw_n; rb++)
-#pragma unroll
-                for (int n = 0; n < kPer; n++) {
-                    const int o = 32 * n + lane;
-                    if (o >= kVec)
-                        break;
-                    float v[4] = {};
-#pragma unroll 4
+            if (o < kPairs)
+                for (int rb = 0; rb < a.rw_n; rb++) {
+                    const float2 *p = red + (buf * kWarps + rb * a.kw_n) * kPairs;
+                    float v[2] = {};
+#pragma unroll 8
                     for (int w = 0; w < a.kw_n; w++) {
-                        const float4 p = red[(rb * a.kw_n + w) * kVec + o];
-                        v[0] += p.x;
-                        v[1] += p.y;
-                        v[2] += p.z;
-                        v[3] += p.w;
+                        const float2 q = p[w * kPairs];
+                        v[0] += q.x;
+                        v[1] += q.y;
                     }
-                    store(set, rb, o, v);
+                    const int row = (set * a.rw_n + rb) * 16 * RT + in_tile;
+                    if (row >= rows)
+                        continue;
+                    const float bias = c.bias ? Q::to_float(static_cast<const T *>(c.bias)[row]) : 0.f;
+#pragma unroll
+                    for (int u = 0; u < 2; u++) {
+                        if (tok + 2 * u >= c.n)
+                            continue;
+                        float s = v[u] + bias;
+                        if (c.residual)
+                            s += Q::to_float(static_cast<const T *>(c.residual)[(tok + 2 * u) * c.ldr + row]);
+                        static_cast<T *>(c.out)[(tok + 2 * u) * c.ldo + row] = Q::from_float(s);
+                    }
                 }
             __syncwarp();
             if (lane == 0)
@@ -689,7 +684,7 @@ cudaError_t launch_fwd_rt(const W4Call &c, int num_sms, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     return launch_pdl(kernel, dim3(std::min(sets, num_sms), (c.n + 7) / 8),
-                      dim3(32 * (a.kw_n * a.rw_n + 1)), FwdGeo<RT>::smem, st, wmap, a);
+                      dim3(32 * (a.kw_n * a.rw_n + kAdders)), FwdGeo<RT>::smem, st, wmap, a);
 }
 
 template <typename T, int GS>
