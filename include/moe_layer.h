@@ -404,12 +404,11 @@ int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const flo
  * bf16 (dtype MOE_FP16 or MOE_BF16); ldx, ldr, ldy are their row strides in
  * elements (at least the row's length; columns beyond it are neither read nor
  * written).  bias and residual may be NULL; y may be residual itself, and must
- * not overlap x.  n_tokens 1 .. 524288.
+ * not overlap x.  n_tokens 1 .. 524280.
  * Sums are fp32, with bias and residual added before the one rounding to the
- * output type.  For groups of 128 and few tokens the group's fp32 sum of x *
- * (q - zero) is scaled; otherwise each weight is rounded once to the
- * activations' type before the product.  The same call gives the same bits
- * every time.
+ * output type.  Up to 8 tokens a group's fp32 sum of x * (q - zero) is scaled;
+ * for more, each weight is rounded once to the activations' type before the
+ * product.  The same call gives the same bits every time.
  * All pointers are DEVICE pointers of the current device: codes and the rows
  * of x 16-byte aligned (ldx a multiple of 8), the others to their element.
  * status (int32 [1], may be NULL) gets MOE_STATUS_TIMEOUT or'ed in when a

@@ -124,6 +124,18 @@ __device__ __forceinline__ float group_scale(const M &m, int i)
     return __half2float(__ushort_as_half((unsigned short)(word_of(m.s, i / 2) >> (16 * (i & 1)))));
 }
 
+// After a wait that gave up: the copies still in flight, waited for with a
+// limit before the shared memory is given back.
+__device__ __forceinline__ void drain(uint32_t full, int stages, unsigned arrived, unsigned issued)
+{
+    for (; arrived < issued; arrived++) {
+        const unsigned long long t0 = now_ns();
+        while (!bar_try(full + 8 * (arrived % stages), arrived / stages & 1) &&
+               now_ns() - t0 < kGWaitNs) {
+        }
+    }
+}
+
 template <typename T, int GS, int RT>
 __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
     linear_kernel(const __grid_constant__ CUtensorMap wmap, const FwdArgs a)
@@ -180,7 +192,9 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 p.set += gridDim.x;
             }
         };
+        unsigned issued = 0, arrived = 0;       // copies
         const auto fetch = [&](const Place &p, int slot) {
+            issued++;
             if (lane == 0) {
                 bar_expect_tx(full + 8 * slot, G::stage);
                 tma_load_2d(ring + slot * G::stage, &wmap, p.slice * 128,
@@ -259,6 +273,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                     ok = false;
                     *abort_flag = 1;
                 }
+                arrived += ok;
                 const uint32_t stage = ring + slot * G::stage;
 #pragma unroll
                 for (int r = 0; r < RT; r++) {
@@ -305,7 +320,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 // every lane's reads are done before the copy engine writes the stage
                 fence_async_shared();
                 __syncwarp();
-                if (filled.set < sets) {
+                if (ok && filled.set < sets) {
                     fetch(filled, slot);
                     advance(filled);
                 }
@@ -332,6 +347,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
             if (!buf)
                 red_parity ^= 1;
         }
+        drain(full, G::stages, arrived, issued);
     } else {
         // ------------------------------------------------------ add and store
         // Two neighbouring lanes' sums per thread: o = 16 (4 r + i) + lane / 2 is row
@@ -436,14 +452,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const T *dy = static_cast<const T *>(c.in);
     const int first = (rank * kWarps + warp) * 32, r_step = splits * kWarps * 32;
 
-    const auto fetch = [&](int r0, int slot) {      // one lane
-        bar_expect_tx(full + 8 * slot, kGradStage);
-        tma_load_2d(ring + slot * kGradStage, &wmap, col0 / 2, r0, full + 8 * slot);
+    unsigned issued = 0, arrived = 0;       // copies
+    const auto fetch = [&](int r0, int slot) {
+        issued++;
+        if (lane == 0) {
+            bar_expect_tx(full + 8 * slot, kGradStage);
+            tma_load_2d(ring + slot * kGradStage, &wmap, col0 / 2, r0, full + 8 * slot);
+        }
     };
-    if (lane == 0)
-        for (int i = 0; i < kGradStages; i++)
-            if (first + i * r_step < rows)
-                fetch(first + i * r_step, i);
+    for (int i = 0; i < kGradStages; i++)
+        if (first + i * r_step < rows)
+            fetch(first + i * r_step, i);
 
     // scales and zero points of a stage: lane l those of row l
     struct Meta {
@@ -523,6 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             *abort_flag = 1;
         }
+        arrived += ok;
         // w[ss][chunk of 32 columns][half]; row r's chunk p sits at p ^ (r / 2 % 4)
         const uint32_t stage = ring + slot * kGradStage;
         uint32_t w[2][4][2];
@@ -541,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // every lane's reads are done before the copy engine writes the stage
         fence_async_shared();
         __syncwarp();
-        if (lane == 0 && r0 + kGradStages * r_step < rows)
+        if (ok && r0 + kGradStages * r_step < rows)
             fetch(r0 + kGradStages * r_step, slot);
 #pragma unroll
         for (int ss = 0; ss < 2; ss++) {
@@ -580,6 +600,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
+    drain(full, kGradStages, arrived, issued);
     __syncthreads();        // the rings become the sums' buffer
 
     constexpr int kOut = 8 * kGradCols;
@@ -744,7 +765,8 @@ int record_success();
 namespace {
 
 constexpr int kFewTokens = 8;
-constexpr int kMaxRows = 1 << 20, kMaxCols = 1 << 16, kMaxTokens = 1 << 19;
+constexpr int kMaxRows = 1 << 20, kMaxCols = 1 << 16;
+constexpr int kMaxTokens = 8 * 65535;     // blocks of 8 tokens along a grid dimension
 
 // The byte range of n rows of `width` 2-byte elements, ld elements apart.
 bool overlap(const void *a, long long lda, int wa, const void *b, long long ldb, int wb, int n)
@@ -769,7 +791,7 @@ int run_linear(const W4Call &c, int dtype, int grad, void *stream)
         return record_failure(MOE_ERR_INVALID_ARG,
                               "cols must be a multiple of group_size in group_size..65536");
     if (c.n < 1 || c.n > kMaxTokens)
-        return record_failure(MOE_ERR_INVALID_ARG, "n_tokens must be in 1..524288");
+        return record_failure(MOE_ERR_INVALID_ARG, "n_tokens must be in 1..524280");
     const int win = grad ? w.rows : w.K, wout = grad ? w.K : w.rows;
     constexpr long long kMaxLd = 1LL << 31;
     if (c.ldi < win || c.ldo < wout || (c.residual && c.ldr < wout) || c.ldi > kMaxLd ||

@@ -734,9 +734,9 @@ Plan plan(int C, int F, int n, int grad, int num_sms, const int *clusters)
     const int mt = (F + kM - 1) / kM, steps = (C + 63) / 64;
     Plan best{};
     double least = 0;
-    for (int nt = (n + 255) / 256; nt <= (n + 15) / 16; nt++) {
-        const int tok = ((n + nt - 1) / nt + 15) / 16 * 16;
-        if ((n + tok - 1) / tok != nt)
+    for (int most = 256; most >= 16; most -= 16) {
+        const int nt = (n + most - 1) / most, tok = ((n + nt - 1) / nt + 15) / 16 * 16;
+        if (tok == best.tok)
             continue;
         for (int s = 1; s == 1 || (s <= kMaxSplits && tok <= 128 && 4 * s <= steps); s++) {
             const long long ctas = (long long)mt * nt * s;
@@ -751,8 +751,6 @@ Plan plan(int C, int F, int n, int grad, int num_sms, const int *clusters)
                 least = cost;
             }
         }
-        if (tok <= 32)
-            break;
     }
     return best;
 }

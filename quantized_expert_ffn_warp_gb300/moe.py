@@ -419,6 +419,16 @@ def _raw_stream(t, stream):
     return _types()[0]._C._cuda_getCurrentRawStream(index)
 
 
+def _new(torch, stream, like, *specs):
+    """New tensors (shape, dtype) on like's device, from the pool of the stream
+    that will write them."""
+    dev = like.device
+    if stream is None:
+        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt in specs]
+    with torch.cuda.stream(stream):
+        return [torch.empty(shape, dtype=dt, device=dev) for shape, dt in specs]
+
+
 def _types():
     """(torch, its types' codes), looked up once."""
     global _torch
@@ -464,7 +474,7 @@ def linear(x, codes, scales, zeros, group_size=GROUP, bias=None, residual=None, 
     n, dt = x.shape[0], x.dtype
     px, ldx = _rows(x, "x", dt, n, cols)
     if out is None:
-        out, ldy = torch.empty((n, rows), dtype=dt, device=x.device), rows
+        (out,), ldy = _new(torch, stream, x, ((n, rows), dt)), rows
         py = out.data_ptr()
     else:
         py, ldy = _rows(out, "out", dt, n, rows)
@@ -491,7 +501,7 @@ def linear_input_grad(dy, codes, scales, zeros, group_size=GROUP, out=None, stat
     n, dt = dy.shape[0], dy.dtype
     pd, ldd = _rows(dy, "dy", dt, n, rows)
     if out is None:
-        out, ldo = torch.empty((n, cols), dtype=dt, device=dy.device), cols
+        (out,), ldo = _new(torch, stream, dy, ((n, cols), dt)), cols
         po = out.data_ptr()
     else:
         po, ldo = _rows(out, "out", dt, n, cols)
@@ -536,20 +546,16 @@ def balance_loss(logits, topk_idx, seq_offsets=None, mask=None, stream=None):
     if topk_idx is None:
         _bad("topk_idx: need int32 [n, k]")
     n, E, k, S, code, pl, ld, pi, po, pm = _batch(torch, types, logits, topk_idx, seq_offsets, mask)
-    lib, dev, empty = load_library(), logits.device, torch.empty
-    f32, i32 = torch.float32, torch.int32
-    loss, lse = empty(2, dtype=f32, device=dev), empty(n, dtype=f32, device=dev)
-    prob = empty((S, E), dtype=f32, device=dev)
-    counts, tokens = empty((S, E), dtype=i32, device=dev), empty(S, dtype=i32, device=dev)
+    lib, f32, i32 = load_library(), torch.float32, torch.int32
     size = lib.moe_balance_workspace(n, E, S)
-    ws = empty(size, dtype=torch.uint8, device=dev)
+    loss, lse, prob, counts, tokens, ws = _new(
+        torch, stream, logits, ((2,), f32), ((n,), f32), ((S, E), f32), ((S, E), i32), ((S,), i32),
+        ((size,), torch.uint8))
     rc = lib.moe_balance_loss(pl, code, ld, n, E, pi, k, po, S, pm, loss.data_ptr(),
                               counts.data_ptr(), tokens.data_ptr(), prob.data_ptr(),
                               lse.data_ptr(), ws.data_ptr(), size, _raw_stream(logits, stream))
     if rc:
         _check(rc)
-    if stream is not None:      # the workspace is freed to its own stream's pool on return
-        ws.record_stream(stream)
     return dict(loss=loss, counts=counts, tokens=tokens, prob=prob, lse=lse)
 
 
@@ -570,7 +576,7 @@ def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, s
         pw = _dense(topk_w, "topk_w", f32, (n, k))
         pdw = _dense(dtopk_w, "dtopk_w", f32, (n, k))
     if out is None:
-        out, ldo = torch.empty((n, E), dtype=logits.dtype, device=logits.device), E
+        (out,), ldo = _new(torch, stream, logits, ((n, E), logits.dtype)), E
         pout = out.data_ptr()
     else:
         pout, ldo = _rows(out, "out", logits.dtype, n, E)

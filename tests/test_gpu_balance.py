@@ -328,3 +328,68 @@ def test_router_tuning_step():
     rel = (dx.double() - xr.grad).norm() / xr.grad.norm()
     assert rel <= 16 * 2.0 ** -11
     layer.close()
+
+
+@pytest.mark.parametrize("n,E,k,S", [(70000, 8, 2, 65535), (300000, 16, 4, 3), (4000, 1024, 32, 5),
+                                     (256, 512, 8, 4), (257, 512, 8, 4), (256, 513, 8, 4)])
+def test_largest_sizes(n, E, k, S):
+    """The most segments, many tokens, the widest rows, and both sides of the
+    one-launch limit."""
+    moe = _moe()
+    logits, idx, w = batch(n, E, k, 4)
+    g = torch.Generator(device="cuda").manual_seed(4)
+    cuts = torch.sort(torch.randint(0, n + 1, (S + 1,), device="cuda", generator=g)).values.int()
+    cuts = cuts.contiguous()
+    got = moe.balance_loss(logits, idx, cuts)
+    t = torch.arange(n, device="cuda", dtype=torch.int32)
+    seg = torch.searchsorted(cuts, t, right=True).long() - 1
+    live = (seg >= 0) & (seg < S)
+    p = torch.softmax(logits.double(), 1)
+    T = torch.zeros(S, dtype=torch.int64, device="cuda").index_add_(
+        0, seg[live], torch.ones_like(seg[live]))
+    assert torch.equal(got["tokens"].long(), T)
+    counts = torch.zeros(S * E, dtype=torch.int64, device="cuda")
+    flat = (seg[:, None] * E + idx.long())[live].reshape(-1)
+    counts.index_add_(0, flat, torch.ones_like(flat))
+    assert torch.equal(got["counts"].long().flatten(), counts)
+    prob = torch.zeros((S, E), dtype=torch.float64, device="cuda").index_add_(0, seg[live], p[live])
+    prob /= T.clamp(min=1)[:, None]
+    # a segment's sum: at most (tokens of a block per warp + warps + blocks) additions
+    terms = 104 + E + n // 8 + 700
+    assert ((got["prob"].double() - prob).abs() <= terms * H * prob + 1e-38).all()
+    f = counts.view(S, E).double() * E / (k * T.clamp(min=1)[:, None])
+    bal = (f * prob).sum() / (T > 0).sum()
+    lse = torch.logsumexp(logits.double(), 1)
+    z = (lse[live] ** 2).mean()
+    loss = got["loss"].double()
+    assert (loss[0] - bal).abs() <= 2 * terms * H * bal
+    assert (loss[1] - z).abs() <= 2 * terms * H * z + 1e-5 * H * n
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    dw = torch.ones((n, k), device="cuda") * torch.arange(k, device="cuda")
+    out = moe.balance_loss_grad(logits, idx, got, dloss, w, dw, cuts).double()
+    s = seg.clamp(0, S - 1)
+    gs = 0.7 / ((T > 0).sum() * T.clamp(min=1)[s]).double() * live
+    dot = (f[s] * p).sum(1, keepdim=True)
+    zt = (-0.6 * lse / T.sum() * live)[:, None]
+    ref = p * ((f[s] - dot) * gs[:, None] + zt)
+    size = p * ((f[s] + dot) * gs[:, None].abs() + zt.abs())
+    d = w.double() * (dw - (w.double() * dw).sum(1, keepdim=True)) * live[:, None]
+    ref = ref.scatter_add(1, idx.long(), d)
+    size = size.scatter_add(1, idx.long(), w.double() * (dw + (w.double() * dw).sum(1, keepdim=True)))
+    assert ((out - ref).abs() <= (2 * (104 + E) + 200) * H * size + 1e-38).all()
+
+
+def test_offsets_beyond_32_bits():
+    """Rows far enough apart that element offsets pass 2^32."""
+    moe = _moe()
+    n, E, k = 600, 24, 3
+    ld = (1 << 32) // (n - 1) + 64
+    logits, idx, w = batch(n, E, k, 6, torch.bfloat16)
+    far = torch.empty((n - 1) * ld + E, dtype=torch.bfloat16, device="cuda")
+    rows = far.as_strided((n, E), (ld, 1))
+    rows.copy_(logits)
+    near, got = moe.balance_loss(logits, idx), moe.balance_loss(rows, idx)
+    assert all(torch.equal(near[q], got[q]) for q in near)
+    dloss = torch.ones(2, device="cuda")
+    want = moe.balance_loss_grad(logits, idx, near, dloss, w, w)
+    assert torch.equal(moe.balance_loss_grad(rows, idx, got, dloss, w, w, out=rows), want)

@@ -231,3 +231,68 @@ def test_refusals_on_device():
                  lambda: moe.linear_input_grad(x, *m)):
         with pytest.raises(moe.MoeError):
             call()
+
+
+@pytest.mark.parametrize("n,rows,K,group", [
+    (3, 48, 65536, 128), (20, 48, 65536, 64), (2, 1 << 20, 32, 32), (40, 1 << 20, 32, 32),
+    (524280, 9, 32, 32), (8, 4864, 4352, 64), (5, 19500, 256, 128), (7, 40000, 1024, 32),
+])
+def test_largest_sizes(n, rows, K, group):
+    """Both ends of every range: the longest rows, the most rows, the most
+    tokens (dy with odd strides too), several row tiles per CTA."""
+    moe = _moe()
+    m, W = matrix(rows, K, group, seed=rows + K)
+    x = randn((n, K), torch.float16, 1)
+    S = x.double().abs() @ W.t().abs()
+    check(moe.linear(x, *m), x.double() @ W.t(), S, K, torch.float16)
+    dy = randn((n, rows), torch.float16, 2, 0.1)
+    ref, S = dy.double() @ W, dy.double().abs() @ W.abs()
+    check(moe.linear_input_grad(dy, *m), ref, S, rows, torch.float16)
+    if rows % 8:
+        check(moe.linear_input_grad(strided(dy, 8 - rows % 8), *m), ref, S, rows, torch.float16)
+
+
+@pytest.mark.parametrize("n", [4, 12])
+def test_offsets_beyond_32_bits(n):
+    """Rows far enough apart that element offsets pass 2^32."""
+    moe = _moe()
+    rows, K = 40, 128
+    ld = (1 << 32) // (n - 1) // 8 * 8 + 64
+    m, W = matrix(rows, K, 128, seed=1)
+    far = torch.empty((n - 1) * ld + K, dtype=torch.float16, device="cuda")
+    other = torch.empty((n - 1) * ld + K, dtype=torch.float16, device="cuda")
+    x = far.as_strided((n, K), (ld, 1))
+    out = other.as_strided((n, rows), (ld, 1))
+    x.copy_(randn((n, K), torch.float16, 1))
+    got = moe.linear(x, *m, out=out)
+    check(got, x.double() @ W.t(), x.double().abs() @ W.t().abs(), K, torch.float16)
+    dx = far.as_strided((n, K), (ld, 1))
+    want = got.double() @ W
+    S = got.double().abs() @ W.abs()
+    check(moe.linear_input_grad(got, *m, out=dx), want, S, rows, torch.float16)
+
+
+def test_results_on_another_stream_are_that_streams_memory():
+    """Outputs made for an explicit stream come from its pool: work still
+    pending on the current stream cannot own them."""
+    moe = _moe()
+    m, W = matrix(256, 512, 128, seed=1)
+    x = randn((4, 512), torch.float16, 1)
+    want, dwant = moe.linear(x, *m), moe.linear_input_grad(x[:, :256].contiguous(), *m)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        junk = torch.full((4, 256), 7.0, dtype=torch.float16, device="cuda")
+        busy = torch.randn(2048, 2048, device="cuda")
+        for _ in range(4):
+            busy = busy @ busy * 1e-3
+        junk.mul_(2)            # pending behind the products on the current stream
+        del junk
+        y = moe.linear(x, *m, stream=side)
+        side.synchronize()
+        first = y.clone()
+        torch.cuda.synchronize()
+        assert torch.equal(first, want) and torch.equal(y, want)
+    dx = moe.linear_input_grad(x[:, :256].contiguous(), *m, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(dx, dwant)
