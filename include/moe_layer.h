@@ -430,13 +430,20 @@ int moe_linear(const void *codes, const void *scales, const void *zeros, int row
  * lddy, lddx; each weight is rounded once to that type, sums are fp32.  (The
  * gradient of bias is the sum of dy over the tokens, that of residual dy.)
  * Pointers as for moe_linear; codes 16-byte aligned, dy and dx to their
- * element (16-byte aligned rows of dy take the faster kernel when there are
- * many tokens).  dx must not overlap dy.
+ * element.  dx must not overlap dy.
+ * More than 8 rows of dy that do not lie on 16-byte boundaries (an odd number of
+ * rows, for one) are first copied into `workspace`, a 16-byte aligned device
+ * buffer of moe_linear_input_grad_workspace(rows, n_tokens, dy, lddy) bytes, in
+ * use until the call's work is done; with less (or NULL) the product still
+ * runs, 8 tokens per pass over the matrix.  That size is 0 where no copy is
+ * needed.
  * Errors: those of moe_linear.
  */
+size_t moe_linear_input_grad_workspace(int rows, int n_tokens, const void *dy, long long lddy);
 int moe_linear_input_grad(const void *codes, const void *scales, const void *zeros, int rows,
                           int cols, int group_size, const void *dy, long long lddy, int n_tokens,
-                          int dtype, void *dx, long long lddx, int *status, void *stream);
+                          int dtype, void *dx, long long lddx, void *workspace,
+                          size_t workspace_bytes, int *status, void *stream);
 
 /*
  * Routing losses of a batch of router logits (moe_router_logits) and their

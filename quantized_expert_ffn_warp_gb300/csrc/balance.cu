@@ -41,14 +41,6 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-__device__ __forceinline__ float warp_max(float v)
-{
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-    return v;
-}
-
 // A pair of values as one word (or two), so that it is loaded and stored whole.
 template <typename T>
 struct Pair {

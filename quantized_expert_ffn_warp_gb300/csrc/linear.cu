@@ -776,7 +776,25 @@ bool overlap(const void *a, long long lda, int wa, const void *b, long long ldb,
     return p < q + nb && q < p + na;
 }
 
-int run_linear(const W4Call &c, int dtype, int grad, void *stream)
+// Rows of 2-byte elements, `ld` apart, to rows `ldo` apart (a multiple of 8
+// elements), the gap filled with zeros: a plain coalesced copy, bound by its
+// latency at the sizes it serves.
+__global__ void __launch_bounds__(256) realign_kernel(const uint16_t *__restrict__ in, long long ld,
+                                                      int width, uint16_t *__restrict__ out, int ldo)
+{
+    pdl_enter();
+    const uint16_t *src = in + blockIdx.x * ld;
+    uint16_t *dst = out + (long long)blockIdx.x * ldo;
+#pragma unroll 8
+    for (int i = blockIdx.y * 2048 + threadIdx.x; i < min(ldo, (int)(blockIdx.y + 1) * 2048); i += 256)
+        dst[i] = i < width ? src[i] : 0;
+}
+
+// Elements per row, and bytes, of an aligned copy of n rows.
+int aligned_ld(int width) { return (width + 7) / 8 * 8; }
+size_t aligned_bytes(int width, int n) { return 2 * (size_t)aligned_ld(width) * n; }
+
+int run_linear(W4Call c, int dtype, int grad, void *workspace, size_t workspace_bytes, void *stream)
 {
     const W4Matrix &w = c.w;
     if (!w.codes || !w.scales || !w.zeros || !c.in || !c.out)
@@ -811,22 +829,35 @@ int run_linear(const W4Call &c, int dtype, int grad, void *stream)
         overlap(c.out, c.ldo, wout, c.residual, c.ldr, wout, c.n))
         return record_failure(MOE_ERR_INVALID_ARG,
                               "y overlaps residual (it may be residual itself)");
+    const bool copy = grad && c.n > kFewTokens && !linear_gemm_fits(c) && workspace &&
+                      workspace_bytes >= aligned_bytes(w.rows, c.n);
+    if (copy && mis(workspace, 16))
+        return record_failure(MOE_ERR_INVALID_ARG, "misaligned workspace (it needs 16 bytes)");
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {
         cudaGetLastError();
         return record_failure(MOE_ERR_CUDA, "no usable current CUDA device");
     }
-    const void *all[] = {w.codes, w.scales, w.zeros, c.in, c.out, c.bias, c.residual, c.status};
+    const void *all[] = {w.codes, w.scales, w.zeros, c.in, c.out, c.bias, c.residual, c.status,
+                         copy ? workspace : nullptr};
     for (const void *p : all)
         if (p && !device_pointer_here(p, dev))
             return record_failure(MOE_ERR_INVALID_ARG,
                                   "arguments must be device pointers of the current device");
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    cudaError_t e;
-    if (c.n > kFewTokens && linear_gemm_fits(c))
+    cudaError_t e = cudaSuccess;
+    if (copy) {
+        const int ldo = aligned_ld(w.rows);
+        e = launch_pdl(realign_kernel, dim3(c.n, (ldo + 2047) / 2048), dim3(256), 0, st,
+                       static_cast<const uint16_t *>(c.in), c.ldi, w.rows,
+                       static_cast<uint16_t *>(workspace), ldo);
+        c.in = workspace;
+        c.ldi = ldo;
+    }
+    if (e == cudaSuccess && c.n > kFewTokens && linear_gemm_fits(c))
         e = launch_linear_gemm(c, dtype == MOE_BF16, grad, dev, sms, st);
-    else
+    else if (e == cudaSuccess)
         e = dtype == MOE_FP16 ? launch_group_size<__half>(c, grad, dev, sms, st)
                               : launch_group_size<__nv_bfloat16>(c, grad, dev, sms, st);
     if (e != cudaSuccess) {
@@ -857,13 +888,14 @@ extern "C" int moe_linear(const void *codes, const void *scales, const void *zer
     c.out = y;
     c.ldo = ldy;
     c.status = status;
-    return qe::run_linear(c, dtype, 0, stream);
+    return qe::run_linear(c, dtype, 0, nullptr, 0, stream);
 }
 
 extern "C" int moe_linear_input_grad(const void *codes, const void *scales, const void *zeros,
                                      int rows, int cols, int group_size, const void *dy,
                                      long long lddy, int n_tokens, int dtype, void *dx,
-                                     long long lddx, int *status, void *stream)
+                                     long long lddx, void *workspace, size_t workspace_bytes,
+                                     int *status, void *stream)
 {
     qe::W4Call c{};
     c.w = {static_cast<const uint8_t *>(codes), static_cast<const uint16_t *>(scales),
@@ -874,5 +906,17 @@ extern "C" int moe_linear_input_grad(const void *codes, const void *scales, cons
     c.out = dx;
     c.ldo = lddx;
     c.status = status;
-    return qe::run_linear(c, dtype, 1, stream);
+    return qe::run_linear(c, dtype, 1, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t moe_linear_input_grad_workspace(int rows, int n_tokens, const void *dy,
+                                                  long long lddy)
+{
+    qe::W4Call c{};
+    c.in = dy;
+    c.ldi = lddy;
+    if (rows < 1 || rows > qe::kMaxRows || n_tokens <= qe::kFewTokens ||
+        n_tokens > qe::kMaxTokens || qe::linear_gemm_fits(c))
+        return 0;
+    return qe::aligned_bytes(rows, n_tokens);
 }

@@ -384,7 +384,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         __syncwarp();
     } else {
         // -------------------------------------------------------- dequant
-        const int q = warp & 3, wg = warp >> 2, g = lane >> 2, tq = lane & 3;
+        const int q = warp & 3, wg = warp >> 2, tq = lane & 3;
         const uint32_t tlane = (uint32_t)(32 * q) << 16;
         const int ng = c.w.K / c.w.group, gsh = c.w.group == 128 ? 7 : c.w.group == 64 ? 6 : 5;
         const int per_blk = kBlk / c.w.group;       // groups along 128 K

@@ -36,7 +36,8 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_route_topk", "moe_route
            "moe_route_topk_noalloc", "moe_layer_set_gemm_min_tokens", "moe_rmsnorm",
            "moe_forward_prenorm", "moe_copy", "moe_layer_set_residency", "moe_residency_plan",
            "moe_layer_tier_stats", "moe_layer_tier_slots", "moe_ep_dispatch", "moe_ep_combine",
-           "moe_linear", "moe_linear_input_grad", "moe_balance_workspace", "moe_balance_loss",
+           "moe_linear", "moe_linear_input_grad", "moe_linear_input_grad_workspace",
+           "moe_balance_workspace", "moe_balance_loss",
            "moe_balance_loss_grad")
 
 
@@ -104,7 +105,9 @@ def load_library(path: str = LIB_PATH):
     lib.moe_ep_combine.argtypes = [P, I, I, I, P, P, P, P, P, I, P, P]
     L, Z = C.c_longlong, C.c_size_t
     lib.moe_linear.argtypes = [P, P, P, I, I, I, P, L, I, I, P, P, L, P, L, P, P]
-    lib.moe_linear_input_grad.argtypes = [P, P, P, I, I, I, P, L, I, I, P, L, P, P]
+    lib.moe_linear_input_grad.argtypes = [P, P, P, I, I, I, P, L, I, I, P, L, P, Z, P, P]
+    lib.moe_linear_input_grad_workspace.argtypes = [I, I, P, L]
+    lib.moe_linear_input_grad_workspace.restype = Z
     lib.moe_balance_workspace.argtypes = [I, I, I]
     lib.moe_balance_workspace.restype = Z
     lib.moe_balance_loss.argtypes = [P, I, L, I, I, P, I, P, I, P, P, P, P, P, P, P, Z, P]
@@ -506,9 +509,14 @@ def linear_input_grad(dy, codes, scales, zeros, group_size=GROUP, out=None, stat
     else:
         po, ldo = _rows(out, "out", dt, n, cols)
     pst = None if status is None else _dense(status, "status", torch.int32, (1,))
-    rc = load_library().moe_linear_input_grad(pc, ps, pz, rows, cols, group_size, pd, ldd, n,
-                                              _code_of(dt, types), po, ldo, pst,
-                                              _raw_stream(dy, stream))
+    lib, ws, size = load_library(), None, 0
+    if n > 8 and (ldd % 8 or pd % 16):
+        size = lib.moe_linear_input_grad_workspace(rows, n, pd, ldd)
+        (ws,) = _new(torch, stream, dy, ((size,), torch.uint8))
+    rc = lib.moe_linear_input_grad(pc, ps, pz, rows, cols, group_size, pd, ldd, n,
+                                   _code_of(dt, types), po, ldo,
+                                   None if ws is None else ws.data_ptr(), size, pst,
+                                   _raw_stream(dy, stream))
     if rc:
         _check(rc)
     return out

@@ -296,3 +296,19 @@ def test_results_on_another_stream_are_that_streams_memory():
     dx = moe.linear_input_grad(x[:, :256].contiguous(), *m, stream=side)
     torch.cuda.synchronize()
     assert torch.equal(dx, dwant)
+
+
+@pytest.mark.parametrize("n", [9, 40, 700])
+def test_gradient_without_a_workspace(n):
+    """Unaligned gradients through the C call without the workspace: the same
+    product, several passes over the matrix."""
+    moe = _moe()
+    rows, K = 301, 640
+    (codes, scales, zeros, group), W = matrix(rows, K, 128, seed=3)
+    dy = randn((n, rows), torch.bfloat16, 2)
+    dx = torch.empty((n, K), dtype=torch.bfloat16, device="cuda")
+    rc = moe.load_library().moe_linear_input_grad(
+        codes.data_ptr(), scales.data_ptr(), zeros.data_ptr(), rows, K, group, dy.data_ptr(), rows,
+        n, moe.MOE_BF16, dx.data_ptr(), K, None, 0, None, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    check(dx, dy.double() @ W, dy.double().abs() @ W.abs(), rows, torch.bfloat16)

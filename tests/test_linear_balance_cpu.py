@@ -28,11 +28,12 @@ def linear(lib, **kw):
 
 
 def linear_grad(lib, **kw):
-    a = dict(LIN, x=0x40000, ldx=96, y=0x50000, ldy=256)
+    a = dict(LIN, x=0x40000, ldx=96, y=0x50000, ldy=256, ws=None, ws_bytes=0)
     a.update(kw)
     return lib.moe_linear_input_grad(P(a["codes"]), P(a["scales"]), P(a["zeros"]), a["rows"],
                                      a["cols"], a["group"], P(a["x"]), L(a["ldx"]), a["n"],
-                                     a["dtype"], P(a["y"]), L(a["ldy"]), P(a["status"]), None)
+                                     a["dtype"], P(a["y"]), L(a["ldy"]), P(a["ws"]), Z(a["ws_bytes"]),
+                                     P(a["status"]), None)
 
 
 BOTH = [
@@ -56,7 +57,10 @@ def test_linear_refuses(lib, kw, code):
     assert linear(lib, **kw) == code and lib.moe_last_error().decode()
 
 
-@pytest.mark.parametrize("kw,code", BOTH + [(dict(x=0x40001), -1)])
+@pytest.mark.parametrize("kw,code", BOTH + [
+    (dict(x=0x40001), -1),
+    (dict(n=20, rows=95, ldx=95, ws=0x80008, ws_bytes=96 * 40), -1),
+])
 def test_linear_input_grad_refuses(lib, kw, code):
     assert linear_grad(lib, **kw) == code and lib.moe_last_error().decode()
 
@@ -112,6 +116,14 @@ def test_balance_loss_refuses(lib, kw, code):
 ])
 def test_balance_loss_grad_refuses(lib, kw, code):
     assert balance_grad(lib, **kw) == code and lib.moe_last_error().decode()
+
+
+def test_linear_input_grad_workspace_sizes(lib):
+    ws = lib.moe_linear_input_grad_workspace
+    assert ws(96, 8, P(0x40002), L(97)) == 0 and ws(96, 20, P(0x40000), L(96)) == 0
+    assert ws(97, 20, P(0x40000), L(97)) == 20 * 104 * 2
+    assert ws(96, 20, P(0x40002), L(96)) == 20 * 96 * 2
+    assert ws(0, 20, P(0x40002), L(97)) == 0 and ws(97, 1 << 20, P(0x40002), L(97)) == 0
 
 
 def test_balance_workspace_sizes(lib):
