@@ -52,7 +52,10 @@ struct LGeo {
     static constexpr int a_cols = 32;                   // 64 contraction elements, two per column
     static constexpr int b_stage = TOK * 128;           // TOK rows of 64 elements
     // A and B stages (64 contraction elements each), in lockstep
-    static constexpr int as = TOK > 128 ? 5 : TOK > 64 ? 8 : 12;
+    static constexpr int as = TOK > 128 ? 5 : TOK > 64 ? 7 : 12;
+    // tensor-memory columns behind the A stages: the residual of the tokens from
+    // 64 on, two per column
+    static constexpr int res0 = acc_cols + as * a_cols, res_cols = (TOK - 64) / 2;
     // code blocks: a multiple of the groups, so that a group always reads the same ones
     static constexpr int cs = TOK > 64 ? 6 : 12;
     static constexpr int b_off = 0, c_off = as * b_stage;
@@ -68,7 +71,7 @@ template <int TOK, bool GRAD>
 constexpr bool lgeo_ok()
 {
     using G = LGeo<TOK, GRAD>;
-    return G::smem <= 227 * 1024 && G::acc_cols + G::as * G::a_cols <= 512 && G::cs % kGroups == 0 && G::as >= 5 &&
+    return G::smem <= 227 * 1024 && G::res0 + G::res_cols <= 512 && G::cs % kGroups == 0 && G::as >= 5 &&
            (TOK > 128 || 128 * TOK * 4 <= G::c_off);    // a partial tile fits in the B stages
 }
 static_assert(lgeo_ok<256, false>() && lgeo_ok<128, false>() && lgeo_ok<64, false>() &&
@@ -80,6 +83,7 @@ struct GemmCall {
     int tok;            // tokens per tile: a multiple of 16, at most TOK
     int mt, nt;         // tiles along the features and the tokens
     int splits;         // CTAs of a cluster along the contraction
+    int vec_meta;       // a row's scales and zero points of 128 K allow vector loads
 };
 
 // 16 lanes x 32 columns from the warp's registers, 16x256b layout: of every 8
@@ -112,6 +116,28 @@ template <typename S>
 struct alignas(2 * sizeof(S)) ScalePair {
     S a, b;
 };
+
+// 16 columns to, and 8 from, this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+          "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+          "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]),
+                   "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
 
 template <typename T>
 __device__ __forceinline__ void store_out(const W4Call &c, float v, int tok, int f)
@@ -324,11 +350,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const int q = warp & 3;
         unsigned ti = 0;
         for (int t = tile0; t < tiles && ok; t += tile_step, ti++) {
-            if (!warp_wait(acc_full, ti & 1, abort_flag)) {
-                ok = false;
-                break;
-            }
-            tc_fence_after();
             const int f = t % a.mt * kM + lane_feature<GRAD>(32 * q + lane);
             const int tok0 = t / a.mt * a.tok;
             const uint32_t taddr = tmem + ((uint32_t)(32 * q) << 16);
@@ -339,8 +360,42 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const bool in = f < F;
             const float bias = c.bias && in ? Q::to_float(static_cast<const T *>(c.bias)[f]) : 0.f;
             T *out = static_cast<T *>(c.out) + tok0 * c.ldo + f;
-            const T *res = static_cast<const T *>(c.residual) + (c.residual ? tok0 * c.ldr + f : 0);
-            for (int c0 = 0; c0 < cols; c0 += 16) {
+            // The residual is read while the tile is still multiplied (with the
+            // next tile's operands under way a load would take microseconds in the
+            // epilogue): 64 tokens into registers, the others, as pairs, into
+            // tensor-memory columns of their own.
+            const bool add = !GRAD && c.residual && a.splits == 1;
+            uint32_t held[2][16];
+            if (add) {
+                const T *res = static_cast<const T *>(c.residual) + tok0 * c.ldr + f;
+                const auto load32 = [&](int c0, uint32_t (&h)[16]) {
+                    uint16_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        v[i] = 0;
+                        if (in && c0 + i < cols)
+                            v[i] = *reinterpret_cast<const uint16_t *>(res + (c0 + i) * c.ldr);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 16; i++)
+                        h[i] = v[2 * i] | (uint32_t)v[2 * i + 1] << 16;
+                };
+                for (int c0 = 64; c0 < cols; c0 += 32) {
+                    load32(c0, held[0]);
+                    __syncwarp();
+                    tmem_st16(taddr + G::res0 + (c0 - 64) / 2, held[0]);
+                }
+                load32(0, held[0]);
+                load32(32, held[1]);
+                __syncwarp();
+            }
+            if (!warp_wait(acc_full, ti & 1, abort_flag)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            // 16 tokens' sums, with 8 words of their residual, to the output
+            const auto finish = [&](int c0, const uint32_t (&h)[8]) {
                 float d[16], e[16];
                 tmem_ld16(taddr + c0, d);
                 if (two) {
@@ -349,18 +404,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     for (int i = 0; i < 16; i++)
                         d[i] += e[i];
                 }
-                if (a.splits > 1) {
+                if (a.splits > 1) {     // uniform over the grid
 #pragma unroll
                     for (int i = 0; i < 16; i++)
                         part[(c0 + i) * kM] = d[i];
-                    continue;       // uniform over the grid
+                    return;
                 }
                 const int left = in ? cols - c0 : 0;
-                if (c.residual) {
+                if (add) {
 #pragma unroll
-                    for (int i = 0; i < 16; i++, res += c.ldr)
-                        if (i < left)
-                            d[i] += Q::to_float(*res);
+                    for (int i = 0; i < 8; i++) {
+                        d[2 * i] += Q::low(h[i]);
+                        d[2 * i + 1] += Q::high(h[i]);
+                    }
                 }
                 if (left >= 16) {
 #pragma unroll
@@ -373,6 +429,21 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             *out = Q::from_float(d[i] + bias);
                 }
                 __syncwarp();
+            };
+#pragma unroll
+            for (int u = 0; u < 4; u++)
+                if (16 * u < cols) {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        h[i] = held[u >> 1][8 * (u & 1) + i];
+                    finish(16 * u, h);
+                }
+            for (int c0 = 64; c0 < cols; c0 += 16) {
+                uint32_t h[8];
+                if (add)
+                    tmem_ld8(taddr + G::res0 + (c0 - 64) / 2, h);
+                finish(c0, h);
             }
             tc_fence_before();
             __syncwarp();
@@ -395,19 +466,41 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         // first touched a block later: a warp stalls on a loaded value where it
         // is used.
         struct Meta {
-            uint32_t s[4], z[4];
+            uint32_t s[2], z;       // group j's scale in half j, zero point in byte j
+            __device__ __forceinline__ uint32_t scale(int j) const
+            {
+                return j & 1 ? s[j >> 1] >> 16 : s[j >> 1] & 0xffff;
+            }
+            __device__ __forceinline__ uint32_t zero(int j) const { return z >> (8 * j) & 0xff; }
         };
         const auto load_meta = [&](int m0, int b, Meta &m) {
             const int row = (GRAD ? b * kBlk : m0) + r;
             const int g0 = (GRAD ? m0 : b * kBlk) >> gsh;
-            const long long at = (long long)row * ng + g0;
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                m.s[j] = m.z[j] = 0;
-                if (j < per_blk && g0 + j < ng && row < c.w.rows) {
-                    m.s[j] = c.w.scales[at + j];
-                    m.z[j] = c.w.zeros[at + j];
+            m.s[0] = m.s[1] = m.z = 0;
+            if (row >= c.w.rows)
+                return;
+            const uint16_t *sp = c.w.scales + (long long)row * ng + g0;
+            const uint8_t *zp = c.w.zeros + (long long)row * ng + g0;
+            if (per_blk == 1) {
+                m.s[0] = *sp;       // g0 < ng: a block begins inside the matrix
+                m.z = *zp;
+            } else if (a.vec_meta) {
+                if (per_blk == 2) {
+                    m.s[0] = *reinterpret_cast<const uint32_t *>(sp);
+                    m.z = *reinterpret_cast<const uint16_t *>(zp);
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2 *>(sp);
+                    m.s[0] = v.x;
+                    m.s[1] = v.y;
+                    m.z = *reinterpret_cast<const uint32_t *>(zp);
                 }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; j++)
+                    if (j < per_blk && g0 + j < ng) {
+                        m.s[j >> 1] |= (uint32_t)sp[j] << (16 * (j & 1));
+                        m.z |= (uint32_t)zp[j] << (8 * j);
+                    }
             }
         };
         // this group's place in the CTA's blocks: every kGroups-th one of them
@@ -450,12 +543,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 4; j++)
                     if (j < per_blk) {      // a row pair's two words, one by each of its lanes
-                        const uint32_t s2 = __shfl_xor_sync(0xffffffffu, meta.s[j], 1);
-                        const uint32_t z2 = __shfl_xor_sync(0xffffffffu, meta.z[j], 1);
+                        const uint32_t s1 = meta.scale(j), z1 = meta.zero(j);
+                        const uint32_t s2 = __shfl_xor_sync(0xffffffffu, s1, 1);
+                        const uint32_t z2 = __shfl_xor_sync(0xffffffffu, z1, 1);
                         if (lane & 1)
-                            sw[64 * j + (r >> 1)] = Q::scale(s2, meta.s[j]);
+                            sw[64 * j + (r >> 1)] = Q::scale(s2, s1);
                         else
-                            zw[64 * j + (r >> 1)] = Q::zero(meta.z[j], z2).lo;
+                            zw[64 * j + (r >> 1)] = Q::zero(z1, z2).lo;
                     }
             }
             bool have = ok && warp_wait(code_full + 8 * s, (cc / G::cs) & 1, abort_flag);
@@ -473,13 +567,6 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 for (int i = 0; i < 4; i++)
                     cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
                                                              ((i ^ ((r >> 1) & 3)) << 4));
-                // every quarter of the block its group's
-#pragma unroll
-                for (int j = 3; j > 0; j--) {
-                    const int from = c.w.group == 128 ? 0 : c.w.group == 64 ? j / 2 : j;
-                    meta.s[j] = from == 0 ? meta.s[0] : from == 1 ? meta.s[1] : meta.s[j];
-                    meta.z[j] = from == 0 ? meta.z[0] : from == 1 ? meta.z[1] : meta.z[j];
-                }
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(code_empty + 8 * s);
@@ -493,7 +580,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 if (!GRAD) {
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        const uint32_t zb = meta.z[2 * h + i], sb = meta.s[2 * h + i];
+                        // quarter 2 h + i of the block: its group's
+                        const int j = 2 * h + i;
+                        const uint32_t zb = per_blk == 1   ? meta.zero(0)
+                                            : per_blk == 2 ? meta.zero(j / 2)
+                                                           : meta.zero(j);
+                        const uint32_t sb = per_blk == 1   ? meta.scale(0)
+                                            : per_blk == 2 ? meta.scale(j / 2)
+                                                           : meta.scale(j);
                         const typename Q::Zero z = Q::zero(zb, zb);
                         const typename Q::Scale sc = Q::scale(sb, sb);
                         const uint4 v = cw[2 * h + i];
@@ -806,7 +900,9 @@ cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int
 {
     const int C = grad ? c.w.rows : c.w.K, F = grad ? c.w.K : c.w.rows;
     const Plan p = plan(C, F, c.n, grad, num_sms, cluster_table(dev));
-    GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits};
+    const int vec_meta = c.w.K % 128 == 0 && reinterpret_cast<uintptr_t>(c.w.scales) % 8 == 0 &&
+                         reinterpret_cast<uintptr_t>(c.w.zeros) % 4 == 0;
+    GemmCall a{c, p.tok, (F + kM - 1) / kM, p.nt, p.splits, vec_meta};
     CUtensorMap wmap, bmap;
     if (!encode_map(&wmap, CU_TENSOR_MAP_DATA_TYPE_UINT8, c.w.codes, c.w.K / 2, c.w.rows, c.w.K / 2, 64,
                 128, CU_TENSOR_MAP_SWIZZLE_64B) ||

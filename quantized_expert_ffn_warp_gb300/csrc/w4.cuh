@@ -73,6 +73,8 @@ struct W4<__half> {
     {
         return u(__hmul2(h(v), h(s0 | (s1 << 16))));
     }
+    static __device__ __forceinline__ float low(uint32_t v) { return __low2float(h(v)); }
+    static __device__ __forceinline__ float high(uint32_t v) { return __high2float(h(v)); }
     static __device__ __forceinline__ float to_float(__half v) { return __half2float(v); }
     static __device__ __forceinline__ __half from_float(float v) { return __float2half_rn(v); }
 };
@@ -123,6 +125,8 @@ struct W4<__nv_bfloat16> {
             f.x * __half2float(__ushort_as_half((unsigned short)s0)),
             f.y * __half2float(__ushort_as_half((unsigned short)s1))));
     }
+    static __device__ __forceinline__ float low(uint32_t v) { return __low2float(h(v)); }
+    static __device__ __forceinline__ float high(uint32_t v) { return __high2float(h(v)); }
     static __device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
     static __device__ __forceinline__ __nv_bfloat16 from_float(float v) { return __float2bfloat16_rn(v); }
 };
