@@ -745,11 +745,15 @@ template <typename T, int V>
 cudaError_t launch_stats(const FwdArgs &a, cudaStream_t st)
 {
     if (V <= 16 && one_block(a.n, a.E, a.segs.S)) {
-        auto kernel = balance_stats_kernel<T, V <= 16 ? V : 16, true>;
+        constexpr int VO = V <= 16 ? V : 16;
+        auto kernel = balance_stats_kernel<T, VO, true>;
         const size_t smem = sizeof(float) * (kOneWarps + 1) * a.E;
-        if (smem > 48 * 1024) {
+        // the kernel's largest, whatever this call needs: a smaller value set
+        // by one call would fail a larger one on another thread
+        constexpr size_t most = sizeof(float) * (kOneWarps + 1) * 32 * VO;
+        if (most > 48 * 1024) {
             const cudaError_t e = cudaFuncSetAttribute(
-                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+                kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
             if (e != cudaSuccess)
                 return e;
         }
