@@ -29,6 +29,7 @@
 // caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "tcgen05.cuh"
 #include "w4.cuh"
@@ -395,7 +396,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             }
             tc_fence_after();
             // 16 tokens' sums, with 8 words of their residual, to the output
-            const auto finish = [&](int c0, const uint32_t (&h)[8]) {
+            const auto finish = [&](int c0, auto with, const uint32_t (&h)[8]) {
                 float d[16], e[16];
                 tmem_ld16(taddr + c0, d);
                 if (two) {
@@ -411,7 +412,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     return;
                 }
                 const int left = in ? cols - c0 : 0;
-                if (add) {
+                if (with.value) {
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
                         d[2 * i] += Q::low(h[i]);
@@ -430,20 +431,25 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 __syncwarp();
             };
+            if (!add) {
+                const uint32_t none[8] = {};
+                for (int c0 = 0; c0 < cols; c0 += 16)
+                    finish(c0, std::false_type(), none);
+            } else {
 #pragma unroll
-            for (int u = 0; u < 4; u++)
-                if (16 * u < cols) {
+                for (int u = 0; u < 4; u++)
+                    if (16 * u < cols) {
+                        uint32_t h[8];
+#pragma unroll
+                        for (int i = 0; i < 8; i++)
+                            h[i] = held[u >> 1][8 * (u & 1) + i];
+                        finish(16 * u, std::true_type(), h);
+                    }
+                for (int c0 = 64; c0 < cols; c0 += 16) {
                     uint32_t h[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        h[i] = held[u >> 1][8 * (u & 1) + i];
-                    finish(16 * u, h);
-                }
-            for (int c0 = 64; c0 < cols; c0 += 16) {
-                uint32_t h[8];
-                if (add)
                     tmem_ld8(taddr + G::res0 + (c0 - 64) / 2, h);
-                finish(c0, h);
+                    finish(c0, std::true_type(), h);
+                }
             }
             tc_fence_before();
             __syncwarp();
