@@ -199,12 +199,12 @@ struct BalanceWs {
     size_t bytes;
 };
 
-// Tokens of a block: about four blocks per SM of the largest parts, and at
-// least one token per warp.
-int block_tokens(int n)
+// Tokens of a block: as many blocks as run at once on the 152 SMs (four per SM,
+// two and one for the widest rows), and at least one token per warp.
+int block_tokens(int n, int E)
 {
-    const int per = (n + 607) / 608;
-    return (std::max(per, 1) + kWarps - 1) / kWarps * kWarps;
+    const int blocks = 152 * (E <= 256 ? 4 : E <= 512 ? 2 : 1);
+    return ((n + blocks - 1) / blocks + kWarps - 1) / kWarps * kWarps;
 }
 
 // Whether one CTA of kOneWarps warps handles the whole batch: it takes about a
@@ -215,7 +215,7 @@ bool one_block(int n, int E, int S) { return n <= 8 * kOneWarps && E <= 512 && S
 
 BalanceWs balance_ws(void *base, int n, int E, int S)
 {
-    const int C = block_tokens(n);
+    const int C = block_tokens(n, E);
     const size_t slots = (size_t)(n + C - 1) / C + S;
     BalanceWs w{};
     char *b = static_cast<char *>(base);
@@ -254,7 +254,7 @@ struct FwdArgs {
 // the tokens, so a slot belongs to one pair.  ONE: the block is the batch and
 // writes the results themselves.
 template <typename T, int V, bool ONE>
-__global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : 0)
+__global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : V <= 8 ? 4 : V <= 16 ? 2 : 1)
     balance_stats_kernel(FwdArgs a)
 {
     constexpr int NW = ONE ? kOneWarps : kWarps, NT = 32 * NW;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : 0)
     int all = 0, segs = 0;
 
     // U tokens at a time: one's reductions run in the other's shadow
-    constexpr int U = V <= 16 ? 2 : 1;
+    constexpr int U = V <= (ONE ? 8 : 16) ? 2 : 1;
     struct Token {
         R row;
         int id;
@@ -917,7 +917,7 @@ extern "C" int moe_balance_loss(const void *logits, int dtype, long long ld, int
     a.n = n_tokens;
     a.E = n_experts;
     a.k = top_k;
-    a.C = one_block(n_tokens, n_experts, n_segments) ? n_tokens : block_tokens(n_tokens);
+    a.C = one_block(n_tokens, n_experts, n_segments) ? n_tokens : block_tokens(n_tokens, n_experts);
     a.wide = pairs(logits, ld, n_experts, size_of(dtype));
     a.loss = loss;
     a.counts = counts;
