@@ -573,6 +573,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 for (int i = 0; i < 4; i++)
                     cw[i] = *reinterpret_cast<const uint4 *>(blk + r * 64 +
                                                              ((i ^ ((r >> 1) & 3)) << 4));
+                // the codes are in registers before the copy engine writes the block
+                // again: without the fence these reads may still be on their way
+                fence_async_shared();
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(code_empty + 8 * s);
@@ -648,6 +651,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                         }
                     }
                     if (h + 1 == steps) {
+                        fence_async_shared();       // as above
                         __syncwarp();
                         if (lane == 0)
                             bar_arrive(code_empty + 8 * s);

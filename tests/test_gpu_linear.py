@@ -312,3 +312,27 @@ def test_gradient_without_a_workspace(n):
         n, moe.MOE_BF16, dx.data_ptr(), K, None, 0, None, torch.cuda.current_stream().cuda_stream)
     assert rc == 0
     check(dx, dy.double() @ W, dy.double().abs() @ W.abs(), rows, torch.bfloat16)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,rows,K,group", [
+    (33, 6144, 4096, 64), (200, 4096, 4096, 32), (200, 4096, 4096, 64), (120, 4096, 4096, 128),
+    (300, 4096, 2048, 32), (8, 4096, 14336, 64), (3, 9000, 4096, 32),
+])
+def test_pipelines_at_length(n, rows, K, group, dtype):
+    """Long contractions back to back, where every ring turns over many times
+    and all SMs compete for memory: each of 30 calls in turn over three sets
+    of inputs is within the bounds, and the same inputs give the same bits."""
+    moe = _moe()
+    sets = []
+    for i in range(3):
+        m, W = matrix(rows, K, group, seed=i)
+        x, dy = randn((n, K), DT[dtype], i), randn((n, rows), DT[dtype], 9 + i, 0.1)
+        sets.append((m, x, dy, moe.linear(x, *m), moe.linear_input_grad(dy, *m)))
+        check(sets[-1][3], x.double() @ W.t(), x.double().abs() @ W.t().abs(), K, DT[dtype])
+        check(sets[-1][4], dy.double() @ W, dy.double().abs() @ W.abs(), rows, DT[dtype])
+        del W
+    again = [(moe.linear(sets[i % 3][1], *sets[i % 3][0]),
+              moe.linear_input_grad(sets[i % 3][2], *sets[i % 3][0])) for i in range(30)]
+    for i, (y, dx) in enumerate(again):
+        assert torch.equal(y, sets[i % 3][3]) and torch.equal(dx, sets[i % 3][4]), i
