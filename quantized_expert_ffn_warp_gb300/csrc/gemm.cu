@@ -507,6 +507,7 @@ __global__ void __launch_bounds__(GGeo<GU, TOK>::threads, 1)
                         cw[v] = *reinterpret_cast<const uint4 *>(rec + kh * kChunkBytes +
                                                                  chunk_slot(g, v) * 16);
                 }
+                fence_async_shared();
                 __syncwarp();
                 if (lane == 0)   // the codes are in registers: the stage may be refilled
                     bar_arrive(code_empty + 8 * s);

@@ -63,6 +63,13 @@ __device__ __forceinline__ bool bar_wait(uint32_t b, uint32_t parity, volatile i
     }
 }
 
+// Orders this thread's accesses to shared memory before later ones of the copy
+// engine (TMA): a read still on its way is not overtaken by a refill.
+__device__ __forceinline__ void fence_async_shared()
+{
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one()
 {

@@ -205,13 +205,6 @@ __device__ __forceinline__ bool warp_wait(uint32_t b, uint32_t parity, volatile 
     return __all_sync(0xffffffffu, bar_wait(b, parity, abort_flag));
 }
 
-// Orders this thread's accesses to shared memory before later ones of the copy
-// engine (TMA): a read still on its way is not overtaken by a refill.
-__device__ __forceinline__ void fence_async_shared()
-{
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
 // A lane's word(s) read from lane `src`.
 template <typename S>
 __device__ __forceinline__ S shfl_of(const S &v, int src)
