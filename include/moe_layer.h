@@ -427,8 +427,10 @@ int moe_linear(const void *codes, const void *scales, const void *zeros, int row
  * Gradient of moe_linear's input through the frozen 4-bit matrix:
  *   dx[t][k] = sum_r dy[t][r] W[r][k]
  * dy [n_tokens][rows] and dx [n_tokens][cols] of type dtype with row strides
- * lddy, lddx; each weight is rounded once to that type, sums are fp32.  (The
- * gradient of bias is the sum of dy over the tokens, that of residual dy.)
+ * lddy, lddx; sums are fp32, and each weight is rounded once to that type (for
+ * bf16 and groups of 128, up to 8 tokens, each product of a gradient and its
+ * scale instead).  (The gradient of bias is the sum of dy over the tokens, that
+ * of residual dy.)
  * Pointers as for moe_linear; codes 16-byte aligned, dy and dx to their
  * element.  dx must not overlap dy.
  * More than 8 rows of dy that do not lie on 16-byte boundaries (an odd number of

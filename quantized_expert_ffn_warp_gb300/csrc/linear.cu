@@ -14,6 +14,12 @@
 // and its own ring in shared memory, which TMA fills ahead; the warp refills a
 // stage itself as soon as it has read it, so that about 128 KB per SM are under
 // way whatever the arithmetic does, and no warp waits for another.
+//
+// Measured in a replayed graph over more inputs than L2 holds: 1 token 2048 x
+// 2048 fp16 3.2 us (latency); 8 tokens 4096 x 14336 bf16 14.8 us; 3 tokens 32003
+// x 4096 fp16 19.8 us; 8 tokens 256000 x 4096 fp16 116 us, 4.8 TB/s: the issue of
+// unpacking and MMA together bounds it (without both 75 us).  Gradient: 2 tokens
+// 1027 x 2048 fp16 7.5 us, 8 tokens 14336 x 4096 bf16 15.3 us.
 #include <algorithm>
 
 #include "w4.cuh"
