@@ -466,7 +466,8 @@ int moe_linear_input_grad(const void *codes, const void *scales, const void *zer
  *   tokens[s]    = T_s; lse[t] = 0 for tokens that take no part
  * A logit of -inf has probability 0; a row of nothing but -inf has p = 0,
  * lse = -inf, adds 0 to the losses and counts in T_s.  Other non-finite values
- * propagate.
+ * propagate, and an lse^2 above the largest fp32 number (a row of nothing but
+ * the type's lowest value) is infinite in loss[1].
  * logits [n_tokens][n_experts] of type dtype (MOE_FP32, MOE_FP16, MOE_BF16)
  * with row stride ld; topk_idx int32 [n][top_k]; loss fp32 [2]; counts int32
  * [S][E]; tokens int32 [S]; prob fp32 [S][E]; lse fp32 [n].  n_experts 1 ..

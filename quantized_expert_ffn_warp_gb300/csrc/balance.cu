@@ -17,8 +17,8 @@
 // on timing.  A batch that one CTA handles needs neither partial rows nor the
 // second kernel.
 // Measured in a replayed graph: losses of 64 tokens x 64 experts 4.0 us (one
-// CTA, latency), of 32768 x 256 fp32 17.7 us (issue slots and the second
-// kernel's latency); gradient of 65521 x 256 bf16 with top-8 weights 29.0 us,
+// CTA, latency), of 32768 x 256 fp32 18.3 us (issue slots and the second
+// kernel's latency); gradient of 65521 x 256 bf16 with top-8 weights 29.3 us,
 // bound by issue slots.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -350,7 +350,15 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : V <
                 // itself, holds to an fp32 step
                 constexpr float kLog2e = 1.4426950408889634f;
                 m[u] = m[u] == -INFINITY ? 0.f : m[u];
-                const float ml = -m[u] * kLog2e;
+                float ml = -m[u] * kLog2e;
+                // beyond 2^16 (rows of a mask's lowest value) that factor, or
+                // m log2 e itself, could overflow: m is subtracted first
+                if (fabsf(m[u]) > 65536.f) {
+                    ml = 0.f;
+#pragma unroll
+                    for (int i = 0; i < V; i++)
+                        l[u][i] -= m[u];
+                }
                 sum[u] = 0.f;
 #pragma unroll
                 for (int i = 0; i < V; i++) {
@@ -717,7 +725,21 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
                 d[i] = exp_neg(d[i] - lse);
                 dot = fmaf(f[i], d[i], dot);
             }
-            const float all = gz * lse - warp_sum(dot);
+            dot = warp_sum(dot);
+            // lse holds log(sum) to an fp32 step of lse only: rows of large
+            // logits are normalised again (p is off by at most a factor E)
+            if (fabsf(lse) > 64.f) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    sum += d[i];
+                const float inv = 1.f / warp_sum(sum);
+                dot *= inv;
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    d[i] *= inv;
+            }
+            const float all = gz * lse - dot;
 #pragma unroll
             for (int i = 0; i < V; i++)
                 d[i] *= f[i] + all;

@@ -51,7 +51,7 @@ def reference(logits, idx, seq, mask):
         live &= mask != 0
     l = logits.double()
     lse = torch.where(live, torch.logsumexp(l, 1), 0.0)
-    p = torch.where(live[:, None], torch.exp(l - lse[:, None]), 0.0)
+    p = torch.where(live[:, None], torch.softmax(l, 1), 0.0)
     empty = live & (l == -INF).all(1)
     p[empty] = 0
     counts = torch.zeros((S, E), dtype=torch.int64)
@@ -222,6 +222,40 @@ def test_masked_experts_rows_and_ids():
     free = torch.ones(E, dtype=torch.bool, device="cuda")
     free[idx[6].long()] = False
     assert (out[6][free] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n", [18, 600])
+def test_rows_of_large_logits(n, dtype):
+    """Rows of the type's lowest value (a mask that leaves nothing) and rows
+    about large numbers, whose lse cannot hold log(sum): p is still the
+    softmax of the logits as stored.  600 tokens run in many blocks."""
+    moe = _moe()
+    E, k, t = 96, 4, DT[dtype]
+    logits, idx, w = batch(n, E, k, 21, torch.float32)
+    top = torch.finfo(t).max
+    base = [0.0, 60.0, 70.0, -70.0, 1e3, -1e3, 6e4, -6e4, 7e4, -1e5, 1e6, 1e9, -1e9, 1e20, -1e38,
+            top, -top, 2e38]
+    base = torch.tensor(base, device="cuda").clamp(-top, top)
+    rows = base[torch.arange(n, device="cuda") % len(base)]
+    logits = (logits + rows[:, None]).clamp(-top, top).to(t)
+    logits[rows == -top] = -top
+    small = rows.abs() <= 1e5
+    for mask, dloss in ((None, [0.7, 0.0]), (small, [0.7, -0.3])):
+        dloss = torch.tensor(dloss, device="cuda")
+        got = moe.balance_loss(logits, idx, None, mask)
+        ref = reference(logits, idx, None, mask)
+        if mask is None:
+            terms = 104 + E + n
+            assert torch.isfinite(got["lse"]).all()
+            assert ((got["prob"].double() - ref["prob"]).abs() <= terms * H * ref["prob"]).all()
+            assert (got["loss"][0] - ref["loss"][0]).abs() <= (terms + 8) * H * ref["loss"][0]
+            assert t == torch.float16 or got["loss"][1] == INF      # lse^2 above fp32
+        else:
+            check_forward(got, ref, n, E)
+        out = moe.balance_loss_grad(logits, idx, got, dloss, None, None, None, mask)
+        rg, size = reference_grad(logits, idx, ref, dloss, None, None, None)
+        check_grad(out, rg, size, E, t)
 
 
 def test_non_finite_logits_propagate():
