@@ -404,7 +404,8 @@ int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const flo
  * bf16 (dtype MOE_FP16 or MOE_BF16); ldx, ldr, ldy are their row strides in
  * elements (at least the row's length; columns beyond it are neither read nor
  * written).  bias and residual may be NULL; y may be residual itself, and must
- * not overlap x.  n_tokens 1 .. 524280.
+ * not overlap x (column slices of one buffer, at its stride, do not overlap).
+ * n_tokens 1 .. 524280.
  * Sums are fp32, with bias and residual added before the one rounding to the
  * output type.  Up to 8 tokens a group's fp32 sum of x * (q - zero) is scaled;
  * for more, each weight is rounded once to the activations' type before the

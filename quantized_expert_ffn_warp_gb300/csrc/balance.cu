@@ -843,6 +843,8 @@ bool pairs(const void *p, long long ld, int E, size_t size)
 
 }  // namespace
 
+bool rows_overlap(const void *a, long long lda, int wa, const void *b, long long ldb, int wb, int n,
+                  int size);
 bool device_pointer_here(const void *p, int dev);
 int record_failure(int code, const char *msg);
 int record_success();
@@ -980,14 +982,10 @@ extern "C" int moe_balance_loss_grad(const void *logits, int dtype, long long ld
         misaligned(counts, 4) || misaligned(tokens, 4) || misaligned(dloss, 4) ||
         misaligned(topk_w, 4) || misaligned(dtopk_w, 4))
         return record_failure(MOE_ERR_INVALID_ARG, "misaligned pointer");
-    {
-        const char *p = static_cast<const char *>(logits), *q = static_cast<const char *>(dlogits);
-        const long long np = (long long)size_of(dtype) * ((n_tokens - 1) * ld + n_experts);
-        const long long nq = (long long)size_of(dtype) * ((n_tokens - 1) * ldd + n_experts);
-        if (!(p == q && ld == ldd) && p < q + nq && q < p + np)
-            return record_failure(MOE_ERR_INVALID_ARG,
-                                  "dlogits overlaps logits (it may be logits itself)");
-    }
+    if (!(logits == dlogits && ld == ldd) &&
+        rows_overlap(logits, ld, n_experts, dlogits, ldd, n_experts, n_tokens, (int)size_of(dtype)))
+        return record_failure(MOE_ERR_INVALID_ARG,
+                              "dlogits overlaps logits (it may be logits itself)");
     const int dev = current_device();
     int sms = 0;
     if (dev < 0 || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -761,6 +761,20 @@ cudaError_t launch_group_size(const W4Call &c, int grad, int dev, int num_sms, c
 
 }  // namespace
 
+// Whether n rows of wa elements, lda apart, share bytes with n rows of wb, ldb
+// apart: ranges that meet do, unless equal strides keep the one's rows in the
+// gaps of the other's (column slices of one buffer).  Strides are at least the
+// rows' lengths.
+bool rows_overlap(const void *a, long long lda, int wa, const void *b, long long ldb, int wb, int n,
+                  int size)
+{
+    const char *p = static_cast<const char *>(a), *q = static_cast<const char *>(b);
+    if (p >= q + size * ((n - 1) * ldb + wb) || q >= p + size * ((n - 1) * lda + wa))
+        return false;
+    const long long ld = size * lda, d = ((q - p) % ld + ld) % ld;
+    return lda != ldb || d < (long long)size * wa || d + (long long)size * wb > ld;
+}
+
 bool linear_gemm_fits(const W4Call &c);
 cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int num_sms,
                                cudaStream_t st);
@@ -773,14 +787,6 @@ namespace {
 constexpr int kFewTokens = 8;
 constexpr int kMaxRows = 1 << 20, kMaxCols = 1 << 16;
 constexpr int kMaxTokens = 8 * 65535;     // blocks of 8 tokens along a grid dimension
-
-// The byte range of n rows of `width` 2-byte elements, ld elements apart.
-bool overlap(const void *a, long long lda, int wa, const void *b, long long ldb, int wb, int n)
-{
-    const char *p = static_cast<const char *>(a), *q = static_cast<const char *>(b);
-    const long long na = 2 * ((n - 1) * lda + wa), nb = 2 * ((n - 1) * ldb + wb);
-    return p < q + nb && q < p + na;
-}
 
 // Rows of 2-byte elements, `ld` apart, to rows `ldo` apart (a multiple of 8
 // elements), the gap filled with zeros: a plain coalesced copy, bound by its
@@ -829,10 +835,10 @@ int run_linear(W4Call c, int dtype, int grad, void *workspace, size_t workspace_
                               grad ? "misaligned pointer (codes need 16 bytes)"
                                    : "misaligned pointer or stride (codes and the rows of x need "
                                      "16 bytes)");
-    if (overlap(c.out, c.ldo, wout, c.in, c.ldi, win, c.n))
+    if (rows_overlap(c.out, c.ldo, wout, c.in, c.ldi, win, c.n, 2))
         return record_failure(MOE_ERR_INVALID_ARG, "the output overlaps the input");
     if (c.residual && !(c.residual == c.out && c.ldr == c.ldo) &&
-        overlap(c.out, c.ldo, wout, c.residual, c.ldr, wout, c.n))
+        rows_overlap(c.out, c.ldo, wout, c.residual, c.ldr, wout, c.n, 2))
         return record_failure(MOE_ERR_INVALID_ARG,
                               "y overlaps residual (it may be residual itself)");
     const bool copy = grad && c.n > kFewTokens && !linear_gemm_fits(c) && workspace &&

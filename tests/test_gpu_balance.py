@@ -427,3 +427,20 @@ def test_offsets_beyond_32_bits():
     dloss = torch.ones(2, device="cuda")
     want = moe.balance_loss_grad(logits, idx, near, dloss, w, w)
     assert torch.equal(moe.balance_loss_grad(rows, idx, got, dloss, w, w, out=rows), want)
+
+
+def test_slices_of_one_buffer():
+    """Logits and their gradient as column slices of one buffer."""
+    moe = _moe()
+    n, E, k = 70, 40, 2
+    logits, idx, w = batch(n, E, k, 4)
+    dloss = torch.tensor([1.0, 0.5], device="cuda")
+    want = moe.balance_loss_grad(logits, idx, moe.balance_loss(logits, idx), dloss)
+    buf = torch.full((n, 2 * E + 6), 7.0, device="cuda")
+    buf[:, :E] = logits
+    left, right = buf[:, :E], buf[:, E + 3:2 * E + 3]
+    moe.balance_loss_grad(left, idx, moe.balance_loss(left, idx), dloss, out=right)
+    assert torch.equal(left, logits) and torch.equal(right, want)
+    assert (buf[:, E:E + 3] == 7).all() and (buf[:, 2 * E + 3:] == 7).all()
+    with pytest.raises(moe.MoeError):
+        moe.balance_loss_grad(left, idx, moe.balance_loss(left, idx), dloss, out=buf[:, 3:E + 3])

@@ -336,3 +336,27 @@ def test_pipelines_at_length(n, rows, K, group, dtype):
               moe.linear_input_grad(sets[i % 3][2], *sets[i % 3][0])) for i in range(30)]
     for i, (y, dx) in enumerate(again):
         assert torch.equal(y, sets[i % 3][3]) and torch.equal(dx, sets[i % 3][4]), i
+
+
+@pytest.mark.parametrize("n", [3, 40, 300])
+def test_slices_of_one_buffer(n):
+    """Input, residual and output as column slices of one buffer."""
+    moe = _moe()
+    rows, K = 129, 256
+    m, _ = matrix(rows, K, 128, seed=9)
+    x, res, dy = (randn((n, w), torch.float16, n + w) for w in (K, rows, rows))
+    want, dwant = moe.linear(x, *m, residual=res), moe.linear_input_grad(dy, *m)
+    buf = torch.full((n, 680), 5.0, dtype=torch.float16, device="cuda")
+    xs, rs, ys = buf[:, :K], buf[:, K:K + rows], buf[:, K + rows:K + 2 * rows]
+    xs.copy_(x)
+    rs.copy_(res)
+    moe.linear(xs, *m, residual=rs, out=ys)
+    assert torch.equal(xs, x) and torch.equal(rs, res) and torch.equal(ys, want)
+    assert (buf[:, K + 2 * rows:] == 5).all()
+    ds, xo = buf[:, 3:3 + rows], buf[:, 200:200 + K]
+    buf.fill_(5.0)
+    ds.copy_(dy)
+    moe.linear_input_grad(ds, *m, out=xo)
+    assert torch.equal(ds, dy) and torch.equal(xo, dwant)
+    with pytest.raises(moe.MoeError):
+        moe.linear_input_grad(ds, *m, out=buf[:, 130:130 + K])

@@ -118,6 +118,17 @@ def test_balance_loss_grad_refuses(lib, kw, code):
     assert balance_grad(lib, **kw) == code and lib.moe_last_error().decode()
 
 
+@pytest.mark.parametrize("at,overlaps", [
+    (0, False), (64, False), (60, True), (136, False), (137, True), (-64, False), (-63, True),
+    (4 * 200 + 64, False), (7 * 200 + 30, True), (7 * 200 + 64, False), (-7 * 200 - 64, False),
+    (-7 * 200 - 63, True)])
+def test_column_slices_of_one_buffer_do_not_overlap(lib, at, overlaps):
+    """Rows of 64 in a buffer of stride 200, `at` elements from one slice to
+    the other (0: in place).  What does not overlap is refused for its device."""
+    rc = balance_grad(lib, logits=0x20000, out=0x20000 + 4 * at, ld=200, ldd=200, n=8)
+    assert rc != 0 and ("overlap" in lib.moe_last_error().decode()) == overlaps
+
+
 def test_linear_input_grad_workspace_sizes(lib):
     ws = lib.moe_linear_input_grad_workspace
     assert ws(96, 8, P(0x40002), L(97)) == 0 and ws(96, 20, P(0x40000), L(96)) == 0
