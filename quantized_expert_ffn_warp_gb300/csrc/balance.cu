@@ -296,7 +296,8 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : V <
     };
 
     int t = t_lo;       // next token without a segment
-    for (int s = a.segs.first_after(t_lo); s < a.segs.S && (t < t_hi || ONE); s++) {
+    // ONE writes every segment's results, the empty ones in front of token 0 too
+    for (int s = ONE ? 0 : a.segs.first_after(t_lo); s < a.segs.S && (t < t_hi || ONE); s++) {
         const int b = min(max(a.segs.begin(s), t), t_hi), e = min(a.segs.end(s), t_hi);
         for (int i = t + threadIdx.x; i < b; i += NT)
             a.lse[i] = 0.f;             // tokens in front of the first segment

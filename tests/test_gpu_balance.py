@@ -444,3 +444,39 @@ def test_slices_of_one_buffer():
     assert (buf[:, E:E + 3] == 7).all() and (buf[:, 2 * E + 3:] == 7).all()
     with pytest.raises(moe.MoeError):
         moe.balance_loss_grad(left, idx, moe.balance_loss(left, idx), dloss, out=buf[:, 3:E + 3])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,seq", [
+    (5, [0, 0, 5]), (5, [0, 0]), (200, [0, 0, 0, 0, 200]), (7, [0, 0, 3, 3, 7]), (6, [0, 0, 0]),
+    (9, [0, 0, 4]), (9, [2, 2, 9]), (300, [0, 0, 300]), (40, [0, 0, 0, 0, 0, 40])])
+def test_leading_empty_segments(n, seq, dtype):
+    """Empty segments in front of the first token are written like any other,
+    whatever the output memory held: the C call on outputs full of a pattern,
+    and the gradient that reads them."""
+    moe = _moe()
+    E, k, S = 40, 3, len(seq) - 1
+    logits, idx, w = batch(n, E, k, n, DT[dtype])
+    s, _ = tensors(seq, None, n)
+    lib = moe.load_library()
+    size = lib.moe_balance_workspace(n, E, S)
+    spec = dict(loss=((2,), torch.float32), counts=((S, E), torch.int32),
+                tokens=((S,), torch.int32), prob=((S, E), torch.float32),
+                lse=((n,), torch.float32), ws=((size,), torch.uint8))
+    out = {q: torch.empty(shape, dtype=t, device="cuda") for q, (shape, t) in spec.items()}
+    for t in out.values():
+        t.view(torch.uint8).fill_(0x5A)
+    code = {"fp32": moe.MOE_FP32, "fp16": moe.MOE_FP16, "bf16": moe.MOE_BF16}[dtype]
+    rc = lib.moe_balance_loss(logits.data_ptr(), code, E, n, E, idx.data_ptr(), k, s.data_ptr(), S,
+                              None, *(out[q].data_ptr() for q in spec), size,
+                              torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    ref = reference(logits, idx, s, None)
+    check_forward(out, ref, n, E)
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    dw = torch.linspace(-1, 1, n * k, device="cuda").view(n, k)
+    for d in (None, dw):
+        got = moe.balance_loss_grad(logits, idx, out, dloss, w, d, s)
+        rg, size = reference_grad(logits, idx, ref, dloss, w, d, s)
+        check_grad(got, rg, size, E, DT[dtype])
+        assert (got[~ref["live"]] == 0).all()
