@@ -579,7 +579,8 @@ struct BwdArgs {
 // mostly stays in registers.  The gradients of the top-k weights are computed
 // for as many tokens as fill a warp, and reach their experts' lanes through two
 // rows of shared memory in turn: a token writes one and clears what the token
-// before it wrote in the other, so that one warp barrier separates them.
+// before it wrote in the other.  One warp barrier stands between that token's
+// reads and the clearing, a second between this token's writes and its reads.
 template <typename T, int V>
 __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
 {
@@ -684,6 +685,7 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
             load_w(tok + batch);
         }
         const int mine = lane / kp == tok - batch0 ? to : -1;
+        __syncwarp();
         if (was >= 0)
             add[(row ^ 1) * 32 * V + was] = 0.f;
         if (mine >= 0)

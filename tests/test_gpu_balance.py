@@ -480,3 +480,26 @@ def test_leading_empty_segments(n, seq, dtype):
         rg, size = reference_grad(logits, idx, ref, dloss, w, d, s)
         check_grad(got, rg, size, E, DT[dtype])
         assert (got[~ref["live"]] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,E,k", [(60000, 8, 4), (60001, 33, 1), (40000, 256, 8), (9000, 1024, 32)])
+def test_successive_tokens_meet_in_the_same_experts(n, E, k, dtype):
+    """Runs of tokens whose weights reach the same few experts, so that an entry
+    of shared memory is written, read and cleared by different lanes from one
+    token to the next: within the bounds, and the same bits every time."""
+    moe = _moe()
+    logits, _, _ = batch(n, E, k, 31, DT[dtype])
+    g = torch.Generator(device="cuda").manual_seed(3)
+    turn = torch.rand((n, k), device="cuda", generator=g).argsort(1)
+    idx = (turn + E - k).to(torch.int32).contiguous()    # the last k experts in any order
+    w = torch.softmax(torch.gather(logits.float(), 1, idx.long()), 1).contiguous()
+    dw = torch.randn((n, k), device="cuda", generator=g)
+    got = moe.balance_loss(logits, idx)
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    first = moe.balance_loss_grad(logits, idx, got, dloss, w, dw)
+    ref = reference(logits, idx, None, None)
+    rg, size = reference_grad(logits, idx, ref, dloss, w, dw, None)
+    check_grad(first, rg, size, E, DT[dtype])
+    for _ in range(20):
+        assert torch.equal(moe.balance_loss_grad(logits, idx, got, dloss, w, dw), first)
