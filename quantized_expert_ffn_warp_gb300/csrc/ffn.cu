@@ -1054,8 +1054,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(FfnArgs a)
         float tot0[4] = {0.f, 0.f, 0.f, 0.f}, tot1[4] = {0.f, 0.f, 0.f, 0.f};
         for (unsigned k = 0; k < N && ok; k++, u++) {
             // refill the stage freed by the previous unit, kS - 1 units ahead
-            // (the stage's previous contents were read into registers and
-            // consumed before the __syncwarp that ended the previous unit)
+            // (every lane's reads of it were ordered before the copy engine's
+            // writes by the fence and the __syncwarp that ended that unit)
             if (lane == 0 && issued < c.U) {
                 issue_next<WB, GU>(is, a, tab, c, wr, issued % kS);
                 ++issued;
@@ -1076,7 +1076,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_kernel(FfnArgs a)
                     load_b<WB, GU>(lc, g0 + i, b, xs, a.xsum);
                 group_mma<WB, GU>(stage + i * G::rec, b, xs, tot0, tot1);
             }
-            __syncwarp();   // every lane has read the stage before it is refilled
+            // every lane has read the stage before it is refilled: a barrier alone
+            // does not order these reads before writes of the copy engine
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
         }
         if (!ok)
             break;

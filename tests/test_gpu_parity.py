@@ -557,3 +557,41 @@ def test_layers_of_different_sizes_coexist(env):
     finally:
         lb.close()
         ls.close()
+
+
+@pytest.mark.parametrize("name,n", [("e64_top2_zipf", 8), ("e64_top2_zipf", 1),
+                                    ("e512_top4_shared_2bit", 16), ("ragged", 40)])
+def test_decode_rings_under_load(env, name, n):
+    """The decode kernels' rings turn over many times while another stream
+    competes for memory: each refill waits for the reads of what it replaces,
+    so the same inputs give the same bits in every call, within the oracle's
+    tolerance."""
+    import oracle
+    spec = RAGGED if name == "ragged" else synth.CONFIGS[name]
+    packed, layer = get_layer(env, spec)
+    m0 = layer.info()["gemm_min_tokens"]
+    if spec.wbits == 4:
+        layer.set_gemm_min_tokens(0)
+    try:
+        xs = [synth.make_tokens(spec, n, batch=40 + i) for i in range(3)]
+        ins = [dev(x) for x in xs]
+        want = [layer.forward(x).clone() for x in ins]
+        side = torch.cuda.Stream()
+        a = torch.ones(1 << 28, dtype=torch.uint8, device="cuda")
+        b = torch.empty_like(a)
+        torch.cuda.synchronize()
+        outs = []
+        for i in range(60):
+            with torch.cuda.stream(side):
+                b.copy_(a)
+            outs.append(layer.forward(ins[i % 3], torch.empty_like(ins[i % 3])))
+        torch.cuda.synchronize()
+        for i, out in enumerate(outs):
+            assert torch.equal(out, want[i % 3]), i
+        tokens = np.array([0, n - 1] if n > 1 else [0], dtype=np.int32)
+        ref = oracle.forward(packed, xs[0], tokens=tokens)
+        parity.assert_close(want[0].cpu().numpy().view(np.uint16)[tokens], ref["out64"], name)
+        assert layer.check_status() == 0
+    finally:
+        if spec.wbits == 4:
+            layer.set_gemm_min_tokens(m0)
