@@ -568,14 +568,22 @@ def balance_loss(logits, topk_idx, seq_offsets=None, mask=None, stream=None):
 
 
 def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, seq_offsets=None,
-                      mask=None, out=None, stream=None):
+                      mask=None, out=None, stream=None, top_k=None):
     """Gradient of balance_loss in the logits (moe_balance_loss_grad): fwd is
     balance_loss's result (its lse, counts and tokens are read), dloss fp32 [2]
     the gradients of the two losses on the device.  With dtopk_w fp32 [n, k],
     the gradient of the renormalised top-k weights topk_w fp32 [n, k], the
-    gradient through them is added.  out may be logits itself."""
+    gradient through them is added.  Without dtopk_w the ids are not read:
+    topk_idx may be None, with top_k = k given in its place (the counts' scale
+    depends on it).  out may be logits itself."""
     torch, types = _types()
     n, E, k, S, code, pl, ld, pi, po, pm = _batch(torch, types, logits, topk_idx, seq_offsets, mask)
+    if topk_idx is None:
+        if top_k is None:
+            _bad("topk_idx is None: need top_k, the experts per token of fwd's counts")
+        k = top_k
+    elif top_k is not None and top_k != k:
+        _bad("top_k = %s, but topk_idx has %d columns" % (top_k, k))
     f32, i32 = torch.float32, torch.int32
     pw = pdw = None
     if dtopk_w is not None:

@@ -503,3 +503,22 @@ def test_successive_tokens_meet_in_the_same_experts(n, E, k, dtype):
     check_grad(first, rg, size, E, DT[dtype])
     for _ in range(20):
         assert torch.equal(moe.balance_loss_grad(logits, idx, got, dloss, w, dw), first)
+
+
+@pytest.mark.parametrize("k", [1, 4])
+def test_gradient_without_ids(k):
+    """Without top-k weights the ids are not read: the gradient with k alone is
+    that with the ids, bit for bit, and that of the definition."""
+    moe = _moe()
+    n, E = 50, 24
+    logits, idx, w = batch(n, E, k, 2)
+    f = moe.balance_loss(logits, idx)
+    dloss = torch.tensor([0.7, -0.3], device="cuda")
+    got = moe.balance_loss_grad(logits, None, f, dloss, top_k=k)
+    assert torch.equal(got, moe.balance_loss_grad(logits, idx, f, dloss))
+    rg, size = reference_grad(logits, idx, reference(logits, idx, None, None), dloss, None, None,
+                              None)
+    check_grad(got, rg, size, E, torch.float32)
+    for bad in (None, 0, 33, E + 1):
+        with pytest.raises(moe.MoeError):
+            moe.balance_loss_grad(logits, None, f, dloss, top_k=bad)

@@ -161,3 +161,32 @@ def test_binding_refuses_wrong_tensors():
                  lambda: moe.balance_loss(x.double(), torch.zeros((2, 1), dtype=torch.int32))):
         with pytest.raises(moe.MoeError):
             call()
+
+
+def test_gradient_without_ids_needs_top_k(monkeypatch):
+    """The counts' scale E / (k T) needs k: without ids it has to be given, and
+    it reaches the library; with ids it has to agree with them."""
+    torch = pytest.importorskip("torch")
+    from quantized_expert_ffn_warp_gb300 import moe
+    seen = []
+
+    class Lib:
+        def moe_balance_loss_grad(self, *a):
+            seen.append((a[5], a[6]))
+            return 0
+
+    monkeypatch.setattr(moe, "load_library", Lib)
+    monkeypatch.setattr(moe, "_raw_stream", lambda t, stream: 0)
+    logits, idx = torch.zeros((6, 8)), torch.zeros((6, 3), dtype=torch.int32)
+    fwd = dict(lse=torch.zeros(6), counts=torch.zeros((1, 8), dtype=torch.int32),
+               tokens=torch.zeros(1, dtype=torch.int32))
+    dloss = torch.zeros(2)
+    with pytest.raises(moe.MoeError, match="top_k"):
+        moe.balance_loss_grad(logits, None, fwd, dloss)
+    with pytest.raises(moe.MoeError, match="top_k"):
+        moe.balance_loss_grad(logits, idx, fwd, dloss, top_k=2)
+    assert not seen
+    moe.balance_loss_grad(logits, None, fwd, dloss, top_k=3)
+    moe.balance_loss_grad(logits, idx, fwd, dloss)
+    moe.balance_loss_grad(logits, idx, fwd, dloss, top_k=3)
+    assert seen == [(None, 3), (idx.data_ptr(), 3), (idx.data_ptr(), 3)]
