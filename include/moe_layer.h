@@ -500,7 +500,8 @@ int moe_balance_loss(const void *logits, int dtype, long long ld, int n_tokens, 
  * (fp32 [n][k]) the gradient that arrives at them; it is left out when dtopk_w
  * is NULL (topk_idx and topk_w may then be NULL).  An id outside [0, E) gets
  * no gradient.  dloss fp32 [2] is device memory.  Tokens that take no part
- * get 0 in their whole row.
+ * get 0 in their whole row, and rows of nothing but -inf 0 from the losses,
+ * whatever dloss holds.
  * dlogits has the type of logits, row stride ldd, and may be logits itself.
  * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes,
  * overlap), UNSUPPORTED (dtype), CUDA.

@@ -746,6 +746,11 @@ __global__ void __launch_bounds__(kThreads) balance_grad_kernel(BwdArgs a)
 #pragma unroll
             for (int i = 0; i < V; i++)
                 d[i] *= f[i] + all;
+            if (none) {     // 0 whatever dloss holds (0 times its infinity is not)
+#pragma unroll
+                for (int i = 0; i < V; i++)
+                    d[i] = 0.f;
+            }
             if (a.dw) {
                 scatter(tok);
                 if (on) {

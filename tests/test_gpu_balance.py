@@ -522,3 +522,34 @@ def test_gradient_without_ids(k):
     for bad in (None, 0, 33, E + 1):
         with pytest.raises(moe.MoeError):
             moe.balance_loss_grad(logits, None, f, dloss, top_k=bad)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("dloss", [[INF, 0.0], [0.0, -INF], [float("nan"), 1.0], [1.0, float("nan")]])
+def test_loss_gradients_that_are_not_finite(dloss, dtype):
+    """An overflowed loss gradient stays in the tokens that take part: the
+    others, and rows of nothing but -inf, get 0 (there: their weights'
+    gradient)."""
+    moe = _moe()
+    n, E, k = 60, 70, 4
+    logits, idx, w = batch(n, E, k, 12, DT[dtype])
+    logits[6] = -INF
+    mask = torch.ones(n, dtype=torch.bool, device="cuda")
+    mask[::3] = False       # token 6 comes back below
+    mask[6] = True
+    seq = torch.tensor([0, 20, 20, 55], dtype=torch.int32, device="cuda")
+    live = mask.clone()
+    live[55:] = False
+    f = moe.balance_loss(logits, idx, seq, mask)
+    dloss = torch.tensor(dloss, device="cuda")
+    dw = torch.linspace(-2, 1, n * k, device="cuda").view(n, k)
+    plain = moe.balance_loss_grad(logits, idx, f, dloss, None, None, seq, mask)
+    both = moe.balance_loss_grad(logits, idx, f, dloss, w, dw, seq, mask)
+    for got in (plain, both):
+        assert (got[~live] == 0).all()
+        live[6] = False
+        assert not torch.isfinite(got[live]).all(1).any()
+        live[6] = True
+    assert (plain[6] == 0).all()
+    alone = moe.balance_loss_grad(logits, idx, f, torch.zeros_like(dloss), w, dw, seq, mask)
+    assert torch.equal(both[6], alone[6]) and torch.isfinite(both[6]).all() and (both[6] != 0).any()
