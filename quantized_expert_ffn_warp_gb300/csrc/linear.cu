@@ -94,7 +94,8 @@ struct RowMeta<32> {
     }
 };
 
-// The same by single loads, the last group repeated past the row's end.
+// The same by single loads; 0 past the row's end (its scale times the padding's
+// zeros has to be 0, whatever the last group's scale).
 template <int GS>
 __device__ __forceinline__ void load_each(RowMeta<GS> &m, const uint16_t *sp, const uint8_t *zp,
                                           int left)
@@ -103,9 +104,10 @@ __device__ __forceinline__ void load_each(RowMeta<GS> &m, const uint16_t *sp, co
     uint32_t s[(N + 1) / 2] = {}, z[(N + 3) / 4] = {};
 #pragma unroll
     for (int i = 0; i < N; i++) {
-        const int at = min(i, left - 1);
-        s[i / 2] |= (uint32_t)sp[at] << (16 * (i & 1));
-        z[i / 4] |= (uint32_t)zp[at] << (8 * (i & 3));
+        if (i < left) {
+            s[i / 2] |= (uint32_t)sp[i] << (16 * (i & 1));
+            z[i / 4] |= (uint32_t)zp[i] << (8 * (i & 3));
+        }
     }
     memcpy(&m.s, s, sizeof(m.s));
     memcpy(&m.z, z, sizeof(m.z));
@@ -475,13 +477,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t s[kMeta], z[kMeta];
     };
     const auto load_meta = [&](int r0, Meta &m) {
-        // rows past the matrix repeat its last row, against gradients of zero
-        const long long at = (long long)min(r0 + lane, rows - 1) * ng;
+        // rows past the matrix: scales of 0 (the last row's, infinite, would make
+        // NaN of the padding's zeros)
+        const bool in = r0 + lane < rows;
+        const long long at = (long long)(in ? r0 + lane : 0) * ng;
 #pragma unroll
         for (int i = 0; i < kMeta; i++) {
             const int grp = min(col0 / GS + i, ng - 1);
-            m.s[i] = c.w.scales[at + grp];
-            m.z[i] = c.w.zeros[at + grp];
+            m.s[i] = in ? c.w.scales[at + grp] : 0;
+            m.z[i] = in ? c.w.zeros[at + grp] : 0;
         }
     };
 

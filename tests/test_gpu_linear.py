@@ -360,3 +360,23 @@ def test_slices_of_one_buffer(n):
     assert torch.equal(ds, dy) and torch.equal(xo, dwant)
     with pytest.raises(moe.MoeError):
         moe.linear_input_grad(ds, *m, out=buf[:, 130:130 + K])
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n", [2, 8, 24, 200])
+@pytest.mark.parametrize("rows,K,group", [
+    (33, 256, 128), (33, 256, 32), (64, 384, 128), (64, 288, 32), (95, 192, 64), (1, 32, 32)])
+def test_infinite_scale_of_the_last_group(n, rows, K, group, dtype):
+    """An infinite scale in the matrix's last group makes infinities where the
+    formula does, and no NaN of the padding behind the last row and column."""
+    moe = _moe()
+    codes = torch.full((rows, K // 2), 0x99, dtype=torch.uint8, device="cuda")
+    scales = torch.full((rows, K // group), 0.01, dtype=torch.float16, device="cuda")
+    scales[-1, -1] = float("inf")
+    zeros = torch.full((rows, K // group), 3, dtype=torch.uint8, device="cuda")
+    y = moe.linear(torch.ones((n, K), dtype=DT[dtype], device="cuda"), codes, scales, zeros, group)
+    dx = moe.linear_input_grad(torch.ones((n, rows), dtype=DT[dtype], device="cuda"), codes, scales,
+                               zeros, group)
+    inf = float("inf")
+    assert (y[:, -1] == inf).all() and torch.isfinite(y[:, :-1]).all()
+    assert (dx[:, K - group:] == inf).all() and torch.isfinite(dx[:, :K - group]).all()
