@@ -474,9 +474,10 @@ int moe_linear_input_grad(const void *codes, const void *scales, const void *zer
  * [S][E]; tokens int32 [S]; prob fp32 [S][E]; lse fp32 [n].  n_experts 1 ..
  * 1024, top_k 1 .. min(32, E), n_segments 1 .. 65535, n_tokens 1 .. 67108864.
  * workspace: moe_balance_workspace(n, E, S) bytes, 256-byte aligned, any
- * contents, used by one call at a time.  Sums are fp32 or wider in a fixed
- * order: the same call gives the same bits every time.  All pointers are
- * DEVICE pointers of the current device.  No allocation; asynchronous.
+ * contents, used by one call at a time.  Sums are fp32 in a fixed order (the
+ * same call gives the same bits every time), their rounding errors bounded
+ * whatever the batch's length.  All pointers are DEVICE pointers of the current
+ * device.  No allocation; asynchronous.
  * moe_balance_workspace returns 0 for sizes out of range.
  * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes),
  * UNSUPPORTED (dtype), CUDA.

@@ -17,7 +17,7 @@
 // on timing.  A batch that one CTA handles needs neither partial rows nor the
 // second kernel.
 // Measured in a replayed graph: losses of 64 tokens x 64 experts 4.0 us (one
-// CTA, latency), of 32768 x 256 fp32 18.3 us (issue slots and the second
+// CTA, latency), of 32768 x 256 fp32 18.7 us (issue slots and the second
 // kernel's latency); gradient of 65521 x 256 bf16 with top-8 weights 29.3 us,
 // bound by issue slots.
 #include <cuda_bf16.h>
@@ -189,7 +189,28 @@ struct Segs {
     }
 };
 
-// Sums are fp32 trees of short chains (64-bit arithmetic is slow on this GPU).
+// Sums are fp32 (64-bit arithmetic is slow on this GPU) in chains whose length
+// does not grow with the batch: kChain tokens in a warp's registers, folded into
+// pairs (sum, rounding errors); the warps of a block; the blocks of a segment, at
+// most 20 in each of 32 chains or, with more than 150 segments, 153 in each of 4;
+// pairs again over the segments.  A sum of non-negative terms is off by at most
+// 64 + 8 + 157 fp32 roundings and a few more at any size.
+constexpr int kChain = 64;
+
+// Adds v to the pair (sum, err) without loss: the rounding of each addition goes
+// into err (two-sum).
+__device__ __forceinline__ void fold(float &sum, float &err, float v)
+{
+    const float s = __fadd_rn(sum, v), b = __fsub_rn(s, sum);
+    err += __fadd_rn(__fsub_rn(sum, __fsub_rn(s, b)), __fsub_rn(v, b));
+    sum = s;
+}
+// The pair's value (behind an infinity the errors are NaN).
+__device__ __forceinline__ float unfold(float sum, float err)
+{
+    return err == err ? sum + err : sum;
+}
+
 // Workspace: [ticket, 256 B][loss parts f32 [S][ceil(E/32)]][z sums f32 [slots]]
 // [z sums f32 [S]][valid tokens int [slots]][prob sums f32 [slots][E]][counts int [slots][E]]
 struct BalanceWs {
@@ -263,8 +284,9 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : V <
 {
     constexpr int NW = ONE ? kOneWarps : kWarps, NT = 32 * NW;
     using R = Row<T, V>;
-    extern __shared__ float sm[];       // prob [NW][E], then counts int [E]
-    __shared__ float zred[NW];
+    // prob [NW][E], counts int [E], and in long blocks the prob sums' errors [NW][E]
+    extern __shared__ float sm[];
+    __shared__ float zred[NW], zerr[NW];
     __shared__ int vred[NW];
     __shared__ float lred[NW];
     pdl_enter();
@@ -318,82 +340,122 @@ __global__ void __launch_bounds__(ONE ? 32 * kOneWarps : kThreads, ONE ? 1 : V <
             psum[i] = 0.f;
         float zsum = 0.f;
         int valid = 0;
-        for (int tok = b + warp; tok < e; tok += U * NW) {
-            float l[U][V], m[U], sum[U];
-            bool on[U];
+        // A long block's tokens in spans of kChain per warp; behind each span the
+        // warp's sums go into its shared row and zred.
+        constexpr int kSpan = kChain * NW;
+        const auto fold_all = [&](bool first) {
+            float *sum = sm + warp * E + lane, *err = sum + (NW + 1) * E;
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                on[u] = next[u].on;
-                valid += on[u];
-                if (on[u] && next[u].id >= 0 && next[u].id < E)
-                    atomicAdd(hist + next[u].id, 1);
-                next[u].row.get(l[u]);
-                m[u] = -INFINITY;
-                if (!on[u]) {   // a row of -inf: p = 0
+            for (int i = 0; i < V; i++) {
+                const int x = R::at(i, lane) - lane;
+                if (x + lane < E) {
+                    if (first)
+                        sum[x] = err[x] = 0.f;
+                    fold(sum[x], err[x], psum[i]);
+                }
+                psum[i] = 0.f;
+            }
+            if (lane == 0) {
+                if (first)
+                    zred[warp] = zerr[warp] = 0.f;
+                fold(zred[warp], zerr[warp], zsum);
+            }
+            zsum = 0.f;
+        };
+        int tok = b + warp;
+        for (int stop = ONE ? e : min(e, b + kSpan);; stop = min(e, stop + kSpan)) {
+            for (; tok < stop; tok += U * NW) {
+                float l[U][V], m[U], sum[U];
+                bool on[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    on[u] = next[u].on;
+                    valid += on[u];
+                    if (on[u] && next[u].id >= 0 && next[u].id < E)
+                        atomicAdd(hist + next[u].id, 1);
+                    next[u].row.get(l[u]);
+                    m[u] = -INFINITY;
+                    if (!on[u]) {   // a row of -inf: p = 0
+#pragma unroll
+                        for (int i = 0; i < V; i++)
+                            l[u][i] = -INFINITY;
+                    }
 #pragma unroll
                     for (int i = 0; i < V; i++)
-                        l[u][i] = -INFINITY;
+                        m[u] = fmaxf(m[u], l[u][i]);
+                    load(tok + (U + u) * NW, e, next[u]);
                 }
 #pragma unroll
-                for (int i = 0; i < V; i++)
-                    m[u] = fmaxf(m[u], l[u][i]);
-                load(tok + (U + u) * NW, e, next[u]);
-            }
+                for (int d = 16; d > 0; d >>= 1)
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
+                    for (int u = 0; u < U; u++)
+                        m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], d));
 #pragma unroll
-                for (int u = 0; u < U; u++)
-                    m[u] = fmaxf(m[u], __shfl_xor_sync(0xffffffffu, m[u], d));
+                for (int u = 0; u < U; u++) {
+                    // exp(l - m) = 2^(l log2 e - m log2 e): the rounding of m log2 e is a
+                    // common factor of the row, which p does not see and lse, about m
+                    // itself, holds to an fp32 step
+                    constexpr float kLog2e = 1.4426950408889634f;
+                    m[u] = m[u] == -INFINITY ? 0.f : m[u];
+                    float ml = -m[u] * kLog2e;
+                    // beyond 2^16 (rows of a mask's lowest value) that factor, or
+                    // m log2 e itself, could overflow: m is subtracted first
+                    if (fabsf(m[u]) > 65536.f) {
+                        ml = 0.f;
 #pragma unroll
-            for (int u = 0; u < U; u++) {
-                // exp(l - m) = 2^(l log2 e - m log2 e): the rounding of m log2 e is a
-                // common factor of the row, which p does not see and lse, about m
-                // itself, holds to an fp32 step
-                constexpr float kLog2e = 1.4426950408889634f;
-                m[u] = m[u] == -INFINITY ? 0.f : m[u];
-                float ml = -m[u] * kLog2e;
-                // beyond 2^16 (rows of a mask's lowest value) that factor, or
-                // m log2 e itself, could overflow: m is subtracted first
-                if (fabsf(m[u]) > 65536.f) {
-                    ml = 0.f;
+                        for (int i = 0; i < V; i++)
+                            l[u][i] -= m[u];
+                    }
+                    sum[u] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < V; i++) {
+                        l[u][i] = exp2_fast(fmaf(l[u][i], kLog2e, ml));
+                        sum[u] += l[u][i];
+                    }
+                }
+#pragma unroll
+                for (int d = 16; d > 0; d >>= 1)
+#pragma unroll
+                    for (int u = 0; u < U; u++)
+                        sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    // a row of -inf (every expert masked) has no distribution: p = 0
+                    const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.0f, sum[u]);
 #pragma unroll
                     for (int i = 0; i < V; i++)
-                        l[u][i] -= m[u];
-                }
-                sum[u] = 0.f;
-#pragma unroll
-                for (int i = 0; i < V; i++) {
-                    l[u][i] = exp2_fast(fmaf(l[u][i], kLog2e, ml));
-                    sum[u] += l[u][i];
+                        psum[i] = fmaf(l[u][i], inv, psum[i]);
+                    const float lse = m[u] + __logf(sum[u]);
+                    if (sum[u] != 0.f)
+                        zsum = fmaf(lse, lse, zsum);
+                    if (lane == 0 && tok + u * NW < e)
+                        a.lse[tok + u * NW] = on[u] ? lse : 0.f;
                 }
             }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1)
-#pragma unroll
-                for (int u = 0; u < U; u++)
-                    sum[u] += __shfl_xor_sync(0xffffffffu, sum[u], d);
-#pragma unroll
-            for (int u = 0; u < U; u++) {
-                // a row of -inf (every expert masked) has no distribution: p = 0
-                const float inv = sum[u] == 0.f ? 0.f : __fdividef(1.0f, sum[u]);
-#pragma unroll
-                for (int i = 0; i < V; i++)
-                    psum[i] = fmaf(l[u][i], inv, psum[i]);
-                const float lse = m[u] + __logf(sum[u]);
-                if (sum[u] != 0.f)
-                    zsum = fmaf(lse, lse, zsum);
-                if (lane == 0 && tok + u * NW < e)
-                    a.lse[tok + u * NW] = on[u] ? lse : 0.f;
-            }
+            if (ONE || stop == e)
+                break;
+            fold_all(stop == b + kSpan);
         }
+        if (!ONE && e - b > kSpan) {
+            fold_all(false);
 #pragma unroll
-        for (int i = 0; i < V; i++)
-            if (R::at(i, lane) < E)
-                sm[warp * E + R::at(i, lane)] = psum[i];
-        if (lane == 0) {
-            zred[warp] = zsum;
+            for (int i = 0; i < V; i++)
+                if (R::at(i, lane) < E) {
+                    float *sum = sm + warp * E + R::at(i, lane);
+                    *sum = unfold(*sum, sum[(NW + 1) * E]);
+                }
+            if (lane == 0)
+                zred[warp] = unfold(zred[warp], zerr[warp]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; i++)
+                if (R::at(i, lane) < E)
+                    sm[warp * E + R::at(i, lane)] = psum[i];
+            if (lane == 0)
+                zred[warp] = zsum;
+        }
+        if (lane == 0)
             vred[warp] = valid;
-        }
         __syncthreads();
         int v = 0;
         float z = 0.f;
@@ -520,17 +582,19 @@ __global__ void __launch_bounds__(kFinalThreads) balance_final_kernel(FwdArgs a)
     if (!last)
         return;
     __threadfence();
-    float bal = 0.f;
+    float bal = 0.f, bal_err = 0.f, z_err = 0.f;
     z = 0.f;
     int tokens = 0, live = 0;
     for (int i = threadIdx.x; i < (int)(gridDim.x * gridDim.y); i += blockDim.x)
-        bal += __ldcg(a.ws.part + i);
+        fold(bal, bal_err, __ldcg(a.ws.part + i));
     for (int q = threadIdx.x; q < a.segs.S; q += blockDim.x) {
         const int t = __ldcg(a.tokens + q);
         tokens += t;
         live += t > 0;
-        z += __ldcg(a.ws.zseg + q);
+        fold(z, z_err, __ldcg(a.ws.zseg + q));
     }
+    bal = unfold(bal, bal_err);
+    z = unfold(z, z_err);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
         bal += __shfl_xor_sync(0xffffffffu, bal, d);
@@ -793,9 +857,15 @@ cudaError_t launch_stats(const FwdArgs &a, cudaStream_t st)
         }
         return launch_pdl(kernel, dim3(1), dim3(32 * kOneWarps), smem, st, a);
     }
-    const cudaError_t e =
-        launch_pdl(balance_stats_kernel<T, V, false>, dim3((a.n + a.C - 1) / a.C),
-                   dim3(kThreads), sizeof(float) * (kWarps + 1) * a.E, st, a);
+    cudaError_t e = cudaSuccess;
+    const int rows = a.C > kChain * kWarps ? 2 * kWarps + 1 : kWarps + 1;
+    constexpr size_t most = sizeof(float) * (2 * kWarps + 1) * 32 * V;
+    if (most > 48 * 1024)
+        e = cudaFuncSetAttribute(balance_stats_kernel<T, V, false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
+    if (e == cudaSuccess)
+        e = launch_pdl(balance_stats_kernel<T, V, false>, dim3((a.n + a.C - 1) / a.C),
+                       dim3(kThreads), sizeof(float) * rows * a.E, st, a);
     if (e != cudaSuccess)
         return e;
     // a warp for each block that a segment meets on average, up to 32

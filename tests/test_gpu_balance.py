@@ -553,3 +553,47 @@ def test_loss_gradients_that_are_not_finite(dloss, dtype):
     assert (plain[6] == 0).all()
     alone = moe.balance_loss_grad(logits, idx, f, torch.zeros_like(dloss), w, dw, seq, mask)
     assert torch.equal(both[6], alone[6]) and torch.isfinite(both[6]).all() and (both[6] != 0).any()
+
+
+@pytest.mark.parametrize("n,E,S,dtype,top", [
+    (1 << 26, 8, 1, "fp16", 10.3), (1 << 26, 8, 1, "bf16", 3.1), (1 << 24, 16, 5, "fp32", 7.7),
+    (1 << 22, 300, 3, "bf16", 4.4), (1 << 20, 600, 1, "fp16", 5.3), (1 << 21, 1024, 200, "bf16", 2.2),
+    (131070, 1024, 65535, "fp16", 6.1)])
+def test_long_batches_of_equal_rows(n, E, S, dtype, top):
+    """Equal terms round alike, so that a chain's error grows with its length:
+    the bound here does not.  Of an fp32 sum it is 64 + 8 + 157 roundings (the
+    span of a warp, the warps, the blocks) and up to 8 of folding; a term adds
+    (1.3 |d| + 3) H twice for its exponential and the row's sum, E / 32 + 5 for
+    that sum, 5 for the quotient, with |d| <= 2; lse^2 twice that of lse, whose
+    logarithm is good to 12 H here, over lse >= 4."""
+    moe = _moe()
+    row = (torch.linspace(-1, 1, E, device="cuda") + top).to(DT[dtype])
+    logits = row.expand(n, E).contiguous()
+    idx = torch.full((n, 1), E - 1, dtype=torch.int32, device="cuda")
+    seq = torch.linspace(0, n, S + 1, dtype=torch.float64).round().int().cuda()
+    got = moe.balance_loss(logits, idx, seq if S > 1 else None)
+    p, lse = torch.softmax(row.double(), 0), torch.logsumexp(row.double(), 0)
+    chain, term = 64 + 8 + 157 + 8, 2 * 6 + E / 32 + 5 + 5
+    assert torch.equal(got["tokens"].long(), (seq[1:] - seq[:-1]).long())
+    assert ((got["prob"].double() - p).abs() <= (chain + term) * H * p).all()
+    assert ((got["lse"].double() - lse).abs() <= (term + 12 + 2 * lse) * H).all()
+    bal = E * p[E - 1]
+    assert (got["loss"][0].double() - bal).abs() <= (chain + term + 16) * H * bal
+    z = lse ** 2
+    assert (got["loss"][1].double() - z).abs() <= (chain + 8 + 2 * ((term + 12) / lse + 2)) * H * z
+
+
+def test_long_batches_with_infinite_squares():
+    """lse^2 above fp32 is an infinity in loss[1], in long batches too, and
+    NaN stays NaN."""
+    moe = _moe()
+    n, E, k = 1 << 20, 8, 2
+    logits, idx, w = batch(n, E, k, 3)
+    logits[::1000] = torch.finfo(torch.float32).min
+    got = moe.balance_loss(logits, idx)
+    ref = torch.softmax(logits.double(), 1).mean(0)
+    assert got["loss"][1] == INF and torch.isfinite(got["loss"][0])
+    assert ((got["prob"][0].double() - ref).abs() <= 400 * H * ref).all()
+    logits[70000] = float("nan")
+    got = moe.balance_loss(logits, idx)
+    assert torch.isnan(got["loss"]).all() and torch.isnan(got["prob"]).all()
