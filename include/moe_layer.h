@@ -404,7 +404,8 @@ int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const flo
  * bf16 (dtype MOE_FP16 or MOE_BF16); ldx, ldr, ldy are their row strides in
  * elements (at least the row's length; columns beyond it are neither read nor
  * written).  bias and residual may be NULL; y may be residual itself, and must
- * not overlap x (column slices of one buffer, at its stride, do not overlap).
+ * overlap nothing else (column slices of one buffer, at its stride, do not
+ * overlap).
  * n_tokens 1 .. 524280.
  * Sums are fp32, with bias and residual added before the one rounding to the
  * output type.  Up to 8 tokens a group's fp32 sum of x * (q - zero) is scaled;
@@ -433,7 +434,7 @@ int moe_linear(const void *codes, const void *scales, const void *zeros, int row
  * scale instead).  (The gradient of bias is the sum of dy over the tokens, that
  * of residual dy.)
  * Pointers as for moe_linear; codes 16-byte aligned, dy and dx to their
- * element.  dx must not overlap dy.
+ * element.  dx and the workspace must overlap nothing else.
  * More than 8 rows of dy that do not lie on 16-byte boundaries (an odd number of
  * rows, for one) are first copied into `workspace`, a 16-byte aligned device
  * buffer of moe_linear_input_grad_workspace(rows, n_tokens, dy, lddy) bytes, in
@@ -474,12 +475,13 @@ int moe_linear_input_grad(const void *codes, const void *scales, const void *zer
  * [S][E]; tokens int32 [S]; prob fp32 [S][E]; lse fp32 [n].  n_experts 1 ..
  * 1024, top_k 1 .. min(32, E), n_segments 1 .. 65535, n_tokens 1 .. 67108864.
  * workspace: moe_balance_workspace(n, E, S) bytes, 256-byte aligned, any
- * contents, used by one call at a time.  Sums are fp32 in a fixed order (the
- * same call gives the same bits every time), their rounding errors bounded
- * whatever the batch's length.  All pointers are DEVICE pointers of the current
- * device.  No allocation; asynchronous.
+ * contents, used by one call at a time.  It and the outputs must overlap nothing
+ * else.  Sums are fp32 in a fixed order (the same call gives the same bits every
+ * time), their rounding errors bounded whatever the batch's length.  All
+ * pointers are DEVICE pointers of the current device.  No allocation;
+ * asynchronous.
  * moe_balance_workspace returns 0 for sizes out of range.
- * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes),
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, overlap),
  * UNSUPPORTED (dtype), CUDA.
  */
 size_t moe_balance_workspace(int n_tokens, int n_experts, int n_segments);

@@ -923,6 +923,8 @@ bool pairs(const void *p, long long ld, int E, size_t size)
 
 bool rows_overlap(const void *a, long long lda, int wa, const void *b, long long ldb, int wb, int n,
                   int size);
+bool rows_meet(const void *p, long long ld, int w, int n, int size, const void *q, size_t bytes);
+bool ranges_meet(const void *p, size_t n, const void *q, size_t m);
 bool device_pointer_here(const void *p, int dev);
 int record_failure(int code, const char *msg);
 int record_success();
@@ -1007,6 +1009,24 @@ extern "C" int moe_balance_loss(const void *logits, int dtype, long long ld, int
     if (workspace_bytes < a.ws.bytes)
         return record_failure(MOE_ERR_INVALID_ARG,
                               "workspace below moe_balance_workspace(n, n_experts, n_segments)");
+    // what the call writes against everything else
+    const size_t n = n_tokens, S = n_segments;
+    const struct {
+        const void *p;
+        size_t bytes;
+    } range[] = {{workspace, a.ws.bytes}, {loss, 8}, {counts, 4 * S * n_experts}, {tokens, 4 * S},
+                 {prob, 4 * S * n_experts}, {lse, 4 * n}, {topk_idx, 4 * n * top_k},
+                 {seq_offsets, seq_offsets ? 4 * (S + 1) : 0}, {mask, mask ? n : 0}};
+    constexpr int kWritten = 6, kRanges = sizeof(range) / sizeof(range[0]);
+    for (int i = 0; i < kWritten; i++) {
+        bool meet = rows_meet(logits, ld, n_experts, n_tokens, (int)size_of(dtype), range[i].p,
+                              range[i].bytes);
+        for (int j = i + 1; j < kRanges; j++)
+            meet = meet || ranges_meet(range[i].p, range[i].bytes, range[j].p, range[j].bytes);
+        if (meet)
+            return record_failure(MOE_ERR_INVALID_ARG,
+                                  "an output or the workspace overlaps another argument");
+    }
     const int dev = current_device();
     if (dev < 0)
         return record_failure(MOE_ERR_CUDA, "no usable current CUDA device");

@@ -779,6 +779,24 @@ bool rows_overlap(const void *a, long long lda, int wa, const void *b, long long
     return lda != ldb || d < (long long)size * wa || d + (long long)size * wb > ld;
 }
 
+// Whether n rows of w elements of `size` bytes, ld apart, share bytes with the
+// range of `bytes` at q: none does when q lies in the gap behind a row.
+bool rows_meet(const void *p, long long ld, int w, int n, int size, const void *q, size_t bytes)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    const uintptr_t pitch = size * (uintptr_t)ld, row = size * (uintptr_t)w;
+    if (!bytes || b >= a + (n - 1) * pitch + row || b + bytes <= a)
+        return false;
+    return b < a || (b - a) % pitch < row || (b - a) % pitch + bytes > pitch;
+}
+
+// Whether two ranges share bytes.
+bool ranges_meet(const void *p, size_t n, const void *q, size_t m)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+    return n && m && a < b + m && b < a + n;
+}
+
 bool linear_gemm_fits(const W4Call &c);
 cudaError_t launch_linear_gemm(const W4Call &c, int bf16, int grad, int dev, int num_sms,
                                cudaStream_t st);
@@ -849,6 +867,24 @@ int run_linear(W4Call c, int dtype, int grad, void *workspace, size_t workspace_
                       workspace_bytes >= aligned_bytes(w.rows, c.n);
     if (copy && mis(workspace, 16))
         return record_failure(MOE_ERR_INVALID_ARG, "misaligned workspace (it needs 16 bytes)");
+    // what the call writes against what it reads besides
+    const size_t n_meta = (size_t)w.rows * (w.K / w.group);
+    const struct {
+        const void *p;
+        size_t bytes;
+    } read[] = {{w.codes, (size_t)w.rows * (w.K / 2)}, {w.scales, 2 * n_meta}, {w.zeros, n_meta},
+                {c.bias, c.bias ? 2 * (size_t)wout : 0}, {c.status, c.status ? 4u : 0u}};
+    const size_t ws_bytes = copy ? aligned_bytes(w.rows, c.n) : 0;
+    for (const auto &r : read) {
+        if (rows_meet(c.out, c.ldo, wout, c.n, 2, r.p, r.bytes))
+            return record_failure(MOE_ERR_INVALID_ARG,
+                                  "the output overlaps the matrix, the bias or the status word");
+        if (ranges_meet(workspace, ws_bytes, r.p, r.bytes))
+            return record_failure(MOE_ERR_INVALID_ARG, "the workspace overlaps another argument");
+    }
+    if (rows_meet(c.out, c.ldo, wout, c.n, 2, workspace, ws_bytes) ||
+        rows_meet(c.in, c.ldi, win, c.n, 2, workspace, ws_bytes))
+        return record_failure(MOE_ERR_INVALID_ARG, "the workspace overlaps another argument");
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) {

@@ -190,3 +190,61 @@ def test_gradient_without_ids_needs_top_k(monkeypatch):
     moe.balance_loss_grad(logits, idx, fwd, dloss)
     moe.balance_loss_grad(logits, idx, fwd, dloss, top_k=3)
     assert seen == [(None, 3), (idx.data_ptr(), 3), (idx.data_ptr(), 3)]
+
+
+def _overlaps(lib, rc):
+    return rc == -1 and "overlap" in lib.moe_last_error().decode()
+
+
+W = 96 * 128          # bytes of the codes of LIN, of which y's 4 rows take 768
+
+
+@pytest.mark.parametrize("kw,overlaps", [
+    (dict(bias=0x50000), True), (dict(bias=0x50000 + 766), True), (dict(bias=0x50000 + 768), False),
+    (dict(bias=0x50000 - 192), False), (dict(bias=0x50000 - 190), True),
+    (dict(bias=0x50000 + 192, ldy=192), False), (dict(bias=0x50000 + 194, ldy=192), True),
+    (dict(bias=0x50000 + 190, ldy=192), True), (dict(y=0x10000), True),
+    (dict(y=0x10000 + W - 2), True), (dict(y=0x10000 + W), False), (dict(y=0x20000 + 382), True),
+    (dict(y=0x20000 + 384), False), (dict(y=0x30000 - 766), True), (dict(y=0x30000 - 768), False),
+    (dict(status=0x50000 + 764), True), (dict(status=0x50000 + 768), False)])
+def test_linear_output_overlaps(lib, kw, overlaps):
+    """y against the matrix, the bias and the status word; a bias may lie in the
+    gaps between y's rows.  What does not overlap is refused for its device."""
+    rc = linear(lib, **kw)
+    assert rc != 0 and _overlaps(lib, rc) == overlaps
+
+
+COPY = dict(n=20, rows=95, ldx=95, ws=0x80000, ws_bytes=96 * 40)
+
+
+@pytest.mark.parametrize("kw,overlaps", [
+    (dict(), False), (dict(ws=0x40000), True), (dict(ws=0x40000 + 3792), True),
+    (dict(ws=0x40000 + 3808), False), (dict(ws=0x40000 - 96 * 40), False),
+    (dict(ws=0x40000 - 96 * 40 + 16), True), (dict(ws=0x50000 + 16), True),
+    (dict(ws=0x50000 + 20 * 512), False), (dict(ws=0x10000 + 95 * 128 - 16), True),
+    (dict(ws=0x10000 + 95 * 128), False), (dict(ws=0x20000 + 368), True),
+    (dict(ws=0x30000 + 176), True), (dict(ws=0x60000, status=0x60000 + 96 * 40 - 4), True),
+    (dict(ws=0x60000, status=0x60000 + 96 * 40), False),
+    # one that is too small, or not needed, is not used
+    (dict(ws=0x40000, ws_bytes=96 * 40 - 1), False), (dict(ws=0x40000, ldx=96), False)])
+def test_linear_input_grad_workspace_overlaps(lib, kw, overlaps):
+    rc = linear_grad(lib, **dict(COPY, **kw))
+    assert rc != 0 and _overlaps(lib, rc) == overlaps
+
+
+@pytest.mark.parametrize("kw,overlaps", [
+    (dict(), False), (dict(ws=0x10000), True), (dict(ws=0x10000 + 2048), False),
+    (dict(ws=0x20000), True), (dict(ws=0x30000), True), (dict(ws=0x40000), True),
+    (dict(ws=0x50000), True), (dict(ws=0x60000), True), (dict(ws=0x70000), True),
+    (dict(ws=0x90000, mask=0x90000 + 7), True), (dict(ws=0x90000, seq=0x90004), True),
+    (dict(lse=0x10000), True), (dict(lse=0x20000 + 60), True), (dict(lse=0x20000 + 64), False),
+    (dict(prob=0x40000 + 252), True), (dict(prob=0x40000 + 256), False),
+    (dict(loss=0x50000), True), (dict(tokens=0x30000 + 4), True), (dict(tokens=0x30000 + 8), False),
+    (dict(lse=0x10000 + 256, ld=96), False), (dict(lse=0x10000 + 352, ld=96), False),
+    (dict(lse=0x10000 + 356, ld=96), True), (dict(counts=0x10000 + 512, ld=192), False),
+    (dict(counts=0x10000 + 516, ld=192), True)])
+def test_balance_loss_overlaps(lib, kw, overlaps):
+    """The workspace and the outputs against everything; an output may lie in
+    the gaps between the logits' rows."""
+    rc = balance(lib, **kw)
+    assert rc != 0 and _overlaps(lib, rc) == overlaps
