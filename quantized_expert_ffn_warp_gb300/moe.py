@@ -537,6 +537,9 @@ def _batch(torch, types, logits, topk_idx, seq_offsets, mask):
         pi = _dense(topk_idx, "topk_idx", torch.int32, (n, k))
     if seq_offsets is not None:
         S = seq_offsets.numel() - 1
+        if S < 1:
+            _bad("seq_offsets: need int32 [S + 1] with S >= 1, got shape %s"
+                 % (tuple(seq_offsets.shape),))
         po = _dense(seq_offsets, "seq_offsets", torch.int32, (S + 1,))
     if mask is not None:
         pm = _dense(mask, "mask", torch.bool if mask.dtype is torch.bool else torch.uint8, (n,))

@@ -248,3 +248,15 @@ def test_balance_loss_overlaps(lib, kw, overlaps):
     the gaps between the logits' rows."""
     rc = balance(lib, **kw)
     assert rc != 0 and _overlaps(lib, rc) == overlaps
+
+
+@pytest.mark.parametrize("shape", [(0,), (1,), ()])
+def test_binding_refuses_offsets_without_a_segment(shape):
+    torch = pytest.importorskip("torch")
+    from quantized_expert_ffn_warp_gb300 import moe
+    seq = torch.zeros(shape, dtype=torch.int32)
+    logits, idx = torch.zeros((2, 4)), torch.zeros((2, 1), dtype=torch.int32)
+    with pytest.raises(moe.MoeError, match="seq_offsets"):
+        moe.balance_loss(logits, idx, seq)
+    with pytest.raises(moe.MoeError, match="seq_offsets"):
+        moe.balance_loss_grad(logits, idx, {}, torch.zeros(2), seq_offsets=seq)
