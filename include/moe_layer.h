@@ -413,10 +413,10 @@ int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const flo
  * product.  The same call gives the same bits every time.
  * All pointers are DEVICE pointers of the current device: codes and the rows
  * of x 16-byte aligned (ldx a multiple of 8), the others to their element.
- * status (int32 [1], may be NULL) gets MOE_STATUS_TIMEOUT or'ed in when a
- * pipeline wait gave up (the output of that call is incomplete); it is never
- * cleared here.  Asynchronous on `stream`; calls on different streams are
- * independent.
+ * When a pipeline wait gives up (after 2 s), the outputs that it concerns are
+ * NaN, and status (int32 [1], may be NULL) gets MOE_STATUS_TIMEOUT or'ed in; it
+ * is never cleared here.  Asynchronous on `stream`; calls on different streams
+ * are independent.
  * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, strides,
  * overlap), UNSUPPORTED (dtype, group_size), CUDA.
  */

@@ -21,6 +21,7 @@
 // unpacking and MMA together bounds it (without both 75 us).  Gradient: 2 tokens
 // 1027 x 2048 fp16 7.5 us, 8 tokens 14336 x 4096 bf16 15.3 us.
 #include <algorithm>
+#include <cmath>
 
 #include "w4.cuh"
 
@@ -343,11 +344,13 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 *abort_flag = 1;
             }
             float *red = reinterpret_cast<float *>(smem + G::red_off) + (buf * kWarps + warp) * G::out;
+            if (ok) {       // else the adders may still read what is there
 #pragma unroll
-            for (int r = 0; r < RT; r++)
+                for (int r = 0; r < RT; r++)
 #pragma unroll
-                for (int i = 0; i < 4; i++)
-                    red[(4 * r + i) * 32 + lane] = acc[r][i];
+                    for (int i = 0; i < 4; i++)
+                        red[(4 * r + i) * 32 + lane] = acc[r][i];
+            }
             __syncwarp();
             if (lane == 0)
                 bar_arrive(red_full + 8 * buf);
@@ -372,10 +375,13 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 ok = false;
                 *abort_flag = 1;
             }
+            // A sum that some warp did not wait for is no result.  A warp that gave up
+            // set the flag before its arrivals, which may complete this phase.
+            const float spoil = *abort_flag ? NAN : 0.f;
             if (o < kPairs)
                 for (int rb = 0; rb < a.rw_n; rb++) {
                     const float2 *p = red + (buf * kWarps + rb * a.kw_n) * kPairs;
-                    float v[2] = {};
+                    float v[2] = {spoil, spoil};
 #pragma unroll 8
                     for (int w = 0; w < a.kw_n; w++) {
                         const float2 q = p[w * kPairs];
@@ -612,6 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     drain(full, kGradStages, arrived, issued);
     __syncthreads();        // the rings become the sums' buffer
+    const bool spoilt = *abort_flag;        // what some warp did not wait for is no result
 
     constexpr int kOut = 8 * kGradCols;
     static_assert(4 * kWarps * kOut <= kWarps * kRing, "the sums fit in the rings");
@@ -627,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int w = 1; w < kWarps; w++)
             s += red[w * kOut + o];
-        red[o] = s;
+        red[o] = spoilt ? NAN : s;
     }
     if (splits > 1) {
         cluster_arrive();

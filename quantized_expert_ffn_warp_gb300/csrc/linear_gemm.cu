@@ -28,9 +28,10 @@
 // Measured in a replayed graph: 4096 tokens 14336 x 4096 fp16 278 us, 1730
 // TFLOP/s, bound by the tensor cores; gradient, 2000 tokens 4096 x 4096 bf16 44.5
 // us, 1510 TFLOP/s (288 tiles for 152 SMs: the second wave is not full); 33 tokens 6144 x 4096 bf16 15.4 us, bound by the dequantisation.
-// Every wait is bounded in time; on expiry the output is incomplete and the
-// caller's status word gets MOE_STATUS_TIMEOUT.
+// Every wait is bounded in time; on expiry the CTA's outputs (its cluster's) are
+// NaN and the caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -701,8 +702,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     if (warp == kMma0)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512u)
                      : "memory");
-    if (threadIdx.x == 0 && *abort_flag && c.status)
-        atomicOr(c.status, MOE_STATUS_TIMEOUT);
+    if (*abort_flag) {      // what a wait that gave up left out is no result: NaN
+        if (threadIdx.x == 0 && c.status)
+            atomicOr(c.status, MOE_STATUS_TIMEOUT);
+        float *part = reinterpret_cast<float *>(smem + G::b_off);
+        for (int t = tile0; t < tiles; t += tile_step)
+            for (int i = threadIdx.x; i < a.tok * kM; i += kGemmThreads) {
+                const int tok = t / a.mt * a.tok + i / kM, f = t % a.mt * kM + i % kM;
+                if (a.splits > 1)       // the sum over the cluster
+                    part[i] = NAN;
+                else if (tok < c.n && f < F)
+                    static_cast<T *>(c.out)[tok * c.ldo + f] = Q::from_float(NAN);
+            }
+    }
     if (a.splits > 1) {
         // the one tile of this cluster: rank r adds its share of the tokens
         cluster_arrive();
