@@ -380,3 +380,34 @@ def test_infinite_scale_of_the_last_group(n, rows, K, group, dtype):
     inf = float("inf")
     assert (y[:, -1] == inf).all() and torch.isfinite(y[:, :-1]).all()
     assert (dx[:, K - group:] == inf).all() and torch.isfinite(dx[:, :K - group]).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("n,rows,K,group", [
+    (2, 1 << 20, 32, 32), (8, 1 << 20, 128, 128), (40, 1 << 20, 32, 32), (300, 1 << 18, 64, 64),
+    (3, 48, 65536, 128), (8, 2000, 65536, 32), (20, 48, 65536, 64), (300, 200, 65536, 128),
+    (9, 5, 65536, 128), (1, 1 << 20, 256, 64), (524280, 9, 32, 32)])
+def test_long_contractions_exactly(n, rows, K, group, dtype):
+    """Activations of -1, 0 and 1, scales that are powers of two, so that every
+    weight is exact and every partial sum a multiple of the least scale below
+    2^24 of it: the output is the rounded exact sum, and a block that is left
+    out, read twice or taken from elsewhere shows."""
+    moe = _moe()
+    g = torch.Generator(device="cuda").manual_seed(rows + K)
+    codes = torch.randint(0, 256, (rows, K // 2), dtype=torch.uint8, device="cuda", generator=g)
+    zeros = torch.randint(0, 16, (rows, K // group), dtype=torch.uint8, device="cuda", generator=g)
+    # |q - z| <= 15 and 2^20 terms: one scale over the longest contraction
+    # (15 * 2^20 < 2^24), two where it is 2^16 long
+    exps = torch.zeros((rows, K // group), dtype=torch.int32, device="cuda")
+    if max(rows, K) <= 1 << 18:
+        exps = torch.randint(0, 2, exps.shape, dtype=torch.int32, device="cuda", generator=g)
+    scales = torch.ldexp(torch.full(exps.shape, 2.0 ** -6, device="cuda"), exps).half()
+    q = torch.stack((codes & 15, codes >> 4), 2).reshape(rows, K).float()
+    W = ((q - zeros.float().repeat_interleave(group, 1))
+         * scales.float().repeat_interleave(group, 1))
+    for call, width, w in ((moe.linear, K, W.t()), (moe.linear_input_grad, rows, W)):
+        x = torch.randint(-1, 2, (n, width), device="cuda", generator=g).to(DT[dtype])
+        assert width * 15 * (2 if exps.any() else 1) < 1 << 24
+        ref = (x.double() @ w.double()).to(DT[dtype])
+        got = call(x, codes, scales, zeros, group)
+        assert torch.equal(got, ref), (got != ref).sum()
