@@ -201,14 +201,6 @@ __device__ __forceinline__ uint4 ld_act(const void *p)
     return __ldg(reinterpret_cast<const uint4 *>(p));
 }
 
-// (a & mask) | 0x64006400: the two selected fields become fp16 1024 + field.
-__device__ __forceinline__ uint32_t lop_magic(uint32_t a, uint32_t mask)
-{
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(0x64006400u));
-    return d;
-}
-
 __device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b)
 {
     uint32_t d;

@@ -126,13 +126,6 @@ __device__ __forceinline__ int step_groups(const PackedRecs &pr, int j)
     return min(gps, pr.n_groups - j * gps);
 }
 
-__device__ __forceinline__ uint32_t lop_magic(uint32_t a, uint32_t mask)
-{
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(0x64006400u));
-    return d;
-}
-
 __device__ __forceinline__ uint32_t h2u(__half2 h)
 {
     return *reinterpret_cast<uint32_t *>(&h);

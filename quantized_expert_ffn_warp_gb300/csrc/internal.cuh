@@ -19,6 +19,16 @@ __device__ __forceinline__ void pdl_enter()
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// (a & mask) | magic: the word's two selected fields become fp16 1024 + field (with
+// 0x43004300, bf16 128 + field).
+__device__ __forceinline__ uint32_t lop_magic(uint32_t a, uint32_t mask,
+                                              uint32_t magic = 0x64006400u)
+{
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(a), "r"(mask), "r"(magic));
+    return d;
+}
+
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t st, Args... args)

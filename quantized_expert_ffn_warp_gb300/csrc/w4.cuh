@@ -13,13 +13,6 @@
 
 namespace qe {
 
-__device__ __forceinline__ uint32_t w4_field(uint32_t w, uint32_t mask, uint32_t magic)
-{
-    uint32_t d;
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(d) : "r"(w), "r"(mask), "r"(magic));
-    return d;
-}
-
 // A pair type's arithmetic.  Pairs are 32-bit words; fields of a word are the
 // nibbles i and i + 4 (its low and high half), i = 0..3.
 template <typename T>
@@ -51,10 +44,10 @@ struct W4<__half> {
     {
         const __half2 sixteenth = __float2half2_rn(0.0625f);
         const uint32_t w8 = w >> 8;
-        p[0] = u(__hsub2(h(w4_field(w, 0x000F000Fu, 0x64006400u)), h(z.lo)));
-        p[1] = u(__hfma2(h(w4_field(w, 0x00F000F0u, 0x64006400u)), sixteenth, h(z.hi)));
-        p[2] = u(__hsub2(h(w4_field(w8, 0x000F000Fu, 0x64006400u)), h(z.lo)));
-        p[3] = u(__hfma2(h(w4_field(w8, 0x00F000F0u, 0x64006400u)), sixteenth, h(z.hi)));
+        p[0] = u(__hsub2(h(lop_magic(w, 0x000F000Fu)), h(z.lo)));
+        p[1] = u(__hfma2(h(lop_magic(w, 0x00F000F0u)), sixteenth, h(z.hi)));
+        p[2] = u(__hsub2(h(lop_magic(w8, 0x000F000Fu)), h(z.lo)));
+        p[3] = u(__hfma2(h(lop_magic(w8, 0x00F000F0u)), sixteenth, h(z.hi)));
     }
     struct Scale {
         uint32_t s;
@@ -96,7 +89,7 @@ struct W4<__nv_bfloat16> {
     {
 #pragma unroll
         for (int i = 0; i < 4; i++)
-            p[i] = u(__hsub2(h(w4_field(w >> (4 * i), 0x000F000Fu, 0x43004300u)), h(z.lo)));
+            p[i] = u(__hsub2(h(lop_magic(w >> (4 * i), 0x000F000Fu, 0x43004300u)), h(z.lo)));
     }
     // An fp16 scale has 11 significant bits, bf16 8: the scale travels as the
     // sum of two bf16 values, so that the product below is rounded once.
