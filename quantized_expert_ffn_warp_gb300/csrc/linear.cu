@@ -16,10 +16,10 @@
 // way whatever the arithmetic does, and no warp waits for another.
 //
 // Measured in a replayed graph over more inputs than L2 holds: 1 token 2048 x
-// 2048 fp16 3.2 us (latency); 8 tokens 4096 x 14336 bf16 14.8 us; 3 tokens 32003
-// x 4096 fp16 19.8 us; 8 tokens 256000 x 4096 fp16 116 us, 4.8 TB/s: the issue of
+// 2048 fp16 3.2 us (latency); 8 tokens 4096 x 14336 bf16 14.9 us; 3 tokens 32003
+// x 4096 fp16 19.7 us; 8 tokens 256000 x 4096 fp16 114 us, 4.9 TB/s: the issue of
 // unpacking and MMA together bounds it (without both 75 us).  Gradient: 2 tokens
-// 1027 x 2048 fp16 7.5 us, 8 tokens 14336 x 4096 bf16 15.3 us.
+// 1027 x 2048 fp16 7.4 us, 8 tokens 14336 x 4096 bf16 15.4 us.
 #include <algorithm>
 #include <cmath>
 
@@ -281,6 +281,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 if (ok && !warp_wait(full + 8 * slot, parity, abort_flag)) {
                     ok = false;
                     *abort_flag = 1;
+                    __threadfence_block();
                 }
                 arrived += ok;
                 const uint32_t stage = ring + slot * G::stage;
@@ -342,15 +343,14 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
             if (ok && !warp_wait(red_empty + 8 * buf, red_parity, abort_flag)) {
                 ok = false;
                 *abort_flag = 1;
+                __threadfence_block();
             }
             float *red = reinterpret_cast<float *>(smem + G::red_off) + (buf * kWarps + warp) * G::out;
-            if (ok) {       // else the adders may still read what is there
 #pragma unroll
-                for (int r = 0; r < RT; r++)
+            for (int r = 0; r < RT; r++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        red[(4 * r + i) * 32 + lane] = acc[r][i];
-            }
+                for (int i = 0; i < 4; i++)
+                    red[(4 * r + i) * 32 + lane] = acc[r][i];
             __syncwarp();
             if (lane == 0)
                 bar_arrive(red_full + 8 * buf);
@@ -375,19 +375,21 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                 ok = false;
                 *abort_flag = 1;
             }
-            // A sum that some warp did not wait for is no result.  A warp that gave up
-            // set the flag before its arrivals, which may complete this phase.
-            const float spoil = *abort_flag ? NAN : 0.f;
             if (o < kPairs)
                 for (int rb = 0; rb < a.rw_n; rb++) {
                     const float2 *p = red + (buf * kWarps + rb * a.kw_n) * kPairs;
-                    float v[2] = {spoil, spoil};
+                    float v[2] = {};
 #pragma unroll 8
                     for (int w = 0; w < a.kw_n; w++) {
                         const float2 q = p[w * kPairs];
                         v[0] += q.x;
                         v[1] += q.y;
                     }
+                    // A sum that some warp did not wait for is no result: NaN.  A warp
+                    // that gave up set the flag before it arrives, or writes sums, out
+                    // of turn.
+                    __threadfence_block();
+                    const bool spoilt = *abort_flag;
                     const int row = (set * a.rw_n + rb) * 16 * RT + in_tile;
                     if (row >= rows)
                         continue;
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
                     for (int u = 0; u < 2; u++) {
                         if (tok + 2 * u >= c.n)
                             continue;
-                        float s = v[u] + bias;
+                        float s = spoilt ? NAN : v[u] + bias;
                         if (c.residual)
                             s += Q::to_float(static_cast<const T *>(c.residual)[(tok + 2 * u) * c.ldr + row]);
                         static_cast<T *>(c.out)[(tok + 2 * u) * c.ldo + row] = Q::from_float(s);
