@@ -410,7 +410,9 @@ int moe_ep_combine(const void *x, int n_tokens, int hidden, int top_k, const flo
  * Sums are fp32, with bias and residual added before the one rounding to the
  * output type.  Up to 8 tokens a group's fp32 sum of x * (q - zero) is scaled;
  * for more, each weight is rounded once to the activations' type before the
- * product.  The same call gives the same bits every time.
+ * product (in fp16 one above 65504 becomes an infinity), so that a token's
+ * result may differ by that rounding between calls of up to 8 and of more
+ * tokens.  The same call gives the same bits every time.
  * All pointers are DEVICE pointers of the current device: codes and the rows
  * of x 16-byte aligned (ldx a multiple of 8), the others to their element.
  * When a pipeline wait gives up (after 2 s), the outputs that it concerns are
@@ -429,10 +431,10 @@ int moe_linear(const void *codes, const void *scales, const void *zeros, int row
  * Gradient of moe_linear's input through the frozen 4-bit matrix:
  *   dx[t][k] = sum_r dy[t][r] W[r][k]
  * dy [n_tokens][rows] and dx [n_tokens][cols] of type dtype with row strides
- * lddy, lddx; sums are fp32, and each weight is rounded once to that type (for
- * bf16 and groups of 128, up to 8 tokens, each product of a gradient and its
- * scale instead).  (The gradient of bias is the sum of dy over the tokens, that
- * of residual dy.)
+ * lddy, lddx; sums are fp32, and each weight is rounded once to that type (in
+ * fp16 one above 65504 becomes an infinity; for bf16 and groups of 128, up to 8
+ * tokens, each product of a gradient and its scale is rounded instead).  (The
+ * gradient of bias is the sum of dy over the tokens, that of residual dy.)
  * Pointers as for moe_linear; codes 16-byte aligned, dy and dx to their
  * element.  dx and the workspace must overlap nothing else.
  * More than 8 rows of dy that do not lie on 16-byte boundaries (an odd number of

@@ -425,7 +425,13 @@ __global__ void __launch_bounds__(32 * (kWarps + kAdders), 1)
 //   bf16, groups of 128: one scale per row holds for all columns of the CTA, so
 //     it multiplies the gradients, dy * s rounded once to bf16 (fp32 range);
 //   otherwise it is folded into the weights, (q - z) * s rounded once (in fp16
-//     a product of gradient and scale could fall below the normal range).
+//     a product of gradient and scale could fall below the normal range; a
+//     weight above 65504 becomes an infinity).
+// Either way one factor of each term has the activations' type: exact q - z and
+// sums scaled per group, as in the forward product, are open only where the
+// contraction runs along a group.  Relative error of the output (2-norm, against
+// 64 bits) 0.0024 instead of the 0.0017 of its own rounding in bf16, 0.00027
+// instead of 0.00021 in fp16.
 // The warps of a CTA and the CTAs of a cluster (1 to 8) split the rows; the
 // partial sums meet in shared and distributed shared memory, in a fixed order.
 constexpr int kThreads = 32 * kWarps;

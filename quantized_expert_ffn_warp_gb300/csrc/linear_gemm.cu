@@ -16,6 +16,16 @@
 //     puts two rows' nibbles into one word) and stores them in the 16-lane x
 //     256-bit tensor memory layout, lane 8 j + g of a quarter holding column
 //     4 g + j.
+// Why the weights are rounded: an MMA multiplies operands of one 16-bit type, and
+// a scale changes with the feature and along the contraction, so it can be
+// folded neither into the tokens nor into the finished sums.  The weights in two
+// 16-bit parts would take twice the MMAs (4096 tokens 14336 x 4096 fp16 280 us;
+// with the contraction twice as long 543 us), scaled sums per group a pass over the
+// accumulators every 32 to 128 steps of the contraction.  With the weights as the
+// activations' type holds them the output's relative error (2-norm, against 64
+// bits) is 0.0023 instead of the 0.0017 of its own rounding in bf16, 0.00028
+// instead of 0.00021 in fp16.  A weight beyond fp16's range (a scale above 4366)
+// becomes an infinity.
 // Roles of a persistent CTA (one per SM): a code producer and a B producer
 // (TMA), three groups of four dequant warps taking blocks in turn, one or two
 // MMA warps, four epilogue warps.  Tiles of more than 128 tokens need one MMA
@@ -25,9 +35,10 @@
 // A matrix with too few tiles for the SMs is split along the contraction over a
 // cluster of 2 to 8 CTAs, whose partial tiles meet in distributed shared
 // memory, in rank order.
-// Measured in a replayed graph: 4096 tokens 14336 x 4096 fp16 278 us, 1730
-// TFLOP/s, bound by the tensor cores; gradient, 2000 tokens 4096 x 4096 bf16 44.5
-// us, 1510 TFLOP/s (288 tiles for 152 SMs: the second wave is not full); 33 tokens 6144 x 4096 bf16 15.4 us, bound by the dequantisation.
+// Measured in a replayed graph: 4096 tokens 14336 x 4096 fp16 280 us, 1720
+// TFLOP/s, bound by the tensor cores; gradient, 2000 tokens 4096 x 4096 bf16 44.4
+// us, 1510 TFLOP/s (288 tiles for 152 SMs: the second wave is not full); 33 tokens
+// 6144 x 4096 bf16 15.6 us, bound by the dequantisation.
 // Every wait is bounded in time; on expiry the CTA's outputs (its cluster's) are
 // NaN and the caller's status word gets MOE_STATUS_TIMEOUT.
 #include <algorithm>
