@@ -518,6 +518,113 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
                           const float *dloss, const float *topk_w, const float *dtopk_w,
                           void *dlogits, long long ldd, void *stream);
 
+/*
+ * Log probabilities of given tokens from the logits of a vocabulary head
+ * (moe_linear), with the entropy of their distribution and its likeliest tokens.
+ * The pages have no counterpart: they sample on the host.  It serves whoever
+ * scores or samples what the model answers, and whoever tunes it (the loss of a
+ * batch is a weighted sum of -logp).
+ * For token t with m = max_v l[t][v] and logsum = log sum_v exp(l[t][v] - m):
+ *   logp[t]     = l[t][targets[t]] - m - logsum; 0 for a target outside
+ *                 [0, vocab), a position without one
+ *   entropy[t]  = -sum_v p_v log p_v, p = softmax(l[t])
+ *   stats[t]    = (m, logsum): kept apart, so that log p keeps logsum next to a
+ *                 large m; m + logsum is the log-sum-exp
+ *   top_ids[t]  = the `top` tokens of the largest logits in falling order, ties to
+ *                 the lower id (a NaN ranks like -inf), top_logp[t] their log
+ *                 probabilities
+ * A logit of -inf has probability 0 and adds nothing to the entropy; a row of
+ * nothing but -inf has stats (-inf, 0), entropy 0 and log probabilities -inf.  A
+ * NaN or +inf makes its row's stats[1], entropy and log probabilities NaN.
+ * logits [n_tokens][vocab] of type dtype (MOE_FP32, MOE_FP16, MOE_BF16) with row
+ * stride ld, rows at any element; targets int32 [n] and logp fp32 [n] (both may be
+ * NULL); entropy fp32 [n]; stats fp32 [n][2], 8-byte aligned; top_ids int32
+ * [n][top] and top_logp fp32 [n][top] (not read for top = 0).  n_tokens 1 ..
+ * 67108864, vocab 1 .. 1048576, top 0 .. min(32, vocab).
+ * workspace: moe_token_logprobs_workspace(n, vocab, dtype, top) bytes, 256-byte
+ * aligned, any contents, used by one call at a time; the size is 0, and workspace
+ * may be NULL, when a row is not divided (more than some hundred tokens).
+ * It and the outputs must overlap nothing else.  The same call gives the same
+ * bits every time.  All pointers are DEVICE pointers of the current device.  No
+ * allocation; asynchronous.  moe_token_logprobs_workspace returns 0 for sizes out
+ * of range.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, overlap),
+ * UNSUPPORTED (dtype), CUDA.
+ */
+size_t moe_token_logprobs_workspace(int n_tokens, int vocab, int dtype, int top);
+int moe_token_logprobs(const void *logits, int dtype, long long ld, int n_tokens, int vocab,
+                       const int32_t *targets, int top, float *logp, float *entropy,
+                       float *stats, int32_t *top_ids, float *top_logp, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Gradient of moe_token_logprobs's logp and entropy in the logits:
+ *   dlogits[t][v] = dlogp[t] (1[v = targets[t]] - p_v)
+ *                 - dentropy[t] p_v (log p_v + entropy[t])
+ * from its stats and entropy.  dlogp, dentropy fp32 [n]: one of them may be NULL
+ * and adds nothing then (entropy is not read without dentropy, targets not without
+ * dlogp).  A target outside [0, vocab) takes nothing from dlogp, whatever it holds;
+ * without dentropy its row is 0 and its logits are not read.  Rows of nothing but
+ * -inf get 0, and so does a logit of -inf from the entropy.
+ * dlogits has the type of logits, row stride ldd, and may be logits itself.
+ * Errors: those of moe_token_logprobs.
+ */
+int moe_token_logprobs_grad(const void *logits, int dtype, long long ld, int n_tokens, int vocab,
+                            const int32_t *targets, const float *stats, const float *entropy,
+                            const float *dlogp, const float *dentropy, void *dlogits,
+                            long long ldd, void *stream);
+
+/*
+ * The norm behind a block, its gate, the scaled residual stream, and the norm in
+ * front of the next block ("Flash-MoE" article, section 3: two-pass RMSNorm and
+ * the residual among the kernels of a layer), in one pass:
+ *   v      = gain * y / sqrt(mean(y^2) + eps)     (gain NULL: v = y)
+ *   out    = scale * resid + gate * v             (gate NULL: no gate)
+ *   xn     = next_gain * out / sqrt(mean(out^2) + eps)     (xn NULL: left out)
+ *   stats[t] = the two factors 1 / sqrt(...), 1 where one is left out
+ * The means and the sums are fp32, xn is computed from out before its rounding,
+ * and out and xn are rounded once.  (moe_rmsnorm keeps its own, fixed arithmetic:
+ * it is what moe_forward_prenorm routes on.)
+ * resid, y, out, xn [n_tokens][hidden] are fp16 or bf16 (dtype), rows 16-byte
+ * aligned with strides ld_*, multiples of 8; gain, next_gain [hidden] of that type,
+ * 16-byte aligned; gate of that type [hidden], 16-byte aligned, or with
+ * gate_per_token = 1 [n_tokens]; stats fp32 [n][2], 8-byte aligned.  out may be
+ * resid itself; otherwise the outputs must overlap nothing else.  hidden a multiple
+ * of 8 in 8 .. 16384, n_tokens 1 .. 67108864, eps finite and >= 0, scale finite.
+ * The same call gives the same bits every time.  All pointers are DEVICE pointers of
+ * the current device.  No allocation; asynchronous.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, strides,
+ * overlap), UNSUPPORTED (dtype), CUDA.
+ */
+int moe_residual_norm(const void *resid, long long ld_resid, const void *y, long long ld_y,
+                      int dtype, int n_tokens, int hidden, const void *gain, const void *gate,
+                      int gate_per_token, float scale, const void *next_gain, float eps,
+                      void *out, long long ld_out, void *xn, long long ld_xn, float *stats,
+                      void *stream);
+
+/*
+ * Gradients of moe_residual_norm, from the gradients dout and dxn that arrive at
+ * out and xn (one of them may be NULL), its out and stats, and y:
+ *   dresid, dy [n][hidden] of type dtype; dgain, dnext_gain fp32 [hidden];
+ *   dgate fp32 [hidden], or [n] with gate_per_token = 1.
+ * out and next_gain are not read without dxn.  dgain, dgate and dnext_gain may be
+ * NULL; they are summed in fp32 in a fixed order, in chains of at most 256 tokens
+ * and a compensated sum of those.  dresid may be dout itself.
+ * workspace: moe_residual_norm_grad_workspace(n, hidden) bytes, 16-byte aligned, any
+ * contents, used by one call at a time; only dresid, dy and a dgate per token need
+ * none (NULL).  The function returns 0 for sizes out of range.
+ * Errors: those of moe_residual_norm.
+ */
+size_t moe_residual_norm_grad_workspace(int n_tokens, int hidden);
+int moe_residual_norm_grad(const void *dout, long long ld_dout, const void *dxn,
+                           long long ld_dxn, const void *out, long long ld_out, const void *y,
+                           long long ld_y, const float *stats, int dtype, int n_tokens,
+                           int hidden, const void *gain, const void *gate, int gate_per_token,
+                           float scale, const void *next_gain, void *dresid,
+                           long long ld_dresid, void *dy, long long ld_dy, float *dgain,
+                           float *dgate, float *dnext_gain, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /* Facts about the layer (no device work). */
 int moe_layer_info(const moe_layer_t *layer, moe_layer_info_t *info);
 

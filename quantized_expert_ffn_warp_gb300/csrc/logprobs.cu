@@ -1,0 +1,578 @@
+// Log probabilities of given tokens, the entropy of their distribution, and the
+// likeliest tokens, from rows of logits l [V]; and the gradient of the first two.
+//   m = max l,  s = sum_v e^(l_v - m),  logsum = log s
+//   logp    = (l_target - m) - logsum
+//   entropy = logsum - (1/s) sum_v e^(l_v - m) (l_v - m)     (a sum of terms >= 0)
+//   dl_v    = g_logp (1[v = target] - p_v) - g_ent p_v (log p_v + entropy)
+// m and logsum are kept apart: their sum could not hold logsum next to a large m.
+//
+// One pass over the row: each thread holds the running max of its values and the
+// two sums against it.  The likeliest tokens come from the same pass: a warp keeps
+// its best 32 in its lanes, sorted, and looks only at words whose largest value
+// reaches the best k-th value that a warp of the block holds; a key is the value's
+// order and the complement of its index, so that ties go to the lowest index in
+// whatever order they are met.
+#include <algorithm>
+
+#include "args.cuh"
+#include "vec.cuh"
+
+namespace qe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kMaxTokens = 1 << 26, kMaxVocab = 1 << 20, kMaxTop = 32;
+constexpr int kWordsPerThread = 4;      // 16-byte loads that a thread has under way
+constexpr int kMaxSplits = 64;          // blocks of one row
+constexpr float kFar = -150.f;          // e^kFar is 0 in fp32, kFar is finite
+
+// fp32 values as unsigned numbers in their order; a NaN like -inf, -0 like 0.
+__device__ __forceinline__ unsigned order_of(float x)
+{
+    x = x == x ? x + 0.f : -INFINITY;
+    const unsigned u = __float_as_uint(x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(unsigned o)
+{
+    return __uint_as_float(o & 0x80000000u ? o ^ 0x80000000u : ~o);
+}
+using Key = unsigned long long;
+__device__ __forceinline__ Key key_of(float x, int i)
+{
+    return (Key)order_of(x) << 32 | (unsigned)~i;
+}
+
+// Running max and the sums against it.
+struct Sums {
+    float m, s, sd;     // max, sum e^(l - m), sum e^(l - m) (l - m)
+
+    __device__ __forceinline__ float ref() const { return m == -INFINITY ? 0.f : m; }
+    // Sums against a max of at least m.
+    __device__ __forceinline__ void raise(float max)
+    {
+        const float d = fmaxf(m - (max == -INFINITY ? 0.f : max), kFar);
+        const float f = ex2(d * kLog2E);
+        sd = f * (sd + s * d);
+        s *= f;
+        m = max;
+    }
+    __device__ __forceinline__ void join(float m2, float s2, float sd2)
+    {
+        Sums o = {m2, s2, sd2};
+        const float max = fmaxf(m, m2);
+        raise(max);
+        o.raise(max);
+        s += o.s;
+        sd += o.sd;
+    }
+};
+
+__device__ __forceinline__ Key shfl_key(Key k, int src)
+{
+    return __shfl_sync(0xffffffffu, k, src);
+}
+
+// Puts c into the warp's list, sorted in falling order over its lanes.
+__device__ __forceinline__ void insert(Key &list, Key c)
+{
+    const int lane = threadIdx.x & 31;
+    const int at = __popc(__ballot_sync(0xffffffffu, list > c));
+    const Key up = __shfl_up_sync(0xffffffffu, list, 1);
+    list = lane < at ? list : lane == at ? c : up;
+}
+
+// The best 32 of two sorted lists, sorted: the larger of each value and its
+// mirror image are a bitonic sequence.
+__device__ __forceinline__ Key merge(Key a, Key b)
+{
+    const int lane = threadIdx.x & 31;
+    const Key r = shfl_key(b, 31 - lane);
+    a = a > r ? a : r;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const Key o = __shfl_xor_sync(0xffffffffu, a, d);
+        a = ((lane & d) == 0) == (a > o) ? a : o;
+    }
+    return a;
+}
+
+// The k-th largest of the lanes' values (a bitonic sort).
+__device__ __forceinline__ float kth_of_lanes(float v, int k)
+{
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+        for (int d = size / 2; d > 0; d >>= 1) {
+            const float o = __shfl_xor_sync(0xffffffffu, v, d);
+            const bool larger = ((lane & d) == 0) == ((lane & size) == 0);
+            v = larger ? fmaxf(v, o) : fminf(v, o);
+        }
+    return __shfl_sync(0xffffffffu, v, k - 1);
+}
+
+struct LogprobArgs {
+    const void *logits;
+    long long ld;
+    int n, V, top;
+    int splits, per;        // blocks of a row, words of one
+    const int32_t *targets;
+    float *logp, *entropy;
+    float2 *stats;
+    int32_t *top_ids;
+    float *top_logp;
+    float4 *part;           // [n][splits] sums of the blocks
+    Key *part_keys;         // [n][splits][32]
+};
+
+struct Block {
+    float4 sums[kWarps];
+    Key keys[kWarps][32];
+    unsigned bound;         // order of the best k-th value that a warp holds
+};
+
+// Joins the warps' sums and lists; every thread of warp 0 gets the result.
+template <bool TOP>
+__device__ __forceinline__ void join_warps(Block &sm, Sums &t, Key &list)
+{
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1)
+        t.join(__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
+               __shfl_xor_sync(0xffffffffu, t.sd, d));
+    if (lane == 0)
+        sm.sums[warp] = make_float4(t.m, t.s, t.sd, 0.f);
+    if (TOP)
+        sm.keys[warp][lane] = list;
+    __syncthreads();
+    if (warp == 0) {
+        const float4 q = lane < kWarps ? sm.sums[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        t = {q.x, q.y, q.z};
+#pragma unroll
+        for (int d = kWarps / 2; d > 0; d >>= 1)
+            t.join(__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
+                   __shfl_xor_sync(0xffffffffu, t.sd, d));
+        t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0),
+             __shfl_sync(0xffffffffu, t.sd, 0)};
+    }
+    if (TOP) {
+#pragma unroll
+        for (int half = kWarps / 2; half > 0; half >>= 1) {
+            if (warp < half) {
+                list = merge(list, sm.keys[warp + half][lane]);
+                sm.keys[warp][lane] = list;
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// A row's results, by warp 0.
+template <typename T, bool TOP>
+__device__ __forceinline__ void finish_row(const LogprobArgs &a, long long t, const Sums &u,
+                                           Key list)
+{
+    const int lane = threadIdx.x & 31;
+    const bool empty = u.m == -INFINITY && u.s == 0.f;  // nothing but -inf
+    const float logsum = empty ? 0.f : logf(u.s);
+    if (lane == 0) {
+        a.stats[t] = make_float2(u.m, logsum);
+        a.entropy[t] = empty ? 0.f : logsum - u.sd / u.s;
+        if (a.targets) {
+            const int v = a.targets[t];
+            float lp = 0.f;
+            if (v >= 0 && v < a.V) {
+                const float x = to_float<T>(static_cast<const T *>(a.logits)[t * a.ld + v]);
+                lp = empty ? -INFINITY : (x - u.m) - logsum;
+            }
+            a.logp[t] = lp;
+        }
+    }
+    if (TOP && lane < a.top) {
+        a.top_ids[t * a.top + lane] = ~(unsigned)list;
+        a.top_logp[t * a.top + lane] =
+            empty ? -INFINITY : (value_of((unsigned)(list >> 32)) - u.m) - logsum;
+    }
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
+{
+    constexpr int N = Vec<T>::N, U = kWordsPerThread;
+    __shared__ Block sm;
+    pdl_enter();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
+        const RowWords<T> row(static_cast<const T *>(a.logits) + t * a.ld, a.V);
+        const int lo = blockIdx.x * a.per, hi = min(row.count, lo + a.per);
+        Sums u = {-INFINITY, 0.f, 0.f};
+        Key list = 0, kth = 0;
+        if (TOP) {
+            if (threadIdx.x == 0)
+                sm.bound = 0;
+            __syncthreads();
+        }
+        float low[N];
+#pragma unroll
+        for (int e = 0; e < N; e++)
+            low[e] = -INFINITY;
+        const uint4 none = pack<T>(low);
+        uint4 next[U];
+        const auto load = [&](int at) {
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                const int v = at + i * kThreads;
+                next[i] = v < hi ? row.load(v, -INFINITY) : none;
+            }
+        };
+        load(lo + threadIdx.x);
+        for (int at = lo + warp * 32; at < hi; at += U * kThreads) {
+            float x[U][N], top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                unpack<T>(next[i], x[i]);
+#pragma unroll
+                for (int e = 0; e < N; e++)
+                    top = fmaxf(top, x[i][e]);
+            }
+            load(at + lane + U * kThreads);
+            if (TOP) {
+                float bound = value_of(max(*(volatile unsigned *)&sm.bound, order_of(-INFINITY)));
+                if (at == lo + warp * 32)
+                    bound = fmaxf(bound, kth_of_lanes(top, a.top));
+                if (__any_sync(0xffffffffu, top >= bound)) {
+                    unsigned mask = 0;
+#pragma unroll
+                    for (int i = 0; i < U; i++)
+#pragma unroll
+                        for (int e = 0; e < N; e++)
+                            mask |= !(x[i][e] < bound) ? 1u << (i * N + e) : 0u;
+                    const Key before = kth;
+                    while (__any_sync(0xffffffffu, mask != 0)) {
+                        Key c = 0;
+                        if (mask) {
+                            const int b = __ffs(mask) - 1;
+                            const int i = row.first(at + lane + b / N * kThreads) + b % N;
+                            // words past the block's end were filled
+                            if (i >= 0 && i < a.V && at + lane + b / N * kThreads < hi)
+                                c = key_of(to_float<T>(row.row[i]), i);
+                            mask &= mask - 1;
+                        }
+                        unsigned offers = __ballot_sync(0xffffffffu, c > kth);
+                        while (offers) {
+                            const Key k = shfl_key(c, __ffs(offers) - 1);
+                            if (k > kth) {
+                                insert(list, k);
+                                kth = shfl_key(list, a.top - 1);
+                            }
+                            offers &= offers - 1;
+                        }
+                    }
+                    if (lane == 0 && kth != before)
+                        atomicMax(&sm.bound, (unsigned)(kth >> 32));
+                }
+            }
+            if (top > u.m)
+                u.raise(top);
+            const float m = u.ref();
+            float s[U], sd[U];
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                s[i] = sd[i] = 0.f;
+#pragma unroll
+                for (int e = 0; e < N; e++) {
+                    const float d = max_nan(x[i][e] - m, kFar);
+                    const float p = ex2(d * kLog2E);
+                    s[i] += p;
+                    sd[i] = fmaf(p, d, sd[i]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                u.s += s[i];
+                u.sd += sd[i];
+            }
+        }
+        join_warps<TOP>(sm, u, list);
+        if (warp == 0) {
+            if (a.splits == 1) {
+                finish_row<T, TOP>(a, t, u, list);
+            } else {
+                const long long at = t * a.splits + blockIdx.x;
+                if (lane == 0)
+                    a.part[at] = make_float4(u.m, u.s, u.sd, 0.f);
+                if (TOP)
+                    a.part_keys[at * 32 + lane] = list;
+            }
+        }
+        __syncthreads();        // the next row's sums go into the same memory
+    }
+}
+
+// Joins the blocks of each row.
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
+{
+    __shared__ Block sm;
+    pdl_enter();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long t = blockIdx.x, at = t * a.splits;
+    Sums u = {-INFINITY, 0.f, 0.f};
+    if (threadIdx.x < a.splits) {       // at most kMaxSplits of them
+        const float4 q = a.part[at + threadIdx.x];
+        u = {q.x, q.y, q.z};
+    }
+    Key list = 0;
+    if (TOP)
+        for (int i = warp; i < a.splits; i += kWarps)
+            list = merge(list, a.part_keys[(at + i) * 32 + lane]);
+    join_warps<TOP>(sm, u, list);
+    if (warp == 0)
+        finish_row<T, TOP>(a, t, u, list);
+}
+
+// Words of the longest row, whatever its address.
+int most_words(int V, int per) { return (V + per - 1 + per - 1) / per; }
+
+// Blocks of a row: enough for a block on every SM four times over, each with a
+// load of kWordsPerThread / 2 words per thread at least.  Asks no device, since
+// the workspace's size follows from it.
+int row_splits(int n, int V, int size)
+{
+    const int words = most_words(V, 16 / size);
+    const int want = 4 * 152 / std::min(n, 4 * 152);
+    const int most = (words + kThreads * kWordsPerThread / 2 - 1) / (kThreads * kWordsPerThread / 2);
+    return std::max(1, std::min({want, most, kMaxSplits}));
+}
+
+size_t key_offset(int n, int splits) { return ((size_t)n * splits * sizeof(float4) + 255) / 256 * 256; }
+
+size_t logprob_ws(int n, int V, int size, int top)
+{
+    const int splits = row_splits(n, V, size);
+    if (splits == 1)
+        return 0;
+    return key_offset(n, splits) + (top ? (size_t)n * splits * 32 * sizeof(Key) : 0);
+}
+
+template <typename T, bool TOP>
+cudaError_t launch_top(const LogprobArgs &a, cudaStream_t st)
+{
+    cudaError_t e = launch_pdl(logprobs_kernel<T, TOP>, dim3(a.splits, std::min(a.n, 65535)),
+                               dim3(kThreads), 0, st, a);
+    if (e == cudaSuccess && a.splits > 1)
+        e = launch_pdl(logprobs_join_kernel<T, TOP>, dim3(a.n), dim3(kThreads), 0, st, a);
+    return e;
+}
+template <typename T>
+cudaError_t launch_logprobs(const LogprobArgs &a, cudaStream_t st)
+{
+    return a.top ? launch_top<T, true>(a, st) : launch_top<T, false>(a, st);
+}
+
+struct LogprobGradArgs {
+    const void *logits;
+    long long ld;
+    int n, V;
+    const int32_t *targets;
+    const float2 *stats;
+    const float *entropy, *dlogp, *dent;
+    void *out;
+    long long ldo;
+    bool aligned;       // the rows of both lie alike in their 16-byte words
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a)
+{
+    constexpr int N = Vec<T>::N, U = kWordsPerThread;
+    pdl_enter();
+    for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
+        const RowWords<T> row(static_cast<const T *>(a.logits) + t * a.ld, a.V);
+        T *out = static_cast<T *>(a.out) + t * a.ldo;
+        int target = a.targets ? a.targets[t] : -1;
+        if (target >= a.V)
+            target = -1;
+        const float gl = target >= 0 && a.dlogp ? a.dlogp[t] : 0.f;
+        const float2 st = a.stats[t];
+        const float ge = a.dent ? a.dent[t] : 0.f, ent = a.dent ? a.entropy[t] : 0.f;
+        // a token that takes no part, or a row of nothing but -inf
+        const bool zero = (target < 0 || !a.dlogp) && !a.dent;
+        const bool none = zero || (st.x == -INFINITY && st.y == 0.f);
+        const int v0 = blockIdx.x * (U * kThreads) + threadIdx.x;
+        uint4 q[U];
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int v = v0 + i * kThreads;
+            if (!none && v < row.count)
+                q[i] = row.load(v, 0.f);
+        }
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int v = v0 + i * kThreads;
+            if (v >= row.count)
+                break;
+            float x[N];
+            if (none) {
+#pragma unroll
+                for (int e = 0; e < N; e++)
+                    x[e] = 0.f;
+            } else {
+                unpack<T>(q[i], x);
+#pragma unroll
+                for (int e = 0; e < N; e++) {
+                    const float d = max_nan((x[e] - st.x) - st.y, kFar);
+                    const float p = ex2(d * kLog2E);
+                    x[e] = -p * fmaf(ge, d + ent, gl);
+                    if (row.first(v) + e == target)
+                        x[e] += gl;
+                }
+            }
+            if (a.aligned && row.whole(v)) {
+                *reinterpret_cast<uint4 *>(out + row.first(v)) = pack<T>(x);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; e++) {
+                    const int c = row.first(v) + e;
+                    if (c >= 0 && c < a.V)
+                        out[c] = from_float<T>(x[e]);
+                }
+            }
+        }
+    }
+}
+
+template <typename T>
+cudaError_t launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t st)
+{
+    constexpr int per = kThreads * kWordsPerThread;
+    const int words = most_words(a.V, Vec<T>::N);
+    return launch_pdl(logprobs_grad_kernel<T>, dim3((words + per - 1) / per, std::min(a.n, 65535)),
+                      dim3(kThreads), 0, st, a);
+}
+
+int check_sizes(int dtype, int n, int V)
+{
+    if (dtype != MOE_FP16 && dtype != MOE_BF16 && dtype != MOE_FP32)
+        return record_failure(MOE_ERR_UNSUPPORTED, "dtype must be MOE_FP16, MOE_BF16 or MOE_FP32");
+    if (n < 1 || n > kMaxTokens)
+        return record_failure(MOE_ERR_INVALID_ARG, "n_tokens must be in 1..67108864");
+    if (V < 1 || V > kMaxVocab)
+        return record_failure(MOE_ERR_INVALID_ARG, "vocab must be in 1..1048576");
+    return MOE_OK;
+}
+
+int size_of(int dtype) { return dtype == MOE_FP32 ? 4 : 2; }
+
+}  // namespace
+
+}  // namespace qe
+
+extern "C" size_t moe_token_logprobs_workspace(int n_tokens, int vocab, int dtype, int top)
+{
+    using namespace qe;
+    if (n_tokens < 1 || n_tokens > kMaxTokens || vocab < 1 || vocab > kMaxVocab || top < 0 ||
+        top > kMaxTop || dtype < MOE_FP16 || dtype > MOE_FP32)
+        return 0;
+    return logprob_ws(n_tokens, vocab, size_of(dtype), top);
+}
+
+extern "C" int moe_token_logprobs(const void *logits, int dtype, long long ld, int n_tokens,
+                                  int vocab, const int32_t *targets, int top, float *logp,
+                                  float *entropy, float *stats, int32_t *top_ids, float *top_logp,
+                                  void *workspace, size_t workspace_bytes, void *stream)
+{
+    using namespace qe;
+    const int rc = check_sizes(dtype, n_tokens, vocab);
+    if (rc)
+        return rc;
+    if (top < 0 || top > kMaxTop || top > vocab)
+        return record_failure(MOE_ERR_INVALID_ARG, "top must be in 0..min(32, vocab)");
+    if (!logits || !entropy || !stats || (targets && !logp) || (top && (!top_ids || !top_logp)))
+        return record_failure(MOE_ERR_INVALID_ARG, "null pointer argument");
+    const int size = size_of(dtype);
+    const size_t need = logprob_ws(n_tokens, vocab, size, top), n = n_tokens;
+    if (need && (!workspace || workspace_bytes < need))
+        return record_failure(MOE_ERR_INVALID_ARG,
+                              "workspace below moe_token_logprobs_workspace(...)");
+    const Arg args[] = {rows_arg(logits, ld, vocab, n_tokens, size, size),
+                        flat_arg(targets, n, 4),
+                        flat_arg(targets ? logp : nullptr, n, 4, true),
+                        flat_arg(entropy, n, 4, true),
+                        flat_arg(stats, n, 8, true),
+                        flat_arg(top ? top_ids : nullptr, n * top, 4, true),
+                        flat_arg(top ? top_logp : nullptr, n * top, 4, true),
+                        flat_arg(need ? workspace : nullptr, (need + 255) / 256, 256, true)};
+    int dev, sms;
+    if (const int bad = check_args(args, sizeof(args) / sizeof(args[0]), &dev, &sms))
+        return bad;
+    LogprobArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.n = n_tokens;
+    a.V = vocab;
+    a.top = top;
+    a.splits = row_splits(n_tokens, vocab, size);
+    a.per = (most_words(vocab, 16 / size) + a.splits - 1) / a.splits;
+    a.targets = targets;
+    a.logp = logp;
+    a.entropy = entropy;
+    a.stats = reinterpret_cast<float2 *>(stats);
+    a.top_ids = top_ids;
+    a.top_logp = top_logp;
+    a.part = static_cast<float4 *>(workspace);
+    a.part_keys = reinterpret_cast<Key *>(static_cast<char *>(workspace) +
+                                          key_offset(n_tokens, a.splits));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launch_result(dtype == MOE_FP32   ? launch_logprobs<float>(a, st)
+                         : dtype == MOE_FP16 ? launch_logprobs<__half>(a, st)
+                                             : launch_logprobs<__nv_bfloat16>(a, st));
+}
+
+extern "C" int moe_token_logprobs_grad(const void *logits, int dtype, long long ld, int n_tokens,
+                                       int vocab, const int32_t *targets, const float *stats,
+                                       const float *entropy, const float *dlogp,
+                                       const float *dentropy, void *dlogits, long long ldd,
+                                       void *stream)
+{
+    using namespace qe;
+    const int rc = check_sizes(dtype, n_tokens, vocab);
+    if (rc)
+        return rc;
+    if (!logits || !stats || !dlogits || (dentropy && !entropy) || (dlogp && !targets))
+        return record_failure(MOE_ERR_INVALID_ARG, "null pointer argument");
+    if (!dlogp && !dentropy)
+        return record_failure(MOE_ERR_INVALID_ARG, "need dlogp or dentropy");
+    const int size = size_of(dtype);
+    const size_t n = n_tokens;
+    const Arg args[] = {rows_arg(logits, ld, vocab, n_tokens, size, size),
+                        flat_arg(dlogp ? targets : nullptr, n, 4),
+                        flat_arg(stats, n, 8),
+                        flat_arg(dentropy ? entropy : nullptr, n, 4),
+                        flat_arg(dlogp, n, 4),
+                        flat_arg(dentropy, n, 4),
+                        rows_arg(dlogits, ldd, vocab, n_tokens, size, size, true, logits)};
+    int dev, sms;
+    if (const int bad = check_args(args, sizeof(args) / sizeof(args[0]), &dev, &sms))
+        return bad;
+    LogprobGradArgs a{};
+    a.logits = logits;
+    a.ld = ld;
+    a.n = n_tokens;
+    a.V = vocab;
+    a.targets = dlogp ? targets : nullptr;
+    a.stats = reinterpret_cast<const float2 *>(stats);
+    a.entropy = entropy;
+    a.dlogp = dlogp;
+    a.dent = dentropy;
+    a.out = dlogits;
+    a.ldo = ldd;
+    a.aligned = ((uintptr_t)logits - (uintptr_t)dlogits) % 16 == 0 &&
+                (n_tokens == 1 || (ld - ldd) * size % 16 == 0);
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return launch_result(dtype == MOE_FP32   ? launch_logprobs_grad<float>(a, st)
+                         : dtype == MOE_FP16 ? launch_logprobs_grad<__half>(a, st)
+                                             : launch_logprobs_grad<__nv_bfloat16>(a, st));
+}

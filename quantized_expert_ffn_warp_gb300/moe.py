@@ -38,7 +38,9 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_route_topk", "moe_route
            "moe_layer_tier_stats", "moe_layer_tier_slots", "moe_ep_dispatch", "moe_ep_combine",
            "moe_linear", "moe_linear_input_grad", "moe_linear_input_grad_workspace",
            "moe_balance_workspace", "moe_balance_loss",
-           "moe_balance_loss_grad")
+           "moe_balance_loss_grad", "moe_token_logprobs_workspace", "moe_token_logprobs",
+           "moe_token_logprobs_grad", "moe_residual_norm", "moe_residual_norm_grad_workspace",
+           "moe_residual_norm_grad")
 
 
 class MoeError(RuntimeError):
@@ -112,6 +114,16 @@ def load_library(path: str = LIB_PATH):
     lib.moe_balance_workspace.restype = Z
     lib.moe_balance_loss.argtypes = [P, I, L, I, I, P, I, P, I, P, P, P, P, P, P, P, Z, P]
     lib.moe_balance_loss_grad.argtypes = [P, I, L, I, I, P, I, P, I, P, P, P, P, P, P, P, P, L, P]
+    F = C.c_float
+    lib.moe_token_logprobs_workspace.argtypes = [I, I, I, I]
+    lib.moe_token_logprobs_workspace.restype = Z
+    lib.moe_token_logprobs.argtypes = [P, I, L, I, I, P, I, P, P, P, P, P, P, Z, P]
+    lib.moe_token_logprobs_grad.argtypes = [P, I, L, I, I, P, P, P, P, P, P, L, P]
+    lib.moe_residual_norm.argtypes = [P, L, P, L, I, I, I, P, P, I, F, P, F, P, L, P, L, P, P]
+    lib.moe_residual_norm_grad_workspace.argtypes = [I, I]
+    lib.moe_residual_norm_grad_workspace.restype = Z
+    lib.moe_residual_norm_grad.argtypes = [P, L, P, L, P, L, P, L, P, I, I, I, P, P, I, F, P, P, L,
+                                           P, L, P, P, P, P, Z, P]
     lib.moe_last_error.restype = C.c_char_p
     lib.moe_last_error.argtypes = []
     _lib = lib
@@ -606,6 +618,181 @@ def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, s
     if rc:
         _check(rc)
     return out
+
+
+def token_logprobs(logits, targets=None, top=0, stream=None):
+    """Log probabilities of given tokens (moe_token_logprobs): logits fp32, fp16 or
+    bf16 [n, vocab] (rows may be strided), targets int32 [n] or None (one outside
+    [0, vocab): no target), top the number of likeliest tokens, up to 32.  Returns
+    dict(entropy fp32 [n], stats fp32 [n, 2] = (largest logit, log of the sum of
+    exponentials against it)), with targets logp fp32 [n], and with top top_ids
+    int32 [n, top] and top_logp fp32 [n, top]; token_logprobs_grad takes it."""
+    torch, types = _types()
+    if logits.dim() != 2:
+        _bad("logits: need [n, vocab], got shape %s" % (tuple(logits.shape),))
+    n, V = logits.shape
+    code = _code_of(logits.dtype, types)
+    pl, ld = _rows(logits, "logits", logits.dtype, n, V)
+    pt = None if targets is None else _dense(targets, "targets", torch.int32, (n,))
+    if not 0 <= top <= 32:
+        _bad("top must be in 0..32, got %s" % (top,))
+    lib, f32 = load_library(), torch.float32
+    size = lib.moe_token_logprobs_workspace(n, V, code, top)
+    specs = [((n,), f32), ((n, 2), f32)]
+    if targets is not None:
+        specs.append(((n,), f32))
+    if top:
+        specs += [((n, top), torch.int32), ((n, top), f32)]
+    if size:
+        specs.append(((size,), torch.uint8))
+    new = _new(torch, stream, logits, *specs)
+    res = dict(entropy=new[0], stats=new[1])
+    at = 2
+    logp = ids = tlp = None
+    if targets is not None:
+        res["logp"], logp, at = new[at], new[at].data_ptr(), at + 1
+    if top:
+        res["top_ids"], res["top_logp"] = new[at], new[at + 1]
+        ids, tlp = new[at].data_ptr(), new[at + 1].data_ptr()
+    rc = lib.moe_token_logprobs(pl, code, ld, n, V, pt, top, logp, new[0].data_ptr(),
+                                new[1].data_ptr(), ids, tlp, new[-1].data_ptr() if size else None,
+                                size, _raw_stream(logits, stream))
+    if rc:
+        _check(rc)
+    return res
+
+
+def token_logprobs_grad(logits, targets, fwd, dlogp=None, dentropy=None, out=None, stream=None):
+    """Gradient of token_logprobs in the logits (moe_token_logprobs_grad): fwd is
+    its result (stats, and with dentropy entropy, are read), dlogp and dentropy
+    fp32 [n] the gradients of logp and entropy (either may be None; targets may be
+    None without dlogp).  out may be logits itself."""
+    torch, types = _types()
+    if logits.dim() != 2:
+        _bad("logits: need [n, vocab], got shape %s" % (tuple(logits.shape),))
+    n, V = logits.shape
+    dt, f32 = logits.dtype, torch.float32
+    code = _code_of(dt, types)
+    pl, ld = _rows(logits, "logits", dt, n, V)
+    pt = pg = pe = pent = None
+    if dlogp is not None:
+        if targets is None:
+            _bad("dlogp needs targets")
+        pg = _dense(dlogp, "dlogp", f32, (n,))
+    if targets is not None:
+        pt = _dense(targets, "targets", torch.int32, (n,))
+    if dentropy is not None:
+        pe = _dense(dentropy, "dentropy", f32, (n,))
+        pent = _dense(fwd["entropy"], "entropy", f32, (n,))
+    if out is None:
+        (out,), ldo = _new(torch, stream, logits, ((n, V), dt)), V
+        po = out.data_ptr()
+    else:
+        po, ldo = _rows(out, "out", dt, n, V)
+    rc = load_library().moe_token_logprobs_grad(
+        pl, code, ld, n, V, pt, _dense(fwd["stats"], "stats", f32, (n, 2)), pent, pg, pe, po, ldo,
+        _raw_stream(logits, stream))
+    if rc:
+        _check(rc)
+    return out
+
+
+def _gate(gate, dtype, n, H):
+    """Address of a gate and whether it is one for each token ([n, 1])."""
+    if gate is None:
+        return None, 0
+    if gate.dim() == 2:
+        return _dense(gate, "gate", dtype, (n, 1)), 1
+    return _dense(gate, "gate", dtype, (H,)), 0
+
+
+def residual_norm(resid, y, gain=None, gate=None, scale=1.0, next_gain=None, eps=1e-6, out=None,
+                  stream=None):
+    """The norm behind a block, its gate, the scaled residual and the next block's
+    norm (moe_residual_norm): resid and y fp16 or bf16 [n, H] (rows may be strided),
+    gain and next_gain [H] of that type or None, gate [H] (one for each channel) or
+    [n, 1] (one for each token) or None.  Returns dict(out [n, H] = scale resid +
+    gate gain y / rms(y), stats fp32 [n, 2]), and with next_gain xn [n, H] =
+    next_gain out / rms(out); residual_norm_grad takes out and stats.  out may be
+    resid itself."""
+    torch, types = _types()
+    if resid.dim() != 2:
+        _bad("resid: need [n, H], got shape %s" % (tuple(resid.shape),))
+    n, H = resid.shape
+    dt = resid.dtype
+    pr, ldr = _rows(resid, "resid", dt, n, H)
+    py, ldy = _rows(y, "y", dt, n, H)
+    pg = None if gain is None else _dense(gain, "gain", dt, (H,))
+    pn = None if next_gain is None else _dense(next_gain, "next_gain", dt, (H,))
+    pa, per_token = _gate(gate, dt, n, H)
+    specs = [((n, 2), torch.float32)]
+    if out is None:
+        specs.append(((n, H), dt))
+    if pn is not None:
+        specs.append(((n, H), dt))
+    new = _new(torch, stream, resid, *specs)
+    if out is None:
+        out, ldo = new[1], H
+        po = out.data_ptr()
+    else:
+        po, ldo = _rows(out, "out", dt, n, H)
+    res = dict(out=out, stats=new[0])
+    px = None
+    if pn is not None:
+        res["xn"], px = new[-1], new[-1].data_ptr()
+    rc = load_library().moe_residual_norm(pr, ldr, py, ldy, _code_of(dt, types), n, H, pg, pa,
+                                          per_token, float(scale), pn, float(eps), po, ldo, px, H,
+                                          new[0].data_ptr(), _raw_stream(resid, stream))
+    if rc:
+        _check(rc)
+    return res
+
+
+def residual_norm_grad(dout, dxn, out, y, stats, gain=None, gate=None, scale=1.0, next_gain=None,
+                       stream=None):
+    """Gradients of residual_norm (moe_residual_norm_grad): dout and dxn are the
+    gradients of its out and xn (either may be None), out and stats its results
+    (out is read with dxn only), the others its arguments.  Returns dict(dresid, dy
+    of y's type; dgain fp32 [H] with gain, dgate fp32 of gate's shape with gate,
+    dnext_gain fp32 [H] with dxn)."""
+    torch, types = _types()
+    if y.dim() != 2:
+        _bad("y: need [n, H], got shape %s" % (tuple(y.shape),))
+    n, H = y.shape
+    dt, f32 = y.dtype, torch.float32
+    py, ldy = _rows(y, "y", dt, n, H)
+    pd, ldd = (None, 0) if dout is None else _rows(dout, "dout", dt, n, H)
+    px = po = pn = None
+    ldx = ldo = 0
+    if dxn is not None:
+        if next_gain is None:
+            _bad("dxn needs next_gain")
+        px, ldx = _rows(dxn, "dxn", dt, n, H)
+        po, ldo = _rows(out, "out", dt, n, H)
+        pn = _dense(next_gain, "next_gain", dt, (H,))
+    ps = _dense(stats, "stats", f32, (n, 2))
+    pg = None if gain is None else _dense(gain, "gain", dt, (H,))
+    pa, per_token = _gate(gate, dt, n, H)
+    names, specs = ["dresid", "dy"], [((n, H), dt), ((n, H), dt)]
+    for name, used, shape in (("dgain", gain, (H,)), ("dgate", gate, (n, 1) if per_token else (H,)),
+                              ("dnext_gain", dxn, (H,))):
+        if used is not None:
+            names.append(name)
+            specs.append((shape, f32))
+    lib, size = load_library(), 0
+    if gain is not None or dxn is not None or (gate is not None and not per_token):
+        size = lib.moe_residual_norm_grad_workspace(n, H)
+        specs.append(((size,), torch.uint8))
+    new = _new(torch, stream, y, *specs)
+    res = dict(zip(names, new))
+    p = {k: t.data_ptr() for k, t in res.items()}
+    rc = lib.moe_residual_norm_grad(
+        pd, ldd, px, ldx, po, ldo, py, ldy, ps, _code_of(dt, types), n, H, pg, pa, per_token,
+        float(scale), pn, p["dresid"], H, p["dy"], H, p.get("dgain"), p.get("dgate"),
+        p.get("dnext_gain"), new[-1].data_ptr() if size else None, size, _raw_stream(y, stream))
+    if rc:
+        _check(rc)
+    return res
 
 
 def forward_host(layer: MoeLayer, x_host, out_host, stream=None, norm=None):
