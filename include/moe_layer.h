@@ -519,6 +519,59 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
                           void *dlogits, long long ldd, void *stream);
 
 /*
+ * Low-rank adapters of many requests beside one shared projection (moe_linear, or any
+ * other): each token has the adapter of its request, or none.  The pages have no
+ * counterpart: they serve one set of weights.
+ *   h[t]   = A_a x[t],  out[t] = base[t] + scale[a] B_a h[t],   a = ids[t]
+ * A token whose id lies outside [0, n_adapters) has no adapter: its h is 0 and its
+ * out is base (0 without base), to the bit.  base NULL: out is the delta alone.
+ * x [n_tokens][cols], base and out [n_tokens][rows] of type dtype (MOE_FP16 or
+ * MOE_BF16) with row strides ldx, ldb, ldo; ids int32 [n] in any order; A
+ * [n_adapters][rank][cols] and B [n_adapters][rows][rank] of type dtype, 16-byte
+ * aligned; scale fp32 [n_adapters] (NULL: 1); h [n][rank] of type dtype (NULL: not
+ * kept), what moe_adapter_grad takes.  out may be base itself.
+ * Sums are fp32; between the two products h is held as the sum of two values of
+ * dtype, so that it adds no rounding of its own (in fp16, an h above 65504 is an
+ * infinity); out and h are rounded once.  Rows on 16-byte boundaries are read by
+ * wide loads, others (odd widths) value by value.
+ * rank a multiple of 8 in 8 .. 128; n_adapters 1 .. 1024; n_tokens, cols and rows 1 ..
+ * 1048576.
+ * workspace: moe_adapter_workspace(n, n_adapters, rank, cols, rows) bytes, 256-byte
+ * aligned, any contents, used by one call at a time.  It and the outputs must overlap
+ * nothing else.  The same call gives the same bits every time.  All pointers are DEVICE
+ * pointers of the current device.  No allocation; asynchronous.
+ * moe_adapter_workspace returns 0 for sizes out of range.
+ * Errors: INVALID_ARG (null, misaligned or non-device pointer, sizes, strides,
+ * overlap), UNSUPPORTED (dtype), CUDA.
+ */
+size_t moe_adapter_workspace(int n_tokens, int n_adapters, int rank, int cols, int rows);
+int moe_adapter(const void *x, long long ldx, int dtype, int n_tokens, int cols, int rows,
+                const int32_t *ids, int n_adapters, int rank, const void *A, const void *B,
+                const float *scale, const void *base, long long ldb, void *out, long long ldo,
+                void *h, void *workspace, size_t workspace_bytes, void *stream);
+
+/*
+ * Gradients of moe_adapter, with u[t] = B_a^T dy[t]:
+ *   dx[t] = base[t] + scale[a] A_a^T u[t]     (base: the gradient through the shared
+ *           projection, moe_linear_input_grad, or NULL; the tokens without an adapter
+ *           get base, or 0)
+ *   dA_a  = scale[a] sum_t u[t] x[t]^T,  dB_a = scale[a] sum_t dy[t] h[t]^T over the
+ *           tokens of adapter a (0 for an adapter without tokens)
+ * (the gradient of moe_adapter's base is dy).  dy [n][rows], x, base and dx [n][cols],
+ * h [n][rank] (16-byte aligned, from moe_adapter), dA [n_adapters][rank][cols] and dB
+ * [n_adapters][rows][rank] (16-byte aligned), all of type dtype; ids, A, B, scale as
+ * there.  dx, dA and dB may be NULL and are left out then; x is read for dA, h for dB.
+ * dx may be base itself.  Sums are fp32 in a fixed order, u is held as the sum of two
+ * values of dtype, the results are rounded once.  The workspace is that of moe_adapter.
+ * Errors: those of moe_adapter.
+ */
+int moe_adapter_grad(const void *dy, long long lddy, const void *x, long long ldx, const void *h,
+                     int dtype, int n_tokens, int cols, int rows, const int32_t *ids,
+                     int n_adapters, int rank, const void *A, const void *B, const float *scale,
+                     const void *base, long long ldb, void *dx, long long lddx, void *dA, void *dB,
+                     void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Log probabilities of given tokens from the logits of a vocabulary head
  * (moe_linear), with the entropy of their distribution and its likeliest tokens.
  * The pages have no counterpart: they sample on the host.  It serves whoever

@@ -40,7 +40,7 @@ EXPORTS = ("moe_layer_create", "moe_layer_destroy", "moe_route_topk", "moe_route
            "moe_balance_workspace", "moe_balance_loss",
            "moe_balance_loss_grad", "moe_token_logprobs_workspace", "moe_token_logprobs",
            "moe_token_logprobs_grad", "moe_residual_norm", "moe_residual_norm_grad_workspace",
-           "moe_residual_norm_grad")
+           "moe_residual_norm_grad", "moe_adapter_workspace", "moe_adapter", "moe_adapter_grad")
 
 
 class MoeError(RuntimeError):
@@ -124,6 +124,11 @@ def load_library(path: str = LIB_PATH):
     lib.moe_residual_norm_grad_workspace.restype = Z
     lib.moe_residual_norm_grad.argtypes = [P, L, P, L, P, L, P, L, P, I, I, I, P, P, I, F, P, P, L,
                                            P, L, P, P, P, P, Z, P]
+    lib.moe_adapter_workspace.argtypes = [I, I, I, I, I]
+    lib.moe_adapter_workspace.restype = Z
+    lib.moe_adapter.argtypes = [P, L, I, I, I, I, P, I, I, P, P, P, P, L, P, L, P, P, Z, P]
+    lib.moe_adapter_grad.argtypes = [P, L, P, L, P, I, I, I, I, P, I, I, P, P, P, P, L, P, L, P, P,
+                                     P, Z, P]
     lib.moe_last_error.restype = C.c_char_p
     lib.moe_last_error.argtypes = []
     _lib = lib
@@ -618,6 +623,96 @@ def balance_loss_grad(logits, topk_idx, fwd, dloss, topk_w=None, dtopk_w=None, s
     if rc:
         _check(rc)
     return out
+
+
+def _adapters(torch, dtype, ids, A, B, scale, n):
+    """Sizes and addresses of a call's adapters."""
+    if A.dim() != 3 or B.dim() != 3:
+        _bad("A, B: need [adapters, rank, cols] and [adapters, rows, rank], got shapes %s and %s"
+             % (tuple(A.shape), tuple(B.shape)))
+    count, rank, cols = A.shape
+    rows = B.shape[1]
+    ps = None if scale is None else _dense(scale, "scale", torch.float32, (count,))
+    return (count, rank, cols, rows, _dense(ids, "ids", torch.int32, (n,)),
+            _dense(A, "A", dtype, (count, rank, cols)), _dense(B, "B", dtype, (count, rows, rank)),
+            ps)
+
+
+def adapter(x, ids, A, B, scale=None, base=None, out=None, stream=None):
+    """Low-rank adapters of many requests beside one projection (moe_adapter): x fp16
+    or bf16 [n, cols], ids int32 [n] the adapter of each token (outside [0, adapters):
+    none), A [adapters, rank, cols] and B [adapters, rows, rank] of x's type, scale
+    fp32 [adapters] or None, base [n, rows] what the projection gave (rows of x, base
+    and out may be strided) or None.  Returns (out, h): out [n, rows] = base + scale B A
+    x, which may be base itself, and h [n, rank] = A x for adapter_grad."""
+    torch, types = _types()
+    if x.dim() != 2:
+        _bad("x: need [n, cols], got shape %s" % (tuple(x.shape),))
+    n, dt = x.shape[0], x.dtype
+    count, rank, cols, rows, pi, pa, pb, ps = _adapters(torch, dt, ids, A, B, scale, n)
+    px, ldx = _rows(x, "x", dt, n, cols)
+    pbase, ldb = (None, 0) if base is None else _rows(base, "base", dt, n, rows)
+    lib = load_library()
+    size = lib.moe_adapter_workspace(n, count, rank, cols, rows)
+    specs = [((n, rank), dt), ((size,), torch.uint8)]
+    if out is None:
+        h, ws, out = _new(torch, stream, x, *specs, ((n, rows), dt))
+        po, ldo = out.data_ptr(), rows
+    else:
+        po, ldo = _rows(out, "out", dt, n, rows)
+        h, ws = _new(torch, stream, x, *specs)
+    rc = lib.moe_adapter(px, ldx, _code_of(dt, types), n, cols, rows, pi, count, rank, pa, pb, ps,
+                         pbase, ldb, po, ldo, h.data_ptr(), ws.data_ptr(), size,
+                         _raw_stream(x, stream))
+    if rc:
+        _check(rc)
+    return out, h
+
+
+def adapter_grad(dy, x, h, ids, A, B, scale=None, base=None, out=None, input_grad=True,
+                 weight_grad=True, stream=None):
+    """Gradients of adapter (moe_adapter_grad): dy [n, rows] the gradient of its out, h
+    its second result, base [n, cols] a gradient of x to add to (linear_input_grad's) or
+    None.  Returns dict(dx [n, cols], which may be base itself as `out`, dA, dB of the
+    adapters' shapes and type); input_grad=False leaves dx out, weight_grad=False dA and
+    dB (x and h may be None then)."""
+    torch, types = _types()
+    if dy.dim() != 2:
+        _bad("dy: need [n, rows], got shape %s" % (tuple(dy.shape),))
+    n, dt = dy.shape[0], dy.dtype
+    count, rank, cols, rows, pi, pa, pb, ps = _adapters(torch, dt, ids, A, B, scale, n)
+    pd, ldd = _rows(dy, "dy", dt, n, rows)
+    px = ph = pbase = pdx = None
+    ldx = ldb = lddx = 0
+    names, specs = [], []
+    if weight_grad:
+        px, ldx = _rows(x, "x", dt, n, cols)
+        ph = _dense(h, "h", dt, (n, rank))
+        names, specs = ["dA", "dB"], [(A.shape, dt), (B.shape, dt)]
+    if input_grad:
+        if base is not None:
+            pbase, ldb = _rows(base, "base", dt, n, cols)
+        if out is None:
+            names.append("dx")
+            specs.append(((n, cols), dt))
+        else:
+            pdx, lddx = _rows(out, "out", dt, n, cols)
+    lib = load_library()
+    size = lib.moe_adapter_workspace(n, count, rank, cols, rows)
+    new = _new(torch, stream, dy, *specs, ((size,), torch.uint8))
+    res = dict(zip(names, new))
+    if "dx" in res:
+        pdx, lddx = res["dx"].data_ptr(), cols
+    elif input_grad:
+        res["dx"] = out
+    rc = lib.moe_adapter_grad(pd, ldd, px, ldx, ph, _code_of(dt, types), n, cols, rows, pi, count,
+                              rank, pa, pb, ps, pbase, ldb, pdx, lddx,
+                              res["dA"].data_ptr() if weight_grad else None,
+                              res["dB"].data_ptr() if weight_grad else None, new[-1].data_ptr(),
+                              size, _raw_stream(dy, stream))
+    if rc:
+        _check(rc)
+    return res
 
 
 def token_logprobs(logits, targets=None, top=0, stream=None):

@@ -6,7 +6,8 @@ import ctypes as C
 import pytest
 
 torch = pytest.importorskip("torch")
-from tuning_refs import INF, logprobs, logprobs_grad, residual_norm, residual_norm_grad  # noqa: E402
+from tuning_refs import (INF, adapter, adapter_grad, logprobs, logprobs_grad, residual_norm,  # noqa: E402
+                         residual_norm_grad)
 
 P, L, Z, F = C.c_void_p, C.c_longlong, C.c_size_t, C.c_float
 NAN = float("nan")
@@ -191,6 +192,92 @@ def test_residual_norm_grad_workspace_sizes(lib):
     assert ws(4, 64) == 4 * 64 * 8 and ws(1 << 26, 8) > ws(4096, 8) > 0
 
 
+# ---------------------------------------------------------------- adapters
+
+AD = dict(x=0x100000, ldx=64, dtype=1, n=8, K=64, N=48, ids=0x10000, L=3, r=16, A=0x200000,
+          B=0x300000, scale=0x20000, base=0x400000, ldb=48, out=0x500000, ldo=48, h=0x600000,
+          ws=0x700000, ws_bytes=None)
+
+
+def adapters(lib, **kw):
+    a = dict(AD, **kw)
+    size = a["ws_bytes"]
+    if size is None:
+        size = lib.moe_adapter_workspace(a["n"], a["L"], a["r"], a["K"], a["N"])
+    return lib.moe_adapter(P(a["x"]), L(a["ldx"]), a["dtype"], a["n"], a["K"], a["N"], P(a["ids"]),
+                           a["L"], a["r"], P(a["A"]), P(a["B"]), P(a["scale"]), P(a["base"]),
+                           L(a["ldb"]), P(a["out"]), L(a["ldo"]), P(a["h"]), P(a["ws"]), Z(size),
+                           None)
+
+
+def adapters_grad(lib, **kw):
+    a = dict(AD, dy=0x800000, lddy=48, ldb=64, dx=0x500000, lddx=64, dA=0x900000, dB=0xA00000)
+    a.update(kw)
+    size = a["ws_bytes"]
+    if size is None:
+        size = lib.moe_adapter_workspace(a["n"], a["L"], a["r"], a["K"], a["N"])
+    return lib.moe_adapter_grad(P(a["dy"]), L(a["lddy"]), P(a["x"]), L(a["ldx"]), P(a["h"]),
+                                a["dtype"], a["n"], a["K"], a["N"], P(a["ids"]), a["L"], a["r"],
+                                P(a["A"]), P(a["B"]), P(a["scale"]), P(a["base"]), L(a["ldb"]),
+                                P(a["dx"]), L(a["lddx"]), P(a["dA"]), P(a["dB"]), P(a["ws"]),
+                                Z(size), None)
+
+
+AD_BOTH = [(dict(x=None), -1), (dict(ids=None), -1), (dict(A=None), -1), (dict(B=None), -1),
+           (dict(ws=None), -1), (dict(dtype=2), -2), (dict(n=0), -1), (dict(n=(1 << 20) + 1), -1),
+           (dict(L=0), -1), (dict(L=1025), -1), (dict(r=0), -1), (dict(r=12), -1), (dict(r=136), -1),
+           (dict(K=0), -1), (dict(N=0), -1), (dict(K=(1 << 20) + 1, ldx=1 << 21), -1),
+           (dict(N=(1 << 20) + 1), -1), (dict(ldx=63), -1), (dict(x=0x100001), -1),
+           (dict(ids=0x10002), -1), (dict(A=0x200008), -1), (dict(B=0x300002), -1),
+           (dict(scale=0x20002), -1), (dict(ldb=40), -1), (dict(ws=0x700010), -1),
+           (dict(ws_bytes=100), -1), (dict(ldb=(1 << 31) + 1), -1)]
+
+
+@pytest.mark.parametrize("kw,code", AD_BOTH + [
+    (dict(out=None), -1), (dict(out=0x500001), -1), (dict(ldo=47), -1), (dict(h=0x600001), -1)])
+def test_adapter_refuses(lib, kw, code):
+    assert refused(lib, adapters(lib, **kw), code)
+
+
+@pytest.mark.parametrize("kw,code", AD_BOTH + [
+    (dict(dy=None), -1), (dict(h=None), -1), (dict(dx=None, dA=None, dB=None), -1),
+    (dict(h=0x600008), -1), (dict(dA=0x900008), -1), (dict(dB=0xA00002), -1), (dict(lddy=47), -1),
+    (dict(lddx=63), -1), (dict(dy=0x800001), -1)])
+def test_adapter_grad_refuses(lib, kw, code):
+    assert refused(lib, adapters_grad(lib, **kw), code)
+
+
+@pytest.mark.parametrize("kw,hit", [
+    (dict(), False), (dict(out=0x400000), False), (dict(out=0x400000, ldo=64), True),
+    (dict(out=0x400002), True), (dict(out=0x100000), True), (dict(out=0x200000), True),
+    (dict(out=0x300000 + 3 * 16 * 48 * 2), False), (dict(out=0x300000 + 3 * 16 * 48 * 2 - 2), True),
+    (dict(h=0x100000), True), (dict(h=0x10000), True), (dict(h=None), False),
+    (dict(ws=0x100000), True), (dict(ws=0x10000), True), (dict(out=0x400000, n=1), False)])
+def test_adapter_overlaps(lib, kw, hit):
+    rc = adapters(lib, **kw)
+    assert rc != 0 and overlaps(lib, rc) == hit
+
+
+@pytest.mark.parametrize("kw,hit", [
+    (dict(), False), (dict(dx=0x400000), False), (dict(dx=0x100000), True),
+    (dict(dx=0x100000, dA=None, x=None), False), (dict(dA=0x200000), True), (dict(dB=0x900010), True),
+    (dict(dB=0x600000), True), (dict(h=None, dB=None, dA=0x600000), False),
+    # base is read for dx only
+    (dict(dx=None, dA=0x400000), False), (dict(ws=0x800000), True)])
+def test_adapter_grad_overlaps(lib, kw, hit):
+    rc = adapters_grad(lib, **kw)
+    assert rc != 0 and overlaps(lib, rc) == hit
+
+
+def test_adapter_workspace_sizes(lib):
+    ws = lib.moe_adapter_workspace
+    for bad in ((0, 1, 8, 8, 8), (1, 0, 8, 8, 8), (1, 1, 4, 8, 8), (1, 1, 8, 0, 8), (1, 1, 8, 8, 0),
+                (1, 1025, 8, 8, 8), (1, 1, 136, 8, 8), (1 << 21, 1, 8, 8, 8)):
+        assert ws(*bad) == 0
+    assert ws(1, 1, 8, 8, 8) > 0 and ws(64, 4, 16, 8, 65536) == ws(64, 4, 16, 65536, 8)
+    assert ws(64, 4, 16, 65536, 8) >= ws(64, 4, 16, 8, 8)
+
+
 # ---------------------------------------------------------------- the binding
 
 def test_binding_refuses_wrong_tensors():
@@ -198,6 +285,7 @@ def test_binding_refuses_wrong_tensors():
     logits, t = torch.zeros((4, 10)), torch.zeros(4, dtype=torch.int32)
     x = torch.zeros((4, 64), dtype=torch.float16)
     fwd = dict(stats=torch.zeros((4, 2)), entropy=torch.zeros(4))
+    w = torch.zeros((2, 8, 64), dtype=torch.float16)
     for call in (lambda: moe.token_logprobs(logits, t),                 # no GPU tensors
                  lambda: moe.token_logprobs(logits[0], t),
                  lambda: moe.token_logprobs(logits.double(), t),
@@ -214,7 +302,15 @@ def test_binding_refuses_wrong_tensors():
                  lambda: moe.residual_norm(x, x, gate=torch.zeros((4, 2), dtype=torch.float16)),
                  lambda: moe.residual_norm(x, x, gain=torch.zeros(64)),
                  lambda: moe.residual_norm_grad(x, x, x, x, torch.zeros((4, 2))),
-                 lambda: moe.residual_norm_grad(x, None, None, x, torch.zeros((4, 1)))):
+                 lambda: moe.residual_norm_grad(x, None, None, x, torch.zeros((4, 1))),
+                 lambda: moe.adapter(x, t, w, w.transpose(1, 2).contiguous()),
+                 lambda: moe.adapter(x, t, w[0], w),
+                 lambda: moe.adapter(x, t.long(), w, w.transpose(1, 2).contiguous()),
+                 lambda: moe.adapter(x, t, w.float(), w.transpose(1, 2).contiguous()),
+                 lambda: moe.adapter(x, t, w, w.transpose(1, 2)),
+                 lambda: moe.adapter_grad(x, x, x, t, w, w.transpose(1, 2).contiguous()),
+                 lambda: moe.adapter_grad(x, x[:, :32], x[:, :8].contiguous(), t, w,
+                                          w.transpose(1, 2).contiguous())):
         with pytest.raises(moe.MoeError):
             call()
 
@@ -269,3 +365,27 @@ def test_residual_norm_gradients_against_differences(gate, gain):
             q = forward(**{name[1:]: v})
             return (wo * q["out"]).sum() + (wx * q["xn"]).sum()
         assert (g - differences(loss, x[name[1:]])).abs().max() < 1e-7, name
+
+
+@pytest.mark.parametrize("scaled", [True, False])
+def test_adapter_gradients_against_differences(scaled):
+    torch.manual_seed(3)
+    f = torch.float64
+    import tuning_refs
+    tuning_refs.PAIR[f], tuning_refs.TINY[f] = 0.0, 0.0
+    ids = torch.tensor([1, 0, -1, 1, 5])
+    x = dict(x=torch.randn((5, 6), dtype=f), A=torch.randn((3, 2, 6), dtype=f),
+             B=torch.randn((3, 4, 2), dtype=f), base=torch.randn((5, 4), dtype=f))
+    scale = torch.rand(3, dtype=f) if scaled else None
+    wo = torch.randn((5, 4), dtype=f)
+
+    def forward(**kw):
+        a = dict(x, **kw)
+        return adapter(a["x"], ids, a["A"], a["B"], scale, a["base"])
+    h = forward()[1][0]
+    got = adapter_grad(wo, x["x"], h, ids, x["A"], x["B"], scale, None)
+    for name, (g, _) in got.items():
+        def loss(v):
+            return (wo * forward(**{name[1:]: v})[0][0]).sum()
+        # the loss is of second order in each argument: differences are off by roundings
+        assert (g - differences(loss, x[name[1:]], 1e-3)).abs().max() < 1e-9, name

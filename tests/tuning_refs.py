@@ -159,3 +159,68 @@ def residual_norm_grad(dout, dxn, out, y, stats, gain, gate, scale, next_gain):
     g["dy"] = r1 * (q - z * mean)
     b["dy"] = r1 * (qe + z.abs() * me + 8 * H * (q.abs() + (z * mean).abs()))
     return g, b
+
+
+# ---------------------------------------------------------------- adapters
+
+# A product's sums: fp32 chains in the matrix units and joins, at most a term's worth of
+# rounding for each of `terms` terms, and the two-part h or u within 2^-16 (bf16) or
+# 2^-22 (fp16) of itself, two roundings each (an absolute 2^-25 where fp16 runs out).
+PAIR = {torch.bfloat16: 2.0 ** -16, torch.float16: 2.0 ** -21}
+TINY = {torch.bfloat16: 0.0, torch.float16: 2.0 ** -24}
+
+
+def _by_token(ids, count, n):
+    on = (ids >= 0) & (ids < count)
+    return on, torch.where(on, ids, 0).long()
+
+
+def adapter(x, ids, A, B, scale, base):
+    """(out, bound), (h, bound) in 64 bits; the bounds are those of fp32 sums."""
+    f = torch.float64
+    n, (count, rank, cols), rows = x.shape[0], A.shape, B.shape[1]
+    h = torch.zeros((n, rank), dtype=f, device=x.device)
+    he = torch.zeros_like(h)
+    out = torch.zeros((n, rows), dtype=f, device=x.device) if base is None else base.to(f, copy=True)
+    oe = 2 * H * out.abs()
+    for a in range(count):
+        t = (ids == a).nonzero()[:, 0]
+        if not len(t):
+            continue
+        s = 1.0 if scale is None else scale[a].to(f)
+        xa, Aa, Ba = x[t].to(f), A[a].to(f), B[a].to(f)
+        ha = xa @ Aa.t()
+        ea = cols * H * (xa.abs() @ Aa.abs().t())
+        h[t], he[t] = ha, ea
+        ea = ea + PAIR[x.dtype] * ha.abs() + TINY[x.dtype]
+        out[t] += s * (ha @ Ba.t())
+        oe[t] += abs(s) * (ea @ Ba.abs().t() + (2 * rank + 4) * H * (ha.abs() @ Ba.abs().t()))
+    return (out, oe), (h, he)
+
+
+def adapter_grad(dy, x, h, ids, A, B, scale, base):
+    """dict of (gradient, bound)."""
+    f = torch.float64
+    n, (count, rank, cols), rows = x.shape[0], A.shape, B.shape[1]
+    dx = torch.zeros((n, cols), dtype=f, device=x.device) if base is None else base.to(f, copy=True)
+    xe = 2 * H * dx.abs()
+    dA, dB = torch.zeros(A.shape, dtype=f, device=x.device), torch.zeros(B.shape, dtype=f,
+                                                                         device=x.device)
+    Ae, Be = torch.zeros_like(dA), torch.zeros_like(dB)
+    for a in range(count):
+        t = (ids == a).nonzero()[:, 0]
+        if not len(t):
+            continue
+        s = 1.0 if scale is None else scale[a].to(f)
+        xa, da, ha = x[t].to(f), dy[t].to(f), h[t].to(f)
+        Aa, Ba = A[a].to(f), B[a].to(f)
+        u = da @ Ba
+        ue = rows * H * (da.abs() @ Ba.abs()) + PAIR[x.dtype] * u.abs() + TINY[x.dtype]
+        dx[t] += s * (u @ Aa)
+        xe[t] += abs(s) * (ue @ Aa.abs() + (2 * rank + 4) * H * (u.abs() @ Aa.abs()))
+        sums = (2 * len(t) + 16) * H
+        dA[a] = s * (u.t() @ xa)
+        Ae[a] = abs(s) * (ue.t() @ xa.abs() + sums * (u.abs().t() @ xa.abs()))
+        dB[a] = s * (da.t() @ ha)
+        Be[a] = abs(s) * sums * (da.abs().t() @ ha.abs())
+    return dict(dx=(dx, xe), dA=(dA, Ae), dB=(dB, Be))
