@@ -22,10 +22,11 @@ namespace qe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;   // of a forward block
 constexpr int kMaxTokens = 1 << 26, kMaxVocab = 1 << 20, kMaxTop = 32;
 constexpr int kWordsPerThread = 4;      // 16-byte loads that a thread has under way
 constexpr int kMaxSplits = 64;          // blocks of one row
-constexpr float kFar = -150.f;          // e^kFar is 0 in fp32, kFar is finite
+constexpr float kFar = -220.f;          // 2^kFar and e^kFar are 0 in fp32, kFar is finite
 
 // fp32 values as unsigned numbers in their order; a NaN like -inf, -0 like 0.
 __device__ __forceinline__ unsigned order_of(float x)
@@ -48,7 +49,6 @@ __device__ __forceinline__ Key key_of(float x, int i)
 struct Sums {
     float m, s, sd;     // max, sum e^(l - m), sum e^(l - m) (l - m)
 
-    __device__ __forceinline__ float ref() const { return m == -INFINITY ? 0.f : m; }
     // Sums against a max of at least m.
     __device__ __forceinline__ void raise(float max)
     {
@@ -58,16 +58,70 @@ struct Sums {
         s *= f;
         m = max;
     }
-    __device__ __forceinline__ void join(float m2, float s2, float sd2)
+    // Sums over the lanes, in all of them.
+    __device__ __forceinline__ void join_lanes()
     {
-        Sums o = {m2, s2, sd2};
-        const float max = fmaxf(m, m2);
-        raise(max);
-        o.raise(max);
-        s += o.s;
-        sd += o.sd;
+        raise(max_warp(m));
+        s = sum_warp(s);
+        sd = sum_warp(sd);
     }
 };
+
+// Values that a chunk of a row may be raised to without a change of its sums, and the
+// maxima against which that holds: e^(kLow - m) is 0 for |m| <= kMost.  Products with
+// log2 e stay finite.
+template <typename T>
+constexpr float kLow = std::is_same_v<T, __half> ? -65504.f : -0x1p120f;
+template <typename T>
+constexpr float kMost = std::is_same_v<T, __half> ? 32768.f : 0x1p100f;
+
+// Adds the values of U words to the sums; `top` is their largest.
+//   e^(l - m) = 2^(l log2 e - c) 2^-rest,  c + rest = m log2 e:
+// l log2 e - c is one fused operation, rounded at the size of the difference, on pairs of
+// values; a -inf is first raised to a finite number, whose product with its
+// exponential, 0, is 0.
+template <typename T, int U>
+__device__ __forceinline__ void add_words(Sums &u, const uint4 (&q)[U], float top)
+{
+    constexpr int N = Vec<T>::N;
+    if (top > u.m)
+        u.raise(top);
+    if (fabsf(u.m) <= kMost<T>) {
+        const float c = u.m * kLog2E, rest = fmaf(u.m, kLog2E, -c), f = ex2(-rest);
+        const F2 l2e = f2(kLog2E), mc = f2(-c);
+        F2 s[2] = {f2(0.f), f2(0.f)}, sd[2] = {f2(0.f), f2(0.f)};
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            F2 x[N / 2];
+            unpack<T>(word_raise<T>(q[i], kLow<T>), x);
+#pragma unroll
+            for (int e = 0; e < N / 2; e++) {
+                const F2 a = fma(x[e], l2e, mc);
+                const float2 d = split(a);
+                const F2 p = f2(ex2(d.x), ex2(d.y));
+                s[e & 1] = add(s[e & 1], p);
+                sd[e & 1] = fma(p, a, sd[e & 1]);
+            }
+        }
+        const float sum_s = sum(add(s[0], s[1])), sum_sd = sum(add(sd[0], sd[1]));
+        u.s = fmaf(f, sum_s, u.s);
+        u.sd = fmaf(f * kLn2, fmaf(-rest, sum_s, sum_sd), u.sd);
+        return;
+    }
+    // nothing but -inf yet, a mask's lowest value, or no number
+    const float m = u.m == -INFINITY ? 0.f : u.m;
+#pragma unroll
+    for (int i = 0; i < U; i++) {
+        float x[N];
+        unpack<T>(q[i], x);
+#pragma unroll
+        for (int e = 0; e < N; e++) {
+            const float d = max_nan(x[e] - m, kFar), p = ex2(d * kLog2E);
+            u.s += p;
+            u.sd = fmaf(p, d, u.sd);
+        }
+    }
+}
 
 __device__ __forceinline__ Key shfl_key(Key k, int src)
 {
@@ -127,39 +181,32 @@ struct LogprobArgs {
     Key *part_keys;         // [n][splits][32]
 };
 
+template <int W>
 struct Block {
-    float4 sums[kWarps];
-    Key keys[kWarps][32];
+    float4 sums[W];
+    Key keys[W][32];
     unsigned bound;         // order of the best k-th value that a warp holds
 };
 
-// Joins the warps' sums and lists; every thread of warp 0 gets the result.
-template <bool TOP>
-__device__ __forceinline__ void join_warps(Block &sm, Sums &t, Key &list)
+// Joins the W warps' sums and lists; warp 0 gets the result.
+template <bool TOP, int W>
+__device__ __forceinline__ void join_warps(Block<W> &sm, Sums &t, Key &list)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1)
-        t.join(__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
-               __shfl_xor_sync(0xffffffffu, t.sd, d));
+    t.join_lanes();
     if (lane == 0)
         sm.sums[warp] = make_float4(t.m, t.s, t.sd, 0.f);
     if (TOP)
         sm.keys[warp][lane] = list;
     __syncthreads();
     if (warp == 0) {
-        const float4 q = lane < kWarps ? sm.sums[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
+        const float4 q = lane < W ? sm.sums[lane] : make_float4(-INFINITY, 0.f, 0.f, 0.f);
         t = {q.x, q.y, q.z};
-#pragma unroll
-        for (int d = kWarps / 2; d > 0; d >>= 1)
-            t.join(__shfl_xor_sync(0xffffffffu, t.m, d), __shfl_xor_sync(0xffffffffu, t.s, d),
-                   __shfl_xor_sync(0xffffffffu, t.sd, d));
-        t = {__shfl_sync(0xffffffffu, t.m, 0), __shfl_sync(0xffffffffu, t.s, 0),
-             __shfl_sync(0xffffffffu, t.sd, 0)};
+        t.join_lanes();
     }
     if (TOP) {
 #pragma unroll
-        for (int half = kWarps / 2; half > 0; half >>= 1) {
+        for (int half = W / 2; half > 0; half >>= 1) {
             if (warp < half) {
                 list = merge(list, sm.keys[warp + half][lane]);
                 sm.keys[warp][lane] = list;
@@ -197,11 +244,58 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, long long t, co
     }
 }
 
+// Looks for values of the warp's words that belong into its list.  Every lane of the
+// warp calls it, for the words v, v + kRowThreads, .. of the row, none past `hi`.
+template <typename T, int U>
+__device__ __forceinline__ void collect(const RowWords<T> &row, int v, int hi, const float (&most)[U],
+                                        float bound, int top, Key &list, Key &kth, unsigned *shared)
+{
+    constexpr int N = Vec<T>::N;
+    const Key before = kth;
+    unsigned words = 0;
+#pragma unroll
+    for (int i = 0; i < U; i++)
+        words |= most[i] >= bound && v + i * kRowThreads < hi ? 1u << i : 0u;
+    while (__any_sync(0xffffffffu, words != 0)) {
+        unsigned mask = 0;
+        int first = 0;
+        if (words) {
+            const int w = v + (__ffs(words) - 1) * kRowThreads;
+            words &= words - 1;
+            first = row.first(w);
+            float x[N];
+            unpack<T>(row.load(w, -INFINITY), x);
+#pragma unroll
+            for (int e = 0; e < N; e++)     // not below the bound: a NaN counts as -inf
+                mask |= !(x[e] < bound) && first + e >= 0 && first + e < row.len ? 1u << e : 0u;
+        }
+        while (__any_sync(0xffffffffu, mask != 0)) {
+            Key c = 0;
+            if (mask) {
+                const int i = first + __ffs(mask) - 1;
+                c = key_of(to_float<T>(row.row[i]), i);
+                mask &= mask - 1;
+            }
+            unsigned offers = __ballot_sync(0xffffffffu, c > kth);
+            while (offers) {
+                const Key k = shfl_key(c, __ffs(offers) - 1);
+                if (k > kth) {
+                    insert(list, k);
+                    kth = shfl_key(list, top - 1);
+                }
+                offers &= offers - 1;
+            }
+        }
+    }
+    if (kth != before && (threadIdx.x & 31) == 0)
+        atomicMax(shared, (unsigned)(kth >> 32));
+}
+
 template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
+__global__ void __launch_bounds__(kRowThreads) logprobs_kernel(LogprobArgs a)
 {
     constexpr int N = Vec<T>::N, U = kWordsPerThread;
-    __shared__ Block sm;
+    __shared__ Block<kRowWarps> sm;
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
@@ -211,7 +305,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
         Key list = 0, kth = 0;
         if (TOP) {
             if (threadIdx.x == 0)
-                sm.bound = 0;
+                sm.bound = order_of(-INFINITY);
             __syncthreads();
         }
         float low[N];
@@ -220,82 +314,45 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
             low[e] = -INFINITY;
         const uint4 none = pack<T>(low);
         uint4 next[U];
+        const T *src = row.row + row.first(lo + threadIdx.x);
+        // words at + threadIdx.x + i kRowThreads
         const auto load = [&](int at) {
+            if (at + U * kRowThreads <= hi && row.inner(at, U * kRowThreads)) {
 #pragma unroll
-            for (int i = 0; i < U; i++) {
-                const int v = at + i * kThreads;
-                next[i] = v < hi ? row.load(v, -INFINITY) : none;
+                for (int i = 0; i < U; i++)
+                    next[i] = load_stream(src + i * (kRowThreads * N));
+            } else {
+#pragma unroll
+                for (int i = 0; i < U; i++) {
+                    const int v = at + threadIdx.x + i * kRowThreads;
+                    next[i] = v < hi ? row.load(v, -INFINITY) : none;
+                }
             }
+            src += U * kRowThreads * N;
         };
-        load(lo + threadIdx.x);
-        for (int at = lo + warp * 32; at < hi; at += U * kThreads) {
-            float x[U][N], top = -INFINITY;
+        load(lo);
+        for (int at = lo; at < hi; at += U * kRowThreads) {
+            uint4 q[U];
+            float most[U], top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < U; i++) {
-                unpack<T>(next[i], x[i]);
-#pragma unroll
-                for (int e = 0; e < N; e++)
-                    top = fmaxf(top, x[i][e]);
+                q[i] = next[i];
+                most[i] = fmaxf(word_max<T>(q[i]), -INFINITY);     // a word of NaN too
+                top = fmaxf(top, most[i]);
             }
-            load(at + lane + U * kThreads);
+            if (at + U * kRowThreads < hi)
+                load(at + U * kRowThreads);
             if (TOP) {
-                float bound = value_of(max(*(volatile unsigned *)&sm.bound, order_of(-INFINITY)));
-                if (at == lo + warp * 32)
+                float bound = value_of(*(volatile unsigned *)&sm.bound);
+                if (at == lo)
                     bound = fmaxf(bound, kth_of_lanes(top, a.top));
-                if (__any_sync(0xffffffffu, top >= bound)) {
-                    unsigned mask = 0;
-#pragma unroll
-                    for (int i = 0; i < U; i++)
-#pragma unroll
-                        for (int e = 0; e < N; e++)
-                            mask |= !(x[i][e] < bound) ? 1u << (i * N + e) : 0u;
-                    const Key before = kth;
-                    while (__any_sync(0xffffffffu, mask != 0)) {
-                        Key c = 0;
-                        if (mask) {
-                            const int b = __ffs(mask) - 1;
-                            const int i = row.first(at + lane + b / N * kThreads) + b % N;
-                            // words past the block's end were filled
-                            if (i >= 0 && i < a.V && at + lane + b / N * kThreads < hi)
-                                c = key_of(to_float<T>(row.row[i]), i);
-                            mask &= mask - 1;
-                        }
-                        unsigned offers = __ballot_sync(0xffffffffu, c > kth);
-                        while (offers) {
-                            const Key k = shfl_key(c, __ffs(offers) - 1);
-                            if (k > kth) {
-                                insert(list, k);
-                                kth = shfl_key(list, a.top - 1);
-                            }
-                            offers &= offers - 1;
-                        }
-                    }
-                    if (lane == 0 && kth != before)
-                        atomicMax(&sm.bound, (unsigned)(kth >> 32));
-                }
+                if (__any_sync(0xffffffffu, top >= bound))
+                    collect<T, U>(row, at + threadIdx.x, hi, most, bound, a.top, list, kth,
+                                  &sm.bound);
             }
-            if (top > u.m)
-                u.raise(top);
-            const float m = u.ref();
-            float s[U], sd[U];
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                s[i] = sd[i] = 0.f;
-#pragma unroll
-                for (int e = 0; e < N; e++) {
-                    const float d = max_nan(x[i][e] - m, kFar);
-                    const float p = ex2(d * kLog2E);
-                    s[i] += p;
-                    sd[i] = fmaf(p, d, sd[i]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                u.s += s[i];
-                u.sd += sd[i];
-            }
+            add_words<T, U>(u, q, top);
         }
-        join_warps<TOP>(sm, u, list);
+        join_warps<TOP, kRowWarps>(sm, u, list);
         if (warp == 0) {
             if (a.splits == 1) {
                 finish_row<T, TOP>(a, t, u, list);
@@ -315,7 +372,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_kernel(LogprobArgs a)
 template <typename T, bool TOP>
 __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
 {
-    __shared__ Block sm;
+    __shared__ Block<kWarps> sm;
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long t = blockIdx.x, at = t * a.splits;
@@ -328,7 +385,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
     if (TOP)
         for (int i = warp; i < a.splits; i += kWarps)
             list = merge(list, a.part_keys[(at + i) * 32 + lane]);
-    join_warps<TOP>(sm, u, list);
+    join_warps<TOP, kWarps>(sm, u, list);
     if (warp == 0)
         finish_row<T, TOP>(a, t, u, list);
 }
@@ -337,13 +394,13 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
 int most_words(int V, int per) { return (V + per - 1 + per - 1) / per; }
 
 // Blocks of a row: enough for a block on every SM four times over, each with a
-// load of kWordsPerThread / 2 words per thread at least.  Asks no device, since
-// the workspace's size follows from it.
+// load of kWordsPerThread words per thread.  Asks no device, since the workspace's size
+// follows from it.
 int row_splits(int n, int V, int size)
 {
-    const int words = most_words(V, 16 / size);
+    const int words = most_words(V, 16 / size), step = kRowThreads * kWordsPerThread;
     const int want = 4 * 152 / std::min(n, 4 * 152);
-    const int most = (words + kThreads * kWordsPerThread / 2 - 1) / (kThreads * kWordsPerThread / 2);
+    const int most = (words + step - 1) / step;
     return std::max(1, std::min({want, most, kMaxSplits}));
 }
 
@@ -361,7 +418,7 @@ template <typename T, bool TOP>
 cudaError_t launch_top(const LogprobArgs &a, cudaStream_t st)
 {
     cudaError_t e = launch_pdl(logprobs_kernel<T, TOP>, dim3(a.splits, std::min(a.n, 65535)),
-                               dim3(kThreads), 0, st, a);
+                               dim3(kRowThreads), 0, st, a);
     if (e == cudaSuccess && a.splits > 1)
         e = launch_pdl(logprobs_join_kernel<T, TOP>, dim3(a.n), dim3(kThreads), 0, st, a);
     return e;
@@ -384,62 +441,88 @@ struct LogprobGradArgs {
     bool aligned;       // the rows of both lie alike in their 16-byte words
 };
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads) logprobs_grad_kernel(LogprobGradArgs a)
+// p_v = 2^(l_v log2 e - c) with c = (m + logsum) log2 e as a pair: l_v log2 e - c_hi is
+// one fused operation, rounded at the size of the difference, and 2^-c_lo is a factor of
+// the row's coefficients.  The constant's rounding scales l - m alone.
+template <typename T, bool ENT>
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) logprobs_grad_kernel(LogprobGradArgs a)
 {
     constexpr int N = Vec<T>::N, U = kWordsPerThread;
     pdl_enter();
+    const int v0 = blockIdx.x * (U * kThreads) + threadIdx.x;
     for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
         const RowWords<T> row(static_cast<const T *>(a.logits) + t * a.ld, a.V);
         T *out = static_cast<T *>(a.out) + t * a.ldo;
         int target = a.targets ? a.targets[t] : -1;
-        if (target >= a.V)
-            target = -1;
-        const float gl = target >= 0 && a.dlogp ? a.dlogp[t] : 0.f;
+        if (target < 0 || target >= a.V)
+            target = -1 - 2 * N;
+        const float gl = target >= 0 ? a.dlogp[t] : 0.f;
         const float2 st = a.stats[t];
-        const float ge = a.dent ? a.dent[t] : 0.f, ent = a.dent ? a.entropy[t] : 0.f;
         // a token that takes no part, or a row of nothing but -inf
-        const bool zero = (target < 0 || !a.dlogp) && !a.dent;
-        const bool none = zero || (st.x == -INFINITY && st.y == 0.f);
-        const int v0 = blockIdx.x * (U * kThreads) + threadIdx.x;
-        uint4 q[U];
+        const bool none = (!ENT && target < 0) || (st.x == -INFINITY && st.y == 0.f);
+        if (none) {
+            const float zero[N] = {};
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int v = v0 + i * kThreads;
-            if (!none && v < row.count)
-                q[i] = row.load(v, 0.f);
+            for (int i = 0; i < U; i++)
+                if (v0 + i * kThreads < row.count)
+                    row.store(out, v0 + i * kThreads, pack<T>(zero), a.aligned);
+            continue;
         }
+        uint4 q[U];
+        // the block's words lie inside the row: no checks
+        const bool inside = a.aligned && row.inner(blockIdx.x * (U * kThreads), U * kThreads);
+        const T *src = row.row + row.first(v0);
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            if (inside)
+                q[i] = load_stream(src + i * (kThreads * N));
+            else if (v0 + i * kThreads < row.count)
+                q[i] = row.load(v0 + i * kThreads, 0.f);
+        }
+        // beyond 2^100 the product with log2 e may overflow: m is subtracted first
+        const bool far = fabsf(st.x) > 0x1p100f;
+        const float m = far ? 0.f : st.x;
+        const float hi = m * kLog2E, ls = st.y * kLog2E, c = hi + ls;
+        const float rest = fmaf(m, kLog2E, -hi) + (ls - (c - hi)) + fmaf(st.y, kLog2E, -ls);
+        const float f = ex2(-rest);
+        const float ge = ENT ? a.dent[t] : 0.f, ent = ENT ? a.entropy[t] : 0.f;
+        // -p (gl + ge (log p + entropy)), log p = (arg - rest) ln 2
+        const F2 l2e = f2(kLog2E), mc = f2(-c);
+        const F2 slope = f2(-f * ge * kLn2), level = f2(-f * (gl + ge * (ent - rest * kLn2)));
 #pragma unroll
         for (int i = 0; i < U; i++) {
             const int v = v0 + i * kThreads;
-            if (v >= row.count)
+            if (!inside && v >= row.count)
                 break;
-            float x[N];
-            if (none) {
+            F2 x[N / 2];
+            unpack<T>(q[i], x);
+            if (far) {
 #pragma unroll
-                for (int e = 0; e < N; e++)
-                    x[e] = 0.f;
-            } else {
-                unpack<T>(q[i], x);
-#pragma unroll
-                for (int e = 0; e < N; e++) {
-                    const float d = max_nan((x[e] - st.x) - st.y, kFar);
-                    const float p = ex2(d * kLog2E);
-                    x[e] = -p * fmaf(ge, d + ent, gl);
-                    if (row.first(v) + e == target)
-                        x[e] += gl;
+                for (int e = 0; e < N / 2; e++) {
+                    const float2 w = split(x[e]);
+                    x[e] = f2(w.x - st.x, w.y - st.x);
                 }
             }
-            if (a.aligned && row.whole(v)) {
+#pragma unroll
+            for (int e = 0; e < N / 2; e++) {
+                float2 d = split(fma(x[e], l2e, mc));
+                if (ENT) {      // a finite number for a logit of -inf
+                    d.x = max_nan(d.x, kFar);
+                    d.y = max_nan(d.y, kFar);
+                }
+                const F2 p = f2(ex2(d.x), ex2(d.y));
+                x[e] = mul(p, ENT ? fma(f2(d.x, d.y), slope, level) : level);
+            }
+            const unsigned at = target - row.first(v);
+            if (at < N) {
+#pragma unroll
+                for (int e = 0; e < N / 2; e++)
+                    x[e] = add(x[e], f2(at == 2u * e ? gl : 0.f, at == 2u * e + 1 ? gl : 0.f));
+            }
+            if (inside)
                 *reinterpret_cast<uint4 *>(out + row.first(v)) = pack<T>(x);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; e++) {
-                    const int c = row.first(v) + e;
-                    if (c >= 0 && c < a.V)
-                        out[c] = from_float<T>(x[e]);
-                }
-            }
+            else
+                row.store(out, v, pack<T>(x), a.aligned);
         }
     }
 }
@@ -449,8 +532,9 @@ cudaError_t launch_logprobs_grad(const LogprobGradArgs &a, cudaStream_t st)
 {
     constexpr int per = kThreads * kWordsPerThread;
     const int words = most_words(a.V, Vec<T>::N);
-    return launch_pdl(logprobs_grad_kernel<T>, dim3((words + per - 1) / per, std::min(a.n, 65535)),
-                      dim3(kThreads), 0, st, a);
+    const dim3 grid((words + per - 1) / per, std::min(a.n, 65535));
+    return a.dent ? launch_pdl(logprobs_grad_kernel<T, true>, grid, dim3(kThreads), 0, st, a)
+                  : launch_pdl(logprobs_grad_kernel<T, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 int check_sizes(int dtype, int n, int V)

@@ -80,6 +80,10 @@ def logprobs_grad(logits, targets, ref, dlogp, dent):
     rel = (xm + 3 * lp.abs() + logsum + 4 + 4) * H
     size = p * (gl.abs()[:, None] + ge.abs()[:, None] * (lp.abs() + e.abs()[:, None]))
     err = size * rel + p * ge.abs()[:, None] * (xm + lp.abs() + logsum + 4 * e.abs()[:, None]) * H
+    # log p + entropy also holds the rest of (m + logsum) log2 e behind its fp32 value: at
+    # most H times it, rounded in four operations, H of it each
+    m = torch.where(ref["empty"], 0.0, ref["stats"][:, 0]).abs()[:, None]
+    err += p * ge.abs()[:, None] * 4 * 1.45 * (m + logsum) * H * H
     if dlogp is not None:
         row = torch.arange(n, device=p.device)[on]
         g[row, ref["at"][on]] += gl[on]
