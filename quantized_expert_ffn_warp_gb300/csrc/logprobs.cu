@@ -6,12 +6,12 @@
 //   dl_v    = g_logp (1[v = target] - p_v) - g_ent p_v (log p_v + entropy)
 // m and logsum are kept apart: their sum could not hold logsum next to a large m.
 //
-// One pass over the row: each thread holds the running max of its values and the
-// two sums against it.  The likeliest tokens come from the same pass: a warp keeps
-// its best 32 in its lanes, sorted, and looks only at words whose largest value
-// reaches the best k-th value that a warp of the block holds; a key is the value's
-// order and the complement of its index, so that ties go to the lowest index in
-// whatever order they are met.
+// One pass over the row: each thread holds the running max of its values and the two
+// sums against it.  The likeliest tokens cost that pass nothing: behind it, the k-th
+// largest of the threads' maxima bounds the k-th value, and the few threads whose
+// maximum reaches it are gone through again.  Candidates go into lists of 32, sorted
+// over a warp's lanes; a key is the value's order and the complement of its index, so
+// that ties go to the lowest index in whatever order they are met.
 #include <algorithm>
 
 #include "args.cuh"
@@ -22,7 +22,7 @@ namespace qe {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kRowThreads = 128, kRowWarps = kRowThreads / 32;   // of a forward block
+constexpr int kRowWarps = 4;            // of a forward block for one row, or 1
 constexpr int kMaxTokens = 1 << 26, kMaxVocab = 1 << 20, kMaxTop = 32;
 constexpr int kWordsPerThread = 4;      // 16-byte loads that a thread has under way
 constexpr int kMaxSplits = 64;          // blocks of one row
@@ -139,21 +139,22 @@ __device__ __forceinline__ void insert(Key &list, Key c)
 
 // The best 32 of two sorted lists, sorted: the larger of each value and its
 // mirror image are a bitonic sequence.
-__device__ __forceinline__ Key merge(Key a, Key b)
+template <typename V>
+__device__ __forceinline__ V merge(V a, V b)
 {
     const int lane = threadIdx.x & 31;
-    const Key r = shfl_key(b, 31 - lane);
+    const V r = __shfl_sync(0xffffffffu, b, 31 - lane);
     a = a > r ? a : r;
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) {
-        const Key o = __shfl_xor_sync(0xffffffffu, a, d);
+        const V o = __shfl_xor_sync(0xffffffffu, a, d);
         a = ((lane & d) == 0) == (a > o) ? a : o;
     }
     return a;
 }
 
-// The k-th largest of the lanes' values (a bitonic sort).
-__device__ __forceinline__ float kth_of_lanes(float v, int k)
+// The lanes' values in falling order (a bitonic sort).
+__device__ __forceinline__ float sort_lanes(float v)
 {
     const int lane = threadIdx.x & 31;
 #pragma unroll
@@ -164,7 +165,7 @@ __device__ __forceinline__ float kth_of_lanes(float v, int k)
             const bool larger = ((lane & d) == 0) == ((lane & size) == 0);
             v = larger ? fmaxf(v, o) : fminf(v, o);
         }
-    return __shfl_sync(0xffffffffu, v, k - 1);
+    return v;
 }
 
 struct LogprobArgs {
@@ -181,11 +182,21 @@ struct LogprobArgs {
     Key *part_keys;         // [n][splits][32]
 };
 
+// A thread's values are cut into at most kGroups groups of 4 words, 8, 16 .., whose
+// largest values are kept until the row's bound is known.
+constexpr int kGroups = 32, kBatch = 8;     // groups whose words are gone through at once
+
 template <int W>
 struct Block {
     float4 sums[W];
     Key keys[W][32];
-    unsigned bound;         // order of the best k-th value that a warp holds
+};
+template <int W>
+struct Candidates {
+    float most[W][32];              // the threads' largest values, sorted
+    float group[kGroups][32 * W];   // the groups'
+    int queued;
+    int queue[kBatch * 32 * W];     // group * threads + thread
 };
 
 // Joins the W warps' sums and lists; warp 0 gets the result.
@@ -244,115 +255,160 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, long long t, co
     }
 }
 
-// Looks for values of the warp's words that belong into its list.  Every lane of the
-// warp calls it, for the words v, v + kRowThreads, .. of the row, none past `hi`.
-template <typename T, int U>
-__device__ __forceinline__ void collect(const RowWords<T> &row, int v, int hi, const float (&most)[U],
-                                        float bound, int top, Key &list, Key &kth, unsigned *shared)
+// The warp's list of the block's likeliest tokens.  The k-th largest of the threads'
+// largest values bounds the block's k-th largest value from below, and few groups hold a
+// value that reaches it: their words are queued and read again.
+template <typename T, int W>
+__device__ __forceinline__ Key collect(Candidates<W> &sm, const RowWords<T> &row, int lo, int hi,
+                                       float most, int groups, int words, int top)
 {
-    constexpr int N = Vec<T>::N;
-    const Key before = kth;
-    unsigned words = 0;
+    constexpr int N = Vec<T>::N, threads = 32 * W;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float best = sort_lanes(most);
+    if (W > 1) {
+        sm.most[warp][lane] = best;
+        __syncthreads();
+        best = sm.most[0][lane];
 #pragma unroll
-    for (int i = 0; i < U; i++)
-        words |= most[i] >= bound && v + i * kRowThreads < hi ? 1u << i : 0u;
-    while (__any_sync(0xffffffffu, words != 0)) {
-        unsigned mask = 0;
-        int first = 0;
-        if (words) {
-            const int w = v + (__ffs(words) - 1) * kRowThreads;
-            words &= words - 1;
-            first = row.first(w);
-            float x[N];
-            unpack<T>(row.load(w, -INFINITY), x);
-#pragma unroll
-            for (int e = 0; e < N; e++)     // not below the bound: a NaN counts as -inf
-                mask |= !(x[e] < bound) && first + e >= 0 && first + e < row.len ? 1u << e : 0u;
-        }
-        while (__any_sync(0xffffffffu, mask != 0)) {
-            Key c = 0;
-            if (mask) {
-                const int i = first + __ffs(mask) - 1;
-                c = key_of(to_float<T>(row.row[i]), i);
-                mask &= mask - 1;
-            }
-            unsigned offers = __ballot_sync(0xffffffffu, c > kth);
-            while (offers) {
-                const Key k = shfl_key(c, __ffs(offers) - 1);
-                if (k > kth) {
-                    insert(list, k);
-                    kth = shfl_key(list, top - 1);
-                }
-                offers &= offers - 1;
-            }
-        }
+        for (int w = 1; w < W; w++)
+            best = merge(best, sm.most[w][lane]);
     }
-    if (kth != before && (threadIdx.x & 31) == 0)
-        atomicMax(shared, (unsigned)(kth >> 32));
+    const float bound = __shfl_sync(0xffffffffu, best, top - 1);
+    Key list = 0, kth = 0;
+    for (int g0 = 0; g0 < groups; g0 += kBatch) {
+        if (threadIdx.x == 0)
+            sm.queued = 0;
+        __syncthreads();
+        if (most >= bound)
+            for (int g = g0; g < min(groups, g0 + kBatch); g++)
+                if (sm.group[g][threadIdx.x] >= bound)
+                    sm.queue[atomicAdd(&sm.queued, 1)] = g * threads + threadIdx.x;
+        __syncthreads();
+        const int count = sm.queued * words;
+        for (int i0 = warp * 32; i0 < count; i0 += threads) {
+            unsigned mask = 0;
+            int first = 0;
+            float x[N];
+            if (i0 + lane < count) {
+                const int e = sm.queue[(i0 + lane) / words], j = (i0 + lane) % words;
+                const int v = lo + (e / threads * words + j) * threads + e % threads;
+                first = row.first(v);
+                if (v < hi) {
+                    unpack<T>(row.load(v, -INFINITY), x);
+#pragma unroll
+                    for (int n = 0; n < N; n++)     // not below it: a NaN counts as -inf
+                        mask |= !(x[n] < bound) && first + n >= 0 && first + n < row.len ? 1u << n
+                                                                                         : 0u;
+                }
+            }
+            while (__any_sync(0xffffffffu, mask != 0)) {
+                Key c = 0;
+                if (mask) {
+                    const int n = __ffs(mask) - 1;
+                    float v = x[0];
+#pragma unroll
+                    for (int k = 1; k < N; k++)
+                        v = n == k ? x[k] : v;
+                    c = key_of(v, first + n);
+                    mask &= mask - 1;
+                }
+                unsigned offers = __ballot_sync(0xffffffffu, c > kth);
+                while (offers) {
+                    const Key k = shfl_key(c, __ffs(offers) - 1);
+                    if (k > kth) {
+                        insert(list, k);
+                        kth = shfl_key(list, top - 1);
+                    }
+                    offers &= offers - 1;
+                }
+            }
+        }
+        __syncthreads();        // the queue is gone through
+    }
+    return list;
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kRowThreads) logprobs_kernel(LogprobArgs a)
+// W warps a row.
+template <typename T, bool TOP, int W>
+__global__ void __launch_bounds__(32 * W) logprobs_kernel(LogprobArgs a)
 {
-    constexpr int N = Vec<T>::N, U = kWordsPerThread;
-    __shared__ Block<kRowWarps> sm;
+    constexpr int N = Vec<T>::N, U = kWordsPerThread, threads = 32 * W;
+    __shared__ Block<W> sm;
+    __shared__ std::conditional_t<TOP, Candidates<W>, int> cand;
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
-        const RowWords<T> row(static_cast<const T *>(a.logits) + t * a.ld, a.V);
-        const int lo = blockIdx.x * a.per, hi = min(row.count, lo + a.per);
-        Sums u = {-INFINITY, 0.f, 0.f};
-        Key list = 0, kth = 0;
-        if (TOP) {
-            if (threadIdx.x == 0)
-                sm.bound = order_of(-INFINITY);
-            __syncthreads();
-        }
-        float low[N];
+    const auto row_of = [&](long long t) {
+        return RowWords<T>(static_cast<const T *>(a.logits) + t * a.ld, a.V);
+    };
+    const auto block = [&](const RowWords<T> &row) {
+        const int lo = blockIdx.x * a.per;
+        return make_int2(lo, min(row.count, lo + a.per));
+    };
+    float low[N];
 #pragma unroll
-        for (int e = 0; e < N; e++)
-            low[e] = -INFINITY;
-        const uint4 none = pack<T>(low);
-        uint4 next[U];
-        const T *src = row.row + row.first(lo + threadIdx.x);
-        // words at + threadIdx.x + i kRowThreads
-        const auto load = [&](int at) {
-            if (at + U * kRowThreads <= hi && row.inner(at, U * kRowThreads)) {
+    for (int e = 0; e < N; e++)
+        low[e] = -INFINITY;
+    const uint4 none = pack<T>(low);
+    uint4 next[U];
+    // words at + threadIdx.x + i threads
+    const auto load = [&](const RowWords<T> &row, int at, int hi) {
+        if (at + U * threads <= hi && row.inner(at, U * threads)) {
+            const T *src = row.row + row.first(at + threadIdx.x);
 #pragma unroll
-                for (int i = 0; i < U; i++)
-                    next[i] = load_stream(src + i * (kRowThreads * N));
-            } else {
+            for (int i = 0; i < U; i++)
+                next[i] = load_stream(src + i * (threads * N));
+        } else {
 #pragma unroll
-                for (int i = 0; i < U; i++) {
-                    const int v = at + threadIdx.x + i * kRowThreads;
-                    next[i] = v < hi ? row.load(v, -INFINITY) : none;
-                }
+            for (int i = 0; i < U; i++) {
+                const int v = at + threadIdx.x + i * threads;
+                next[i] = v < hi ? row.load(v, -INFINITY) : none;
             }
-            src += U * kRowThreads * N;
-        };
-        load(lo);
-        for (int at = lo; at < hi; at += U * kRowThreads) {
+        }
+    };
+    // chunks of a group
+    int per_group = 1;
+    while (per_group * kGroups * U * threads < a.per)
+        per_group *= 2;
+    {
+        const RowWords<T> row = row_of(blockIdx.y);
+        const int2 b = block(row);
+        load(row, b.x, b.y);
+    }
+    for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
+        const RowWords<T> row = row_of(t);
+        const int lo = block(row).x, hi = block(row).y;
+        Sums u = {-INFINITY, 0.f, 0.f};
+        float most = -INFINITY;
+        int chunk = 0, group = 0;
+        for (int at = lo; at < hi; at += U * threads) {
             uint4 q[U];
-            float most[U], top = -INFINITY;
+            float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < U; i++) {
                 q[i] = next[i];
-                most[i] = fmaxf(word_max<T>(q[i]), -INFINITY);     // a word of NaN too
-                top = fmaxf(top, most[i]);
+                top = fmaxf(top, word_max<T>(q[i]));
             }
-            if (at + U * kRowThreads < hi)
-                load(at + U * kRowThreads);
-            if (TOP) {
-                float bound = value_of(*(volatile unsigned *)&sm.bound);
-                if (at == lo)
-                    bound = fmaxf(bound, kth_of_lanes(top, a.top));
-                if (__any_sync(0xffffffffu, top >= bound))
-                    collect<T, U>(row, at + threadIdx.x, hi, most, bound, a.top, list, kth,
-                                  &sm.bound);
+            if (at + U * threads < hi)
+                load(row, at + U * threads, hi);
+            if constexpr (TOP) {
+                most = fmaxf(most, top);
+                if (++chunk == per_group || at + U * threads >= hi) {
+                    cand.group[group++][threadIdx.x] = most;
+                    most = -INFINITY;
+                    chunk = 0;
+                }
             }
             add_words<T, U>(u, q, top);
         }
-        join_warps<TOP, kRowWarps>(sm, u, list);
+        if (t + gridDim.y < a.n) {      // the next row's first words
+            const RowWords<T> after = row_of(t + gridDim.y);
+            const int2 b = block(after);
+            load(after, b.x, b.y);
+        }
+        Key list = 0;
+        if constexpr (TOP)
+            list = collect<T, W>(cand, row, lo, hi, u.m, group, per_group * U, a.top);
+        join_warps<TOP, W>(sm, u, list);
         if (warp == 0) {
             if (a.splits == 1) {
                 finish_row<T, TOP>(a, t, u, list);
@@ -393,15 +449,22 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
 // Words of the longest row, whatever its address.
 int most_words(int V, int per) { return (V + per - 1 + per - 1) / per; }
 
+// Warps of a row: one where it has no more than eight chunks of words for every lane, so
+// that a row's joins are a warp's own.
+int row_warps(int V, int size)
+{
+    return most_words(V, 16 / size) <= 32 * kWordsPerThread * 8 ? 1 : kRowWarps;
+}
+
 // Blocks of a row: enough for a block on every SM four times over, each with a
 // load of kWordsPerThread words per thread.  Asks no device, since the workspace's size
 // follows from it.
 int row_splits(int n, int V, int size)
 {
-    const int words = most_words(V, 16 / size), step = kRowThreads * kWordsPerThread;
+    const int words = most_words(V, 16 / size), step = 32 * kRowWarps * kWordsPerThread;
     const int want = 4 * 152 / std::min(n, 4 * 152);
     const int most = (words + step - 1) / step;
-    return std::max(1, std::min({want, most, kMaxSplits}));
+    return row_warps(V, size) == 1 ? 1 : std::max(1, std::min({want, most, kMaxSplits}));
 }
 
 size_t key_offset(int n, int splits) { return ((size_t)n * splits * sizeof(float4) + 255) / 256 * 256; }
@@ -414,11 +477,20 @@ size_t logprob_ws(int n, int V, int size, int top)
     return key_offset(n, splits) + (top ? (size_t)n * splits * 32 * sizeof(Key) : 0);
 }
 
+template <typename T, bool TOP, int W>
+cudaError_t launch_rows(const LogprobArgs &a, cudaStream_t st)
+{
+    // rows beyond what runs at once go to the same blocks, evenly
+    const int most = 152 * (W == 1 ? 32 : 8);
+    const int turns = (a.n + most - 1) / most;
+    const int rows = a.splits > 1 ? a.n : (a.n + turns - 1) / turns;
+    return launch_pdl(logprobs_kernel<T, TOP, W>, dim3(a.splits, rows), dim3(32 * W), 0, st, a);
+}
 template <typename T, bool TOP>
 cudaError_t launch_top(const LogprobArgs &a, cudaStream_t st)
 {
-    cudaError_t e = launch_pdl(logprobs_kernel<T, TOP>, dim3(a.splits, std::min(a.n, 65535)),
-                               dim3(kRowThreads), 0, st, a);
+    cudaError_t e = row_warps(a.V, sizeof(T)) == 1 ? launch_rows<T, TOP, 1>(a, st)
+                                                   : launch_rows<T, TOP, kRowWarps>(a, st);
     if (e == cudaSuccess && a.splits > 1)
         e = launch_pdl(logprobs_join_kernel<T, TOP>, dim3(a.n), dim3(kThreads), 0, st, a);
     return e;
