@@ -12,10 +12,10 @@
 //   and, for a gate for each token, from the one row sum that dy needs.
 //
 // Bound by HBM: four arrays of n x H are read or written forward, six backward.
-// A CTA holds a row in registers, two reductions a row, and goes through rows with
-// the vectors that all rows share in registers; the column sums stay there too, and
-// leave as one partial row per kRun rows and CTA, added by a second kernel in a
-// fixed order.
+// A CTA goes through rows, one in registers and the next one's loads under way, two
+// reductions a row.  The vectors that all rows share lie in shared memory as fp32, each
+// thread's part by itself (no barriers).  The column sums stay in registers and leave as
+// one partial row per kRun rows and CTA, added by a second kernel in a fixed order.
 #include <algorithm>
 
 #include "args.cuh"
@@ -41,96 +41,127 @@ struct NormArgs {
 };
 
 // Sum over the block in a fixed order; `part` is one of two buffers used in turn.
-__device__ __forceinline__ float sum_block(float v, float *part, int warps)
+__device__ __forceinline__ float sum_block(float v, float4 *part, int warps)
 {
     v = sum_warp(v);
     if (warps == 1)
         return v;
     if ((threadIdx.x & 31) == 0)
-        part[threadIdx.x >> 5] = v;
+        reinterpret_cast<float *>(part)[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.f;
-    for (int w = 0; w < warps; w++)
-        s += part[w];
+    for (int w = 0; w < warps; w += 4) {
+        const float4 q = part[w / 4];
+        s += (q.x + (w + 1 < warps ? q.y : 0.f)) +
+             ((w + 2 < warps ? q.z : 0.f) + (w + 3 < warps ? q.w : 0.f));
+    }
     return s;
 }
 
-template <typename T>
-__device__ __forceinline__ uint4 ones()
-{
-    const float d[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-    return pack<T>(d);
-}
-
-template <typename T, int V>
+template <int V>
 __device__ __forceinline__ void load_row(uint4 (&q)[V], const void *base, long long at, int vecs)
 {
-    const T *row = static_cast<const T *>(base) + at;
+    const uint16_t *row = static_cast<const uint16_t *>(base) + at;
 #pragma unroll
     for (int i = 0; i < V; i++) {
         const int v = threadIdx.x + i * blockDim.x;
-        q[i] = v < vecs ? load_stream(row + 8 * v) : make_uint4(0, 0, 0, 0);
+        if (v < vecs)
+            q[i] = load_stream(row + 8 * v);
     }
 }
 
-// The vector that all rows share, 1 where there is none.
-template <typename T, int V>
-__device__ __forceinline__ void load_shared(uint4 (&q)[V], const void *base, int vecs)
-{
+// A vector that all rows share, as fp32 in shared memory: word 2 i + j of a thread holds
+// four of its values.  `by` multiplies it; 1 where there is none.
+struct Shared {
+    float4 *mine;
+
+    __device__ __forceinline__ void put(int word, const float *d)
+    {
+        mine[word * blockDim.x] = make_float4(d[0], d[1], d[2], d[3]);
+    }
+    template <typename T, int V>
+    __device__ __forceinline__ void load(const void *base, const void *by, int vecs)
+    {
 #pragma unroll
-    for (int i = 0; i < V; i++) {
-        const int v = threadIdx.x + i * blockDim.x;
-        q[i] = base && v < vecs ? *(reinterpret_cast<const uint4 *>(base) + v) : ones<T>();
+        for (int i = 0; i < V; i++) {
+            const int v = threadIdx.x + i * blockDim.x;
+            float d[8], f[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                d[e] = f[e] = 1.f;
+            if (base && v < vecs)
+                unpack<T>(*(static_cast<const uint4 *>(base) + v), d);
+            if (by && v < vecs)
+                unpack<T>(*(static_cast<const uint4 *>(by) + v), f);
+#pragma unroll
+            for (int e = 0; e < 8; e++)
+                d[e] *= f[e];
+            put(2 * i, d);
+            put(2 * i + 1, d + 4);
+        }
     }
-}
+    // the eight values of the thread's word i, in pairs
+    __device__ __forceinline__ void get(int i, F2 (&d)[4]) const
+    {
+        const ulonglong2 a = *reinterpret_cast<const ulonglong2 *>(mine + 2 * i * blockDim.x);
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2 *>(mine + (2 * i + 1) * blockDim.x);
+        d[0].v = a.x, d[1].v = a.y, d[2].v = b.x, d[3].v = b.y;
+    }
+};
 
+// V words of a row for each thread.
 template <typename T, int V>
-__global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(NormArgs a)
+__global__ void __launch_bounds__(kMaxThreads, V <= 2 ? 2 : 1) residual_norm_kernel(NormArgs a)
 {
     constexpr bool kAhead = V <= 2;     // the next row's loads under way
-    __shared__ float part[2][kMaxWarps];
+    extern __shared__ float4 shared[];  // [2][2 V][threads]
+    __shared__ float4 part[2][kMaxWarps / 4];
     pdl_enter();
     const int warps = blockDim.x / 32;
-    uint4 gain[V], gate[V], next_gain[V], rq[V], yq[V];
-    load_shared<T, V>(gain, a.gain, a.vecs);
-    load_shared<T, V>(gate, a.token_gate ? nullptr : a.gate, a.vecs);
-    load_shared<T, V>(next_gain, a.next_gain, a.vecs);
-    const T *token_gate = a.token_gate ? static_cast<const T *>(a.gate) : nullptr;
+    Shared weight{shared + threadIdx.x}, next_gain{shared + 2 * V * blockDim.x + threadIdx.x};
+    uint4 rq[V], yq[V];
+#pragma unroll
+    for (int i = 0; i < V; i++)
+        rq[i] = yq[i] = make_uint4(0, 0, 0, 0);
     const auto load = [&](long long t) {
-        load_row<T, V>(rq, a.resid, t * a.ld_resid, a.vecs);
-        load_row<T, V>(yq, a.y, t * a.ld_y, a.vecs);
+        load_row<V>(rq, a.resid, t * a.ld_resid, a.vecs);
+        load_row<V>(yq, a.y, t * a.ld_y, a.vecs);
     };
     long long t = blockIdx.x;
-    if (t < a.n)
-        load(t);
+    load(t);
+    weight.load<T, V>(a.gain, a.token_gate ? nullptr : a.gate, a.vecs);
+    next_gain.load<T, V>(a.next_gain, nullptr, a.vecs);
+    const T *token_gate = a.token_gate ? static_cast<const T *>(a.gate) : nullptr;
+    const F2 scale = f2(a.scale);
     for (; t < a.n; t += gridDim.x) {
-        float o[V][8], r[V][8];
-        float ss = 0.f;
+        const float tg = token_gate ? to_float<T>(token_gate[t]) : 1.f;
+        F2 o[V][4], r[V][4];
+        F2 ss = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             unpack<T>(yq[i], o[i]);
             unpack<T>(rq[i], r[i]);
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                ss = fmaf(o[i][e], o[i][e], ss);
+            for (int e = 0; e < 4; e++) {
+                ss = fma(o[i][e], o[i][e], ss);
+                r[i][e] = mul(r[i][e], scale);
+            }
         }
-        const float tg = token_gate ? to_float<T>(token_gate[t]) : 1.f;
         if (kAhead && t + gridDim.x < a.n)
             load(t + gridDim.x);
         float r1 = 1.f, r2 = 1.f;
         if (a.gain)
-            r1 = __frsqrt_rn(fmaf(sum_block(ss, part[0], warps), a.inv_h, a.eps));
-        const float f = r1 * tg;
-        ss = 0.f;
+            r1 = __frsqrt_rn(fmaf(sum_block(sum(ss), part[0], warps), a.inv_h, a.eps));
+        const F2 f = f2(r1 * tg);
+        ss = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            float g[8], c[8];
-            unpack<T>(gain[i], g);
-            unpack<T>(gate[i], c);
+            F2 w[4];
+            weight.get(i, w);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                o[i][e] = fmaf(a.scale, r[i][e], o[i][e] * f * (g[e] * c[e]));
-                ss = fmaf(o[i][e], o[i][e], ss);
+            for (int e = 0; e < 4; e++) {
+                o[i][e] = fma(mul(o[i][e], f), w[e], r[i][e]);
+                ss = fma(o[i][e], o[i][e], ss);
             }
             const int v = threadIdx.x + i * blockDim.x;
             if (v < a.vecs)
@@ -138,14 +169,15 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_kernel(NormArgs 
                     pack<T>(o[i]);
         }
         if (a.xn) {
-            r2 = __frsqrt_rn(fmaf(sum_block(ss, part[1], warps), a.inv_h, a.eps));
+            r2 = __frsqrt_rn(fmaf(sum_block(sum(ss), part[1], warps), a.inv_h, a.eps));
+            const F2 f2nd = f2(r2);
 #pragma unroll
             for (int i = 0; i < V; i++) {
-                float g[8];
-                unpack<T>(next_gain[i], g);
+                F2 g[4];
+                next_gain.get(i, g);
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    g[e] *= o[i][e] * r2;
+                for (int e = 0; e < 4; e++)
+                    g[e] = mul(mul(o[i][e], f2nd), g[e]);
                 const int v = threadIdx.x + i * blockDim.x;
                 if (v < a.vecs)
                     *reinterpret_cast<uint4 *>(static_cast<T *>(a.xn) + t * a.ld_xn + 8 * v) =
@@ -176,47 +208,94 @@ struct NormGradArgs {
     float *dgain, *dgate_ch, *dnext_gain;
 };
 
-// Column sums of V = 4 lie in shared memory: registers hold no more than two words.
+// Rows of four words a thread have their column sums in shared memory, where registers
+// hold no more than two words', and the shared vectors are read from L2 instead.
+// The statistics' products out r2 and y r1 are formed again after each reduction, since
+// their packed words take a quarter of the registers.
 template <typename T, int V>
 __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(NormGradArgs a)
 {
-    constexpr bool kAhead = V <= 2;
-    extern __shared__ float4 sums_sm[];     // V = 4: [2][V][2][threads]
-    __shared__ float part[2][kMaxWarps];
+    constexpr bool kAhead = V <= 2, kRegs = V <= 2;
+    extern __shared__ float4 shared[];  // [2][2 V][threads]
+    __shared__ float4 part[2][kMaxWarps / 4];
     pdl_enter();
     const int warps = blockDim.x / 32;
-    uint4 gain[V], gate[V], next_gain[V];
-    load_shared<T, V>(gain, a.gain, a.vecs);
-    load_shared<T, V>(gate, a.token_gate ? nullptr : a.gate, a.vecs);
-    load_shared<T, V>(next_gain, a.next_gain, a.vecs);
+    // the vectors that all rows share, or the column sums
+    Shared weight{shared + threadIdx.x}, next_gain{shared + 2 * V * blockDim.x + threadIdx.x};
+    Shared &sum1 = weight, &sum2 = next_gain;
     const T *token_gate = a.token_gate ? static_cast<const T *>(a.gate) : nullptr;
     uint4 dq[V], nq[V], oq[V], yq[V];
 #pragma unroll
     for (int i = 0; i < V; i++)
-        dq[i] = nq[i] = oq[i] = make_uint4(0, 0, 0, 0);
+        dq[i] = nq[i] = oq[i] = yq[i] = make_uint4(0, 0, 0, 0);
     const auto load = [&](long long t) {
         if (a.dout)
-            load_row<T, V>(dq, a.dout, t * a.ld_dout, a.vecs);
+            load_row<V>(dq, a.dout, t * a.ld_dout, a.vecs);
         if (a.dxn) {
-            load_row<T, V>(nq, a.dxn, t * a.ld_dxn, a.vecs);
-            load_row<T, V>(oq, a.out, t * a.ld_out, a.vecs);
+            load_row<V>(nq, a.dxn, t * a.ld_dxn, a.vecs);
+            load_row<V>(oq, a.out, t * a.ld_out, a.vecs);
         }
-        load_row<T, V>(yq, a.y, t * a.ld_y, a.vecs);
+        load_row<V>(yq, a.y, t * a.ld_y, a.vecs);
     };
-    constexpr int R = V <= 2 ? V : 1;
-    float s1[R][8], s2[R][8];       // V <= 2: the column sums
+    long long t = blockIdx.x;
+    load(t);
+    const void *channel_gate = a.token_gate ? nullptr : a.gate;
+    if (kRegs) {
+        weight.load<T, V>(a.gain, channel_gate, a.vecs);
+        next_gain.load<T, V>(a.next_gain, nullptr, a.vecs);
+    }
+    const auto vector = [&](const Shared &sm, int i, const void *base, const void *by, F2(&d)[4]) {
+        if constexpr (kRegs) {
+            sm.get(i, d);
+        } else {
+            const int v = threadIdx.x + i * blockDim.x;
+            F2 f[4];
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                d[e] = f[e] = f2(1.f);
+            if (base && v < a.vecs)
+                unpack<T>(*(static_cast<const uint4 *>(base) + v), d);
+            if (by && v < a.vecs)
+                unpack<T>(*(static_cast<const uint4 *>(by) + v), f);
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                d[e] = mul(d[e], f[e]);
+        }
+    };
+    constexpr int R = kRegs ? V : 1;
+    F2 s1[R][4], s2[R][4];      // the column sums
     const auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < V; i++)
-            if constexpr (V <= 2) {
+            if constexpr (kRegs) {
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    s1[i][e] = s2[i][e] = 0.f;
+                for (int e = 0; e < 4; e++)
+                    s1[i][e] = s2[i][e] = f2(0.f);
             } else if (a.sums) {
+                const float zero[4] = {};
 #pragma unroll
-                for (int j = 0; j < 4; j++)
-                    sums_sm[(4 * i + j) * blockDim.x + threadIdx.x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int j = 0; j < 2; j++) {
+                    sum1.put(2 * i + j, zero);
+                    sum2.put(2 * i + j, zero);
+                }
             }
+    };
+    const auto accumulate = [&](F2(&regs)[R][4], Shared &sm, int i, const F2(&c)[4], F2 by) {
+        if constexpr (kRegs) {
+#pragma unroll
+            for (int e = 0; e < 4; e++)
+                regs[i][e] = fma(c[e], by, regs[i][e]);
+        } else if (a.sums) {
+            F2 d[4];
+            sm.get(i, d);
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                const float2 x = split(fma(c[2 * j], by, d[2 * j]));
+                const float2 y = split(fma(c[2 * j + 1], by, d[2 * j + 1]));
+                const float v[4] = {x.x, x.y, y.x, y.y};
+                sm.put(2 * i + j, v);
+            }
+        }
     };
     clear();
     const auto flush = [&](int run) {
@@ -227,114 +306,96 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(Norm
             const int v = threadIdx.x + i * blockDim.x;
             if (v >= a.vecs)
                 continue;
-            float4 w[4];
+            F2 w[2][4];
+            if constexpr (kRegs) {
 #pragma unroll
-            for (int j = 0; j < 4; j++)
-                if constexpr (V <= 2) {
-                    const float *s = j < 2 ? s1[i] + 4 * j : s2[i] + 4 * (j - 2);
-                    w[j] = make_float4(s[0], s[1], s[2], s[3]);
-                } else {
-                    w[j] = sums_sm[(4 * i + j) * blockDim.x + threadIdx.x];
+                for (int e = 0; e < 4; e++) {
+                    w[0][e] = s1[i][e];
+                    w[1][e] = s2[i][e];
                 }
-            *reinterpret_cast<float4 *>(p + 8 * v) = w[0];
-            *reinterpret_cast<float4 *>(p + 8 * v + 4) = w[1];
-            *reinterpret_cast<float4 *>(q + 8 * v) = w[2];
-            *reinterpret_cast<float4 *>(q + 8 * v + 4) = w[3];
+            } else {
+                sum1.get(i, w[0]);
+                sum2.get(i, w[1]);
+            }
+#pragma unroll
+            for (int k = 0; k < 2; k++)
+#pragma unroll
+                for (int j = 0; j < 2; j++)
+                    *reinterpret_cast<ulonglong2 *>((k ? q : p) + 8 * v + 4 * j) =
+                        make_ulonglong2(w[k][2 * j].v, w[k][2 * j + 1].v);
         }
         clear();
     };
-    long long t = blockIdx.x;
-    if (t < a.n)
-        load(t);
+    const F2 one = f2(1.f), scale = f2(a.scale);
     int rows = 0, run = 0;
     for (; t < a.n; t += gridDim.x) {
         const float2 st = a.stats[t];
         const float tg = token_gate ? to_float<T>(token_gate[t]) : 1.f;
-        float d[V][8], z[V][8], n[V][8];
-        float m = 0.f;
+        const F2 r1 = f2(st.x), r2 = f2(st.y);
+        F2 d[V][4];
+        uint4 ok[V], yk[V];
+        F2 m = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            float g[8];
+            F2 x[4], n[4], g[4], c[4];
             unpack<T>(dq[i], d[i]);
-            unpack<T>(oq[i], n[i]);
-            unpack<T>(yq[i], z[i]);
-            unpack<T>(next_gain[i], g);
-            float x[8];
+            unpack<T>(oq[i], n);
             unpack<T>(nq[i], x);
-            float c[8];
+            vector(next_gain, i, a.next_gain, nullptr, g);
+            ok[i] = oq[i];
+            yk[i] = yq[i];
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                n[i][e] *= st.y;
-                z[i][e] *= st.x;
-                c[e] = x[e] * n[i][e];
-                m = fmaf(c[e], g[e], m);
+            for (int e = 0; e < 4; e++) {
+                c[e] = mul(x[e], mul(n[e], r2));
+                m = fma(c[e], g[e], m);
                 // do without its mean's part
-                d[i][e] = fmaf(st.y, x[e] * g[e], d[i][e]);
+                d[i][e] = fma(r2, mul(x[e], g[e]), d[i][e]);
             }
-            if constexpr (V <= 2) {
-#pragma unroll
-                for (int e = 0; e < 8; e++)
-                    s2[i][e] += c[e];
-            } else if (a.sums) {
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    float4 &s = sums_sm[(4 * i + 2 + j) * blockDim.x + threadIdx.x];
-                    s = make_float4(s.x + c[4 * j], s.y + c[4 * j + 1], s.z + c[4 * j + 2],
-                                    s.w + c[4 * j + 3]);
-                }
-            }
+            accumulate(s2, sum2, i, c, one);
         }
         if (kAhead && t + gridDim.x < a.n)
             load(t + gridDim.x);
-        const float mean = a.dxn ? sum_block(m, part[0], warps) * a.inv_h * st.y : 0.f;
-        m = 0.f;
+        const float mean =
+            a.dxn ? sum_block(sum(m), part[0], warps) * a.inv_h * st.y : 0.f;
+        const F2 minus = f2(-mean), gate = f2(tg);
+        m = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            float g[8], c[8], w[8];
-            unpack<T>(gain[i], g);
-            unpack<T>(gate[i], c);
+            F2 n[4], z[4], w[4];
+            unpack<T>(ok[i], n);
+            unpack<T>(yk[i], z);
+            vector(weight, i, a.gain, channel_gate, w);
 #pragma unroll
-            for (int e = 0; e < 8; e++) {
-                d[i][e] = fmaf(-n[i][e], mean, d[i][e]);
-                w[e] = d[i][e] * z[i][e];
-                m = fmaf(w[e], g[e] * c[e], m);
-                w[e] *= tg;
+            for (int e = 0; e < 4; e++) {
+                d[i][e] = fma(mul(n[e], r2), minus, d[i][e]);
+                z[e] = mul(d[i][e], mul(z[e], r1));
+                m = fma(z[e], w[e], m);
             }
-            if constexpr (V <= 2) {
+            accumulate(s1, sum1, i, z, gate);
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    s1[i][e] += w[e];
-            } else if (a.sums) {
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    float4 &s = sums_sm[(4 * i + j) * blockDim.x + threadIdx.x];
-                    s = make_float4(s.x + w[4 * j], s.y + w[4 * j + 1], s.z + w[4 * j + 2],
-                                    s.w + w[4 * j + 3]);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; e++)
-                w[e] = a.scale * d[i][e];
+            for (int e = 0; e < 4; e++)
+                n[e] = mul(d[i][e], scale);
             const int v = threadIdx.x + i * blockDim.x;
             if (v < a.vecs)
                 *reinterpret_cast<uint4 *>(static_cast<T *>(a.dresid) + t * a.ld_dresid + 8 * v) =
-                    pack<T>(w);
+                    pack<T>(n);
         }
         // sum of do gain gate z, the gate of a token left out
-        const float dot = sum_block(m, part[1], warps);
-        const float back = a.gain ? dot * tg * a.inv_h : 0.f, f = a.gain ? st.x : 1.f;
+        const float dot = sum_block(sum(m), part[1], warps);
+        const F2 back = f2(-dot * tg * a.inv_h * st.x), f = f2(st.x * tg);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            float g[8], c[8];
-            unpack<T>(gain[i], g);
-            unpack<T>(gate[i], c);
+            F2 z[4], w[4];
+            unpack<T>(yk[i], z);
+            vector(weight, i, a.gain, channel_gate, w);
 #pragma unroll
-            for (int e = 0; e < 8; e++)
-                g[e] = f * fmaf(-z[i][e], back, d[i][e] * tg * (g[e] * c[e]));
+            for (int e = 0; e < 4; e++)
+                z[e] = a.gain ? fma(mul(z[e], r1), back, mul(mul(d[i][e], f), w[e]))
+                              : mul(mul(d[i][e], f), w[e]);
             const int v = threadIdx.x + i * blockDim.x;
             if (v < a.vecs)
                 *reinterpret_cast<uint4 *>(static_cast<T *>(a.dy) + t * a.ld_dy + 8 * v) =
-                    pack<T>(g);
+                    pack<T>(z);
         }
         if (token_gate && a.dgate && threadIdx.x == 0)
             a.dgate[t] = dot;
@@ -409,35 +470,50 @@ size_t grad_ws(int n, int H)
     return 2 * sizeof(float) * (size_t)grad_blocks(n, H) * grad_runs(n, H) * H;
 }
 
+// Shared memory of `vectors` vectors of a block's columns.
+int shared_bytes(int H, int vectors)
+{
+    return (int)sizeof(float4) * 2 * row_words(H) * row_threads(H) * vectors;
+}
+
+template <typename T, int V>
+cudaError_t launch_norm_as(const NormArgs &a, int sms, cudaStream_t st)
+{
+    const int threads = row_threads(a.H);
+    const cudaError_t e =
+        cudaFuncSetAttribute(residual_norm_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             shared_bytes(V > 2 ? kMaxWidth : kMaxWidth / 2, 2));
+    if (e != cudaSuccess)
+        return e;
+    // as many CTAs as run at once
+    const dim3 grid(std::min(a.n, sms * std::max(1, (V > 2 ? 512 : 1024) / threads)));
+    return launch_pdl(residual_norm_kernel<T, V>, grid, dim3(threads), shared_bytes(a.H, 2), st, a);
+}
 template <typename T>
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t st)
 {
-    const int threads = row_threads(a.H);
-    const dim3 grid(std::min(a.n, sms * std::max(1, 1024 / threads)));
-    return row_words(a.H) == 2
-               ? launch_pdl(residual_norm_kernel<T, 2>, grid, dim3(threads), 0, st, a)
-               : launch_pdl(residual_norm_kernel<T, 4>, grid, dim3(threads), 0, st, a);
+    return row_words(a.H) == 2 ? launch_norm_as<T, 2>(a, sms, st) : launch_norm_as<T, 4>(a, sms, st);
 }
 
+template <typename T, int V>
+cudaError_t launch_norm_grad_as(const NormGradArgs &a, cudaStream_t st)
+{
+    const cudaError_t e = cudaFuncSetAttribute(
+        residual_norm_grad_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        shared_bytes(V > 2 ? kMaxWidth : kMaxWidth / 2, 2));
+    if (e != cudaSuccess)
+        return e;
+    return launch_pdl(residual_norm_grad_kernel<T, V>, dim3(grad_blocks(a.n, a.H)),
+                      dim3(row_threads(a.H)), shared_bytes(a.H, V > 2 && !a.sums ? 0 : 2), st, a);
+}
 template <typename T>
 cudaError_t launch_norm_grad(const NormGradArgs &a, cudaStream_t st)
 {
-    const int threads = row_threads(a.H);
-    const dim3 grid(grad_blocks(a.n, a.H));
-    cudaError_t e = cudaSuccess;
-    if (row_words(a.H) == 2) {
-        e = launch_pdl(residual_norm_grad_kernel<T, 2>, grid, dim3(threads), 0, st, a);
-    } else {
-        const size_t smem = a.sums ? sizeof(float4) * 16 * threads : 0;
-        e = cudaFuncSetAttribute(residual_norm_grad_kernel<T, 4>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)sizeof(float4) * 16 * kMaxThreads);
-        if (e == cudaSuccess)
-            e = launch_pdl(residual_norm_grad_kernel<T, 4>, grid, dim3(threads), smem, st, a);
-    }
+    cudaError_t e = row_words(a.H) == 2 ? launch_norm_grad_as<T, 2>(a, st)
+                                        : launch_norm_grad_as<T, 4>(a, st);
     if (e == cudaSuccess && a.sums)
         e = launch_pdl(residual_norm_sums_kernel<T>, dim3((a.H + 31) / 32, a.dnext_gain ? 2 : 1),
-                       dim3(1024), 0, st, a, (int)grid.x * a.runs);
+                       dim3(1024), 0, st, a, grad_blocks(a.n, a.H) * a.runs);
     return e;
 }
 

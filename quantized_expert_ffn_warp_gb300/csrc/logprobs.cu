@@ -227,10 +227,10 @@ __device__ __forceinline__ void join_warps(Block<W> &sm, Sums &t, Key &list)
     }
 }
 
-// A row's results, by warp 0.
-template <typename T, bool TOP>
+// A row's results, by warp 0; `given` is the target's logit.
+template <bool TOP>
 __device__ __forceinline__ void finish_row(const LogprobArgs &a, long long t, const Sums &u,
-                                           Key list)
+                                           Key list, int target, float given)
 {
     const int lane = threadIdx.x & 31;
     const bool empty = u.m == -INFINITY && u.s == 0.f;  // nothing but -inf
@@ -238,15 +238,10 @@ __device__ __forceinline__ void finish_row(const LogprobArgs &a, long long t, co
     if (lane == 0) {
         a.stats[t] = make_float2(u.m, logsum);
         a.entropy[t] = empty ? 0.f : logsum - u.sd / u.s;
-        if (a.targets) {
-            const int v = a.targets[t];
-            float lp = 0.f;
-            if (v >= 0 && v < a.V) {
-                const float x = to_float<T>(static_cast<const T *>(a.logits)[t * a.ld + v]);
-                lp = empty ? -INFINITY : (x - u.m) - logsum;
-            }
-            a.logp[t] = lp;
-        }
+        if (a.targets)
+            a.logp[t] = target < 0 || target >= a.V ? 0.f
+                        : empty                     ? -INFINITY
+                                                    : (given - u.m) - logsum;
     }
     if (TOP && lane < a.top) {
         a.top_ids[t * a.top + lane] = ~(unsigned)list;
@@ -330,20 +325,13 @@ __device__ __forceinline__ Key collect(Candidates<W> &sm, const RowWords<T> &row
 
 // W warps a row.
 template <typename T, bool TOP, int W>
-__global__ void __launch_bounds__(32 * W) logprobs_kernel(LogprobArgs a)
+__global__ void __launch_bounds__(32 * W, 32 / W) logprobs_kernel(LogprobArgs a)
 {
     constexpr int N = Vec<T>::N, U = kWordsPerThread, threads = 32 * W;
     __shared__ Block<W> sm;
     __shared__ std::conditional_t<TOP, Candidates<W>, int> cand;
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const auto row_of = [&](long long t) {
-        return RowWords<T>(static_cast<const T *>(a.logits) + t * a.ld, a.V);
-    };
-    const auto block = [&](const RowWords<T> &row) {
-        const int lo = blockIdx.x * a.per;
-        return make_int2(lo, min(row.count, lo + a.per));
-    };
     float low[N];
 #pragma unroll
     for (int e = 0; e < N; e++)
@@ -369,14 +357,13 @@ __global__ void __launch_bounds__(32 * W) logprobs_kernel(LogprobArgs a)
     int per_group = 1;
     while (per_group * kGroups * U * threads < a.per)
         per_group *= 2;
-    {
-        const RowWords<T> row = row_of(blockIdx.y);
-        const int2 b = block(row);
-        load(row, b.x, b.y);
-    }
     for (long long t = blockIdx.y; t < a.n; t += gridDim.y) {
-        const RowWords<T> row = row_of(t);
-        const int lo = block(row).x, hi = block(row).y;
+        const RowWords<T> row(static_cast<const T *>(a.logits) + t * a.ld, a.V);
+        const int lo = blockIdx.x * a.per, hi = min(row.count, lo + a.per);
+        load(row, lo, hi);
+        // the target's logit is under way behind them
+        const int target = a.targets ? a.targets[t] : -1;
+        const float given = target >= 0 && target < a.V ? to_float<T>(row.row[target]) : 0.f;
         Sums u = {-INFINITY, 0.f, 0.f};
         float most = -INFINITY;
         int chunk = 0, group = 0;
@@ -400,18 +387,13 @@ __global__ void __launch_bounds__(32 * W) logprobs_kernel(LogprobArgs a)
             }
             add_words<T, U>(u, q, top);
         }
-        if (t + gridDim.y < a.n) {      // the next row's first words
-            const RowWords<T> after = row_of(t + gridDim.y);
-            const int2 b = block(after);
-            load(after, b.x, b.y);
-        }
         Key list = 0;
         if constexpr (TOP)
             list = collect<T, W>(cand, row, lo, hi, u.m, group, per_group * U, a.top);
         join_warps<TOP, W>(sm, u, list);
         if (warp == 0) {
             if (a.splits == 1) {
-                finish_row<T, TOP>(a, t, u, list);
+                finish_row<TOP>(a, t, u, list, target, given);
             } else {
                 const long long at = t * a.splits + blockIdx.x;
                 if (lane == 0)
@@ -432,6 +414,10 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const long long t = blockIdx.x, at = t * a.splits;
+    const int target = a.targets ? a.targets[t] : -1;
+    const float given = target >= 0 && target < a.V
+                            ? to_float<T>(static_cast<const T *>(a.logits)[t * a.ld + target])
+                            : 0.f;
     Sums u = {-INFINITY, 0.f, 0.f};
     if (threadIdx.x < a.splits) {       // at most kMaxSplits of them
         const float4 q = a.part[at + threadIdx.x];
@@ -443,7 +429,7 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
             list = merge(list, a.part_keys[(at + i) * 32 + lane]);
     join_warps<TOP, kWarps>(sm, u, list);
     if (warp == 0)
-        finish_row<T, TOP>(a, t, u, list);
+        finish_row<TOP>(a, t, u, list, target, given);
 }
 
 // Words of the longest row, whatever its address.
@@ -480,11 +466,7 @@ size_t logprob_ws(int n, int V, int size, int top)
 template <typename T, bool TOP, int W>
 cudaError_t launch_rows(const LogprobArgs &a, cudaStream_t st)
 {
-    // rows beyond what runs at once go to the same blocks, evenly
-    const int most = 152 * (W == 1 ? 32 : 8);
-    const int turns = (a.n + most - 1) / most;
-    const int rows = a.splits > 1 ? a.n : (a.n + turns - 1) / turns;
-    return launch_pdl(logprobs_kernel<T, TOP, W>, dim3(a.splits, rows), dim3(32 * W), 0, st, a);
+    return launch_pdl(logprobs_kernel<T, TOP, W>, dim3(a.splits, std::min(a.n, 65535)), dim3(32 * W), 0, st, a);
 }
 template <typename T, bool TOP>
 cudaError_t launch_top(const LogprobArgs &a, cudaStream_t st)
