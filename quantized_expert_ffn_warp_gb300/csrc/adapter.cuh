@@ -1,0 +1,73 @@
+// What the adapters' kernels and calls share.
+#pragma once
+#include <algorithm>
+
+#include "internal.cuh"
+
+namespace qe {
+
+constexpr int kAdapterTile = 128;       // tokens of a tile
+constexpr int kAdapterCols = 128;       // columns of a block
+constexpr int kAdapterStep = 64;        // values of a 128-byte row: the step of a contraction
+constexpr int kAdapterMaxRank = 128, kAdapterMaxCount = 1024;
+
+// Ranks as the products take them; those behind the last are 0.
+__host__ __device__ constexpr int rank_pad(int r)
+{
+    return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+}
+
+struct AdapterPlan {
+    int *off;           // [L + 2] first token of an adapter in perm; then those without one
+    int *perm;          // [n] tokens in the order of their adapters
+    int4 *tiles;        // (adapter, first place in perm, tokens, -); L: none
+    int *n_tiles;
+    unsigned *tickets;  // parts that have arrived: of tiles, then of outer blocks
+};
+
+struct AdapterWorkspace {
+    AdapterPlan p;
+    int slices, splits;         // parts of a contraction: of a tile, of an adapter's tokens
+    int tickets;
+    unsigned *outer_tickets;
+    uint16_t *pair;             // [n][2][rank_pad] h or u in two parts, in perm's order
+    float *part, *outer_part;
+    size_t bytes;
+};
+
+// Most tiles of n tokens: an adapter's tokens end with one that is not full.
+inline int adapter_tiles(int n, int L) { return n / kAdapterTile + std::min(n, L + 1); }
+
+struct AdapterCall {
+    const void *x;
+    long long ldx;
+    const void *A, *B, *base;
+    long long ldb;
+    void *out;
+    long long ldo;
+    void *h;
+    const float *scale;
+    int n, L, r, K, N;
+    AdapterWorkspace w;
+};
+struct AdapterGradCall {
+    const void *dy, *x;
+    long long lddy, ldx;
+    const void *h;
+    const void *A, *B, *base;
+    long long ldb;
+    void *dx;
+    long long lddx;
+    void *dA, *dB;
+    const float *scale;
+    int n, L, r, K, N;
+    AdapterWorkspace w;
+};
+
+// Behind the plan's kernel.
+cudaError_t adapter_fp16(const AdapterCall &c, cudaStream_t st);
+cudaError_t adapter_bf16(const AdapterCall &c, cudaStream_t st);
+cudaError_t adapter_grad_fp16(const AdapterGradCall &c, cudaStream_t st);
+cudaError_t adapter_grad_bf16(const AdapterGradCall &c, cudaStream_t st);
+
+}  // namespace qe

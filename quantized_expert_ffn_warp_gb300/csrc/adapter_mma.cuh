@@ -1,0 +1,907 @@
+// The adapters' products (see adapter.cu), for one type of activations.
+#pragma once
+#include <algorithm>
+
+#include "adapter.cuh"
+#include "tcgen05.cuh"
+#include "vec.cuh"
+
+namespace qe {
+
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kTile = kAdapterTile, kCols = kAdapterCols, kBlk = kAdapterStep;
+
+// Copy of 16 bytes into shared memory; 0 behind the `bytes` that are there.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, int bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+// All but the last N groups of the thread's copies are there.
+template <int N>
+__device__ __forceinline__ void wait_copies()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Values i .. i + 7 of a row of `len` 2-byte values into a slot, 0 behind its end.
+__device__ __forceinline__ void fetch8(uint32_t dst, const uint16_t *row, int i, int len,
+                                       bool aligned)
+{
+    if (aligned) {
+        copy16(dst, i < len ? row + i : row, min(max(2 * (len - i), 0), 16));
+        return;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const uint32_t a = i + 2 * e < len ? row[i + 2 * e] : 0;
+        const uint32_t b = i + 2 * e + 1 < len ? row[i + 2 * e + 1] : 0;
+        w[e] = a | b << 16;
+    }
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst), "r"(w[0]), "r"(w[1]),
+                 "r"(w[2]), "r"(w[3])
+                 : "memory");
+}
+
+// Copies of ROWS rows of CH chunks of 16 bytes each into rows of 128 bytes (blocks of
+// eight chunks, `block` bytes apart), by the whole CTA: a thread has one chunk of every
+// kPass-th row, its places a constant number of bytes apart.
+template <int CH, int ROWS>
+struct Rows {
+    static constexpr int kPass = kThreads / CH;
+    static constexpr int kPasses = (ROWS + kPass - 1) / kPass;
+    int row, chunk;
+    uint32_t at;
+    bool on;
+
+    __device__ __forceinline__ explicit Rows(uint32_t block)
+        : row(threadIdx.x / CH), chunk(threadIdx.x % CH),
+          at((chunk >> 3) * block + sw128_at(row, chunk & 7)), on(kPass <= ROWS || row < ROWS)
+    {
+    }
+    static constexpr uint32_t kNext = kPass * 128;
+};
+
+// ---------------------------------------------------------------- the tensor core
+
+// What a CTA needs around its products.
+struct Tensor {
+    uint32_t bars;          // barriers, one for each stage
+    uint32_t tmem;
+    volatile int *gave_up;
+};
+constexpr int kStages = 4;      // at most
+struct TensorSmem {
+    uint64_t bar[kStages];
+    uint32_t tmem;
+    int gave_up;
+};
+
+__device__ __forceinline__ Tensor tensor_begin(TensorSmem &sm, uint32_t cols)
+{
+    if (threadIdx.x < 32)
+        tmem_alloc(&sm.tmem, cols);
+    if (threadIdx.x == 32) {
+        sm.gave_up = 0;
+        for (int i = 0; i < kStages; i++)
+            bar_init(saddr(&sm.bar[i]), 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    return {saddr(sm.bar), sm.tmem, &sm.gave_up};
+}
+__device__ __forceinline__ void tensor_end(const Tensor &t, uint32_t cols)
+{
+    tc_fence_before();
+    __syncthreads();
+    if (threadIdx.x < 32)
+        tmem_free(t.tmem, cols);
+}
+// Waits for the products of use `use` of barrier i.  A wait that gives up makes the CTA's
+// results NaN; its threads go on, so that all of them meet the CTA's barriers.
+__device__ __forceinline__ void tensor_wait(const Tensor &t, int i, int use)
+{
+    if (!bar_wait(t.bars + 8 * i, use & 1, t.gave_up))
+        *t.gave_up = 1;
+}
+
+__host__ __device__ constexpr uint32_t tmem_cols(int n)
+{
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+}
+// 128-byte rows that hold `r` values.
+__host__ __device__ constexpr int row_blocks(int r) { return (r + kBlk - 1) / kBlk; }
+
+// A multi-stage contraction: fetch(i, stage) starts the copies of step i, multiply(stage,
+// first) issues its products in one elected thread.  Copies of the steps ahead are under
+// way while a step is multiplied; a stage is filled again when its products are done.
+template <int S, typename F, typename M>
+__device__ __forceinline__ void contract(const Tensor &t, int steps, F fetch, M multiply)
+{
+#pragma unroll
+    for (int i = 0; i < S - 1; i++) {
+        if (i < steps)
+            fetch(i, i);
+        commit_copies();
+    }
+    int stage = 0;
+    for (int i = 0; i < steps; i++) {
+        wait_copies<S - 2>();
+        fence_async_shared();
+        __syncthreads();
+        if (threadIdx.x < 32) {
+            tc_fence_after();
+            if (elect_one()) {
+                multiply(stage, i == 0);
+                umma_commit(t.bars + 8 * stage);
+            }
+            __syncwarp();
+        }
+        const int before = stage == 0 ? S - 1 : stage - 1;
+        if (i + S - 1 < steps) {
+            if (i > 0)
+                tensor_wait(t, before, (i - 1) / S);
+            fetch(i + S - 1, before);
+        }
+        commit_copies();
+        stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    wait_copies<0>();
+    if (steps > 0)
+        tensor_wait(t, (steps - 1) % S, (steps - 1) / S);
+    tc_fence_after();
+}
+
+// A call's dynamic shared memory from a 1024-byte boundary on, as the swizzle needs.
+__device__ __forceinline__ uint32_t smem_base()
+{
+    extern __shared__ uint8_t adapter_smem[];
+    return (saddr(adapter_smem) + 1023) & ~1023u;
+}
+constexpr int kSmemSlack = 1024;
+
+// ---------------------------------------------------------------- shrink
+
+struct ShrinkArgs {
+    AdapterPlan p;
+    const uint16_t *x;      // [n][K]
+    long long ldx;
+    const uint16_t *w;      // [L][r][K], or (BY_ROW) [L][K][r]
+    int n, L, K, r, slices;
+    bool vec_x, vec_w;
+    float *part;            // [slices][n][PAD] partial sums
+    uint16_t *pair;         // [n][2][PAD]
+    uint16_t *h;            // [n][r], or null
+};
+
+template <typename T>
+__device__ __forceinline__ uint16_t bits(T v)
+{
+    return *reinterpret_cast<const uint16_t *>(&v);
+}
+
+// Four of a token's results from rank k on: two parts at its place, and h.
+template <typename T, int PAD>
+__device__ __forceinline__ void put_results(const ShrinkArgs &a, int place, int token, int k,
+                                            const float (&v)[4])
+{
+    float rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const float f = to_float<T>(from_float<T>(v[e]));
+        // an infinity or a NaN has no remainder
+        rest[e] = fabsf(f) <= 3.4e38f ? v[e] - f : 0.f;
+    }
+    const uint2 hi = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+    uint16_t *row = a.pair + (long long)place * 2 * PAD + k;
+    *reinterpret_cast<uint2 *>(row) = hi;
+    *reinterpret_cast<uint2 *>(row + PAD) =
+        make_uint2(pack2<T>(rest[0], rest[1]), pack2<T>(rest[2], rest[3]));
+    if (a.h && k < a.r)
+        *reinterpret_cast<uint2 *>(a.h + (long long)token * a.r + k) = hi;
+}
+
+constexpr int kShrinkStages = 4;
+template <bool BY_ROW, int PAD>
+constexpr int kShrinkStage = 128 * kTile + (BY_ROW ? 128 * kBlk * row_blocks(PAD) : 128 * PAD);
+
+// A tile's tokens (the product's rows) times all ranks.  The slices' sums are added by
+// whichever CTA of a tile arrives last, in the slices' order.
+template <typename T, bool BY_ROW, int PAD>
+__global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs a)
+{
+    __shared__ TensorSmem ts;
+    __shared__ int last;
+    pdl_enter();
+    if ((int)blockIdx.x >= *a.p.n_tiles)
+        return;
+    const int4 tile = a.p.tiles[blockIdx.x];
+    const int slice = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (tile.x == a.L) {        // no adapter
+        if (slice == 0 && a.h)
+            for (int i = threadIdx.x; i < tile.z * a.r; i += kThreads)
+                a.h[(long long)a.p.perm[tile.y + i / a.r] * a.r + i % a.r] = 0;
+        return;
+    }
+    constexpr uint32_t cols = tmem_cols(PAD);
+    const Tensor t = tensor_begin(ts, cols);
+    const int blocks = (a.K + kBlk - 1) / kBlk;
+    const int begin = (int)((long long)blocks * slice / a.slices);
+    const int end = (int)((long long)blocks * (slice + 1) / a.slices);
+    const uint32_t smem = smem_base();
+    constexpr int stage_bytes = kShrinkStage<BY_ROW, PAD>;
+    // a thread's chunks of the tokens, and of the matrix: rows of ranks, or (BY_ROW) of K
+    using X = Rows<8, kTile>;
+    using W = std::conditional_t<BY_ROW, Rows<PAD / 8, kBlk>, Rows<8, PAD>>;
+    const X xr(0);
+    const W wr(128 * kBlk);
+    const uint16_t *w = a.w + (long long)tile.x * a.r * a.K;
+    const uint16_t *src[X::kPasses];
+    bool there[X::kPasses];
+#pragma unroll
+    for (int j = 0; j < X::kPasses; j++) {
+        const int at = xr.row + X::kPass * j;
+        there[j] = at < tile.z;
+        src[j] = a.x + (long long)a.p.perm[tile.y + (there[j] ? at : 0)] * a.ldx;
+    }
+    const uint16_t *mat0 = BY_ROW ? w + (long long)wr.row * a.r + 8 * wr.chunk
+                                  : w + (long long)wr.row * a.K + 8 * wr.chunk;
+    const long long mat_pass = (long long)W::kPass * (BY_ROW ? a.r : a.K);
+    const auto fetch = [&](int i, int stage) {
+        const int k0 = (begin + i) * kBlk;
+        const uint32_t xs = smem + stage * stage_bytes + xr.at;
+        const uint32_t ws = smem + stage * stage_bytes + 128 * kTile + wr.at;
+        if (a.vec_x && a.vec_w && k0 + kBlk <= a.K) {
+#pragma unroll
+            for (int j = 0; j < X::kPasses; j++)
+                if (there[j])
+                    copy16(xs + X::kNext * j, src[j] + k0 + 8 * xr.chunk, 16);
+            const uint16_t *m = mat0 + (BY_ROW ? (long long)k0 * a.r : k0);
+#pragma unroll
+            for (int j = 0; j < W::kPasses; j++) {      // 0 for the ranks behind the last
+                const bool in = BY_ROW ? 8 * wr.chunk < a.r : wr.row + W::kPass * j < a.r;
+                if (wr.on)
+                    copy16(ws + W::kNext * j, in ? m + mat_pass * j : w, in ? 16 : 0);
+            }
+            return;
+        }
+#pragma unroll 1
+        for (int j = 0; j < X::kPasses; j++) {
+            const int at = xr.row + X::kPass * j;
+            if (at < tile.z)
+                fetch8(xs + X::kNext * j, a.x + (long long)a.p.perm[tile.y + at] * a.ldx,
+                       k0 + 8 * xr.chunk, a.K, a.vec_x);
+        }
+#pragma unroll 1
+        for (int j = 0; j < W::kPasses && wr.on; j++) {
+            const int row = wr.row + W::kPass * j;
+            if constexpr (BY_ROW) {
+                const bool in = k0 + row < a.K && 8 * wr.chunk < a.r;
+                copy16(ws + W::kNext * j,
+                       in ? w + (long long)(k0 + row) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
+            } else {
+                fetch8(ws + W::kNext * j, row < a.r ? w + (long long)row * a.K : w,
+                       k0 + 8 * wr.chunk, row < a.r ? a.K : 0, a.vec_w);
+            }
+        }
+    };
+    constexpr uint32_t idesc =
+        (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
+        ((uint32_t)(PAD >> 3) << 17) | (8u << 24) | (BY_ROW ? kMnMajorB : 0u);
+    const auto multiply = [&](int stage, bool first) {
+        const uint32_t at = smem + stage * stage_bytes, mat = at + 128 * kTile;
+        const uint64_t da = sw128_desc(at);
+        const uint64_t db = BY_ROW ? sw128_desc_mn(mat, 128 * kBlk) : sw128_desc(mat);
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            umma_ss(t.tmem, da + 2 * k, db + (BY_ROW ? 128 : 2) * k, idesc, !first || k);
+    };
+    contract<kShrinkStages>(t, end - begin, fetch, multiply);
+    const bool failed = *t.gave_up;
+    const int at = 32 * warp + lane, place = tile.y + at;
+    if (warp < 4) {
+        const int token = at < tile.z ? a.p.perm[place] : 0;
+#pragma unroll 1
+        for (int c = 0; c < PAD; c += 16) {
+            float v[16];
+            tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + c, v);
+            if (at >= tile.z)
+                continue;
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                float d[4];
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    d[e] = failed ? NAN : v[4 * q + e];
+                if (a.slices == 1)
+                    put_results<T, PAD>(a, place, token, c + 4 * q, d);
+                else
+                    *reinterpret_cast<float4 *>(
+                        a.part + ((long long)slice * a.n + place) * PAD + c + 4 * q) =
+                        make_float4(d[0], d[1], d[2], d[3]);
+            }
+        }
+    }
+    tensor_end(t, cols);
+    if (a.slices == 1)
+        return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = atomicAdd(a.p.tickets + blockIdx.x, 1u) == a.slices - 1u;
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    for (int i = threadIdx.x; i < tile.z * (PAD / 4); i += kThreads) {
+        const int place = tile.y + i / (PAD / 4), k = i % (PAD / 4) * 4;
+        float v[4] = {};
+        for (int s = 0; s < a.slices; s++) {
+            const float4 q = __ldcg(reinterpret_cast<const float4 *>(
+                a.part + ((long long)s * a.n + place) * PAD + k));
+            v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
+        }
+        put_results<T, PAD>(a, place, a.p.perm[place], k, v);
+    }
+}
+
+// ---------------------------------------------------------------- expand
+
+struct ExpandArgs {
+    AdapterPlan p;
+    const uint16_t *pair;   // [n][2][PAD]
+    const uint16_t *w;      // [L][N][r], or (BY_ROW) [L][r][N]
+    const float *scale;     // [L] or null
+    const uint16_t *base;   // [n][N] or null
+    long long ldb;
+    uint16_t *out;          // [n][N]
+    long long ldo;
+    int L, N, r, steps;     // steps: blocks of kCols columns of a CTA
+    bool vec_w, vec_b, vec_o;
+};
+
+// Values i .. i + 7 of a row of `len` 2-byte values, 0 behind its end; and back.
+__device__ __forceinline__ uint4 load8(const uint16_t *row, int i, int len, bool aligned)
+{
+    if (aligned && i + 8 <= len)
+        return load_stream(row + i);
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {
+        const uint32_t a = i + 2 * e < len ? row[i + 2 * e] : 0;
+        const uint32_t b = i + 2 * e + 1 < len ? row[i + 2 * e + 1] : 0;
+        w[e] = a | b << 16;
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void store8(uint16_t *row, int i, int len, bool aligned, const uint4 &q)
+{
+    if (aligned && i + 8 <= len) {
+        *reinterpret_cast<uint4 *>(row + i) = q;
+        return;
+    }
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        if (i + e < len)
+            row[i + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
+}
+
+// h in 128-byte rows, the upper parts and then the lower: side by side if both fit.
+template <int PAD>
+constexpr int kPairBlocks = 2 * PAD <= kBlk ? 1 : 2 * row_blocks(PAD);
+template <bool BY_ROW, int PAD>
+constexpr int kMatrix = BY_ROW ? 2 * kCols * PAD : 128 * kCols * row_blocks(PAD);
+template <bool BY_ROW, int PAD>
+constexpr int kExpandSmem =
+    128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW, PAD> + 4096 * kWarps + kSmemSlack;
+
+// A tile's tokens (the product's rows) times columns.  The next columns' matrix is copied
+// while a block's sums leave tensor memory; these pass through a warp's shared memory,
+// where a lane finds eight neighbours of a token's row, and meet base, whose next values
+// are loaded as soon as the last ones are used.
+template <typename T, bool BY_ROW, int PAD>
+__global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs a)
+{
+    __shared__ TensorSmem ts;
+    pdl_enter();
+    if ((int)blockIdx.x >= *a.p.n_tiles)
+        return;
+    const int4 tile = a.p.tiles[blockIdx.x];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = blockIdx.y * a.steps * kCols;
+    const int stop = min(a.N, first + a.steps * kCols);
+    if (tile.x == a.L) {        // no adapter: base, or 0
+        if (a.out == a.base)
+            return;
+        for (int i = warp; i < tile.z; i += kWarps) {
+            const long long tok = a.p.perm[tile.y + i];
+            for (int c = first + 8 * lane; c < stop; c += 256)
+                store8(a.out + tok * a.ldo, c, stop, a.vec_o,
+                       a.base ? load8(a.base + tok * a.ldb, c, stop, a.vec_b)
+                              : make_uint4(0, 0, 0, 0));
+        }
+        return;
+    }
+    const Tensor t = tensor_begin(ts, kCols);
+    constexpr int wide = PAD / 8, blocks = row_blocks(PAD), matrix = kMatrix<BY_ROW, PAD>;
+    constexpr bool side = 2 * PAD <= kBlk;
+    const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPairBlocks<PAD>;
+    const uint32_t mine = mats + 2 * matrix + 4096 * warp;
+    // h: chunk c of part p of a row
+    for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kThreads) {
+        const int row = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
+        const int at = side ? c : c - part * wide + part * 8 * blocks;
+        copy16(hs + (at >> 3) * (128 * kTile) + sw128_at(row, at & 7),
+               a.pair + (long long)(tile.y + row) * 2 * PAD + 8 * c, 16);
+    }
+    // the matrix: rows of ranks (0 behind the last), or (BY_ROW) of columns for each rank
+    using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD>, Rows<PAD / 8, kCols>>;
+    const W wr(BY_ROW ? 128 * PAD : 128 * kCols);
+    const uint16_t *w = a.w + (long long)tile.x * a.r * a.N;
+    const uint16_t *mat0 = BY_ROW ? w + (long long)wr.row * a.N + 8 * wr.chunk
+                                  : w + (long long)wr.row * a.r + 8 * wr.chunk;
+    const long long mat_pass = (long long)W::kPass * (BY_ROW ? a.N : a.r);
+    const float scale = a.scale ? a.scale[tile.x] : 1.f;
+    const auto fetch = [&](int c0, int buffer) {
+        const uint32_t ws = mats + buffer * matrix + wr.at;
+        if (a.vec_w && c0 + kCols <= a.N) {
+            const uint16_t *m = mat0 + (BY_ROW ? c0 : (long long)c0 * a.r);
+#pragma unroll
+            for (int j = 0; j < W::kPasses; j++) {
+                const bool in = BY_ROW ? wr.row + W::kPass * j < a.r : 8 * wr.chunk < a.r;
+                if (wr.on)
+                    copy16(ws + W::kNext * j, in ? m + mat_pass * j : w, in ? 16 : 0);
+            }
+        } else {
+#pragma unroll 1
+            for (int j = 0; j < W::kPasses && wr.on; j++) {
+                const int row = wr.row + W::kPass * j;
+                if constexpr (BY_ROW) {
+                    fetch8(ws + W::kNext * j, row < a.r ? w + (long long)row * a.N : w,
+                           c0 + 8 * wr.chunk, row < a.r ? a.N : 0, a.vec_w);
+                } else {
+                    const bool in = c0 + row < a.N && 8 * wr.chunk < a.r;
+                    copy16(ws + W::kNext * j,
+                           in ? w + (long long)(c0 + row) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
+                }
+            }
+        }
+        commit_copies();
+    };
+    constexpr uint32_t idesc =
+        (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
+        ((uint32_t)(kCols >> 3) << 17) | (8u << 24) | (BY_ROW ? kMnMajorB : 0u);
+    fetch(first, 0);
+    // rows of the warp's pass: 8 i + lane / 4 of its 32, columns 8 (lane % 4) .. of 32
+    const int quad = warp & 3, half = warp >> 2, col = 64 * half + 8 * (lane & 3);
+    const bool busy = 32 * quad < tile.z;
+    const uint16_t *from[4];
+    uint16_t *to[4];
+    bool on[4];
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        const int at = 32 * quad + 8 * i + lane / 4;
+        on[i] = at < tile.z;
+        const long long tok = on[i] ? a.p.perm[tile.y + at] : 0;
+        from[i] = a.base + tok * a.ldb;
+        to[i] = a.out + tok * a.ldo;
+    }
+    uint4 b[2][4];
+#pragma unroll
+    for (int p = 0; p < 2; p++)
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            b[p][i] = make_uint4(0, 0, 0, 0);
+    const auto load_base = [&](int p, int c0) {
+        if (!a.base || c0 >= stop)
+            return;
+        const int c = c0 + col + 32 * p;
+        if (a.vec_b && c0 + kCols <= a.N) {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (on[i])
+                    b[p][i] = load_stream(from[i] + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; i++)
+                if (on[i])
+                    b[p][i] = load8(from[i], c, a.N, a.vec_b);
+        }
+    };
+    load_base(0, first);
+    load_base(1, first);
+    int step = 0;
+    for (int c0 = first; c0 < stop; c0 += kCols, step++) {
+        wait_copies<0>();
+        fence_async_shared();
+        tc_fence_before();
+        __syncthreads();
+        if (warp == 0) {
+            tc_fence_after();
+            if (elect_one()) {
+                const uint32_t mat = mats + (step & 1) * matrix;
+#pragma unroll
+                for (int part = 0; part < 2; part++)
+#pragma unroll
+                    for (int k = 0; k < PAD / 16; k++) {
+                        const int ka = side ? part * (PAD / 16) + k : part * 4 * blocks + k;
+                        const uint64_t da =
+                            sw128_desc(hs + (ka >> 2) * (128 * kTile)) + 2 * (ka & 3);
+                        const uint64_t db =
+                            BY_ROW ? sw128_desc_mn(mat, 128 * PAD) + 128 * k
+                                   : sw128_desc(mat + (k >> 2) * (128 * kCols)) + 2 * (k & 3);
+                        umma_ss(t.tmem, da, db, idesc, part || k);
+                    }
+                umma_commit(t.bars);
+            }
+            __syncwarp();
+        }
+        if (c0 + kCols < stop)      // its buffer's products were waited for
+            fetch(c0 + kCols, (step + 1) & 1);
+        tensor_wait(t, 0, step);
+        tc_fence_after();
+        const F2 factor = f2(*t.gave_up ? NAN : scale);
+        const bool inside = a.vec_o && c0 + kCols <= a.N;
+#pragma unroll
+        for (int p = 0; p < 2; p++) {
+            if (!busy || c0 + 64 * half + 32 * p >= a.N)
+                break;
+#pragma unroll
+            for (int j = 0; j < 2; j++) {
+                float v[16];
+                tmem_ld16(t.tmem + ((uint32_t)(32 * quad) << 16) + 64 * half + 32 * p + 16 * j, v);
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                     mine + sw128_at(lane, 4 * j + q)),
+                                 "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]),
+                                 "f"(v[4 * q + 3])
+                                 : "memory");
+            }
+            __syncwarp();
+            const int c = c0 + col + 32 * p;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int row = 8 * i + lane / 4;
+                F2 v[4], d[4];
+#pragma unroll
+                for (int q = 0; q < 2; q++)
+                    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                                 : "=l"(v[2 * q].v), "=l"(v[2 * q + 1].v)
+                                 : "r"(mine + sw128_at(row, 2 * (lane & 3) + q))
+                                 : "memory");
+                unpack<T>(b[p][i], d);
+#pragma unroll
+                for (int e = 0; e < 4; e++)
+                    d[e] = fma(factor, v[e], d[e]);
+                if (!on[i])
+                    continue;
+                if (inside)
+                    *reinterpret_cast<uint4 *>(to[i] + c) = pack<T>(d);
+                else
+                    store8(to[i], c, a.N, a.vec_o, pack<T>(d));
+            }
+            __syncwarp();
+            load_base(p, c0 + kCols);
+        }
+    }
+    wait_copies<0>();
+    tensor_end(t, kCols);
+}
+
+// ---------------------------------------------------------------- outer
+
+struct OuterSide {
+    const uint16_t *src;    // [n][C] by token
+    long long ld;
+    bool vec;
+    int C, blocks;          // columns, blocks of kCols of them
+    const uint16_t *v;      // ranks: of a token (h [n][r]), or of a place (pair)
+    uint16_t *out;
+};
+struct OuterArgs {
+    AdapterPlan p;
+    OuterSide a, b;         // dA [L][r][K] from x and u, dB [L][N][r] from dy and h
+    const float *scale;
+    int L, r, splits;
+    float *part;            // [splits][L][blocks of both][kCols][PAD]
+    unsigned *tickets;      // [L][blocks of both]
+};
+constexpr int kOuterStages = 3, kOuterList = 16;    // steps whose tokens are at hand
+template <int PAD>
+constexpr int kOuterStage = 128 * kBlk * (kCols / kBlk + 2 * row_blocks(PAD));
+
+// Sixteen ranks of a column from rank k on, at the end of a sum over tokens.
+template <typename T>
+__device__ __forceinline__ void put_outer(const OuterArgs &a, const OuterSide &o, bool of_a,
+                                          int adapter, int c, int k, const float (&v)[16])
+{
+    uint16_t *out = o.out + (long long)adapter * a.r * o.C;
+    if (c >= o.C)
+        return;
+    if (of_a) {     // lanes are neighbours in c
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+            if (k + e < a.r)
+                out[(long long)(k + e) * o.C + c] = bits(from_float<T>(v[e]));
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; e += 8)
+        if (k + e < a.r)
+            *reinterpret_cast<uint4 *>(out + (long long)c * a.r + k + e) =
+                make_uint4(pack2<T>(v[e], v[e + 1]), pack2<T>(v[e + 2], v[e + 3]),
+                           pack2<T>(v[e + 4], v[e + 5]), pack2<T>(v[e + 6], v[e + 7]));
+}
+
+// The sum over an adapter's tokens of kCols columns (the product's rows) times all ranks.
+// Both operands are read along their rows: the tokens are the contraction.
+template <typename T, int PAD>
+__global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
+{
+    __shared__ TensorSmem ts;
+    __shared__ int toks[kOuterList * kBlk];
+    __shared__ int last;
+    pdl_enter();
+    const bool of_a = (int)blockIdx.x < a.a.blocks;
+    const OuterSide &o = of_a ? a.a : a.b;
+    const int c0 = kCols * (of_a ? blockIdx.x : blockIdx.x - a.a.blocks);
+    const int adapter = blockIdx.y, split = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lo = a.p.off[adapter], count = a.p.off[adapter + 1] - lo;
+    const int all = (count + kBlk - 1) / kBlk;
+    const int begin = (int)((long long)all * split / a.splits);
+    const int steps = (int)((long long)all * (split + 1) / a.splits) - begin;
+    const int c = 32 * warp + lane;
+    const float scale = a.scale ? a.scale[adapter] : 1.f;
+    if (count == 0) {
+        const float zero[16] = {};
+        if (split == 0 && warp < 4)
+            for (int k = 0; k < PAD; k += 16)
+                put_outer<T>(a, o, of_a, adapter, c0 + c, k, zero);
+        return;
+    }
+    constexpr uint32_t cols = tmem_cols(PAD);
+    const Tensor t = tensor_begin(ts, cols);
+    const uint32_t smem = smem_base();
+    constexpr int stage_bytes = kOuterStage<PAD>, part_bytes = 128 * kBlk * row_blocks(PAD);
+    using X = Rows<kCols / 8, kBlk>;
+    using V = Rows<PAD / 8, kBlk>;
+    const X xr(128 * kBlk);
+    const V vr(128 * kBlk);
+    const uint16_t *src = o.src + c0 + 8 * xr.chunk;
+    const bool whole = o.vec && c0 + kCols <= o.C;
+    const int rank_bytes = 8 * vr.chunk < a.r ? 16 : 0;     // 0 for the ranks behind the last
+    const uint16_t *ranks = rank_bytes ? o.v + 8 * vr.chunk : o.v;
+    const auto fetch = [&](int i, int stage) {
+        const int s0 = (begin + i) * kBlk;
+        if (i % kOuterList == 0) {      // the list that the next steps take their tokens from
+            for (int j = threadIdx.x; j < kOuterList * kBlk; j += kThreads)
+                toks[j] = s0 + j < count ? a.p.perm[lo + s0 + j] : -1;
+            __syncthreads();
+        }
+        const int *list = toks + i % kOuterList * kBlk;
+        const uint32_t xs = smem + stage * stage_bytes + xr.at;
+        const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk) + vr.at;
+        if (whole && s0 + kBlk <= count) {
+#pragma unroll
+            for (int j = 0; j < X::kPasses; j++)
+                copy16(xs + X::kNext * j, src + list[xr.row + X::kPass * j] * o.ld, 16);
+        } else {                        // 0 behind the last token
+#pragma unroll 1
+            for (int j = 0; j < X::kPasses; j++) {
+                const int tok = list[xr.row + X::kPass * j];
+                fetch8(xs + X::kNext * j, o.src + max(tok, 0) * o.ld, c0 + 8 * xr.chunk,
+                       tok >= 0 ? o.C : 0, o.vec);
+            }
+        }
+        if (!vr.on)
+            return;
+        if (of_a) {
+            const uint16_t *v = ranks + (long long)(lo + s0 + vr.row) * 2 * PAD;
+#pragma unroll
+            for (int j = 0; j < V::kPasses; j++) {
+                const bool in = rank_bytes && s0 + vr.row + V::kPass * j < count;
+                const uint16_t *p = in ? v + V::kPass * 2 * PAD * j : o.v;
+                copy16(vs + V::kNext * j, p, in ? 16 : 0);
+                copy16(vs + V::kNext * j + part_bytes, in ? p + PAD : p, in ? 16 : 0);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V::kPasses; j++) {
+                const int tok = list[vr.row + V::kPass * j];
+                copy16(vs + V::kNext * j, ranks + (long long)max(tok, 0) * a.r,
+                       tok >= 0 ? rank_bytes : 0);
+            }
+        }
+    };
+    constexpr uint32_t idesc =
+        (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
+        ((uint32_t)(PAD >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
+    const auto multiply = [&](int stage, bool first) {
+        const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * kBlk * (kCols / kBlk);
+        const uint64_t da = sw128_desc_mn(at, 128 * kBlk);
+        for (int part = 0; part < (of_a ? 2 : 1); part++) {
+            const uint64_t db = sw128_desc_mn(vs + part * part_bytes, 128 * kBlk);
+#pragma unroll
+            for (int k = 0; k < kBlk / 16; k++)
+                umma_ss(t.tmem, da + 128 * k, db + 128 * k, idesc, !first || part || k);
+        }
+    };
+    contract<kOuterStages>(t, steps, fetch, multiply);
+    const bool failed = *t.gave_up;
+    const int block = adapter * (a.a.blocks + a.b.blocks) + blockIdx.x;
+    const long long slots = (long long)a.L * (a.a.blocks + a.b.blocks);
+    if (warp < 4)
+#pragma unroll 1
+        for (int k = 0; k < PAD; k += 16) {
+            float v[16];
+            tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + k, v);
+#pragma unroll
+            for (int e = 0; e < 16; e++)
+                v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
+            if (a.splits == 1) {
+#pragma unroll
+                for (int e = 0; e < 16; e++)
+                    v[e] *= scale;
+                put_outer<T>(a, o, of_a, adapter, c0 + c, k, v);
+                continue;
+            }
+            float4 *p = reinterpret_cast<float4 *>(
+                a.part + ((split * slots + block) * kCols + c) * PAD + k);
+#pragma unroll
+            for (int q = 0; q < 4; q++)
+                p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+        }
+    tensor_end(t, cols);
+    if (a.splits == 1)
+        return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = atomicAdd(a.tickets + block, 1u) == a.splits - 1u;
+    __syncthreads();
+    if (!last)
+        return;
+    __threadfence();
+    for (int i = threadIdx.x; i < kCols * (PAD / 16); i += kThreads) {
+        const int col = i % kCols, k = i / kCols * 16;
+        float v[16] = {};
+        for (int s = 0; s < a.splits; s++) {
+            const float4 *p = reinterpret_cast<const float4 *>(
+                a.part + ((s * slots + block) * kCols + col) * PAD + k);
+#pragma unroll
+            for (int q = 0; q < 4; q++) {
+                const float4 d = __ldcg(p + q);
+                v[4 * q] += d.x, v[4 * q + 1] += d.y, v[4 * q + 2] += d.z, v[4 * q + 3] += d.w;
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 16; e++)
+            v[e] *= scale;
+        put_outer<T>(a, o, of_a, adapter, c0 + col, k, v);
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+// A kernel with more dynamic shared memory than the default.
+template <typename... P, typename A>
+cudaError_t launch_wide(void (*kernel)(P...), dim3 grid, int smem, cudaStream_t st, const A &a)
+{
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), smem, st, a);
+}
+
+template <typename T, bool BY_ROW, int PAD>
+cudaError_t launch_shrink(const ShrinkArgs &a, int tiles, cudaStream_t st)
+{
+    return launch_wide(adapter_shrink_kernel<T, BY_ROW, PAD>, dim3(tiles, a.slices),
+                       kShrinkStages * kShrinkStage<BY_ROW, PAD> + kSmemSlack, st, a);
+}
+
+template <typename T, bool BY_ROW, int PAD>
+cudaError_t launch_expand(ExpandArgs a, int tiles, cudaStream_t st)
+{
+    const int blocks = (a.N + kCols - 1) / kCols;
+    // four waves of CTAs and more; up to eight blocks of columns save reading h again
+    a.steps = std::max(1, std::min(8, (int)((long long)blocks * tiles / 1216)));
+    return launch_wide(adapter_expand_kernel<T, BY_ROW, PAD>,
+                       dim3(tiles, (blocks + a.steps - 1) / a.steps), kExpandSmem<BY_ROW, PAD>, st,
+                       a);
+}
+
+bool vec_rows(const void *p, long long ld, int n)
+{
+    return (uintptr_t)p % 16 == 0 && (n == 1 || ld % 8 == 0);
+}
+
+const uint16_t *half_words(const void *p) { return static_cast<const uint16_t *>(p); }
+
+template <typename T, int PAD>
+cudaError_t run_adapter(const AdapterCall &c, cudaStream_t st)
+{
+    const int tiles = adapter_tiles(c.n, c.L);
+    const ShrinkArgs s = {c.w.p, half_words(c.x), c.ldx, half_words(c.A), c.n, c.L, c.K, c.r,
+                          c.w.slices, vec_rows(c.x, c.ldx, c.n), c.K % 8 == 0, c.w.part, c.w.pair,
+                          static_cast<uint16_t *>(c.h)};
+    const cudaError_t e = launch_shrink<T, false, PAD>(s, tiles, st);
+    if (e != cudaSuccess)
+        return e;
+    const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.B), c.scale, half_words(c.base), c.ldb,
+                          static_cast<uint16_t *>(c.out), c.ldo, c.L, c.N, c.r, 0, true,
+                          vec_rows(c.base, c.ldb, c.n), vec_rows(c.out, c.ldo, c.n)};
+    return launch_expand<T, false, PAD>(x, tiles, st);
+}
+
+template <typename T, int PAD>
+cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
+{
+    const int tiles = adapter_tiles(c.n, c.L);
+    const ShrinkArgs s = {c.w.p, half_words(c.dy), c.lddy, half_words(c.B), c.n, c.L, c.N, c.r,
+                          c.w.slices, vec_rows(c.dy, c.lddy, c.n), true, c.w.part, c.w.pair, nullptr};
+    cudaError_t e = launch_shrink<T, true, PAD>(s, tiles, st);
+    if (e != cudaSuccess)
+        return e;
+    if (c.dx) {
+        const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.A), c.scale, half_words(c.base), c.ldb,
+                              static_cast<uint16_t *>(c.dx), c.lddx, c.L, c.K, c.r, 0,
+                              c.K % 8 == 0, vec_rows(c.base, c.ldb, c.n),
+                              vec_rows(c.dx, c.lddx, c.n)};
+        e = launch_expand<T, true, PAD>(x, tiles, st);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (!c.dA && !c.dB)
+        return e;
+    OuterArgs o{};
+    o.p = c.w.p;
+    o.scale = c.scale;
+    o.L = c.L;
+    o.r = c.r;
+    o.splits = c.w.splits;
+    o.part = c.w.outer_part;
+    o.tickets = c.w.outer_tickets;
+    if (c.dA)
+        o.a = {half_words(c.x), c.ldx, vec_rows(c.x, c.ldx, c.n), c.K, (c.K + kCols - 1) / kCols,
+               c.w.pair, static_cast<uint16_t *>(c.dA)};
+    if (c.dB)
+        o.b = {half_words(c.dy), c.lddy, vec_rows(c.dy, c.lddy, c.n), c.N,
+               (c.N + kCols - 1) / kCols, half_words(c.h), static_cast<uint16_t *>(c.dB)};
+    return launch_wide(adapter_outer_kernel<T, PAD>,
+                       dim3(o.a.blocks + o.b.blocks, c.L, o.splits),
+                       kOuterStages * kOuterStage<PAD> + kSmemSlack, st, o);
+}
+
+template <typename T>
+cudaError_t run_adapter(const AdapterCall &c, cudaStream_t st)
+{
+    switch (rank_pad(c.r)) {
+    case 16: return run_adapter<T, 16>(c, st);
+    case 32: return run_adapter<T, 32>(c, st);
+    case 64: return run_adapter<T, 64>(c, st);
+    default: return run_adapter<T, 128>(c, st);
+    }
+}
+template <typename T>
+cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
+{
+    switch (rank_pad(c.r)) {
+    case 16: return run_adapter_grad<T, 16>(c, st);
+    case 32: return run_adapter_grad<T, 32>(c, st);
+    case 64: return run_adapter_grad<T, 64>(c, st);
+    default: return run_adapter_grad<T, 128>(c, st);
+    }
+}
+
+}  // namespace
+
+}  // namespace qe
