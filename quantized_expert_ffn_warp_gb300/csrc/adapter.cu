@@ -264,7 +264,7 @@ extern "C" int moe_adapter(const void *x, long long ldx, int dtype, int n_tokens
     if (const int bad = check_args(args, sizeof(args) / sizeof(args[0]), &dev, &sms))
         return bad;
     const AdapterCall c = {x, ldx, A, B, base, ldb, out, ldo, h, scale, n_tokens, n_adapters,
-                           rank, cols, rows,
+                           rank, cols, rows, sms,
                            adapter_ws(workspace, n_tokens, n_adapters, rank, cols, rows, false)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch_plan(ids, n_tokens, n_adapters, c.w, st);
@@ -311,7 +311,7 @@ extern "C" int moe_adapter_grad(const void *dy, long long lddy, const void *x, l
     if (const int bad = check_args(args, sizeof(args) / sizeof(args[0]), &dev, &sms))
         return bad;
     const AdapterGradCall c = {dy, x, lddy, ldx, h, A, B, in, ldb, dx, lddx, dA, dB, scale,
-                               n_tokens, n_adapters, rank, cols, rows,
+                               n_tokens, n_adapters, rank, cols, rows, sms,
                                adapter_ws(workspace, n_tokens, n_adapters, rank, cols, rows, true)};
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = launch_plan(ids, n_tokens, n_adapters, c.w, st);

@@ -47,7 +47,7 @@ struct AdapterCall {
     long long ldo;
     void *h;
     const float *scale;
-    int n, L, r, K, N;
+    int n, L, r, K, N, sms;
     AdapterWorkspace w;
 };
 struct AdapterGradCall {
@@ -60,7 +60,7 @@ struct AdapterGradCall {
     long long lddx;
     void *dA, *dB;
     const float *scale;
-    int n, L, r, K, N;
+    int n, L, r, K, N, sms;
     AdapterWorkspace w;
 };
 

@@ -362,7 +362,7 @@ struct ExpandArgs {
     long long ldb;
     uint16_t *out;          // [n][N]
     long long ldo;
-    int L, N, r, steps;     // steps: blocks of kCols columns of a CTA
+    int L, N, r;
     bool vec_w, vec_b, vec_o;
 };
 
@@ -402,198 +402,228 @@ template <bool BY_ROW, int PAD>
 constexpr int kExpandSmem =
     128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW, PAD> + 4096 * kWarps + kSmemSlack;
 
-// A tile's tokens (the product's rows) times columns.  The next columns' matrix is copied
-// while a block's sums leave tensor memory; these pass through a warp's shared memory,
-// where a lane finds eight neighbours of a token's row, and meet base, whose next values
-// are loaded as soon as the last ones are used.
+// Tiles of tokens (the product's rows) times blocks of columns: a CTA takes an equal share
+// of all (tile, block) pairs, tile after tile.  While a block's sums leave tensor memory,
+// the next block is multiplied beside it and the matrix of the one behind that is copied.
+// The sums pass through a warp's shared memory, where a lane finds eight neighbours of a
+// token's row, and meet base, whose next values are loaded as soon as the last ones are
+// used.
 template <typename T, bool BY_ROW, int PAD>
 __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs a)
 {
     __shared__ TensorSmem ts;
     pdl_enter();
-    if ((int)blockIdx.x >= *a.p.n_tiles)
+    const int blocks = (a.N + kCols - 1) / kCols;
+    const long long total = (long long)*a.p.n_tiles * blocks;
+    long long at = total * blockIdx.x / gridDim.x;
+    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    if (at >= end)
         return;
-    const int4 tile = a.p.tiles[blockIdx.x];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = blockIdx.y * a.steps * kCols;
-    const int stop = min(a.N, first + a.steps * kCols);
-    if (tile.x == a.L) {        // no adapter: base, or 0
-        if (a.out == a.base)
-            return;
-        for (int i = warp; i < tile.z; i += kWarps) {
-            const long long tok = a.p.perm[tile.y + i];
-            for (int c = first + 8 * lane; c < stop; c += 256)
-                store8(a.out + tok * a.ldo, c, stop, a.vec_o,
-                       a.base ? load8(a.base + tok * a.ldb, c, stop, a.vec_b)
-                              : make_uint4(0, 0, 0, 0));
-        }
-        return;
-    }
-    const Tensor t = tensor_begin(ts, kCols);
-    constexpr int wide = PAD / 8, blocks = row_blocks(PAD), matrix = kMatrix<BY_ROW, PAD>;
+    const Tensor t = tensor_begin(ts, 2 * kCols);
+    constexpr int wide = PAD / 8, row_blks = row_blocks(PAD), matrix = kMatrix<BY_ROW, PAD>;
     constexpr bool side = 2 * PAD <= kBlk;
     const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPairBlocks<PAD>;
     const uint32_t mine = mats + 2 * matrix + 4096 * warp;
-    // h: chunk c of part p of a row
-    for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kThreads) {
-        const int row = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
-        const int at = side ? c : c - part * wide + part * 8 * blocks;
-        copy16(hs + (at >> 3) * (128 * kTile) + sw128_at(row, at & 7),
-               a.pair + (long long)(tile.y + row) * 2 * PAD + 8 * c, 16);
-    }
     // the matrix: rows of ranks (0 behind the last), or (BY_ROW) of columns for each rank
     using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD>, Rows<PAD / 8, kCols>>;
     const W wr(BY_ROW ? 128 * PAD : 128 * kCols);
-    const uint16_t *w = a.w + (long long)tile.x * a.r * a.N;
-    const uint16_t *mat0 = BY_ROW ? w + (long long)wr.row * a.N + 8 * wr.chunk
-                                  : w + (long long)wr.row * a.r + 8 * wr.chunk;
     const long long mat_pass = (long long)W::kPass * (BY_ROW ? a.N : a.r);
-    const float scale = a.scale ? a.scale[tile.x] : 1.f;
-    const auto fetch = [&](int c0, int buffer) {
-        const uint32_t ws = mats + buffer * matrix + wr.at;
-        if (a.vec_w && c0 + kCols <= a.N) {
-            const uint16_t *m = mat0 + (BY_ROW ? c0 : (long long)c0 * a.r);
-#pragma unroll
-            for (int j = 0; j < W::kPasses; j++) {
-                const bool in = BY_ROW ? wr.row + W::kPass * j < a.r : 8 * wr.chunk < a.r;
-                if (wr.on)
-                    copy16(ws + W::kNext * j, in ? m + mat_pass * j : w, in ? 16 : 0);
-            }
-        } else {
-#pragma unroll 1
-            for (int j = 0; j < W::kPasses && wr.on; j++) {
-                const int row = wr.row + W::kPass * j;
-                if constexpr (BY_ROW) {
-                    fetch8(ws + W::kNext * j, row < a.r ? w + (long long)row * a.N : w,
-                           c0 + 8 * wr.chunk, row < a.r ? a.N : 0, a.vec_w);
-                } else {
-                    const bool in = c0 + row < a.N && 8 * wr.chunk < a.r;
-                    copy16(ws + W::kNext * j,
-                           in ? w + (long long)(c0 + row) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
-                }
-            }
-        }
-        commit_copies();
-    };
     constexpr uint32_t idesc =
         (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
         ((uint32_t)(kCols >> 3) << 17) | (8u << 24) | (BY_ROW ? kMnMajorB : 0u);
-    fetch(first, 0);
-    // rows of the warp's pass: 8 i + lane / 4 of its 32, columns 8 (lane % 4) .. of 32
+    // a warp's pass: rows 8 i + lane / 4 of its 32, columns 8 (lane % 4) .. of 32
     const int quad = warp & 3, half = warp >> 2, col = 64 * half + 8 * (lane & 3);
-    const bool busy = 32 * quad < tile.z;
-    const uint16_t *from[4];
-    uint16_t *to[4];
-    bool on[4];
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const int at = 32 * quad + 8 * i + lane / 4;
-        on[i] = at < tile.z;
-        const long long tok = on[i] ? a.p.perm[tile.y + at] : 0;
-        from[i] = a.base + tok * a.ldb;
-        to[i] = a.out + tok * a.ldo;
-    }
-    uint4 b[2][4];
-#pragma unroll
-    for (int p = 0; p < 2; p++)
-#pragma unroll
-        for (int i = 0; i < 4; i++)
-            b[p][i] = make_uint4(0, 0, 0, 0);
-    const auto load_base = [&](int p, int c0) {
-        if (!a.base || c0 >= stop)
-            return;
-        const int c = c0 + col + 32 * p;
-        if (a.vec_b && c0 + kCols <= a.N) {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                if (on[i])
-                    b[p][i] = load_stream(from[i] + c);
-        } else {
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                if (on[i])
-                    b[p][i] = load8(from[i], c, a.N, a.vec_b);
+    int done = 0;       // products so far: their tensor memory and barrier alternate
+    while (at < end) {
+        const int4 tile = a.p.tiles[at / blocks];
+        const int first = (int)(at % blocks), steps = (int)min(end - at, (long long)blocks - first);
+        at += steps;
+        if (tile.x == a.L) {        // no adapter: base, or 0
+            const int stop = min(a.N, (first + steps) * kCols);
+            for (int i = warp; i < tile.z && a.out != a.base; i += kWarps) {
+                const long long tok = a.p.perm[tile.y + i];
+                for (int c = first * kCols + 8 * lane; c < stop; c += 256)
+                    store8(a.out + tok * a.ldo, c, stop, a.vec_o,
+                           a.base ? load8(a.base + tok * a.ldb, c, stop, a.vec_b)
+                                  : make_uint4(0, 0, 0, 0));
+            }
+            continue;
         }
-    };
-    load_base(0, first);
-    load_base(1, first);
-    int step = 0;
-    for (int c0 = first; c0 < stop; c0 += kCols, step++) {
-        wait_copies<0>();
-        fence_async_shared();
-        tc_fence_before();
-        __syncthreads();
-        if (warp == 0) {
-            tc_fence_after();
-            if (elect_one()) {
-                const uint32_t mat = mats + (step & 1) * matrix;
+        // h: chunk c of part p of a row
+        for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kThreads) {
+            const int row = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
+            const int to = side ? c : c - part * wide + part * 8 * row_blks;
+            copy16(hs + (to >> 3) * (128 * kTile) + sw128_at(row, to & 7),
+                   a.pair + (long long)(tile.y + row) * 2 * PAD + 8 * c, 16);
+        }
+        const uint16_t *w = a.w + (long long)tile.x * a.r * a.N;
+        const uint16_t *mat0 = BY_ROW ? w + (long long)wr.row * a.N + 8 * wr.chunk
+                                      : w + (long long)wr.row * a.r + 8 * wr.chunk;
+        const float scale = a.scale ? a.scale[tile.x] : 1.f;
+        const auto fetch = [&](int step) {
+            const int c0 = (first + step) * kCols;
+            const uint32_t ws = mats + (step & 1) * matrix + wr.at;
+            if (step >= steps) {
+            } else if (a.vec_w && c0 + kCols <= a.N) {
+                const uint16_t *m = mat0 + (BY_ROW ? c0 : (long long)c0 * a.r);
 #pragma unroll
-                for (int part = 0; part < 2; part++)
-#pragma unroll
-                    for (int k = 0; k < PAD / 16; k++) {
-                        const int ka = side ? part * (PAD / 16) + k : part * 4 * blocks + k;
-                        const uint64_t da =
-                            sw128_desc(hs + (ka >> 2) * (128 * kTile)) + 2 * (ka & 3);
-                        const uint64_t db =
-                            BY_ROW ? sw128_desc_mn(mat, 128 * PAD) + 128 * k
-                                   : sw128_desc(mat + (k >> 2) * (128 * kCols)) + 2 * (k & 3);
-                        umma_ss(t.tmem, da, db, idesc, part || k);
+                for (int j = 0; j < W::kPasses; j++) {
+                    const bool in = BY_ROW ? wr.row + W::kPass * j < a.r : 8 * wr.chunk < a.r;
+                    if (wr.on)
+                        copy16(ws + W::kNext * j, in ? m + mat_pass * j : w, in ? 16 : 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int j = 0; j < W::kPasses && wr.on; j++) {
+                    const int row = wr.row + W::kPass * j;
+                    if constexpr (BY_ROW) {
+                        fetch8(ws + W::kNext * j, row < a.r ? w + (long long)row * a.N : w,
+                               c0 + 8 * wr.chunk, row < a.r ? a.N : 0, a.vec_w);
+                    } else {
+                        const bool in = c0 + row < a.N && 8 * wr.chunk < a.r;
+                        copy16(ws + W::kNext * j,
+                               in ? w + (long long)(c0 + row) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
                     }
-                umma_commit(t.bars);
+                }
             }
-            __syncwarp();
+            commit_copies();
+        };
+        const auto multiply = [&](int step) {
+            if (warp == 0 && step < steps) {
+                tc_fence_after();
+                if (elect_one()) {
+                    const uint32_t mat = mats + (step & 1) * matrix;
+                    const int buffer = (done + step) & 1;
+#pragma unroll
+                    for (int part = 0; part < 2; part++)
+#pragma unroll
+                        for (int k = 0; k < PAD / 16; k++) {
+                            const int ka = side ? part * (PAD / 16) + k : part * 4 * row_blks + k;
+                            const uint64_t da =
+                                sw128_desc(hs + (ka >> 2) * (128 * kTile)) + 2 * (ka & 3);
+                            const uint64_t db =
+                                BY_ROW ? sw128_desc_mn(mat, 128 * PAD) + 128 * k
+                                       : sw128_desc(mat + (k >> 2) * (128 * kCols)) + 2 * (k & 3);
+                            umma_ss(t.tmem + kCols * buffer, da, db, idesc, part || k);
+                        }
+                    umma_commit(t.bars + 8 * buffer);
+                }
+                __syncwarp();
+            }
+        };
+        fetch(0);
+        fetch(1);
+        const bool busy = 32 * quad < tile.z;
+        const uint16_t *from[4];
+        uint16_t *to[4];
+        bool on[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int row = 32 * quad + 8 * i + lane / 4;
+            on[i] = row < tile.z;
+            const long long tok = on[i] ? a.p.perm[tile.y + row] : 0;
+            from[i] = a.base + tok * a.ldb;
+            to[i] = a.out + tok * a.ldo;
         }
-        if (c0 + kCols < stop)      // its buffer's products were waited for
-            fetch(c0 + kCols, (step + 1) & 1);
-        tensor_wait(t, 0, step);
-        tc_fence_after();
-        const F2 factor = f2(*t.gave_up ? NAN : scale);
-        const bool inside = a.vec_o && c0 + kCols <= a.N;
+        uint4 b[2][4];
 #pragma unroll
-        for (int p = 0; p < 2; p++) {
-            if (!busy || c0 + 64 * half + 32 * p >= a.N)
-                break;
+        for (int p = 0; p < 2; p++)
 #pragma unroll
-            for (int j = 0; j < 2; j++) {
-                float v[16];
-                tmem_ld16(t.tmem + ((uint32_t)(32 * quad) << 16) + 64 * half + 32 * p + 16 * j, v);
+            for (int i = 0; i < 4; i++)
+                b[p][i] = make_uint4(0, 0, 0, 0);
+        const auto load_base = [&](int p, int step) {
+            if (!a.base || step >= steps)
+                return;
+            const int c0 = (first + step) * kCols, c = c0 + col + 32 * p;
+            if (a.vec_b && c0 + kCols <= a.N) {
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                     mine + sw128_at(lane, 4 * j + q)),
-                                 "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]),
-                                 "f"(v[4 * q + 3])
-                                 : "memory");
+                for (int i = 0; i < 4; i++)
+                    if (on[i])
+                        b[p][i] = load_stream(from[i] + c);
+            } else {
+#pragma unroll 1
+                for (int i = 0; i < 4; i++) {
+                    const int row = 32 * quad + 8 * i + lane / 4;
+                    const uint4 q =
+                        row < tile.z
+                            ? load8(a.base + a.p.perm[tile.y + row] * a.ldb, c, a.N, a.vec_b)
+                            : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        if (k == i)
+                            b[p][k] = q;
+                }
             }
-            __syncwarp();
-            const int c = c0 + col + 32 * p;
+        };
+        load_base(0, 0);
+        load_base(1, 0);
+        wait_copies<1>();
+        fence_async_shared();
+        __syncthreads();
+        multiply(0);
+        for (int step = 0; step < steps; step++) {
+            const int c0 = (first + step) * kCols, buffer = (done + step) & 1;
+            wait_copies<0>();
+            fence_async_shared();
+            tc_fence_before();
+            __syncthreads();
+            multiply(step + 1);
+            tensor_wait(t, buffer, (done + step) >> 1);
+            tc_fence_after();
+            fetch(step + 2);        // in the place of this step's matrix
+            const F2 factor = f2(*t.gave_up ? NAN : scale);
+            const bool inside = a.vec_o && c0 + kCols <= a.N;
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int row = 8 * i + lane / 4;
-                F2 v[4], d[4];
+            for (int p = 0; p < 2; p++) {
+                if (!busy || c0 + 64 * half + 32 * p >= a.N)
+                    break;
+                const uint32_t sums =
+                    t.tmem + ((uint32_t)(32 * quad) << 16) + kCols * buffer + 64 * half + 32 * p;
 #pragma unroll
-                for (int q = 0; q < 2; q++)
-                    asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
-                                 : "=l"(v[2 * q].v), "=l"(v[2 * q + 1].v)
-                                 : "r"(mine + sw128_at(row, 2 * (lane & 3) + q))
-                                 : "memory");
-                unpack<T>(b[p][i], d);
+                for (int j = 0; j < 2; j++) {
+                    float v[16];
+                    tmem_ld16(sums + 16 * j, v);
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    d[e] = fma(factor, v[e], d[e]);
-                if (!on[i])
-                    continue;
-                if (inside)
-                    *reinterpret_cast<uint4 *>(to[i] + c) = pack<T>(d);
-                else
-                    store8(to[i], c, a.N, a.vec_o, pack<T>(d));
+                    for (int q = 0; q < 4; q++)
+                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                         mine + sw128_at(lane, 4 * j + q)),
+                                     "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]),
+                                     "f"(v[4 * q + 3])
+                                     : "memory");
+                }
+                __syncwarp();
+                const int c = c0 + col + 32 * p;
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    const int row = 8 * i + lane / 4;
+                    F2 v[4], d[4];
+#pragma unroll
+                    for (int q = 0; q < 2; q++)
+                        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
+                                     : "=l"(v[2 * q].v), "=l"(v[2 * q + 1].v)
+                                     : "r"(mine + sw128_at(row, 2 * (lane & 3) + q))
+                                     : "memory");
+                    unpack<T>(b[p][i], d);
+#pragma unroll
+                    for (int e = 0; e < 4; e++)
+                        d[e] = fma(factor, v[e], d[e]);
+                    if (!on[i])
+                        continue;
+                    if (inside)
+                        *reinterpret_cast<uint4 *>(to[i] + c) = pack<T>(d);
+                    else
+                        store8(to[i], c, a.N, a.vec_o, pack<T>(d));
+                }
+                __syncwarp();
+                load_base(p, step + 1);
             }
-            __syncwarp();
-            load_base(p, c0 + kCols);
         }
+        done += steps;
+        tc_fence_before();
     }
     wait_copies<0>();
-    tensor_end(t, kCols);
+    tensor_end(t, 2 * kCols);
 }
 
 // ---------------------------------------------------------------- outer
@@ -809,14 +839,13 @@ cudaError_t launch_shrink(const ShrinkArgs &a, int tiles, cudaStream_t st)
 }
 
 template <typename T, bool BY_ROW, int PAD>
-cudaError_t launch_expand(ExpandArgs a, int tiles, cudaStream_t st)
+cudaError_t launch_expand(const ExpandArgs &a, int tiles, int sms, cudaStream_t st)
 {
-    const int blocks = (a.N + kCols - 1) / kCols;
-    // four waves of CTAs and more; up to eight blocks of columns save reading h again
-    a.steps = std::max(1, std::min(8, (int)((long long)blocks * tiles / 1216)));
+    const long long total = (long long)((a.N + kCols - 1) / kCols) * tiles;
+    // as many CTAs as run at once
     return launch_wide(adapter_expand_kernel<T, BY_ROW, PAD>,
-                       dim3(tiles, (blocks + a.steps - 1) / a.steps), kExpandSmem<BY_ROW, PAD>, st,
-                       a);
+                       dim3((unsigned)std::min(total, (PAD <= 64 ? 2LL : 1LL) * sms)),
+                       kExpandSmem<BY_ROW, PAD>, st, a);
 }
 
 bool vec_rows(const void *p, long long ld, int n)
@@ -837,9 +866,9 @@ cudaError_t run_adapter(const AdapterCall &c, cudaStream_t st)
     if (e != cudaSuccess)
         return e;
     const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.B), c.scale, half_words(c.base), c.ldb,
-                          static_cast<uint16_t *>(c.out), c.ldo, c.L, c.N, c.r, 0, true,
+                          static_cast<uint16_t *>(c.out), c.ldo, c.L, c.N, c.r, true,
                           vec_rows(c.base, c.ldb, c.n), vec_rows(c.out, c.ldo, c.n)};
-    return launch_expand<T, false, PAD>(x, tiles, st);
+    return launch_expand<T, false, PAD>(x, tiles, c.sms, st);
 }
 
 template <typename T, int PAD>
@@ -853,10 +882,10 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
         return e;
     if (c.dx) {
         const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.A), c.scale, half_words(c.base), c.ldb,
-                              static_cast<uint16_t *>(c.dx), c.lddx, c.L, c.K, c.r, 0,
+                              static_cast<uint16_t *>(c.dx), c.lddx, c.L, c.K, c.r,
                               c.K % 8 == 0, vec_rows(c.base, c.ldb, c.n),
                               vec_rows(c.dx, c.lddx, c.n)};
-        e = launch_expand<T, true, PAD>(x, tiles, st);
+        e = launch_expand<T, true, PAD>(x, tiles, c.sms, st);
         if (e != cudaSuccess)
             return e;
     }
