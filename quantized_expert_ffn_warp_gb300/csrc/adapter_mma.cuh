@@ -50,9 +50,9 @@ __device__ __forceinline__ void fetch8(uint32_t dst, const uint16_t *row, int i,
 // Copies of ROWS rows of CH chunks of 16 bytes each into rows of 128 bytes (blocks of
 // eight chunks, `block` bytes apart), by the whole CTA: a thread has one chunk of every
 // kPass-th row, its places a constant number of bytes apart.
-template <int CH, int ROWS>
+template <int CH, int ROWS, int THREADS = kThreads>
 struct Rows {
-    static constexpr int kPass = kThreads / CH;
+    static constexpr int kPass = THREADS / CH;
     static constexpr int kPasses = (ROWS + kPass - 1) / kPass;
     int row, chunk;
     uint32_t at;
@@ -398,20 +398,30 @@ template <int PAD>
 constexpr int kPairBlocks = 2 * PAD <= kBlk ? 1 : 2 * row_blocks(PAD);
 template <bool BY_ROW, int PAD>
 constexpr int kMatrix = BY_ROW ? 2 * kCols * PAD : 128 * kCols * row_blocks(PAD);
+// A tile's rows of base, then of out, for one block of columns: rows 16 bytes longer than
+// their values lie in different banks at equal columns.
+constexpr int kExpandThreads = 512;
+constexpr int kPitch = 2 * kCols + 16, kRowsBytes = kTile * kPitch;
+// Blocks of columns whose copies are under way ahead; one more buffer of rows for the
+// block at hand.
+template <int PAD>
+constexpr int kAhead = PAD <= 64 ? 2 : 1;
+template <int PAD>
+constexpr int kRowBuffers = kAhead<PAD> + 1;
 template <bool BY_ROW, int PAD>
-constexpr int kExpandSmem =
-    128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW, PAD> + 4096 * kWarps + kSmemSlack;
+constexpr int kExpandSmem = 128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW, PAD> +
+                            kRowBuffers<PAD> * kRowsBytes + kSmemSlack;
 
 // Tiles of tokens (the product's rows) times blocks of columns: a CTA takes an equal share
 // of all (tile, block) pairs, tile after tile.  While a block's sums leave tensor memory,
-// the next block is multiplied beside it and the matrix of the one behind that is copied.
-// The sums pass through a warp's shared memory, where a lane finds eight neighbours of a
-// token's row, and meet base, whose next values are loaded as soon as the last ones are
-// used.
+// the next block is multiplied beside it, and the matrix and base of the one behind that
+// are copied.  A thread has a quarter of a token's row and adds the sums to base where base
+// lies in shared memory; then the warp stores 64 bytes of every row.
 template <typename T, bool BY_ROW, int PAD>
-__global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs a)
+__global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(ExpandArgs a)
 {
     __shared__ TensorSmem ts;
+    __shared__ int toks[kTile];
     pdl_enter();
     const int blocks = (a.N + kCols - 1) / kCols;
     const long long total = (long long)*a.p.n_tiles * blocks;
@@ -422,18 +432,22 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Tensor t = tensor_begin(ts, 2 * kCols);
     constexpr int wide = PAD / 8, row_blks = row_blocks(PAD), matrix = kMatrix<BY_ROW, PAD>;
+    constexpr int ahead = kAhead<PAD>, buffers = kRowBuffers<PAD>;
     constexpr bool side = 2 * PAD <= kBlk;
     const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPairBlocks<PAD>;
-    const uint32_t mine = mats + 2 * matrix + 4096 * warp;
+    const uint32_t rows = mats + 2 * matrix;
     // the matrix: rows of ranks (0 behind the last), or (BY_ROW) of columns for each rank
-    using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD>, Rows<PAD / 8, kCols>>;
+    using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD, kExpandThreads>,
+                                 Rows<PAD / 8, kCols, kExpandThreads>>;
     const W wr(BY_ROW ? 128 * PAD : 128 * kCols);
     const long long mat_pass = (long long)W::kPass * (BY_ROW ? a.N : a.r);
     constexpr uint32_t idesc =
         (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
         ((uint32_t)(kCols >> 3) << 17) | (8u << 24) | (BY_ROW ? kMnMajorB : 0u);
-    // a warp's pass: rows 8 i + lane / 4 of its 32, columns 8 (lane % 4) .. of 32
-    const int quad = warp & 3, half = warp >> 2, col = 64 * half + 8 * (lane & 3);
+    // the thread's row and 32 of its columns; its chunk of base in every 32nd row
+    const int row = 32 * (warp & 3) + lane, col = 32 * (warp >> 2);
+    const int base_row = threadIdx.x / 16, base_chunk = threadIdx.x % 16;
+    constexpr int kBasePass = kExpandThreads / 16;
     int done = 0;       // products so far: their tensor memory and barrier alternate
     while (at < end) {
         const int4 tile = a.p.tiles[at / blocks];
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs 
         at += steps;
         if (tile.x == a.L) {        // no adapter: base, or 0
             const int stop = min(a.N, (first + steps) * kCols);
-            for (int i = warp; i < tile.z && a.out != a.base; i += kWarps) {
+            for (int i = warp; i < tile.z && a.out != a.base; i += kExpandThreads / 32) {
                 const long long tok = a.p.perm[tile.y + i];
                 for (int c = first * kCols + 8 * lane; c < stop; c += 256)
                     store8(a.out + tok * a.ldo, c, stop, a.vec_o,
@@ -450,22 +464,44 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs 
             }
             continue;
         }
+        __syncthreads();        // the last tile's rows have left
+        if (threadIdx.x < kTile)
+            toks[threadIdx.x] =
+                a.p.perm[tile.y + ((int)threadIdx.x < tile.z ? threadIdx.x : 0)];
         // h: chunk c of part p of a row
-        for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kThreads) {
-            const int row = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
+        for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kExpandThreads) {
+            const int r = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
             const int to = side ? c : c - part * wide + part * 8 * row_blks;
-            copy16(hs + (to >> 3) * (128 * kTile) + sw128_at(row, to & 7),
-                   a.pair + (long long)(tile.y + row) * 2 * PAD + 8 * c, 16);
+            copy16(hs + (to >> 3) * (128 * kTile) + sw128_at(r, to & 7),
+                   a.pair + (long long)(tile.y + r) * 2 * PAD + 8 * c, 16);
         }
+        __syncthreads();
         const uint16_t *w = a.w + (long long)tile.x * a.r * a.N;
         const uint16_t *mat0 = BY_ROW ? w + (long long)wr.row * a.N + 8 * wr.chunk
                                       : w + (long long)wr.row * a.r + 8 * wr.chunk;
         const float scale = a.scale ? a.scale[tile.x] : 1.f;
+        // what the thread stores: 8 columns of rows lane / 4, + 8, .. of the warp's 32
+        uint16_t *to[4];
+        bool on[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int r = 32 * (warp & 3) + 8 * i + lane / 4;
+            on[i] = r < tile.z;
+            to[i] = a.out + (long long)toks[r] * a.ldo + col + 8 * (lane & 3);
+        }
+        const uint16_t *from[kTile / kBasePass];
+#pragma unroll
+        for (int j = 0; j < kTile / kBasePass; j++)
+            from[j] = a.base + (long long)toks[base_row + kBasePass * j] * a.ldb + 8 * base_chunk;
         const auto fetch = [&](int step) {
             const int c0 = (first + step) * kCols;
             const uint32_t ws = mats + (step & 1) * matrix + wr.at;
+            const bool whole = c0 + kCols <= a.N;
             if (step >= steps) {
-            } else if (a.vec_w && c0 + kCols <= a.N) {
+                commit_copies();
+                return;
+            }
+            if (a.vec_w && whole) {
                 const uint16_t *m = mat0 + (BY_ROW ? c0 : (long long)c0 * a.r);
 #pragma unroll
                 for (int j = 0; j < W::kPasses; j++) {
@@ -476,15 +512,30 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs 
             } else {
 #pragma unroll 1
                 for (int j = 0; j < W::kPasses && wr.on; j++) {
-                    const int row = wr.row + W::kPass * j;
+                    const int r = wr.row + W::kPass * j;
                     if constexpr (BY_ROW) {
-                        fetch8(ws + W::kNext * j, row < a.r ? w + (long long)row * a.N : w,
-                               c0 + 8 * wr.chunk, row < a.r ? a.N : 0, a.vec_w);
+                        fetch8(ws + W::kNext * j, r < a.r ? w + (long long)r * a.N : w,
+                               c0 + 8 * wr.chunk, r < a.r ? a.N : 0, a.vec_w);
                     } else {
-                        const bool in = c0 + row < a.N && 8 * wr.chunk < a.r;
+                        const bool in = c0 + r < a.N && 8 * wr.chunk < a.r;
                         copy16(ws + W::kNext * j,
-                               in ? w + (long long)(c0 + row) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
+                               in ? w + (long long)(c0 + r) * a.r + 8 * wr.chunk : w, in ? 16 : 0);
                     }
+                }
+            }
+            if (a.base) {
+                const uint32_t bs =
+                    rows + step % buffers * kRowsBytes + base_row * kPitch + 16 * base_chunk;
+                if (a.vec_b && whole) {
+#pragma unroll
+                    for (int j = 0; j < kTile / kBasePass; j++)
+                        if (base_row + kBasePass * j < tile.z)
+                            copy16(bs + kBasePass * kPitch * j, from[j] + c0, 16);
+                } else {
+#pragma unroll 1
+                    for (int r = base_row; r < tile.z; r += kBasePass)
+                        fetch8(bs + (r - base_row) * kPitch, a.base + toks[r] * a.ldb,
+                               c0 + 8 * base_chunk, a.N, a.vec_b);
                 }
             }
             commit_copies();
@@ -513,110 +564,60 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_expand_kernel(ExpandArgs 
             }
         };
         fetch(0);
-        fetch(1);
-        const bool busy = 32 * quad < tile.z;
-        const uint16_t *from[4];
-        uint16_t *to[4];
-        bool on[4];
-#pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int row = 32 * quad + 8 * i + lane / 4;
-            on[i] = row < tile.z;
-            const long long tok = on[i] ? a.p.perm[tile.y + row] : 0;
-            from[i] = a.base + tok * a.ldb;
-            to[i] = a.out + tok * a.ldo;
+        if (ahead == 2) {
+            fetch(1);
+            wait_copies<1>();
+            fence_async_shared();
+            __syncthreads();
+            multiply(0);
         }
-        uint4 b[2][4];
-#pragma unroll
-        for (int p = 0; p < 2; p++)
-#pragma unroll
-            for (int i = 0; i < 4; i++)
-                b[p][i] = make_uint4(0, 0, 0, 0);
-        const auto load_base = [&](int p, int step) {
-            if (!a.base || step >= steps)
-                return;
-            const int c0 = (first + step) * kCols, c = c0 + col + 32 * p;
-            if (a.vec_b && c0 + kCols <= a.N) {
-#pragma unroll
-                for (int i = 0; i < 4; i++)
-                    if (on[i])
-                        b[p][i] = load_stream(from[i] + c);
-            } else {
-#pragma unroll 1
-                for (int i = 0; i < 4; i++) {
-                    const int row = 32 * quad + 8 * i + lane / 4;
-                    const uint4 q =
-                        row < tile.z
-                            ? load8(a.base + a.p.perm[tile.y + row] * a.ldb, c, a.N, a.vec_b)
-                            : make_uint4(0, 0, 0, 0);
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        if (k == i)
-                            b[p][k] = q;
-                }
-            }
-        };
-        load_base(0, 0);
-        load_base(1, 0);
-        wait_copies<1>();
-        fence_async_shared();
-        __syncthreads();
-        multiply(0);
         for (int step = 0; step < steps; step++) {
             const int c0 = (first + step) * kCols, buffer = (done + step) & 1;
+            // the copies of the next product are through, and the last block's rows have left
             wait_copies<0>();
             fence_async_shared();
             tc_fence_before();
             __syncthreads();
-            multiply(step + 1);
+            multiply(step + ahead - 1);
             tensor_wait(t, buffer, (done + step) >> 1);
             tc_fence_after();
-            fetch(step + 2);        // in the place of this step's matrix
+            fetch(step + ahead);
             const F2 factor = f2(*t.gave_up ? NAN : scale);
-            const bool inside = a.vec_o && c0 + kCols <= a.N;
+            uint8_t *const block = static_cast<uint8_t *>(__cvta_shared_to_generic(rows)) +
+                                   step % buffers * kRowsBytes + 2 * col;
+            uint4 *const mine = reinterpret_cast<uint4 *>(block + row * kPitch);
+            const uint8_t *const theirs =
+                block + (32 * (warp & 3) + lane / 4) * kPitch + 16 * (lane & 3);
+            if (32 * (warp & 3) < tile.z && c0 + col < a.N) {
+                float v[32];
+                tmem_ld32(t.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * buffer + col, v);
 #pragma unroll
-            for (int p = 0; p < 2; p++) {
-                if (!busy || c0 + 64 * half + 32 * p >= a.N)
-                    break;
-                const uint32_t sums =
-                    t.tmem + ((uint32_t)(32 * quad) << 16) + kCols * buffer + 64 * half + 32 * p;
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    float v[16];
-                    tmem_ld16(sums + 16 * j, v);
-#pragma unroll
-                    for (int q = 0; q < 4; q++)
-                        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         mine + sw128_at(lane, 4 * j + q)),
-                                     "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]),
-                                     "f"(v[4 * q + 3])
-                                     : "memory");
-                }
-                __syncwarp();
-                const int c = c0 + col + 32 * p;
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const int row = 8 * i + lane / 4;
-                    F2 v[4], d[4];
-#pragma unroll
-                    for (int q = 0; q < 2; q++)
-                        asm volatile("ld.shared.v2.u64 {%0, %1}, [%2];"
-                                     : "=l"(v[2 * q].v), "=l"(v[2 * q + 1].v)
-                                     : "r"(mine + sw128_at(row, 2 * (lane & 3) + q))
-                                     : "memory");
-                    unpack<T>(b[p][i], d);
+                for (int q = 0; q < 4; q++) {
+                    F2 d[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
+                    if (a.base)
+                        unpack<T>(mine[q], d);
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        d[e] = fma(factor, v[e], d[e]);
-                    if (!on[i])
-                        continue;
-                    if (inside)
-                        *reinterpret_cast<uint4 *>(to[i] + c) = pack<T>(d);
-                    else
-                        store8(to[i], c, a.N, a.vec_o, pack<T>(d));
+                        d[e] = fma(factor, f2(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]), d[e]);
+                    mine[q] = pack<T>(d);
                 }
                 __syncwarp();
-                load_base(p, step + 1);
+                const int c = c0 + col + 8 * (lane & 3);
+                uint4 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    q[i] = *reinterpret_cast<const uint4 *>(theirs + 8 * kPitch * i);
+                if (a.vec_o && c0 + kCols <= a.N) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (on[i])
+                            *reinterpret_cast<uint4 *>(to[i] + c0) = q[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        if (on[i])
+                            store8(to[i] - (col + 8 * (lane & 3)), c, a.N, a.vec_o, q[i]);
+                }
             }
         }
         done += steps;
@@ -824,11 +825,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
 
 // A kernel with more dynamic shared memory than the default.
 template <typename... P, typename A>
-cudaError_t launch_wide(void (*kernel)(P...), dim3 grid, int smem, cudaStream_t st, const A &a)
+cudaError_t launch_wide(void (*kernel)(P...), dim3 grid, int smem, cudaStream_t st, const A &a,
+                        int threads = kThreads)
 {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(kThreads), smem, st, a);
+    return e != cudaSuccess ? e : launch_pdl(kernel, grid, dim3(threads), smem, st, a);
 }
 
 template <typename T, bool BY_ROW, int PAD>
@@ -844,8 +846,8 @@ cudaError_t launch_expand(const ExpandArgs &a, int tiles, int sms, cudaStream_t 
     const long long total = (long long)((a.N + kCols - 1) / kCols) * tiles;
     // as many CTAs as run at once
     return launch_wide(adapter_expand_kernel<T, BY_ROW, PAD>,
-                       dim3((unsigned)std::min(total, (PAD <= 64 ? 2LL : 1LL) * sms)),
-                       kExpandSmem<BY_ROW, PAD>, st, a);
+                       dim3((unsigned)std::min(total, (long long)sms)),
+                       kExpandSmem<BY_ROW, PAD>, st, a, kExpandThreads);
 }
 
 bool vec_rows(const void *p, long long ld, int n)
