@@ -159,10 +159,11 @@ __device__ __forceinline__ void contract(const Tensor &t, int steps, F fetch, M 
 }
 
 // A call's dynamic shared memory from a 1024-byte boundary on, as the swizzle needs.
-__device__ __forceinline__ uint32_t smem_base()
+extern __shared__ uint8_t adapter_smem[];
+__device__ __forceinline__ uint32_t smem_base() { return (saddr(adapter_smem) + 1023) & ~1023u; }
+__device__ __forceinline__ uint8_t *smem_at(uint32_t address)
 {
-    extern __shared__ uint8_t adapter_smem[];
-    return (saddr(adapter_smem) + 1023) & ~1023u;
+    return adapter_smem + (address - saddr(adapter_smem));
 }
 constexpr int kSmemSlack = 1024;
 
@@ -583,27 +584,31 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             tc_fence_after();
             fetch(step + ahead);
             const F2 factor = f2(*t.gave_up ? NAN : scale);
-            uint8_t *const block = static_cast<uint8_t *>(__cvta_shared_to_generic(rows)) +
-                                   step % buffers * kRowsBytes + 2 * col;
+            uint8_t *const block = smem_at(rows + step % buffers * kRowsBytes + 2 * col);
             uint4 *const mine = reinterpret_cast<uint4 *>(block + row * kPitch);
             const uint8_t *const theirs =
                 block + (32 * (warp & 3) + lane / 4) * kPitch + 16 * (lane & 3);
             if (32 * (warp & 3) < tile.z && c0 + col < a.N) {
+                uint4 q[4];
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    q[i] = a.base ? mine[i] : make_uint4(0, 0, 0, 0);
                 float v[32];
                 tmem_ld32(t.tmem + ((uint32_t)(32 * (warp & 3)) << 16) + kCols * buffer + col, v);
 #pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    F2 d[4] = {f2(0.f), f2(0.f), f2(0.f), f2(0.f)};
-                    if (a.base)
-                        unpack<T>(mine[q], d);
+                for (int i = 0; i < 4; i++) {
+                    F2 d[4];
+                    unpack<T>(q[i], d);
 #pragma unroll
                     for (int e = 0; e < 4; e++)
-                        d[e] = fma(factor, f2(v[8 * q + 2 * e], v[8 * q + 2 * e + 1]), d[e]);
-                    mine[q] = pack<T>(d);
+                        d[e] = fma(factor, f2(v[8 * i + 2 * e], v[8 * i + 2 * e + 1]), d[e]);
+                    q[i] = pack<T>(d);
                 }
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    mine[i] = q[i];
                 __syncwarp();
                 const int c = c0 + col + 8 * (lane & 3);
-                uint4 q[4];
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     q[i] = *reinterpret_cast<const uint4 *>(theirs + 8 * kPitch * i);
