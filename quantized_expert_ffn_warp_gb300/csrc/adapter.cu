@@ -47,7 +47,8 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
     const int lo = min(n, warp * per), hi = min(n, lo + per);
     int *mine = hist + warp * G;
     constexpr int U = 8;
-    // calls f(token, group, lanes of the same group) for the warp's tokens, 32 at a time
+    // calls f(token, group, lanes of the same group) for the warp's tokens, 32 at a time;
+    // requests are runs of tokens, so that a group most often fills the warp
     const auto walk = [&](auto f) {
         for (int b = lo; b < hi; b += 32 * U) {
             int g[U];
@@ -63,7 +64,9 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
 #pragma unroll
             for (int i = 0; i < U; i++)
                 if (b + 32 * i < hi) {
-                    f(b + 32 * i + lane, g[i], __match_any_sync(0xffffffffu, g[i]));
+                    const bool one = __all_sync(0xffffffffu, g[i] == __shfl_sync(0xffffffffu, g[i], 0));
+                    f(b + 32 * i + lane, g[i],
+                      one ? 0xffffffffu : __match_any_sync(0xffffffffu, g[i]));
                     __syncwarp();
                 }
         }

@@ -340,15 +340,25 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
     if (!last)
         return;
     __threadfence();
+#pragma unroll 2
     for (int i = threadIdx.x; i < tile.z * (PAD / 4); i += kThreads) {
         const int place = tile.y + i / (PAD / 4), k = i % (PAD / 4) * 4;
+        const float *from = a.part + (long long)place * PAD + k;
+        const long long next = (long long)a.n * PAD;
+        const int token = a.p.perm[place];
         float v[4] = {};
-        for (int s = 0; s < a.slices; s++) {
-            const float4 q = __ldcg(reinterpret_cast<const float4 *>(
-                a.part + ((long long)s * a.n + place) * PAD + k));
-            v[0] += q.x, v[1] += q.y, v[2] += q.z, v[3] += q.w;
+        for (int s0 = 0; s0 < a.slices; s0 += 8) {      // eight loads under way
+            float4 q[8];
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+                if (s0 + s < a.slices)
+                    q[s] = __ldcg(reinterpret_cast<const float4 *>(from + (s0 + s) * next));
+#pragma unroll
+            for (int s = 0; s < 8; s++)
+                if (s0 + s < a.slices)
+                    v[0] += q[s].x, v[1] += q[s].y, v[2] += q[s].z, v[3] += q[s].w;
         }
-        put_results<T, PAD>(a, place, a.p.perm[place], k, v);
+        put_results<T, PAD>(a, place, token, k, v);
     }
 }
 
@@ -455,13 +465,33 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
         const int first = (int)(at % blocks), steps = (int)min(end - at, (long long)blocks - first);
         at += steps;
         if (tile.x == a.L) {        // no adapter: base, or 0
-            const int stop = min(a.N, (first + steps) * kCols);
-            for (int i = warp; i < tile.z && a.out != a.base; i += kExpandThreads / 32) {
-                const long long tok = a.p.perm[tile.y + i];
-                for (int c = first * kCols + 8 * lane; c < stop; c += 256)
-                    store8(a.out + tok * a.ldo, c, stop, a.vec_o,
-                           a.base ? load8(a.base + tok * a.ldb, c, stop, a.vec_b)
-                                  : make_uint4(0, 0, 0, 0));
+            if (a.out == a.base)
+                continue;
+            const int begin = first * kCols, stop = min(a.N, (first + steps) * kCols);
+            const int wide = (stop - begin + 7) / 8;
+            constexpr int U = 8;        // loads of a thread under way
+            for (int i0 = threadIdx.x; i0 < tile.z * wide; i0 += U * kExpandThreads) {
+                uint4 q[U];
+                long long tok[U];
+                int c[U];
+#pragma unroll
+                for (int u = 0; u < U; u++) {
+                    const int i = i0 + u * kExpandThreads;
+                    q[u] = make_uint4(0, 0, 0, 0);
+                    tok[u] = -1;
+                    if (i < tile.z * wide) {
+                        tok[u] = a.p.perm[tile.y + i / wide];
+                        c[u] = begin + i % wide * 8;
+                    }
+                }
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (a.base && tok[u] >= 0)
+                        q[u] = load8(a.base + tok[u] * a.ldb, c[u], stop, a.vec_b);
+#pragma unroll
+                for (int u = 0; u < U; u++)
+                    if (tok[u] >= 0)
+                        store8(a.out + tok[u] * a.ldo, c[u], stop, a.vec_o, q[u]);
             }
             continue;
         }
