@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
 {
     extern __shared__ int sm[];
     const int G = L + 1;        // the last group has no adapter
-    int *hist = sm, *first = sm + 32 * G, *tile0 = first + G + 1;
+    int *hist = sm, *first = sm + 32 * G, *tile0 = first + G + 1, *cost0 = tile0 + G + 1;
     pdl_enter();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     for (int i = threadIdx.x; i < 32 * G; i += 1024)
@@ -87,30 +87,38 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
     }
     __syncthreads();
     if (warp == 0) {
-        int tok = 0, tile = 0;
+        int tok = 0, tile = 0, cost = 0;
         for (int b = 0; b < G; b += 32) {
             const int c = b + lane < G ? first[b + lane] : 0, k = (c + kAdapterTile - 1) / kAdapterTile;
-            int sc = c, sk = k;
+            // as k whole tiles, the tokens of the last one taken back
+            const bool none = b + lane == L;
+            const int e = k * tile_cost(none, 0) + tile_cost(none, c) - tile_cost(none, 0);
+            int sc = c, sk = k, se = e;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
                 const int uc = __shfl_up_sync(0xffffffffu, sc, d);
                 const int uk = __shfl_up_sync(0xffffffffu, sk, d);
+                const int ue = __shfl_up_sync(0xffffffffu, se, d);
                 if (lane >= d) {
                     sc += uc;
                     sk += uk;
+                    se += ue;
                 }
             }
             if (b + lane < G) {
                 first[b + lane] = tok + sc - c;
                 tile0[b + lane] = tile + sk - k;
+                cost0[b + lane] = cost + se - e;
             }
             tok += __shfl_sync(0xffffffffu, sc, 31);
             tile += __shfl_sync(0xffffffffu, sk, 31);
+            cost += __shfl_sync(0xffffffffu, se, 31);
         }
         if (lane == 0) {
             first[G] = n;
             tile0[G] = tile;
-            *p.n_tiles = tile;
+            p.n_tiles[0] = tile;
+            p.n_tiles[1] = cost;
         }
     }
     __syncthreads();
@@ -125,8 +133,9 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
             else
                 b = mid - 1;
         }
-        const int start = first[a] + (i - tile0[a]) * kAdapterTile;
-        p.tiles[i] = make_int4(a, start, min(kAdapterTile, first[a + 1] - start), 0);
+        const int k = i - tile0[a], start = first[a] + k * kAdapterTile;
+        p.tiles[i] = make_int4(a, start, min(kAdapterTile, first[a + 1] - start),
+                               cost0[a] + k * tile_cost(a == L, kAdapterTile));
     }
     walk([&](int t, int g, unsigned same) {
         if (g >= 0)
@@ -171,7 +180,7 @@ AdapterWorkspace adapter_ws(void *base, int n, int L, int r, int K, int N, bool 
     const int tiles = w.slices > 1 ? adapter_tiles(n, L) : 0;
     const int outer = w.splits > 1 ? L * outer_blocks(K, N) : 0;
     w.tickets = tiles + outer;
-    w.p.n_tiles = reinterpret_cast<int *>(take(4));
+    w.p.n_tiles = reinterpret_cast<int *>(take(8));
     w.p.off = reinterpret_cast<int *>(take(4 * ((size_t)L + 2)));
     w.p.perm = reinterpret_cast<int *>(take(4 * (size_t)n));
     w.p.tiles = reinterpret_cast<int4 *>(take(16 * (size_t)adapter_tiles(n, L)));
@@ -188,11 +197,11 @@ AdapterWorkspace adapter_ws(void *base, int n, int L, int r, int K, int N, bool 
 
 cudaError_t launch_plan(const int32_t *ids, int n, int L, const AdapterWorkspace &w, cudaStream_t st)
 {
-    const size_t smem = sizeof(int) * (32 * ((size_t)L + 1) + 2 * ((size_t)L + 2));
+    const size_t smem = sizeof(int) * (32 * ((size_t)L + 1) + 3 * ((size_t)L + 2));
     if (smem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(
             adapter_plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-            (int)(sizeof(int) * (32 * (kAdapterMaxCount + 1) + 2 * (kAdapterMaxCount + 2))));
+            (int)(sizeof(int) * (32 * (kAdapterMaxCount + 1) + 3 * (kAdapterMaxCount + 2))));
         if (e != cudaSuccess)
             return e;
     }

@@ -424,7 +424,7 @@ constexpr int kExpandSmem = 128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW,
                             kRowBuffers<PAD> * kRowsBytes + kSmemSlack;
 
 // Tiles of tokens (the product's rows) times blocks of columns: a CTA takes an equal share
-// of all (tile, block) pairs, tile after tile.  While a block's sums leave tensor memory,
+// of the cost of all (tile, block) pairs, tile after tile.  While a block's sums leave tensor memory,
 // the next block is multiplied beside it, and the matrix and base of the one behind that
 // are copied.  A thread has a quarter of a token's row and adds the sums to base where base
 // lies in shared memory; then the warp stores 64 bytes of every row.
@@ -435,9 +435,27 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
     __shared__ int toks[kTile];
     pdl_enter();
     const int blocks = (a.N + kCols - 1) / kCols;
-    const long long total = (long long)*a.p.n_tiles * blocks;
-    long long at = total * blockIdx.x / gridDim.x;
-    const long long end = total * (blockIdx.x + 1) / gridDim.x;
+    const int n_tiles = a.p.n_tiles[0];
+    const long long cost = (long long)a.p.n_tiles[1] * blocks;
+    // the (tile, block) pairs at which the share of the cost begins and ends: the tiles in
+    // front are counted by all threads at once
+    const long long from_cost = cost * blockIdx.x / gridDim.x;
+    const long long to_cost = cost * (blockIdx.x + 1) / gridDim.x;
+    int tile0 = -1, tile1 = -1;
+    for (int k = 0; k < n_tiles; k += blockDim.x) {
+        const int i = k + threadIdx.x;
+        const long long before = i < n_tiles ? (long long)a.p.tiles[i].w * blocks : cost + 1;
+        tile0 += __syncthreads_count(before <= from_cost);
+        tile1 += __syncthreads_count(before <= to_cost);
+    }
+    const auto place = [&](int tile, long long to) {
+        const int4 q = a.p.tiles[tile];
+        const unsigned block =
+            (unsigned)(to - (long long)q.w * blocks) / (unsigned)tile_cost(q.x == a.L, q.z);
+        return (long long)tile * blocks + min(block, (unsigned)blocks);
+    };
+    long long at = place(tile0, from_cost);
+    const long long end = place(tile1, to_cost);
     if (at >= end)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
