@@ -340,25 +340,42 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
     if (!last)
         return;
     __threadfence();
-#pragma unroll 2
-    for (int i = threadIdx.x; i < tile.z * (PAD / 4); i += kThreads) {
-        const int place = tile.y + i / (PAD / 4), k = i % (PAD / 4) * 4;
-        const float *from = a.part + (long long)place * PAD + k;
-        const long long next = (long long)a.n * PAD;
-        const int token = a.p.perm[place];
-        float v[4] = {};
-        for (int s0 = 0; s0 < a.slices; s0 += 8) {      // eight loads under way
-            float4 q[8];
+    constexpr int I = 4, U = 4;     // places and slices whose loads are under way together
+    const int items = tile.z * (PAD / 4);
+    const long long next = (long long)a.n * PAD;
+    for (int i0 = threadIdx.x; i0 < items; i0 += I * kThreads) {
+        float v[I][4] = {};
+        int token[I];
 #pragma unroll
-            for (int s = 0; s < 8; s++)
-                if (s0 + s < a.slices)
-                    q[s] = __ldcg(reinterpret_cast<const float4 *>(from + (s0 + s) * next));
-#pragma unroll
-            for (int s = 0; s < 8; s++)
-                if (s0 + s < a.slices)
-                    v[0] += q[s].x, v[1] += q[s].y, v[2] += q[s].z, v[3] += q[s].w;
+        for (int j = 0; j < I; j++) {
+            const int i = i0 + j * kThreads;
+            token[j] = i < items ? a.p.perm[tile.y + i / (PAD / 4)] : 0;
         }
-        put_results<T, PAD>(a, place, token, k, v);
+        for (int s0 = 0; s0 < a.slices; s0 += U) {
+            float4 q[I][U];
+#pragma unroll
+            for (int j = 0; j < I; j++) {
+                const int i = i0 + j * kThreads;
+                const float *from = a.part + (s0 * (long long)a.n + tile.y) * PAD + 4 * (long long)i;
+#pragma unroll
+                for (int s = 0; s < U; s++)
+                    if (i < items && s0 + s < a.slices)
+                        q[j][s] = __ldcg(reinterpret_cast<const float4 *>(from + s * next));
+            }
+#pragma unroll
+            for (int j = 0; j < I; j++)
+#pragma unroll
+                for (int s = 0; s < U; s++)
+                    if (s0 + s < a.slices)
+                        v[j][0] += q[j][s].x, v[j][1] += q[j][s].y, v[j][2] += q[j][s].z,
+                            v[j][3] += q[j][s].w;
+        }
+#pragma unroll
+        for (int j = 0; j < I; j++) {
+            const int i = i0 + j * kThreads;
+            if (i < items)
+                put_results<T, PAD>(a, tile.y + i / (PAD / 4), token[j], i % (PAD / 4) * 4, v[j]);
+        }
     }
 }
 
@@ -580,11 +597,26 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
                     for (int j = 0; j < kTile / kBasePass; j++)
                         if (base_row + kBasePass * j < tile.z)
                             copy16(bs + kBasePass * kPitch * j, from[j] + c0, 16);
-                } else {
+                } else if (a.vec_b) {
 #pragma unroll 1
                     for (int r = base_row; r < tile.z; r += kBasePass)
                         fetch8(bs + (r - base_row) * kPitch, a.base + toks[r] * a.ldb,
-                               c0 + 8 * base_chunk, a.N, a.vec_b);
+                               c0 + 8 * base_chunk, a.N, true);
+                } else {        // odd rows: a warp a row, neighbours side by side
+                    constexpr int kWarpsHere = kExpandThreads / 32, E = kCols / 32;
+#pragma unroll 2
+                    for (int r = warp; r < tile.z; r += kWarpsHere) {
+                        const uint16_t *src = a.base + toks[r] * a.ldb + c0;
+                        uint16_t *dst = reinterpret_cast<uint16_t *>(
+                            smem_at(rows + step % buffers * kRowsBytes + r * kPitch));
+                        uint16_t v[E];
+#pragma unroll
+                        for (int e = 0; e < E; e++)
+                            v[e] = c0 + 32 * e + lane < a.N ? src[32 * e + lane] : 0;
+#pragma unroll
+                        for (int e = 0; e < E; e++)
+                            dst[32 * e + lane] = v[e];
+                    }
                 }
             }
             commit_copies();
@@ -657,10 +689,20 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
                     mine[i] = q[i];
                 __syncwarp();
                 const int c = c0 + col + 8 * (lane & 3);
+                if (!a.vec_o) {         // odd rows: neighbours side by side
+                    const uint16_t *from = reinterpret_cast<const uint16_t *>(
+                                               block + 32 * (warp & 3) * kPitch) + lane;
+                    const int many = c0 + col + lane < a.N ? min(32, tile.z - 32 * (warp & 3)) : 0;
+#pragma unroll 4
+                    for (int r = 0; r < many; r++)
+                        a.out[(long long)toks[32 * (warp & 3) + r] * a.ldo + c0 + col + lane] =
+                            from[r * (kPitch / 2)];
+                    continue;
+                }
 #pragma unroll
                 for (int i = 0; i < 4; i++)
                     q[i] = *reinterpret_cast<const uint4 *>(theirs + 8 * kPitch * i);
-                if (a.vec_o && c0 + kCols <= a.N) {
+                if (c0 + kCols <= a.N) {
 #pragma unroll
                     for (int i = 0; i < 4; i++)
                         if (on[i])
