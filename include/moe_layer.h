@@ -528,12 +528,13 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
  * x [n_tokens][cols], base and out [n_tokens][rows] of type dtype (MOE_FP16 or
  * MOE_BF16) with row strides ldx, ldb, ldo; ids int32 [n] in any order; A
  * [n_adapters][rank][cols] and B [n_adapters][rows][rank] of type dtype, 16-byte
- * aligned; scale fp32 [n_adapters] (NULL: 1); h [n][rank] of type dtype (NULL: not
- * kept), what moe_adapter_grad takes.  out may be base itself.
+ * aligned; scale fp32 [n_adapters] (NULL: 1); h [n][rank] of type dtype, 16-byte
+ * aligned (NULL: not kept), what moe_adapter_grad takes.  out may be base itself.
  * Sums are fp32; between the two products h is held as the sum of two values of
  * dtype, so that it adds no rounding of its own (in fp16, an h above 65504 is an
  * infinity); out and h are rounded once.  Rows on 16-byte boundaries are read by
- * wide loads, others (odd widths) value by value.
+ * wide loads, others (odd widths) value by value.  When a wait for the tensor cores
+ * gives up (after 2 s), the outputs that it concerns are NaN.
  * rank a multiple of 8 in 8 .. 128; n_adapters 1 .. 1024; n_tokens, cols and rows 1 ..
  * 1048576.
  * workspace: moe_adapter_workspace(n, n_adapters, rank, cols, rows) bytes, 256-byte

@@ -81,6 +81,8 @@ struct TensorSmem {
     int gave_up;
 };
 
+// Lets the next kernel launch when the CTA has its tensor memory, not before: one that
+// takes all of it and then waits for this kernel would never let it finish.
 __device__ __forceinline__ Tensor tensor_begin(TensorSmem &sm, uint32_t cols)
 {
     if (threadIdx.x < 32)
@@ -94,6 +96,7 @@ __device__ __forceinline__ Tensor tensor_begin(TensorSmem &sm, uint32_t cols)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
+    pdl_launch();
     return {saddr(sm.bar), sm.tmem, &sm.gave_up};
 }
 __device__ __forceinline__ void tensor_end(const Tensor &t, uint32_t cols)
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
 {
     __shared__ TensorSmem ts;
     __shared__ int last;
-    pdl_enter();
+    pdl_wait();
     if ((int)blockIdx.x >= *a.p.n_tiles)
         return;
     const int4 tile = a.p.tiles[blockIdx.x];
@@ -450,7 +453,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
 {
     __shared__ TensorSmem ts;
     __shared__ int toks[kTile];
-    pdl_enter();
+    pdl_wait();
     const int blocks = (a.N + kCols - 1) / kCols;
     const int n_tiles = a.p.n_tiles[0];
     const long long cost = (long long)a.p.n_tiles[1] * blocks;
@@ -775,7 +778,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
     __shared__ TensorSmem ts;
     __shared__ int toks[kOuterList * kBlk];
     __shared__ int last;
-    pdl_enter();
+    pdl_wait();
     const bool of_a = (int)blockIdx.x < a.a.blocks;
     const OuterSide &o = of_a ? a.a : a.b;
     const int c0 = kCols * (of_a ? blockIdx.x : blockIdx.x - a.a.blocks);

@@ -13,10 +13,15 @@ namespace qe {
 // each may start while its predecessor drains; every such kernel first
 // waits for the predecessor's completion (and memory) before it touches
 // global memory, then lets its own successor launch.
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_launch()
+{
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 __device__ __forceinline__ void pdl_enter()
 {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    pdl_wait();
+    pdl_launch();
 }
 
 // (a & mask) | magic: the word's two selected fields become fp16 1024 + field (with
