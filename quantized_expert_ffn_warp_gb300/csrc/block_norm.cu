@@ -26,7 +26,7 @@ namespace qe {
 namespace {
 
 constexpr int kMaxTokens = 1 << 26, kMaxWidth = 16384;
-constexpr int kMaxThreads = 512, kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxThreads = 512, kMaxWarps = 1024 / 32;
 // Rows whose column sums are one fp32 chain.
 constexpr int kRun = 256;
 
@@ -109,11 +109,11 @@ struct Shared {
     }
 };
 
-// V words of a row for each thread.
-template <typename T, int V>
-__global__ void __launch_bounds__(kMaxThreads, V <= 2 ? 2 : 1) residual_norm_kernel(NormArgs a)
+// Two words of a row for each of at most MAX threads.
+template <typename T, int MAX>
+__global__ void __launch_bounds__(MAX, 1024 / MAX) residual_norm_kernel(NormArgs a)
 {
-    constexpr bool kAhead = V <= 2;     // the next row's loads under way
+    constexpr int V = 2;
     extern __shared__ float4 shared[];  // [2][2 V][threads]
     __shared__ float4 part[2][kMaxWarps / 4];
     pdl_enter();
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kMaxThreads, V <= 2 ? 2 : 1) residual_norm_ker
                 r[i][e] = mul(r[i][e], scale);
             }
         }
-        if (kAhead && t + gridDim.x < a.n)
+        if (t + gridDim.x < a.n)        // the next row's loads are under way
             load(t + gridDim.x);
         float r1 = 1.f, r2 = 1.f;
         if (a.gain)
@@ -186,8 +186,6 @@ __global__ void __launch_bounds__(kMaxThreads, V <= 2 ? 2 : 1) residual_norm_ker
         }
         if (threadIdx.x == 0)
             a.stats[t] = make_float2(r1, r2);
-        if (!kAhead && t + gridDim.x < a.n)
-            load(t + gridDim.x);
         // a row with one reduction alone writes the buffer that it reads next time
         if (warps > 1 && !(a.gain && a.xn))
             __syncthreads();
@@ -476,23 +474,25 @@ int shared_bytes(int H, int vectors)
     return (int)sizeof(float4) * 2 * row_words(H) * row_threads(H) * vectors;
 }
 
-template <typename T, int V>
+template <typename T, int MAX>
 cudaError_t launch_norm_as(const NormArgs &a, int sms, cudaStream_t st)
 {
-    const int threads = row_threads(a.H);
-    const cudaError_t e =
-        cudaFuncSetAttribute(residual_norm_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             shared_bytes(V > 2 ? kMaxWidth : kMaxWidth / 2, 2));
+    const int threads = ((a.H + 15) / 16 + 31) / 32 * 32;   // two words a thread
+    constexpr int smem = 2 * 4 * (int)sizeof(float4);       // two vectors, a thread's part
+    const cudaError_t e = cudaFuncSetAttribute(residual_norm_kernel<T, MAX>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               smem * MAX);
     if (e != cudaSuccess)
         return e;
     // as many CTAs as run at once
-    const dim3 grid(std::min(a.n, sms * std::max(1, (V > 2 ? 512 : 1024) / threads)));
-    return launch_pdl(residual_norm_kernel<T, V>, grid, dim3(threads), shared_bytes(a.H, 2), st, a);
+    const dim3 grid(std::min(a.n, sms * std::max(1, 1024 / threads)));
+    return launch_pdl(residual_norm_kernel<T, MAX>, grid, dim3(threads), smem * threads, st, a);
 }
 template <typename T>
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t st)
 {
-    return row_words(a.H) == 2 ? launch_norm_as<T, 2>(a, sms, st) : launch_norm_as<T, 4>(a, sms, st);
+    return a.H <= 16 * kMaxThreads ? launch_norm_as<T, kMaxThreads>(a, sms, st)
+                                   : launch_norm_as<T, 1024>(a, sms, st);
 }
 
 template <typename T, int V>
