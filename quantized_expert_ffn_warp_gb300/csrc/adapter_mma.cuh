@@ -462,7 +462,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
     const long long from_cost = cost * blockIdx.x / gridDim.x;
     const long long to_cost = cost * (blockIdx.x + 1) / gridDim.x;
     int tile0 = -1, tile1 = -1;
-    for (int k = 0; k < n_tiles; k += blockDim.x) {
+    // (few pairs are shared out by number: the search takes 2 us)
+    const long long total = (long long)n_tiles * blocks;
+    const bool few = total <= 2 * (long long)gridDim.x;
+    for (int k = 0; k < n_tiles && !few; k += blockDim.x) {
         const int i = k + threadIdx.x;
         const long long before = i < n_tiles ? (long long)a.p.tiles[i].w * blocks : cost + 1;
         tile0 += __syncthreads_count(before <= from_cost);
@@ -474,8 +477,8 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             (unsigned)(to - (long long)q.w * blocks) / (unsigned)tile_cost(q.x == a.L, q.z);
         return (long long)tile * blocks + min(block, (unsigned)blocks);
     };
-    long long at = place(tile0, from_cost);
-    const long long end = place(tile1, to_cost);
+    long long at = few ? total * blockIdx.x / gridDim.x : place(tile0, from_cost);
+    const long long end = few ? total * (blockIdx.x + 1) / gridDim.x : place(tile1, to_cost);
     if (at >= end)
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;

@@ -12,6 +12,12 @@
 // maximum reaches it are gone through again.  Candidates go into lists of 32, sorted
 // over a warp's lanes; a key is the value's order and the complement of its index, so
 // that ties go to the lowest index in whatever order they are met.
+// Bound by HBM in fp32 (2000 x 131072 with 20 alternatives 168 us, 92% of the measured
+// copy rate).  In 16 bits a value has half the bytes and the same arithmetic: 4096 x
+// 32003 bf16 take 48 us (81%) without alternatives, half of the issue slots used, 61 us
+// with 5 and 69 us with 32, whose search no loads of the block's own cover.  3 x 131072
+// fp32 with 20 alternatives: 9 us in two launches.  The gradient of 4096 x 131072 bf16
+// with an entropy term: 322 us (98% of the measured copy rate).
 #include <algorithm>
 
 #include "args.cuh"
@@ -435,12 +441,14 @@ __global__ void __launch_bounds__(kThreads) logprobs_join_kernel(LogprobArgs a)
 // Words of the longest row, whatever its address.
 int most_words(int V, int per) { return (V + per - 1 + per - 1) / per; }
 
-// Warps of a row: one where it has no more than eight chunks of words for every lane, so
-// that a row's joins are a warp's own.
-int row_warps(int V, int size)
+// Rows of at most eight chunks of words for every lane of a warp.
+bool short_row(int V, int size)
 {
-    return most_words(V, 16 / size) <= 32 * kWordsPerThread * 8 ? 1 : kRowWarps;
+    return most_words(V, 16 / size) <= 32 * kWordsPerThread * 8;
 }
+// Warps of a row: one for short rows, whose joins are the warp's own then (16000 x 4000
+// bf16 with 20 alternatives 145 to 59 us), unless there are too few to fill the SMs.
+int row_warps(int n, int V, int size) { return short_row(V, size) && n >= 4 * 152 ? 1 : kRowWarps; }
 
 // Blocks of a row: enough for a block on every SM four times over, each with a
 // load of kWordsPerThread words per thread.  Asks no device, since the workspace's size
@@ -450,7 +458,7 @@ int row_splits(int n, int V, int size)
     const int words = most_words(V, 16 / size), step = 32 * kRowWarps * kWordsPerThread;
     const int want = 4 * 152 / std::min(n, 4 * 152);
     const int most = (words + step - 1) / step;
-    return row_warps(V, size) == 1 ? 1 : std::max(1, std::min({want, most, kMaxSplits}));
+    return short_row(V, size) ? 1 : std::max(1, std::min({want, most, kMaxSplits}));
 }
 
 size_t key_offset(int n, int splits) { return ((size_t)n * splits * sizeof(float4) + 255) / 256 * 256; }
@@ -471,7 +479,7 @@ cudaError_t launch_rows(const LogprobArgs &a, cudaStream_t st)
 template <typename T, bool TOP>
 cudaError_t launch_top(const LogprobArgs &a, cudaStream_t st)
 {
-    cudaError_t e = row_warps(a.V, sizeof(T)) == 1 ? launch_rows<T, TOP, 1>(a, st)
+    cudaError_t e = row_warps(a.n, a.V, sizeof(T)) == 1 ? launch_rows<T, TOP, 1>(a, st)
                                                    : launch_rows<T, TOP, kRowWarps>(a, st);
     if (e == cudaSuccess && a.splits > 1)
         e = launch_pdl(logprobs_join_kernel<T, TOP>, dim3(a.n), dim3(kThreads), 0, st, a);
