@@ -124,9 +124,12 @@ __host__ __device__ constexpr int row_blocks(int r) { return (r + kBlk - 1) / kB
 // A multi-stage contraction: fetch(i, stage) starts the copies of step i, multiply(stage,
 // first) issues its products in one elected thread.  Copies of the steps ahead are under
 // way while a step is multiplied; a stage is filled again when its products are done.
+// `turn` contractions of as many steps went before it in the CTA.
 template <int S, typename F, typename M>
-__device__ __forceinline__ void contract(const Tensor &t, int steps, F fetch, M multiply)
+__device__ __forceinline__ void contract(const Tensor &t, int steps, int turn, F fetch, M multiply)
 {
+    // uses of a stage's barrier in front of step i
+    const auto use = [&](int i) { return turn * ((steps - i % S + S - 1) / S) + i / S; };
 #pragma unroll
     for (int i = 0; i < S - 1; i++) {
         if (i < steps)
@@ -149,7 +152,7 @@ __device__ __forceinline__ void contract(const Tensor &t, int steps, F fetch, M 
         const int before = stage == 0 ? S - 1 : stage - 1;
         if (i + S - 1 < steps) {
             if (i > 0)
-                tensor_wait(t, before, (i - 1) / S);
+                tensor_wait(t, before, use(i - 1));
             fetch(i + S - 1, before);
         }
         commit_copies();
@@ -157,7 +160,7 @@ __device__ __forceinline__ void contract(const Tensor &t, int steps, F fetch, M 
     }
     wait_copies<0>();
     if (steps > 0)
-        tensor_wait(t, (steps - 1) % S, (steps - 1) / S);
+        tensor_wait(t, (steps - 1) % S, use(steps - 1));
     tc_fence_after();
 }
 
@@ -306,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
         for (int k = 0; k < 4; k++)
             umma_ss(t.tmem, da + 2 * k, db + (BY_ROW ? 128 : 2) * k, idesc, !first || k);
     };
-    contract<kShrinkStages>(t, end - begin, fetch, multiply);
+    contract<kShrinkStages>(t, end - begin, 0, fetch, multiply);
     const bool failed = *t.gave_up;
     const int at = 32 * warp + lane, place = tile.y + at;
     if (warp < 4) {
@@ -742,7 +745,7 @@ struct OuterArgs {
     AdapterPlan p;
     OuterSide a, b;         // dA [L][r][K] from x and u, dB [L][N][r] from dy and h
     const float *scale;
-    int L, r, splits;
+    int L, r, splits, turns;    // turns: blocks of a CTA, one after another
     float *part;            // [splits][L][blocks of both][kCols][PAD]
     unsigned *tickets;      // [L][blocks of both]
 };
@@ -782,10 +785,8 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
     __shared__ int toks[kOuterList * kBlk];
     __shared__ int last;
     pdl_wait();
-    const bool of_a = (int)blockIdx.x < a.a.blocks;
-    const OuterSide &o = of_a ? a.a : a.b;
-    const int c0 = kCols * (of_a ? blockIdx.x : blockIdx.x - a.a.blocks);
-    const int adapter = blockIdx.y, split = blockIdx.z;
+    const int adapter = blockIdx.y, split = blockIdx.z, all_blocks = a.a.blocks + a.b.blocks;
+    const int first = blockIdx.x * a.turns, stop = min(first + a.turns, all_blocks);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lo = a.p.off[adapter], count = a.p.off[adapter + 1] - lo;
     const int all = (count + kBlk - 1) / kBlk;
@@ -795,9 +796,12 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
     const float scale = a.scale ? a.scale[adapter] : 1.f;
     if (count == 0) {
         const float zero[16] = {};
-        if (split == 0 && warp < 4)
+        for (int blk = first; blk < stop && split == 0 && warp < 4; blk++) {
+            const bool of_a = blk < a.a.blocks;
             for (int k = 0; k < PAD; k += 16)
-                put_outer<T>(a, o, of_a, adapter, c0 + c, k, zero);
+                put_outer<T>(a, of_a ? a.a : a.b, of_a, adapter,
+                             kCols * (of_a ? blk : blk - a.a.blocks) + c, k, zero);
+        }
         return;
     }
     constexpr uint32_t cols = tmem_cols(PAD);
@@ -808,118 +812,126 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
     using V = Rows<PAD / 8, kBlk>;
     const X xr(128 * kBlk);
     const V vr(128 * kBlk);
-    const uint16_t *src = o.src + c0 + 8 * xr.chunk;
-    const bool whole = o.vec && c0 + kCols <= o.C;
-    const int rank_bytes = 8 * vr.chunk < a.r ? 16 : 0;     // 0 for the ranks behind the last
-    const uint16_t *ranks = rank_bytes ? o.v + 8 * vr.chunk : o.v;
-    const auto fetch = [&](int i, int stage) {
-        const int s0 = (begin + i) * kBlk;
-        if (i % kOuterList == 0) {      // the list that the next steps take their tokens from
-            for (int j = threadIdx.x; j < kOuterList * kBlk; j += kThreads)
-                toks[j] = s0 + j < count ? a.p.perm[lo + s0 + j] : -1;
-            __syncthreads();
-        }
-        const int *list = toks + i % kOuterList * kBlk;
-        const uint32_t xs = smem + stage * stage_bytes + xr.at;
-        const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk) + vr.at;
-        if (whole && s0 + kBlk <= count) {
+    for (int blk = first; blk < stop; blk++) {
+        const bool of_a = blk < a.a.blocks;
+        const OuterSide &o = of_a ? a.a : a.b;
+        const int c0 = kCols * (of_a ? blk : blk - a.a.blocks);
+        const uint16_t *src = o.src + c0 + 8 * xr.chunk;
+        const bool whole = o.vec && c0 + kCols <= o.C;
+        const int rank_bytes = 8 * vr.chunk < a.r ? 16 : 0;     // 0 for the ranks behind the last
+        const uint16_t *ranks = rank_bytes ? o.v + 8 * vr.chunk : o.v;
+        const auto fetch = [&](int i, int stage) {
+            const int s0 = (begin + i) * kBlk;
+            if (i % kOuterList == 0) {      // the list that the next steps take their tokens from
+                for (int j = threadIdx.x; j < kOuterList * kBlk; j += kThreads)
+                    toks[j] = s0 + j < count ? a.p.perm[lo + s0 + j] : -1;
+                __syncthreads();
+            }
+            const int *list = toks + i % kOuterList * kBlk;
+            const uint32_t xs = smem + stage * stage_bytes + xr.at;
+            const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk) + vr.at;
+            if (whole && s0 + kBlk <= count) {
 #pragma unroll
-            for (int j = 0; j < X::kPasses; j++)
-                copy16(xs + X::kNext * j, src + list[xr.row + X::kPass * j] * o.ld, 16);
-        } else {                        // 0 behind the last token
+                for (int j = 0; j < X::kPasses; j++)
+                    copy16(xs + X::kNext * j, src + list[xr.row + X::kPass * j] * o.ld, 16);
+            } else {                        // 0 behind the last token
 #pragma unroll 1
-            for (int j = 0; j < X::kPasses; j++) {
-                const int tok = list[xr.row + X::kPass * j];
-                fetch8(xs + X::kNext * j, o.src + max(tok, 0) * o.ld, c0 + 8 * xr.chunk,
-                       tok >= 0 ? o.C : 0, o.vec);
+                for (int j = 0; j < X::kPasses; j++) {
+                    const int tok = list[xr.row + X::kPass * j];
+                    fetch8(xs + X::kNext * j, o.src + max(tok, 0) * o.ld, c0 + 8 * xr.chunk,
+                           tok >= 0 ? o.C : 0, o.vec);
+                }
             }
-        }
-        if (!vr.on)
-            return;
-        if (of_a) {
-            const uint16_t *v = ranks + (long long)(lo + s0 + vr.row) * 2 * PAD;
+            if (!vr.on)
+                return;
+            if (of_a) {
+                const uint16_t *v = ranks + (long long)(lo + s0 + vr.row) * 2 * PAD;
 #pragma unroll
-            for (int j = 0; j < V::kPasses; j++) {
-                const bool in = rank_bytes && s0 + vr.row + V::kPass * j < count;
-                const uint16_t *p = in ? v + V::kPass * 2 * PAD * j : o.v;
-                copy16(vs + V::kNext * j, p, in ? 16 : 0);
-                copy16(vs + V::kNext * j + part_bytes, in ? p + PAD : p, in ? 16 : 0);
+                for (int j = 0; j < V::kPasses; j++) {
+                    const bool in = rank_bytes && s0 + vr.row + V::kPass * j < count;
+                    const uint16_t *p = in ? v + V::kPass * 2 * PAD * j : o.v;
+                    copy16(vs + V::kNext * j, p, in ? 16 : 0);
+                    copy16(vs + V::kNext * j + part_bytes, in ? p + PAD : p, in ? 16 : 0);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < V::kPasses; j++) {
+                    const int tok = list[vr.row + V::kPass * j];
+                    copy16(vs + V::kNext * j, ranks + (long long)max(tok, 0) * a.r,
+                           tok >= 0 ? rank_bytes : 0);
+                }
             }
-        } else {
+        };
+        constexpr uint32_t idesc =
+            (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
+            ((uint32_t)(PAD >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
+        const auto multiply = [&](int stage, bool first) {
+            const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * kBlk * (kCols / kBlk);
+            const uint64_t da = sw128_desc_mn(at, 128 * kBlk);
+            for (int part = 0; part < (of_a ? 2 : 1); part++) {
+                const uint64_t db = sw128_desc_mn(vs + part * part_bytes, 128 * kBlk);
 #pragma unroll
-            for (int j = 0; j < V::kPasses; j++) {
-                const int tok = list[vr.row + V::kPass * j];
-                copy16(vs + V::kNext * j, ranks + (long long)max(tok, 0) * a.r,
-                       tok >= 0 ? rank_bytes : 0);
+                for (int k = 0; k < kBlk / 16; k++)
+                    umma_ss(t.tmem, da + 128 * k, db + 128 * k, idesc, !first || part || k);
             }
-        }
-    };
-    constexpr uint32_t idesc =
-        (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
-        ((uint32_t)(PAD >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
-    const auto multiply = [&](int stage, bool first) {
-        const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * kBlk * (kCols / kBlk);
-        const uint64_t da = sw128_desc_mn(at, 128 * kBlk);
-        for (int part = 0; part < (of_a ? 2 : 1); part++) {
-            const uint64_t db = sw128_desc_mn(vs + part * part_bytes, 128 * kBlk);
-#pragma unroll
-            for (int k = 0; k < kBlk / 16; k++)
-                umma_ss(t.tmem, da + 128 * k, db + 128 * k, idesc, !first || part || k);
-        }
-    };
-    contract<kOuterStages>(t, steps, fetch, multiply);
-    const bool failed = *t.gave_up;
-    const int block = adapter * (a.a.blocks + a.b.blocks) + blockIdx.x;
-    const long long slots = (long long)a.L * (a.a.blocks + a.b.blocks);
-    if (warp < 4)
+        };
+        if (blk > first)
+            __syncthreads();        // the list of tokens is taken again
+        contract<kOuterStages>(t, steps, blk - first, fetch, multiply);
+        const bool failed = *t.gave_up;
+        const int block = adapter * all_blocks + blk;
+        const long long slots = (long long)a.L * all_blocks;
+        if (warp < 4)
 #pragma unroll 1
-        for (int k = 0; k < PAD; k += 16) {
-            float v[16];
-            tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + k, v);
-#pragma unroll
-            for (int e = 0; e < 16; e++)
-                v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
-            if (a.splits == 1) {
+            for (int k = 0; k < PAD; k += 16) {
+                float v[16];
+                tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + k, v);
 #pragma unroll
                 for (int e = 0; e < 16; e++)
-                    v[e] *= scale;
-                put_outer<T>(a, o, of_a, adapter, c0 + c, k, v);
-                continue;
+                    v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
+                if (a.splits == 1) {
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        v[e] *= scale;
+                    put_outer<T>(a, o, of_a, adapter, c0 + c, k, v);
+                    continue;
+                }
+                float4 *p = reinterpret_cast<float4 *>(
+                    a.part + ((split * slots + block) * kCols + c) * PAD + k);
+#pragma unroll
+                for (int q = 0; q < 4; q++)
+                    p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             }
-            float4 *p = reinterpret_cast<float4 *>(
-                a.part + ((split * slots + block) * kCols + c) * PAD + k);
+        tc_fence_before();          // the next block's products write where this one's were read
+        if (a.splits == 1)
+            continue;
+        __threadfence();
+        __syncthreads();
+        if (threadIdx.x == 0)
+            last = atomicAdd(a.tickets + block, 1u) == a.splits - 1u;
+        __syncthreads();
+        if (!last)
+            continue;
+        __threadfence();
+        for (int i = threadIdx.x; i < kCols * (PAD / 16); i += kThreads) {
+            const int col = i % kCols, k = i / kCols * 16;
+            float v[16] = {};
+            for (int s = 0; s < a.splits; s++) {
+                const float4 *p = reinterpret_cast<const float4 *>(
+                    a.part + ((s * slots + block) * kCols + col) * PAD + k);
 #pragma unroll
-            for (int q = 0; q < 4; q++)
-                p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-        }
-    tensor_end(t, cols);
-    if (a.splits == 1)
-        return;
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0)
-        last = atomicAdd(a.tickets + block, 1u) == a.splits - 1u;
-    __syncthreads();
-    if (!last)
-        return;
-    __threadfence();
-    for (int i = threadIdx.x; i < kCols * (PAD / 16); i += kThreads) {
-        const int col = i % kCols, k = i / kCols * 16;
-        float v[16] = {};
-        for (int s = 0; s < a.splits; s++) {
-            const float4 *p = reinterpret_cast<const float4 *>(
-                a.part + ((s * slots + block) * kCols + col) * PAD + k);
-#pragma unroll
-            for (int q = 0; q < 4; q++) {
-                const float4 d = __ldcg(p + q);
-                v[4 * q] += d.x, v[4 * q + 1] += d.y, v[4 * q + 2] += d.z, v[4 * q + 3] += d.w;
+                for (int q = 0; q < 4; q++) {
+                    const float4 d = __ldcg(p + q);
+                    v[4 * q] += d.x, v[4 * q + 1] += d.y, v[4 * q + 2] += d.z, v[4 * q + 3] += d.w;
+                }
             }
-        }
 #pragma unroll
-        for (int e = 0; e < 16; e++)
-            v[e] *= scale;
-        put_outer<T>(a, o, of_a, adapter, c0 + col, k, v);
+            for (int e = 0; e < 16; e++)
+                v[e] *= scale;
+            put_outer<T>(a, o, of_a, adapter, c0 + col, k, v);
+        }
     }
+    tensor_end(t, cols);
 }
 
 // ---------------------------------------------------------------- host
@@ -1008,8 +1020,15 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
     if (c.dB)
         o.b = {half_words(c.dy), c.lddy, vec_rows(c.dy, c.lddy, c.n), c.N,
                (c.N + kCols - 1) / kCols, half_words(c.h), static_cast<uint16_t *>(c.dB)};
+    // Several blocks a CTA once they fill the SMs' two places eight times: few tokens each, so
+    // that a CTA's start weighs.  Measured, one block a CTA against this: 64 adapters of 4096 x
+    // 4096, 500 tokens (rank 16) 82 and 72 us, 8192 tokens (rank 32) 144 and 137; 256 adapters
+    // of 2048 x 2048, 9000 tokens (rank 16) 166 and 137.  With fewer than eight, unequal
+    // adapters end apart: the second takes 148.
+    const int blocks = o.a.blocks + o.b.blocks;
+    o.turns = std::max(1, (int)std::min(8LL, (long long)blocks * c.L / (8 * c.sms)));
     return launch_wide(adapter_outer_kernel<T, PAD>,
-                       dim3(o.a.blocks + o.b.blocks, c.L, o.splits),
+                       dim3((blocks + o.turns - 1) / o.turns, c.L, o.splits),
                        kOuterStages * kOuterStage<PAD> + kSmemSlack, st, o);
 }
 

@@ -175,6 +175,18 @@ def test_tokens_in_any_order_get_the_same_rows():
     assert torch.equal(o2, out[p]) and torch.equal(h2, h[p])
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,cols,rows,rank,count", [(2500, 777, 900, 24, 700),
+                                                    (1900, 1024, 1000, 8, 1024),
+                                                    (4000, 896, 520, 72, 400)])
+def test_many_adapters_of_unequal_size(n, cols, rows, rank, count, dtype):
+    # from one to several hundred tokens an adapter, many of them with none
+    c, wide = case(n, cols, rows, rank, count, dtype)
+    g = torch.Generator(device="cuda").manual_seed(n)
+    c["ids"] = (torch.rand(n, device="cuda", generator=g) ** 6 * (count + 3)).int() - 1
+    check(c, wide)
+
+
 def test_offsets_beyond_32_bits():
     moe = _moe()
     n, rows = 70000, 32768
