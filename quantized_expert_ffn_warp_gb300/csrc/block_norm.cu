@@ -18,12 +18,15 @@
 // one partial row per kRun rows and CTA, added by a second kernel in a fixed order.
 // Measured: 16001 x 4096 bf16 with a gate per token 84 us (92% of the measured copy rate),
 // its gradients for 16384 x 4096 137 us (87%, half of the issue slots used); 4000 x 16384
-// 97 and 269 us (80% and 43%: the gradients of more than 8192 columns keep their sums in
-// shared memory and load no row ahead).
+// 97 and 184 us (80% and 63%).  More than 8192 columns of the gradient take a cluster of two
+// CTAs.  One CTA of four words a thread, its sums in shared memory and no row ahead: 269 us.
+// A cluster's barrier in place of the counted stores, which waits for dresid's stores too:
+// 240 us; four CTAs of 256 threads: 310 us.
 #include <algorithm>
 
 #include "args.cuh"
 #include "vec.cuh"
+#include "w4.cuh"
 
 namespace qe {
 
@@ -210,21 +213,65 @@ struct NormGradArgs {
     float *dgain, *dgate_ch, *dnext_gain;
 };
 
-// Rows of four words a thread have their column sums in shared memory, where registers
-// hold no more than two words', and the shared vectors are read from L2 instead.
+// A row's columns belong to CTAS of a cluster, two words for each thread: a wide row's column
+// sums, shared vectors and next loads would not fit one CTA's registers.
+struct RowSums {
+    float4 part[2][kMaxWarps / 4];
+    unsigned long long bar[2];
+    int gave_up;
+};
+// Sum over the cluster, number `turn`, a row's first or second, in the same order in all
+// CTAs.  Each warp sends its sum to every CTA and goes on when all of them have arrived.  The
+// two buffers take turns: a warp that sends sum i + 2 has sum i + 1 of every warp, which read
+// sum i before.
+template <int CTAS>
+__device__ __forceinline__ float sum_row(float v, RowSums &sm, bool second, int turn, int warps,
+                                         int rank)
+{
+    if constexpr (CTAS == 1)
+        return sum_block(v, sm.part[second], warps);
+    float4 *part = sm.part[turn & 1];
+    constexpr int kEach = kMaxWarps / CTAS;
+    const uint32_t bar = saddr(&sm.bar[turn & 1]);
+    const int lane = threadIdx.x & 31;
+    v = sum_warp(v);
+    if (threadIdx.x == 0)
+        bar_expect_tx(bar, CTAS * warps * sizeof(float));
+    if (lane < CTAS) {      // each lane to one of the CTAs
+        const float *mine = reinterpret_cast<float *>(part) + rank * kEach + (threadIdx.x >> 5);
+        st_async(cluster_addr(saddr(mine), lane), v, cluster_addr(bar, lane));
+    }
+    if (!bar_wait(bar, turn >> 1 & 1, &sm.gave_up)) {
+        sm.gave_up = 1;
+        return NAN;
+    }
+    float s = 0.f;
+#pragma unroll
+    for (int r = 0; r < CTAS; r++) {
+        const float4 *p = part + r * (kEach / 4);
+        for (int w = 0; w < warps; w += 4) {
+            const float4 q = p[w / 4];
+            s += (q.x + (w + 1 < warps ? q.y : 0.f)) +
+                 ((w + 2 < warps ? q.z : 0.f) + (w + 3 < warps ? q.w : 0.f));
+        }
+    }
+    return s;
+}
+
 // The statistics' products out r2 and y r1 are formed again after each reduction, since
 // their packed words take a quarter of the registers.
-template <typename T, int V>
+template <typename T, int CTAS>
 __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(NormGradArgs a)
 {
-    constexpr bool kAhead = V <= 2, kRegs = V <= 2;
+    constexpr int V = 2;
     extern __shared__ float4 shared[];  // [2][2 V][threads]
-    __shared__ float4 part[2][kMaxWarps / 4];
+    __shared__ RowSums sums;
     pdl_enter();
-    const int warps = blockDim.x / 32;
-    // the vectors that all rows share, or the column sums
+    const int warps = blockDim.x / 32, rank = blockIdx.x % CTAS;
+    const int share = (a.vecs + CTAS - 1) / CTAS, vec0 = rank * share;
+    const int vecs = min(share, a.vecs - vec0), col0 = 8 * vec0;
+    const long long step = gridDim.x / CTAS;
     Shared weight{shared + threadIdx.x}, next_gain{shared + 2 * V * blockDim.x + threadIdx.x};
-    Shared &sum1 = weight, &sum2 = next_gain;
     const T *token_gate = a.token_gate ? static_cast<const T *>(a.gate) : nullptr;
     uint4 dq[V], nq[V], oq[V], yq[V];
 #pragma unroll
@@ -232,105 +279,61 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(Norm
         dq[i] = nq[i] = oq[i] = yq[i] = make_uint4(0, 0, 0, 0);
     const auto load = [&](long long t) {
         if (a.dout)
-            load_row<V>(dq, a.dout, t * a.ld_dout, a.vecs);
+            load_row<V>(dq, a.dout, t * a.ld_dout + col0, vecs);
         if (a.dxn) {
-            load_row<V>(nq, a.dxn, t * a.ld_dxn, a.vecs);
-            load_row<V>(oq, a.out, t * a.ld_out, a.vecs);
+            load_row<V>(nq, a.dxn, t * a.ld_dxn + col0, vecs);
+            load_row<V>(oq, a.out, t * a.ld_out + col0, vecs);
         }
-        load_row<V>(yq, a.y, t * a.ld_y, a.vecs);
+        load_row<V>(yq, a.y, t * a.ld_y + col0, vecs);
     };
-    long long t = blockIdx.x;
+    long long t = blockIdx.x / CTAS;
     load(t);
-    const void *channel_gate = a.token_gate ? nullptr : a.gate;
-    if (kRegs) {
-        weight.load<T, V>(a.gain, channel_gate, a.vecs);
-        next_gain.load<T, V>(a.next_gain, nullptr, a.vecs);
-    }
-    const auto vector = [&](const Shared &sm, int i, const void *base, const void *by, F2(&d)[4]) {
-        if constexpr (kRegs) {
-            sm.get(i, d);
-        } else {
-            const int v = threadIdx.x + i * blockDim.x;
-            F2 f[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                d[e] = f[e] = f2(1.f);
-            if (base && v < a.vecs)
-                unpack<T>(*(static_cast<const uint4 *>(base) + v), d);
-            if (by && v < a.vecs)
-                unpack<T>(*(static_cast<const uint4 *>(by) + v), f);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
-                d[e] = mul(d[e], f[e]);
-        }
+    const auto columns = [&](const void *base) {
+        return base ? static_cast<const T *>(base) + col0 : nullptr;
     };
-    constexpr int R = kRegs ? V : 1;
-    F2 s1[R][4], s2[R][4];      // the column sums
+    weight.load<T, V>(columns(a.gain), columns(a.token_gate ? nullptr : a.gate), vecs);
+    next_gain.load<T, V>(columns(a.next_gain), nullptr, vecs);
+    if constexpr (CTAS > 1) {       // the other CTAs run: their memory may be written
+        if (threadIdx.x == 0) {
+            sums.gave_up = 0;
+            bar_init(saddr(&sums.bar[0]), 1);
+            bar_init(saddr(&sums.bar[1]), 1);
+            asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        }
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
+    F2 s1[V][4], s2[V][4];      // the column sums
     const auto clear = [&]() {
 #pragma unroll
         for (int i = 0; i < V; i++)
-            if constexpr (kRegs) {
-#pragma unroll
-                for (int e = 0; e < 4; e++)
-                    s1[i][e] = s2[i][e] = f2(0.f);
-            } else if (a.sums) {
-                const float zero[4] = {};
-#pragma unroll
-                for (int j = 0; j < 2; j++) {
-                    sum1.put(2 * i + j, zero);
-                    sum2.put(2 * i + j, zero);
-                }
-            }
-    };
-    const auto accumulate = [&](F2(&regs)[R][4], Shared &sm, int i, const F2(&c)[4], F2 by) {
-        if constexpr (kRegs) {
 #pragma unroll
             for (int e = 0; e < 4; e++)
-                regs[i][e] = fma(c[e], by, regs[i][e]);
-        } else if (a.sums) {
-            F2 d[4];
-            sm.get(i, d);
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                const float2 x = split(fma(c[2 * j], by, d[2 * j]));
-                const float2 y = split(fma(c[2 * j + 1], by, d[2 * j + 1]));
-                const float v[4] = {x.x, x.y, y.x, y.y};
-                sm.put(2 * i + j, v);
-            }
-        }
+                s1[i][e] = s2[i][e] = f2(0.f);
     };
     clear();
     const auto flush = [&](int run) {
-        float *p = a.part + ((long long)blockIdx.x * a.runs + run) * a.H;
-        float *q = p + (long long)gridDim.x * a.runs * a.H;
+        float *p = a.part + (blockIdx.x / CTAS * (long long)a.runs + run) * a.H + col0;
+        float *q = p + step * a.runs * a.H;
 #pragma unroll
         for (int i = 0; i < V; i++) {
             const int v = threadIdx.x + i * blockDim.x;
-            if (v >= a.vecs)
+            if (v >= vecs)
                 continue;
-            F2 w[2][4];
-            if constexpr (kRegs) {
 #pragma unroll
-                for (int e = 0; e < 4; e++) {
-                    w[0][e] = s1[i][e];
-                    w[1][e] = s2[i][e];
-                }
-            } else {
-                sum1.get(i, w[0]);
-                sum2.get(i, w[1]);
+            for (int j = 0; j < 2; j++) {
+                *reinterpret_cast<ulonglong2 *>(p + 8 * v + 4 * j) =
+                    make_ulonglong2(s1[i][2 * j].v, s1[i][2 * j + 1].v);
+                *reinterpret_cast<ulonglong2 *>(q + 8 * v + 4 * j) =
+                    make_ulonglong2(s2[i][2 * j].v, s2[i][2 * j + 1].v);
             }
-#pragma unroll
-            for (int k = 0; k < 2; k++)
-#pragma unroll
-                for (int j = 0; j < 2; j++)
-                    *reinterpret_cast<ulonglong2 *>((k ? q : p) + 8 * v + 4 * j) =
-                        make_ulonglong2(w[k][2 * j].v, w[k][2 * j + 1].v);
         }
         clear();
     };
-    const F2 one = f2(1.f), scale = f2(a.scale);
-    int rows = 0, run = 0;
-    for (; t < a.n; t += gridDim.x) {
+    const F2 scale = f2(a.scale);
+    int rows = 0, run = 0, turn = 0;
+    for (; t < a.n; t += step) {
         const float2 st = a.stats[t];
         const float tg = token_gate ? to_float<T>(token_gate[t]) : 1.f;
         const F2 r1 = f2(st.x), r2 = f2(st.y);
@@ -339,26 +342,26 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(Norm
         F2 m = f2(0.f);
 #pragma unroll
         for (int i = 0; i < V; i++) {
-            F2 x[4], n[4], g[4], c[4];
+            F2 x[4], n[4], g[4];
             unpack<T>(dq[i], d[i]);
             unpack<T>(oq[i], n);
             unpack<T>(nq[i], x);
-            vector(next_gain, i, a.next_gain, nullptr, g);
+            next_gain.get(i, g);
             ok[i] = oq[i];
             yk[i] = yq[i];
 #pragma unroll
             for (int e = 0; e < 4; e++) {
-                c[e] = mul(x[e], mul(n[e], r2));
-                m = fma(c[e], g[e], m);
+                const F2 c = mul(x[e], mul(n[e], r2));
+                m = fma(c, g[e], m);
                 // do without its mean's part
                 d[i][e] = fma(r2, mul(x[e], g[e]), d[i][e]);
+                s2[i][e] = add(s2[i][e], c);
             }
-            accumulate(s2, sum2, i, c, one);
         }
-        if (kAhead && t + gridDim.x < a.n)
-            load(t + gridDim.x);
+        if (t + step < a.n)
+            load(t + step);
         const float mean =
-            a.dxn ? sum_block(sum(m), part[0], warps) * a.inv_h * st.y : 0.f;
+            a.dxn ? sum_row<CTAS>(sum(m), sums, false, turn++, warps, rank) * a.inv_h * st.y : 0.f;
         const F2 minus = f2(-mean), gate = f2(tg);
         m = f2(0.f);
 #pragma unroll
@@ -366,54 +369,55 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(Norm
             F2 n[4], z[4], w[4];
             unpack<T>(ok[i], n);
             unpack<T>(yk[i], z);
-            vector(weight, i, a.gain, channel_gate, w);
+            weight.get(i, w);
 #pragma unroll
             for (int e = 0; e < 4; e++) {
                 d[i][e] = fma(mul(n[e], r2), minus, d[i][e]);
                 z[e] = mul(d[i][e], mul(z[e], r1));
                 m = fma(z[e], w[e], m);
-            }
-            accumulate(s1, sum1, i, z, gate);
-#pragma unroll
-            for (int e = 0; e < 4; e++)
+                s1[i][e] = fma(z[e], gate, s1[i][e]);
                 n[e] = mul(d[i][e], scale);
+            }
             const int v = threadIdx.x + i * blockDim.x;
-            if (v < a.vecs)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dresid) + t * a.ld_dresid + 8 * v) =
-                    pack<T>(n);
+            if (v < vecs)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dresid) + t * a.ld_dresid + col0 +
+                                           8 * v) = pack<T>(n);
         }
         // sum of do gain gate z, the gate of a token left out
-        const float dot = sum_block(sum(m), part[1], warps);
+        const float dot = sum_row<CTAS>(sum(m), sums, true, turn++, warps, rank);
         const F2 back = f2(-dot * tg * a.inv_h * st.x), f = f2(st.x * tg);
 #pragma unroll
         for (int i = 0; i < V; i++) {
             F2 z[4], w[4];
             unpack<T>(yk[i], z);
-            vector(weight, i, a.gain, channel_gate, w);
+            weight.get(i, w);
 #pragma unroll
             for (int e = 0; e < 4; e++)
                 z[e] = a.gain ? fma(mul(z[e], r1), back, mul(mul(d[i][e], f), w[e]))
                               : mul(mul(d[i][e], f), w[e]);
             const int v = threadIdx.x + i * blockDim.x;
-            if (v < a.vecs)
-                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dy) + t * a.ld_dy + 8 * v) =
+            if (v < vecs)
+                *reinterpret_cast<uint4 *>(static_cast<T *>(a.dy) + t * a.ld_dy + col0 + 8 * v) =
                     pack<T>(z);
         }
-        if (token_gate && a.dgate && threadIdx.x == 0)
+        if (token_gate && a.dgate && rank == 0 && threadIdx.x == 0)
             a.dgate[t] = dot;
         if (a.sums && ++rows == kRun) {
             flush(run++);
             rows = 0;
         }
-        if (!kAhead && t + gridDim.x < a.n)
-            load(t + gridDim.x);
-        if (warps > 1 && !a.dxn)
+        if (CTAS == 1 && warps > 1 && !a.dxn)
             __syncthreads();        // one buffer alone is in use
     }
     // runs that this CTA has no rows for are zeros
     if (a.sums)
         for (; run < a.runs; run++)
             flush(run);
+    if constexpr (CTAS > 1) {       // no CTA ends before the others' last sums have left
+        __syncwarp();
+        cluster_arrive();
+        cluster_wait();
+    }
 }
 
 // Column sums over the partial rows: 32 columns a CTA, 32 chains each.
@@ -451,17 +455,20 @@ __global__ void __launch_bounds__(1024) residual_norm_sums_kernel(NormGradArgs a
         a.dgate_ch[col] = a.gain ? s * to_float<T>(static_cast<const T *>(a.gain)[col]) : s;
 }
 
-// Threads of a row: two words each, four for the widest.
-int row_words(int H) { return H > 16 * kMaxThreads ? 4 : 2; }
+// CTAs of a row of the gradient, and threads of each, with two words a thread.
+int row_ctas(int H) { return H > 16 * kMaxThreads ? 2 : 1; }
 int row_threads(int H)
 {
-    const int per = 8 * row_words(H);
+    const int per = 16 * row_ctas(H);
     return ((H + per - 1) / per + 31) / 32 * 32;
 }
 
-// CTAs of the gradient: as many as run at once on 152 SMs with 128 registers a
+// Rows of the gradient at once: as many as run on 152 SMs with 128 registers a
 // thread.  The workspace's size follows from it, so it asks no device.
-int grad_blocks(int n, int H) { return std::min(n, 152 * std::max(1, 512 / row_threads(H))); }
+int grad_blocks(int n, int H)
+{
+    return std::min(n, 152 * std::max(1, 512 / row_threads(H)) / row_ctas(H));
+}
 int grad_runs(int n, int H)
 {
     const int rows = (n + grad_blocks(n, H) - 1) / grad_blocks(n, H);
@@ -472,25 +479,22 @@ size_t grad_ws(int n, int H)
     return 2 * sizeof(float) * (size_t)grad_blocks(n, H) * grad_runs(n, H) * H;
 }
 
-// Shared memory of `vectors` vectors of a block's columns.
-int shared_bytes(int H, int vectors)
-{
-    return (int)sizeof(float4) * 2 * row_words(H) * row_threads(H) * vectors;
-}
+// Shared memory of a thread: its part of two vectors.
+constexpr int kThreadBytes = 2 * 4 * (int)sizeof(float4);
 
 template <typename T, int MAX>
 cudaError_t launch_norm_as(const NormArgs &a, int sms, cudaStream_t st)
 {
     const int threads = ((a.H + 15) / 16 + 31) / 32 * 32;   // two words a thread
-    constexpr int smem = 2 * 4 * (int)sizeof(float4);       // two vectors, a thread's part
     const cudaError_t e = cudaFuncSetAttribute(residual_norm_kernel<T, MAX>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               smem * MAX);
+                                               kThreadBytes * MAX);
     if (e != cudaSuccess)
         return e;
     // as many CTAs as run at once
     const dim3 grid(std::min(a.n, sms * std::max(1, 1024 / threads)));
-    return launch_pdl(residual_norm_kernel<T, MAX>, grid, dim3(threads), smem * threads, st, a);
+    return launch_pdl(residual_norm_kernel<T, MAX>, grid, dim3(threads), kThreadBytes * threads,
+                      st, a);
 }
 template <typename T>
 cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t st)
@@ -499,22 +503,34 @@ cudaError_t launch_norm(const NormArgs &a, int sms, cudaStream_t st)
                                    : launch_norm_as<T, 1024>(a, sms, st);
 }
 
-template <typename T, int V>
+template <typename T, int CTAS>
 cudaError_t launch_norm_grad_as(const NormGradArgs &a, cudaStream_t st)
 {
-    const cudaError_t e = cudaFuncSetAttribute(
-        residual_norm_grad_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-        shared_bytes(V > 2 ? kMaxWidth : kMaxWidth / 2, 2));
+    const cudaError_t e = cudaFuncSetAttribute(residual_norm_grad_kernel<T, CTAS>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kThreadBytes * kMaxThreads);
     if (e != cudaSuccess)
         return e;
-    return launch_pdl(residual_norm_grad_kernel<T, V>, dim3(grad_blocks(a.n, a.H)),
-                      dim3(row_threads(a.H)), shared_bytes(a.H, V > 2 && !a.sums ? 0 : 2), st, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(CTAS * grad_blocks(a.n, a.H));
+    cfg.blockDim = dim3(row_threads(a.H));
+    cfg.dynamicSmemBytes = kThreadBytes * row_threads(a.H);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CTAS;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CTAS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, residual_norm_grad_kernel<T, CTAS>, a);
 }
 template <typename T>
 cudaError_t launch_norm_grad(const NormGradArgs &a, cudaStream_t st)
 {
-    cudaError_t e = row_words(a.H) == 2 ? launch_norm_grad_as<T, 2>(a, st)
-                                        : launch_norm_grad_as<T, 4>(a, st);
+    cudaError_t e = row_ctas(a.H) == 1 ? launch_norm_grad_as<T, 1>(a, st)
+                                       : launch_norm_grad_as<T, 2>(a, st);
     if (e == cudaSuccess && a.sums)
         e = launch_pdl(residual_norm_sums_kernel<T>, dim3((a.H + 31) / 32, a.dnext_gain ? 2 : 1),
                        dim3(1024), 0, st, a, grad_blocks(a.n, a.H) * a.runs);
@@ -640,7 +656,7 @@ extern "C" int moe_residual_norm_grad(const void *dout, long long ld_dout, const
                         flat_arg(dgain, H, 4, true),
                         flat_arg(dgate, gate_per_token ? n : H, 4, true),
                         flat_arg(dnext_gain, H, 4, true),
-                        rows_arg(need ? workspace : nullptr, 0, need / 4, 1, 4, 16, true)};
+                        flat_arg(need ? workspace : nullptr, need / 16, 16, true)};
     int dev, sms;
     if (const int bad = check_args(args, sizeof(args) / sizeof(args[0]), &dev, &sms))
         return bad;

@@ -236,6 +236,15 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank)
     return r;
 }
 
+// Stores to a shared address of the cluster; counted by barrier `bar` of the same CTA.
+__device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.f32 [%0], %1, [%2];" ::"r"(
+                     addr),
+                 "f"(v), "r"(bar)
+                 : "memory");
+}
+
 // A frozen 4-bit matrix in the canonical layout.
 struct W4Matrix {
     const uint8_t *codes;       // [rows][K/2]

@@ -81,6 +81,27 @@ def test_forward_and_gradient(n, hid, dtype, gate, gain, next_gain):
         check_grad(a, fwd, rows(1.0), None, 0.75)
 
 
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,hid", [(200, 8200), (1000, 12296), (305, 16384), (20000, 8200)])
+def test_gradient_of_wide_rows(n, hid, dtype):
+    """Many rows of two blocks each, with one sum a row and with two, on two streams."""
+    moe = _moe()
+    a, rows = batch(n, hid, dtype, n, "channel", pad=8)
+    fwd = check_forward(a, 0.75)
+    dout, dxn = rows(0.02), rows(0.02)
+    got = check_grad(a, fwd, dout, dxn, 0.75)
+    check_grad(a, fwd, dout, None, 0.75)
+    kw = dict(gain=a["gain"], gate=a["gate"], scale=0.75, next_gain=a["next_gain"])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    again = [moe.residual_norm_grad(dout, dxn, fwd["out"], a["y"], fwd["stats"], **kw, stream=s)
+             for _ in range(3) for s in streams]
+    torch.cuda.synchronize()
+    for r in again:
+        for k, v in got.items():
+            assert torch.equal(r[k], v), k
+
+
 @pytest.mark.parametrize("n,hid,pad", [(5, 520, 8), (33, 1024, 1032), (1, 64, 64)])
 def test_strided_rows_and_in_place(n, hid, pad):
     moe = _moe()
