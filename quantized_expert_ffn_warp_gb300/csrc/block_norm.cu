@@ -18,10 +18,11 @@
 // one partial row per kRun rows and CTA, added by a second kernel in a fixed order.
 // Measured: 16001 x 4096 bf16 with a gate per token 84 us (92% of the measured copy rate),
 // its gradients for 16384 x 4096 137 us (87%, half of the issue slots used); 4000 x 16384
-// 97 and 184 us (80% and 63%).  More than 8192 columns of the gradient take a cluster of two
+// 82 and 163 us (94% and 71%).  More than 8192 columns of the gradient take a cluster of two
 // CTAs.  One CTA of four words a thread, its sums in shared memory and no row ahead: 269 us.
-// A cluster's barrier in place of the counted stores, which waits for dresid's stores too:
-// 240 us; four CTAs of 256 threads: 310 us.
+// Every thread adding all warps' sums: 97 and 184 us; and with a cluster's barrier in place
+// of the counted stores, which waits for dresid's stores too, 240 us; four CTAs of 256
+// threads: 310 us.
 #include <algorithm>
 
 #include "args.cuh"
@@ -56,6 +57,10 @@ __device__ __forceinline__ float sum_block(float v, float4 *part, int warps)
     if ((threadIdx.x & 31) == 0)
         reinterpret_cast<float *>(part)[threadIdx.x >> 5] = v;
     __syncthreads();
+    if (warps > 8) {        // a lane for each: fewer instructions, a longer chain
+        const int lane = threadIdx.x & 31;
+        return sum_warp(lane < warps ? reinterpret_cast<const float *>(part)[lane] : 0.f);
+    }
     float s = 0.f;
     for (int w = 0; w < warps; w += 4) {
         const float4 q = part[w / 4];
@@ -241,21 +246,11 @@ __device__ __forceinline__ float sum_row(float v, RowSums &sm, bool second, int 
         const float *mine = reinterpret_cast<float *>(part) + rank * kEach + (threadIdx.x >> 5);
         st_async(cluster_addr(saddr(mine), lane), v, cluster_addr(bar, lane));
     }
-    if (!bar_wait(bar, turn >> 1 & 1, &sm.gave_up)) {
-        sm.gave_up = 1;
+    if (!__all_sync(0xffffffffu, bar_wait(bar, turn >> 1 & 1, &sm.gave_up))) {
+        sm.gave_up = 1;     // a wait that gives up makes the rest of the rows NaN
         return NAN;
     }
-    float s = 0.f;
-#pragma unroll
-    for (int r = 0; r < CTAS; r++) {
-        const float4 *p = part + r * (kEach / 4);
-        for (int w = 0; w < warps; w += 4) {
-            const float4 q = p[w / 4];
-            s += (q.x + (w + 1 < warps ? q.y : 0.f)) +
-                 ((w + 2 < warps ? q.z : 0.f) + (w + 3 < warps ? q.w : 0.f));
-        }
-    }
-    return s;
+    return sum_warp(lane % kEach < warps ? reinterpret_cast<const float *>(part)[lane] : 0.f);
 }
 
 // The statistics' products out r2 and y r1 are formed again after each reduction, since
