@@ -75,11 +75,12 @@ struct Sums {
 
 // Values that a chunk of a row may be raised to without a change of its sums, and the
 // maxima against which that holds: e^(kLow - m) is 0 for |m| <= kMost.  Products with
-// log2 e stay finite.
+// log2 e stay finite, and `rest` below, half a step of m log2 e at most, stays below 1 / 8:
+// it is an exponent of 2, and one of 128 has no fp32 power (a row of -1e10 has 440).
 template <typename T>
 constexpr float kLow = std::is_same_v<T, __half> ? -65504.f : -0x1p120f;
 template <typename T>
-constexpr float kMost = std::is_same_v<T, __half> ? 32768.f : 0x1p100f;
+constexpr float kMost = std::is_same_v<T, __half> ? 32768.f : 0x1p20f;
 
 // Adds the values of U words to the sums; `top` is their largest.
 //   e^(l - m) = 2^(l log2 e - c) 2^-rest,  c + rest = m log2 e:
@@ -114,7 +115,7 @@ __device__ __forceinline__ void add_words(Sums &u, const uint4 (&q)[U], float to
         u.sd = fmaf(f * kLn2, fmaf(-rest, sum_s, sum_sd), u.sd);
         return;
     }
-    // nothing but -inf yet, a mask's lowest value, or no number
+    // nothing but -inf or a mask's fill yet, large logits, or no number: m is subtracted first
     const float m = u.m == -INFINITY ? 0.f : u.m;
 #pragma unroll
     for (int i = 0; i < U; i++) {
