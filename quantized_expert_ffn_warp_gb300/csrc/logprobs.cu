@@ -542,8 +542,8 @@ __global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 5 : 6) logprobs_gra
             else if (v0 + i * kThreads < row.count)
                 q[i] = row.load(v0 + i * kThreads, 0.f);
         }
-        // beyond 2^100 the product with log2 e may overflow: m is subtracted first
-        const bool far = fabsf(st.x) > 0x1p100f;
+        // where `rest` could leave the exponents' range: m is subtracted first
+        const bool far = fabsf(st.x) > 0x1p20f;
         const float m = far ? 0.f : st.x;
         const float hi = m * kLog2E, ls = st.y * kLog2E, c = hi + ls;
         const float rest = fmaf(m, kLog2E, -hi) + (ls - (c - hi)) + fmaf(st.y, kLog2E, -ls);

@@ -1,4 +1,4 @@
-"""Token log probabilities where the largest logit of a row, or of
+"""Token log probabilities and their gradient where the largest logit of a row, or of
 a thread's first values, is far from 0: the fill of a mask, or logits of any size.
 The bounds are those of tuning_refs.py, derived there for every finite logit."""
 import pytest
@@ -7,8 +7,14 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from test_gpu_logprobs import batch, check  # noqa: E402
+from tuning_refs import DT, half_step, logprobs, logprobs_grad  # noqa: E402
 
 FAR = [-1e10, 1e10, -3e9, -1e9, 1e20, -1e30, 2.0 ** 21, -(2.0 ** 99)]
+
+
+def _moe():
+    from quantized_expert_ffn_warp_gb300 import moe
+    return moe
 
 
 def masked(logits, fill, where):
@@ -40,3 +46,29 @@ def test_forward(n, V, dtype, fill, where):
     targets[0], targets[1] = 99, V - 1
     check(logits, targets, 5)
     check(logits, targets, 0)
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+@pytest.mark.parametrize("fill", FAR)
+@pytest.mark.parametrize("where", ["all", "but_one", "first", "last"])
+@pytest.mark.parametrize("which", ["logp", "entropy", "both"])
+@pytest.mark.parametrize("n,V", [(3, 32003), (300, 8193)])
+def test_gradient(n, V, dtype, fill, where, which):
+    logits, targets = batch(n, V, dtype, 12, pad=1)
+    logits = masked(logits, fill, where)
+    g = torch.Generator(device="cuda").manual_seed(5)
+    dlogp = torch.randn(n, device="cuda", generator=g) if which != "entropy" else None
+    dent = torch.randn(n, device="cuda", generator=g) if which != "logp" else None
+    ref = logprobs(logits, targets)
+    fwd = dict(stats=ref["stats"].float(), entropy=ref["entropy"].float())
+    # where the largest logit m is far, l - m comes first: no term of m's own size in the
+    # bound.  Elsewhere the rest of m log2 e behind its fp32 value is rounded at H^2 m, as
+    # tuning_refs.py counts it (it shows where p = 1 and the entropy is 0: the gradient is 0).
+    m = ref["stats"][:, 0]
+    near = dict(ref, stats=torch.stack((torch.where(m.abs() > 2.0 ** 20, 0.0, m),
+                                        ref["stats"][:, 1]), 1))
+    want, err = logprobs_grad(logits, targets, near, dlogp, dent)
+    got = _moe().token_logprobs_grad(logits, targets, fwd, dlogp, dent)
+    assert ((got.double() - want).abs() <= err + half_step(want, DT[dtype])).all()
+    _moe().token_logprobs_grad(logits, targets, fwd, dlogp, dent, out=logits)
+    assert torch.equal(logits, got)
