@@ -178,6 +178,7 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 constexpr float kLog2E = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2ELow = (float)(1.4426950408889634 - (double)kLog2E);   // what kLog2E lacks
 
 // max(a, b), a NaN if either is one
 __device__ __forceinline__ float max_nan(float a, float b)

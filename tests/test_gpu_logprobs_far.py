@@ -7,7 +7,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 from test_gpu_logprobs import batch, check  # noqa: E402
-from tuning_refs import DT, half_step, logprobs, logprobs_grad  # noqa: E402
+from tuning_refs import DT, H, half_step, logprobs, logprobs_grad  # noqa: E402
 
 FAR = [-1e10, 1e10, -3e9, -1e9, 1e20, -1e30, 2.0 ** 21, -(2.0 ** 99)]
 
@@ -72,3 +72,29 @@ def test_gradient(n, V, dtype, fill, where, which):
     assert ((got.double() - want).abs() <= err + half_step(want, DT[dtype])).all()
     _moe().token_logprobs_grad(logits, targets, fwd, dlogp, dent, out=logits)
     assert torch.equal(logits, got)
+
+
+def test_a_row_of_gradients_sums_to_its_target_in_flat_rows():
+    """sum_v p_v of a wide, flat row from the statistics that the gradient is given.
+
+    Errors that all of a row's values share do not average out: of 2^x 4 H (2 units in
+    the last place) for each value and 4 H for the row's factor; the rounded log2 e
+    scales l - m, below 0.2 * 2^-25.  What differs from value to value (half a step
+    of an argument below 32, 2^-20 ln 2 = 11.1 H, and two roundings) averages to below H
+    over 160001 values.  10 H in all.  What is left of the row's constant
+    (m + logsum) log2 e behind its fp32 value, at logsum log2 e > 16, is up to 11.1 H."""
+    n, V = 512, 160001
+    g = torch.Generator(device="cuda").manual_seed(3)
+    logits = 0.02 * torch.randn((n, V), device="cuda", generator=g)
+    logits += torch.linspace(0.5, 4.0, n, device="cuda")[:, None]
+    ref = logprobs(logits, None)
+    stats = ref["stats"].float()
+    assert (ref["stats"][:, 1] > 11.5).all()
+    del ref
+    targets = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ones = torch.ones(n, device="cuda")
+    got = _moe().token_logprobs_grad(logits, targets, dict(stats=stats), ones)
+    p = (logits.double() - stats[:, :1].double() - stats[:, 1:].double()).exp()
+    want = p[:, 1:].sum(1)
+    off = (got[:, 1:].double().sum(1) + want).abs() / want / H
+    assert off.max() <= 10, off.max()
