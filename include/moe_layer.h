@@ -661,7 +661,7 @@ int moe_residual_norm(const void *resid, long long ld_resid, const void *y, long
  * out and xn (one of them may be NULL), its out and stats, and y:
  *   dresid, dy [n][hidden] of type dtype; dgain, dnext_gain fp32 [hidden];
  *   dgate fp32 [hidden], or [n] with gate_per_token = 1.
- * out and next_gain are not read without dxn.  dgain, dgate and dnext_gain may be
+ * out, next_gain and the second factors of stats take no part without dxn.  dgain, dgate and dnext_gain may be
  * NULL; they are summed in fp32 in a fixed order, in chains of at most 256 tokens
  * and a compensated sum of those.  dresid may be dout itself.
  * workspace: moe_residual_norm_grad_workspace(n, hidden) bytes, 16-byte aligned, any

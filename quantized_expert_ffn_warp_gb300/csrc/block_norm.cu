@@ -329,7 +329,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1) residual_norm_grad_kernel(Norm
     const F2 scale = f2(a.scale);
     int rows = 0, run = 0, turn = 0;
     for (; t < a.n; t += step) {
-        const float2 st = a.stats[t];
+        float2 st = a.stats[t];
+        if (!a.dxn)             // out alone: the second factor, whatever it is, takes no part
+            st.y = 0.f;
         const float tg = token_gate ? to_float<T>(token_gate[t]) : 1.f;
         const F2 r1 = f2(st.x), r2 = f2(st.y);
         F2 d[V][4];
