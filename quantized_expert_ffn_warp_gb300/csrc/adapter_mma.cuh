@@ -193,12 +193,16 @@ __device__ __forceinline__ uint16_t bits(T v)
     return *reinterpret_cast<const uint16_t *>(&v);
 }
 
-// Four of a token's results from rank k on: two parts at its place, and h.
+// Four of a token's results from rank k on: two parts at its place, and h.  Those behind the
+// last rank are 0: the product's are 0 times x, a NaN where x is not finite.
 template <typename T, int PAD>
 __device__ __forceinline__ void put_results(const ShrinkArgs &a, int place, int token, int k,
-                                            const float (&v)[4])
+                                            const float (&sums)[4])
 {
-    float rest[4];
+    float v[4], rest[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++)
+        v[e] = k < a.r ? sums[e] : 0.f;
 #pragma unroll
     for (int e = 0; e < 4; e++) {
         const float f = to_float<T>(from_float<T>(v[e]));
