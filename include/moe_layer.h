@@ -530,9 +530,10 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
  * [n_adapters][rank][cols] and B [n_adapters][rows][rank] of type dtype, 16-byte
  * aligned; scale fp32 [n_adapters] (NULL: 1); h [n][rank] of type dtype, 16-byte
  * aligned (NULL: not kept), what moe_adapter_grad takes.  out may be base itself.
- * Sums are fp32; between the two products h is held as the sum of two values of
- * dtype, so that it adds no rounding of its own (in fp16, an h above 65504 is an
- * infinity); out and h are rounded once.  Rows on 16-byte boundaries are read by
+ * Sums are fp32; between the two products h is the sum of values of dtype that have 22
+ * (fp16) or 16 (bf16) bits of it.  In fp16 they are relative to the token's largest h,
+ * whatever its size: h may be far below fp16's smallest number or above 65504.  out and h
+ * are rounded once (an h above 65504 is kept as an infinity).  Rows on 16-byte boundaries are read by
  * wide loads, others (odd widths) value by value.  When a wait for the tensor cores
  * gives up (after 2 s), the outputs that it concerns are NaN.
  * rank a multiple of 8 in 8 .. 128; n_adapters 1 .. 1024; n_tokens, cols and rows 1 ..
@@ -562,8 +563,10 @@ int moe_adapter(const void *x, long long ldx, int dtype, int n_tokens, int cols,
  * h [n][rank] (16-byte aligned, from moe_adapter), dA [n_adapters][rank][cols] and dB
  * [n_adapters][rows][rank] (16-byte aligned), all of type dtype; ids, A, B, scale as
  * there.  dx, dA and dB may be NULL and are left out then; x is read for dA, h for dB.
- * dx may be base itself.  Sums are fp32 in a fixed order, u is held as the sum of two
- * values of dtype, the results are rounded once.  The workspace is that of moe_adapter.
+ * dx may be base itself.  Sums are fp32 in a fixed order, u is held as h is in moe_adapter
+ * (in the fp16 sums over tokens relative to the adapter's largest u: 22 bits of a token's u
+ * down to 2^-28 of that), the results are rounded once.  The workspace is that of
+ * moe_adapter.
  * Errors: those of moe_adapter.
  */
 int moe_adapter_grad(const void *dy, long long lddy, const void *x, long long ldx, const void *h,

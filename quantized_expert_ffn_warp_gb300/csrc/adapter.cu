@@ -17,9 +17,14 @@
 // slices 20 and the expansion 55 (5.2 TB/s of base and out); the gradients of 8192 tokens
 // through 4096 x 4096 at rank 32 102 us: 6, 20, 35, and 34 for the weights'.  13 tokens of
 // 13 requests take 16 us, three launches of dependent loads.
-// h and u are held as the sum of two values of the activations' type: one would add a
-// rounding of 2^-9 (bf16) to the delta and to dA, and the second product is hidden
-// behind the copies.
+// h and u are kept in fp32 and multiplied as the sum of two values of the activations'
+// type, since the tensor cores take 16-bit operands: one would add a rounding of 2^-9
+// (bf16) to the delta and to dA, and the second product is hidden behind the copies.
+// fp16's two values hold 22 bits of what lies near their largest number only (gradients'
+// u are often below 2^-14, all of its range a subnormal's), so that they are 2^e h and 2^e u
+// with the largest next to 2^15: e of a token where the token's own result is formed, of an
+// adapter in the sums over its tokens, where the second value has 2^11 besides and sums of
+// its own.  The factors are undone in fp32.
 #include <algorithm>
 
 #include "adapter.cuh"
@@ -47,6 +52,8 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
         hist[i] = 0;
     for (int i = threadIdx.x; i < max_tickets; i += 1024)
         p.tickets[i] = 0;
+    for (int i = threadIdx.x; i < L; i += 1024)
+        p.most[i] = 0;
     __syncthreads();
     const int per = ((n + 31) / 32 + 31) / 32 * 32;
     const int lo = min(n, warp * per), hi = min(n, lo + per);
@@ -191,7 +198,8 @@ AdapterWorkspace adapter_ws(void *base, int n, int L, int r, int K, int N, bool 
     w.p.tiles = reinterpret_cast<int4 *>(take(16 * (size_t)adapter_tiles(n, L)));
     w.p.tickets = reinterpret_cast<unsigned *>(take(4 * (size_t)w.tickets));
     w.outer_tickets = w.p.tickets + tiles;
-    w.pair = reinterpret_cast<uint16_t *>(take(4 * (size_t)n * rank_pad(r)));
+    w.p.most = reinterpret_cast<unsigned *>(take(4 * (size_t)L));
+    w.mid = reinterpret_cast<float *>(take(8 * (size_t)n * rank_pad(r)));
     w.part = reinterpret_cast<float *>(
         take(w.slices > 1 ? 4 * (size_t)w.slices * n * rank_pad(r) : 0));
     w.outer_part = reinterpret_cast<float *>(

@@ -24,6 +24,7 @@ struct AdapterPlan {
                         // adapter L: none
     int *n_tiles;       // tiles, and the cost of all
     unsigned *tickets;  // parts that have arrived: of tiles, then of outer blocks
+    unsigned *most;     // [L] largest |u| of an adapter's tokens, the bits of an fp32 value
 };
 
 struct AdapterWorkspace {
@@ -31,7 +32,8 @@ struct AdapterWorkspace {
     int slices, splits;         // parts of a contraction: of a tile, of an adapter's tokens
     int tickets;
     unsigned *outer_tickets;
-    uint16_t *pair;             // [n][2][rank_pad] h or u in two parts, in perm's order
+    float *mid;                 // h or u in perm's order: [n][rank_pad] values, then (or in their
+                                // place) [n][parts][rank_pad] of the activations' type
     float *part, *outer_part;
     size_t bytes;
 };

@@ -116,7 +116,7 @@ __device__ __forceinline__ void tensor_wait(const Tensor &t, int i, int use)
 
 __host__ __device__ constexpr uint32_t tmem_cols(int n)
 {
-    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : 256;
+    return n <= 32 ? 32 : n <= 64 ? 64 : n <= 128 ? 128 : n <= 256 ? 256 : 512;
 }
 // 128-byte rows that hold `r` values.
 __host__ __device__ constexpr int row_blocks(int r) { return (r + kBlk - 1) / kBlk; }
@@ -183,8 +183,10 @@ struct ShrinkArgs {
     int n, L, K, r, slices;
     bool vec_x, vec_w;
     float *part;            // [slices][n][PAD] partial sums
-    uint16_t *pair;         // [n][2][PAD]
+    float *mid;             // [n][PAD], kLifted types
+    uint16_t *parts;        // [n][kParts][PAD], others
     uint16_t *h;            // [n][r], or null
+    bool most;              // keep the largest of each adapter
 };
 
 template <typename T>
@@ -193,29 +195,106 @@ __device__ __forceinline__ uint16_t bits(T v)
     return *reinterpret_cast<const uint16_t *>(&v);
 }
 
-// Four of a token's results from rank k on: two parts at its place, and h.  Those behind the
-// last rank are 0: the product's are 0 times x, a NaN where x is not finite.
+// An fp32 value of h or u is multiplied as the sum of kParts values of T.
+template <typename T>
+constexpr int kParts = 2;
+// The type's own exponents do not reach all fp32 values: 2^e of them are split.
+template <typename T>
+constexpr bool kLifted = std::is_same_v<T, __half>;
+// In the sums over tokens, of a part of u to the one in front of it: lifted, what the first
+// lacks fills the same range, so that a token's u has its 22 bits down to 2^-28 of the
+// adapter's largest.
+template <typename T>
+constexpr float kNext = kLifted<T> ? 2048.f : 1.f;
+
+// (2^e, 2^-e) with 2^e most in [2^14, 2^15); both are normal numbers for any most.
+__device__ __forceinline__ float2 lift_of(float most)
+{
+    const int e = min(141 - (int)(__float_as_uint(most) >> 23), 100);
+    return make_float2(__uint_as_float((uint32_t)(127 + e) << 23),
+                       __uint_as_float((uint32_t)(127 - e) << 23));
+}
+// The parts of N values; each is what those in front of it lack, times `next` for each.
+template <typename T, int P, int N>
+__device__ __forceinline__ void split(float (&v)[N], float next, uint32_t (&q)[P][N / 2])
+{
+#pragma unroll
+    for (int p = 0; p < P; p++)
+#pragma unroll
+        for (int e = 0; e < N; e += 2) {
+            q[p][e / 2] = pack2<T>(v[e], v[e + 1]);
+            const float2 f = unpack2<T>(q[p][e / 2]);
+            // an infinity or a NaN has no remainder
+            v[e] = fabsf(f.x) <= 3.4e38f ? (v[e] - f.x) * next : 0.f;
+            v[e + 1] = fabsf(f.y) <= 3.4e38f ? (v[e + 1] - f.y) * next : 0.f;
+        }
+}
+__device__ __forceinline__ void store_shared(uint32_t at, const uint32_t (&q)[4])
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(q[0]), "r"(q[1]),
+                 "r"(q[2]), "r"(q[3])
+                 : "memory");
+}
+__device__ __forceinline__ void load8(float (&v)[8], const float *p, bool in)
+{
+    const float4 a = in ? *reinterpret_cast<const float4 *>(p) : make_float4(0.f, 0.f, 0.f, 0.f);
+    const float4 b =
+        in ? *reinterpret_cast<const float4 *>(p + 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+// The parts of an adapter's u for the sums over its tokens: eight ranks of a place.
+template <typename T, int PAD>
+__device__ __forceinline__ void put_lifted(uint16_t *parts, long long place, int k,
+                                           const float (&u)[8], float lift)
+{
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        v[e] = u[e] * lift;
+    uint32_t q[kParts<T>][4];
+    split<T>(v, kNext<T>, q);
+#pragma unroll
+    for (int p = 0; p < kParts<T>; p++)
+        *reinterpret_cast<uint4 *>(parts + (place * kParts<T> + p) * PAD + k) =
+            make_uint4(q[p][0], q[p][1], q[p][2], q[p][3]);
+}
+
+// Four of a token's results from rank k on, at its place and in h; those behind the last rank
+// are 0: the product's are 0 times x, a NaN where x is not finite.  `most` takes their size.
 template <typename T, int PAD>
 __device__ __forceinline__ void put_results(const ShrinkArgs &a, int place, int token, int k,
-                                            const float (&sums)[4])
+                                            const float (&sums)[4], float &most)
 {
-    float v[4], rest[4];
+    float v[4];
 #pragma unroll
     for (int e = 0; e < 4; e++)
         v[e] = k < a.r ? sums[e] : 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; e++) {
-        const float f = to_float<T>(from_float<T>(v[e]));
-        // an infinity or a NaN has no remainder
-        rest[e] = fabsf(f) <= 3.4e38f ? v[e] - f : 0.f;
-    }
-    const uint2 hi = make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
-    uint16_t *row = a.pair + (long long)place * 2 * PAD + k;
-    *reinterpret_cast<uint2 *>(row) = hi;
-    *reinterpret_cast<uint2 *>(row + PAD) =
-        make_uint2(pack2<T>(rest[0], rest[1]), pack2<T>(rest[2], rest[3]));
     if (a.h && k < a.r)
-        *reinterpret_cast<uint2 *>(a.h + (long long)token * a.r + k) = hi;
+        *reinterpret_cast<uint2 *>(a.h + (long long)token * a.r + k) =
+            make_uint2(pack2<T>(v[0], v[1]), pack2<T>(v[2], v[3]));
+    if constexpr (kLifted<T>) {
+        *reinterpret_cast<float4 *>(a.mid + (long long)place * PAD + k) =
+            make_float4(v[0], v[1], v[2], v[3]);
+#pragma unroll
+        for (int e = 0; e < 4; e++)
+            most = fmaxf(most, fabsf(v[e]));
+    } else {
+        uint32_t q[kParts<T>][2];
+        split<T>(v, 1.f, q);
+#pragma unroll
+        for (int p = 0; p < kParts<T>; p++)
+            *reinterpret_cast<uint2 *>(a.parts + ((long long)place * kParts<T> + p) * PAD + k) =
+                make_uint2(q[p][0], q[p][1]);
+    }
+}
+// The warp's largest result to its adapter's, whatever the order: a NaN is passed over.
+__device__ __forceinline__ void put_most(const ShrinkArgs &a, int adapter, float most)
+{
+    most = max_warp(most);
+    if ((threadIdx.x & 31) == 0 && most > 0.f)
+        atomicMax(a.p.most + adapter, __float_as_uint(most));
 }
 
 constexpr int kShrinkStages = 4;
@@ -225,7 +304,7 @@ constexpr int kShrinkStage = 128 * kTile + (BY_ROW ? 128 * kBlk * row_blocks(PAD
 // A tile's tokens (the product's rows) times all ranks.  The slices' sums are added by
 // whichever CTA of a tile arrives last, in the slices' order.
 template <typename T, bool BY_ROW, int PAD>
-__global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs a)
+__global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_shrink_kernel(ShrinkArgs a)
 {
     __shared__ TensorSmem ts;
     __shared__ int last;
@@ -316,28 +395,32 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
     contract<kShrinkStages>(t, end - begin, 0, fetch, multiply);
     const bool failed = *t.gave_up;
     const int at = 32 * warp + lane, place = tile.y + at;
+    float most = 0.f;
     if (warp < 4) {
         const int token = at < tile.z ? a.p.perm[place] : 0;
 #pragma unroll 1
         for (int c = 0; c < PAD; c += 16) {
             float v[16];
             tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + c, v);
-            if (at >= tile.z)
-                continue;
+            if (at < tile.z) {
 #pragma unroll
-            for (int q = 0; q < 4; q++) {
-                float d[4];
+                for (int q = 0; q < 4; q++) {
+                    float d[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    d[e] = failed ? NAN : v[4 * q + e];
-                if (a.slices == 1)
-                    put_results<T, PAD>(a, place, token, c + 4 * q, d);
-                else
-                    *reinterpret_cast<float4 *>(
-                        a.part + ((long long)slice * a.n + place) * PAD + c + 4 * q) =
-                        make_float4(d[0], d[1], d[2], d[3]);
+                    for (int e = 0; e < 4; e++)
+                        d[e] = failed ? NAN : v[4 * q + e];
+                    if (a.slices == 1)
+                        put_results<T, PAD>(a, place, token, c + 4 * q, d, most);
+                    else
+                        *reinterpret_cast<float4 *>(
+                            a.part + ((long long)slice * a.n + place) * PAD + c + 4 * q) =
+                            make_float4(d[0], d[1], d[2], d[3]);
+                }
             }
+            __syncwarp();       // the next load is the whole warp's
         }
+        if (a.most && a.slices == 1)
+            put_most(a, tile.x, most);
     }
     tensor_end(t, cols);
     if (a.slices == 1)
@@ -384,16 +467,21 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_shrink_kernel(ShrinkArgs 
         for (int j = 0; j < I; j++) {
             const int i = i0 + j * kThreads;
             if (i < items)
-                put_results<T, PAD>(a, tile.y + i / (PAD / 4), token[j], i % (PAD / 4) * 4, v[j]);
+                put_results<T, PAD>(a, tile.y + i / (PAD / 4), token[j], i % (PAD / 4) * 4, v[j],
+                                    most);
         }
     }
+    __syncwarp();
+    if (a.most)
+        put_most(a, tile.x, most);
 }
 
 // ---------------------------------------------------------------- expand
 
 struct ExpandArgs {
     AdapterPlan p;
-    const uint16_t *pair;   // [n][2][PAD]
+    const float *mid;       // [n][PAD], kLifted types
+    uint16_t *parts;        // [n][kParts][PAD]: read; kLifted, written (or null)
     const uint16_t *w;      // [L][N][r], or (BY_ROW) [L][r][N]
     const float *scale;     // [L] or null
     const uint16_t *base;   // [n][N] or null
@@ -431,9 +519,9 @@ __device__ __forceinline__ void store8(uint16_t *row, int i, int len, bool align
             row[i + e] = (uint16_t)(w[e / 2] >> (16 * (e & 1)));
 }
 
-// h in 128-byte rows, the upper parts and then the lower: side by side if both fit.
-template <int PAD>
-constexpr int kPairBlocks = 2 * PAD <= kBlk ? 1 : 2 * row_blocks(PAD);
+// h in 128-byte rows, part after part.
+template <typename T, int PAD>
+constexpr int kPartBlocks = row_blocks(kParts<T> * PAD);
 template <bool BY_ROW, int PAD>
 constexpr int kMatrix = BY_ROW ? 2 * kCols * PAD : 128 * kCols * row_blocks(PAD);
 // A tile's rows of base, then of out, for one block of columns: rows 16 bytes longer than
@@ -446,8 +534,8 @@ template <int PAD>
 constexpr int kAhead = PAD <= 64 ? 2 : 1;
 template <int PAD>
 constexpr int kRowBuffers = kAhead<PAD> + 1;
-template <bool BY_ROW, int PAD>
-constexpr int kExpandSmem = 128 * kTile * kPairBlocks<PAD> + 2 * kMatrix<BY_ROW, PAD> +
+template <typename T, bool BY_ROW, int PAD>
+constexpr int kExpandSmem = 128 * kTile * kPartBlocks<T, PAD> + 2 * kMatrix<BY_ROW, PAD> +
                             kRowBuffers<PAD> * kRowsBytes + kSmemSlack;
 
 // Tiles of tokens (the product's rows) times blocks of columns: a CTA takes an equal share
@@ -460,6 +548,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
 {
     __shared__ TensorSmem ts;
     __shared__ int toks[kTile];
+    __shared__ float undo[kLifted<T> ? kTile : 1];      // a row's 2^-e
     pdl_wait();
     const int blocks = (a.N + kCols - 1) / kCols;
     const int n_tiles = a.p.n_tiles[0];
@@ -490,10 +579,9 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
         return;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const Tensor t = tensor_begin(ts, 2 * kCols);
-    constexpr int wide = PAD / 8, row_blks = row_blocks(PAD), matrix = kMatrix<BY_ROW, PAD>;
+    constexpr int parts = kParts<T>, matrix = kMatrix<BY_ROW, PAD>;
     constexpr int ahead = kAhead<PAD>, buffers = kRowBuffers<PAD>;
-    constexpr bool side = 2 * PAD <= kBlk;
-    const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPairBlocks<PAD>;
+    const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPartBlocks<T, PAD>;
     const uint32_t rows = mats + 2 * matrix;
     // the matrix: rows of ranks (0 behind the last), or (BY_ROW) of columns for each rank
     using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD, kExpandThreads>,
@@ -507,6 +595,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
     const int row = 32 * (warp & 3) + lane, col = 32 * (warp >> 2);
     const int base_row = threadIdx.x / 16, base_chunk = threadIdx.x % 16;
     constexpr int kBasePass = kExpandThreads / 16;
+    // its eight values of h in every kMidPass-th row
+    constexpr int kMidRow = PAD / 8, kMidPass = kExpandThreads / kMidRow;
+    constexpr int kMidPasses = (kTile + kMidPass - 1) / kMidPass;
+    const int mid_row = threadIdx.x / kMidRow, mid_chunk = threadIdx.x % kMidRow;
     int done = 0;       // products so far: their tensor memory and barrier alternate
     while (at < end) {
         const int4 tile = a.p.tiles[at / blocks];
@@ -547,12 +639,25 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
         if (threadIdx.x < kTile)
             toks[threadIdx.x] =
                 a.p.perm[tile.y + ((int)threadIdx.x < tile.z ? threadIdx.x : 0)];
-        // h: chunk c of part p of a row
-        for (int i = threadIdx.x; i < tile.z * 2 * wide; i += kExpandThreads) {
-            const int r = i / (2 * wide), c = i % (2 * wide), part = c >= wide;
-            const int to = side ? c : c - part * wide + part * 8 * row_blks;
-            copy16(hs + (to >> 3) * (128 * kTile) + sw128_at(r, to & 7),
-                   a.pair + (long long)(tile.y + r) * 2 * PAD + 8 * c, 16);
+        float mid[kMidPasses][8];
+        if constexpr (kLifted<T>) {
+#pragma unroll
+            for (int j = 0; j < kMidPasses; j++) {
+                const int r = mid_row + kMidPass * j;
+                load8(mid[j], a.mid + (long long)(tile.y + r) * PAD + 8 * mid_chunk, r < tile.z);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kMidPasses; j++) {
+                const int r = mid_row + kMidPass * j;
+#pragma unroll
+                for (int p = 0; p < parts; p++) {
+                    const int c = p * kMidRow + mid_chunk;
+                    if (r < tile.z)
+                        copy16(hs + (c >> 3) * (128 * kTile) + sw128_at(r, c & 7),
+                               a.parts + (long long)(tile.y + r) * parts * PAD + 8 * c, 16);
+                }
+            }
         }
         __syncthreads();
         const uint16_t *w = a.w + (long long)tile.x * a.r * a.N;
@@ -641,10 +746,10 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
                     const uint32_t mat = mats + (step & 1) * matrix;
                     const int buffer = (done + step) & 1;
 #pragma unroll
-                    for (int part = 0; part < 2; part++)
+                    for (int part = 0; part < parts; part++)
 #pragma unroll
                         for (int k = 0; k < PAD / 16; k++) {
-                            const int ka = side ? part * (PAD / 16) + k : part * 4 * row_blks + k;
+                            const int ka = part * (PAD / 16) + k;
                             const uint64_t da =
                                 sw128_desc(hs + (ka >> 2) * (128 * kTile)) + 2 * (ka & 3);
                             const uint64_t db =
@@ -658,8 +763,42 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             }
         };
         fetch(0);
-        if (ahead == 2) {
+        if (ahead == 2)
             fetch(1);
+        if constexpr (kLifted<T>) {
+            // whoever has a tile's first block leaves its parts for the sums over tokens
+            const bool leave = a.parts && first == 0;
+            const float all =
+                leave ? lift_of(__uint_as_float(a.p.most[tile.x])).x : 0.f;
+#pragma unroll
+            for (int j = 0; j < kMidPasses; j++) {
+                const int r = mid_row + kMidPass * j;
+                if (leave && r < tile.z)
+                    put_lifted<T, PAD>(a.parts, tile.y + r, 8 * mid_chunk, mid[j], all);
+                float most = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    most = fmaxf(most, fabsf(mid[j][e]));
+#pragma unroll
+                for (int d = 1; d < kMidRow; d <<= 1)
+                    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, d));
+                const float2 lift = lift_of(most);
+#pragma unroll
+                for (int e = 0; e < 8; e++)
+                    mid[j][e] *= lift.x;
+                if (mid_chunk == 0 && r < tile.z)
+                    undo[r] = lift.y;
+                uint32_t q[parts][4];
+                split<T>(mid[j], 1.f, q);
+#pragma unroll
+                for (int p = 0; p < parts; p++) {
+                    const int c = p * kMidRow + mid_chunk;
+                    if (r < tile.z)
+                        store_shared(hs + (c >> 3) * (128 * kTile) + sw128_at(r, c & 7), q[p]);
+                }
+            }
+        }
+        if (ahead == 2) {
             wait_copies<1>();
             fence_async_shared();
             __syncthreads();
@@ -676,7 +815,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             tensor_wait(t, buffer, (done + step) >> 1);
             tc_fence_after();
             fetch(step + ahead);
-            const F2 factor = f2(*t.gave_up ? NAN : scale);
+            const F2 factor = f2(*t.gave_up ? NAN : kLifted<T> ? scale * undo[row] : scale);
             uint8_t *const block = smem_at(rows + step % buffers * kRowsBytes + 2 * col);
             uint4 *const mine = reinterpret_cast<uint4 *>(block + row * kPitch);
             const uint8_t *const theirs =
@@ -742,20 +881,21 @@ struct OuterSide {
     long long ld;
     bool vec;
     int C, blocks;          // columns, blocks of kCols of them
-    const uint16_t *v;      // ranks: of a token (h [n][r]), or of a place (pair)
     uint16_t *out;
 };
 struct OuterArgs {
     AdapterPlan p;
     OuterSide a, b;         // dA [L][r][K] from x and u, dB [L][N][r] from dy and h
+    const uint16_t *u;      // [n][kParts][PAD] by place
+    const uint16_t *h;      // [n][r] by token
     const float *scale;
     int L, r, splits, turns;    // turns: blocks of a CTA, one after another
     float *part;            // [splits][L][blocks of both][kCols][PAD]
     unsigned *tickets;      // [L][blocks of both]
 };
 constexpr int kOuterStages = 3, kOuterList = 16;    // steps whose tokens are at hand
-template <int PAD>
-constexpr int kOuterStage = 128 * kBlk * (kCols / kBlk + 2 * row_blocks(PAD));
+template <typename T, int PAD>
+constexpr int kOuterStage = 128 * kBlk * (kCols / kBlk + kPartBlocks<T, PAD>);
 
 // Sixteen ranks of a column from rank k on, at the end of a sum over tokens.
 template <typename T>
@@ -783,7 +923,7 @@ __device__ __forceinline__ void put_outer(const OuterArgs &a, const OuterSide &o
 // The sum over an adapter's tokens of kCols columns (the product's rows) times all ranks.
 // Both operands are read along their rows: the tokens are the contraction.
 template <typename T, int PAD>
-__global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
+__global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_kernel(OuterArgs a)
 {
     __shared__ TensorSmem ts;
     __shared__ int toks[kOuterList * kBlk];
@@ -808,14 +948,17 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
         }
         return;
     }
-    constexpr uint32_t cols = tmem_cols(PAD);
+    constexpr int parts = kParts<T>;
+    constexpr uint32_t cols = tmem_cols(parts * PAD);
     const Tensor t = tensor_begin(ts, cols);
     const uint32_t smem = smem_base();
-    constexpr int stage_bytes = kOuterStage<PAD>, part_bytes = 128 * kBlk * row_blocks(PAD);
+    constexpr int stage_bytes = kOuterStage<T, PAD>;
     using X = Rows<kCols / 8, kBlk>;
     using V = Rows<PAD / 8, kBlk>;
     const X xr(128 * kBlk);
     const V vr(128 * kBlk);
+    const float2 lift =
+        kLifted<T> ? lift_of(__uint_as_float(a.p.most[adapter])) : make_float2(1.f, 1.f);
     for (int blk = first; blk < stop; blk++) {
         const bool of_a = blk < a.a.blocks;
         const OuterSide &o = of_a ? a.a : a.b;
@@ -823,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
         const uint16_t *src = o.src + c0 + 8 * xr.chunk;
         const bool whole = o.vec && c0 + kCols <= o.C;
         const int rank_bytes = 8 * vr.chunk < a.r ? 16 : 0;     // 0 for the ranks behind the last
-        const uint16_t *ranks = rank_bytes ? o.v + 8 * vr.chunk : o.v;
+        const uint16_t *ranks = rank_bytes ? a.h + 8 * vr.chunk : a.h;
         const auto fetch = [&](int i, int stage) {
             const int s0 = (begin + i) * kBlk;
             if (i % kOuterList == 0) {      // the list that the next steps take their tokens from
@@ -833,7 +976,7 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
             }
             const int *list = toks + i % kOuterList * kBlk;
             const uint32_t xs = smem + stage * stage_bytes + xr.at;
-            const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk) + vr.at;
+            const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk);
             if (whole && s0 + kBlk <= count) {
 #pragma unroll
                 for (int j = 0; j < X::kPasses; j++)
@@ -848,35 +991,40 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
             }
             if (!vr.on)
                 return;
-            if (of_a) {
-                const uint16_t *v = ranks + (long long)(lo + s0 + vr.row) * 2 * PAD;
+            if (of_a) {                     // u in its parts, side by side
+                const uint16_t *from = a.u + (long long)(lo + s0 + vr.row) * parts * PAD + 8 * vr.chunk;
 #pragma unroll
                 for (int j = 0; j < V::kPasses; j++) {
-                    const bool in = rank_bytes && s0 + vr.row + V::kPass * j < count;
-                    const uint16_t *p = in ? v + V::kPass * 2 * PAD * j : o.v;
-                    copy16(vs + V::kNext * j, p, in ? 16 : 0);
-                    copy16(vs + V::kNext * j + part_bytes, in ? p + PAD : p, in ? 16 : 0);
+                    const bool in = s0 + vr.row + V::kPass * j < count;
+#pragma unroll
+                    for (int p = 0; p < parts; p++) {
+                        const int chunk = p * (PAD / 8) + vr.chunk;
+                        copy16(vs + (chunk >> 3) * (128 * kBlk) +
+                                   sw128_at(vr.row + V::kPass * j, chunk & 7),
+                               in ? from + (V::kPass * j * parts + p) * PAD : a.u, in ? 16 : 0);
+                    }
                 }
             } else {
 #pragma unroll
                 for (int j = 0; j < V::kPasses; j++) {
                     const int tok = list[vr.row + V::kPass * j];
-                    copy16(vs + V::kNext * j, ranks + (long long)max(tok, 0) * a.r,
+                    copy16(vs + vr.at + V::kNext * j, ranks + (long long)max(tok, 0) * a.r,
                            tok >= 0 ? rank_bytes : 0);
                 }
             }
         };
-        constexpr uint32_t idesc =
-            (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
-            ((uint32_t)(PAD >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
+        // the parts' sums lie side by side too, at most 256 columns an instruction
         const auto multiply = [&](int stage, bool first) {
             const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * kBlk * (kCols / kBlk);
             const uint64_t da = sw128_desc_mn(at, 128 * kBlk);
-            for (int part = 0; part < (of_a ? 2 : 1); part++) {
-                const uint64_t db = sw128_desc_mn(vs + part * part_bytes, 128 * kBlk);
+            for (int n0 = 0, all = of_a ? parts * PAD : PAD; n0 < all; n0 += 256) {
+                const uint32_t idesc =
+                    (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
+                    ((uint32_t)(min(all - n0, 256) >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
+                const uint64_t db = sw128_desc_mn(vs + n0 / kBlk * (128 * kBlk), 128 * kBlk);
 #pragma unroll
                 for (int k = 0; k < kBlk / 16; k++)
-                    umma_ss(t.tmem, da + 128 * k, db + 128 * k, idesc, !first || part || k);
+                    umma_ss(t.tmem + n0, da + 128 * k, db + 128 * k, idesc, !first || k);
             }
         };
         if (blk > first)
@@ -890,6 +1038,21 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
             for (int k = 0; k < PAD; k += 16) {
                 float v[16];
                 tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + k, v);
+                if (of_a) {
+                    float weight = lift.y;
+#pragma unroll
+                    for (int e = 0; e < 16; e++)
+                        v[e] *= weight;
+#pragma unroll
+                    for (int p = 1; p < parts; p++) {
+                        float rest[16];
+                        tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + p * PAD + k, rest);
+                        weight /= kNext<T>;
+#pragma unroll
+                        for (int e = 0; e < 16; e++)
+                            v[e] = fmaf(rest[e], weight, v[e]);
+                    }
+                }
 #pragma unroll
                 for (int e = 0; e < 16; e++)
                     v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
@@ -938,6 +1101,27 @@ __global__ void __launch_bounds__(kThreads, 2) adapter_outer_kernel(OuterArgs a)
     tensor_end(t, cols);
 }
 
+// What the expansion leaves of u, where none is asked for: a CTA has a tile.
+template <typename T, int PAD>
+__global__ void __launch_bounds__(kThreads) adapter_split_kernel(AdapterPlan p, int L,
+                                                                 const float *mid, uint16_t *parts)
+{
+    pdl_enter();
+    if ((int)blockIdx.x >= *p.n_tiles)
+        return;
+    const int4 tile = p.tiles[blockIdx.x];
+    if (tile.x == L)
+        return;
+    const float lift = lift_of(__uint_as_float(p.most[tile.x])).x;
+    for (int i = threadIdx.x; i < tile.z * (PAD / 8); i += kThreads) {
+        const long long place = tile.y + i / (PAD / 8);
+        const int k = 8 * (i % (PAD / 8));
+        float u[8];
+        load8(u, mid + place * PAD + k, true);
+        put_lifted<T, PAD>(parts, place, k, u, lift);
+    }
+}
+
 // ---------------------------------------------------------------- host
 
 // A kernel with more dynamic shared memory than the default.
@@ -964,7 +1148,7 @@ cudaError_t launch_expand(const ExpandArgs &a, int tiles, int sms, cudaStream_t 
     // as many CTAs as run at once
     return launch_wide(adapter_expand_kernel<T, BY_ROW, PAD>,
                        dim3((unsigned)std::min(total, (long long)sms)),
-                       kExpandSmem<BY_ROW, PAD>, st, a, kExpandThreads);
+                       kExpandSmem<T, BY_ROW, PAD>, st, a, kExpandThreads);
 }
 
 bool vec_rows(const void *p, long long ld, int n)
@@ -974,17 +1158,24 @@ bool vec_rows(const void *p, long long ld, int n)
 
 const uint16_t *half_words(const void *p) { return static_cast<const uint16_t *>(p); }
 
+// Where the parts lie: behind fp32 values where those are kept.
+template <typename T, int PAD>
+uint16_t *parts_of(const AdapterWorkspace &w, int n)
+{
+    return reinterpret_cast<uint16_t *>(w.mid + (kLifted<T> ? (size_t)n * PAD : 0));
+}
+
 template <typename T, int PAD>
 cudaError_t run_adapter(const AdapterCall &c, cudaStream_t st)
 {
     const int tiles = adapter_tiles(c.n, c.L);
     const ShrinkArgs s = {c.w.p, half_words(c.x), c.ldx, half_words(c.A), c.n, c.L, c.K, c.r,
-                          c.w.slices, vec_rows(c.x, c.ldx, c.n), c.K % 8 == 0, c.w.part, c.w.pair,
-                          static_cast<uint16_t *>(c.h)};
+                          c.w.slices, vec_rows(c.x, c.ldx, c.n), c.K % 8 == 0, c.w.part, c.w.mid,
+                          parts_of<T, PAD>(c.w, c.n), static_cast<uint16_t *>(c.h), false};
     const cudaError_t e = launch_shrink<T, false, PAD>(s, tiles, st);
     if (e != cudaSuccess)
         return e;
-    const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.B), c.scale, half_words(c.base), c.ldb,
+    const ExpandArgs x = {c.w.p, c.w.mid, kLifted<T> ? nullptr : s.parts, half_words(c.B), c.scale, half_words(c.base), c.ldb,
                           static_cast<uint16_t *>(c.out), c.ldo, c.L, c.N, c.r, true,
                           vec_rows(c.base, c.ldb, c.n), vec_rows(c.out, c.ldo, c.n)};
     return launch_expand<T, false, PAD>(x, tiles, c.sms, st);
@@ -994,17 +1185,25 @@ template <typename T, int PAD>
 cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
 {
     const int tiles = adapter_tiles(c.n, c.L);
+    uint16_t *parts = parts_of<T, PAD>(c.w, c.n);
     const ShrinkArgs s = {c.w.p, half_words(c.dy), c.lddy, half_words(c.B), c.n, c.L, c.N, c.r,
-                          c.w.slices, vec_rows(c.dy, c.lddy, c.n), true, c.w.part, c.w.pair, nullptr};
+                          c.w.slices, vec_rows(c.dy, c.lddy, c.n), true, c.w.part, c.w.mid, parts,
+                          nullptr, kLifted<T> && c.dA};
     cudaError_t e = launch_shrink<T, true, PAD>(s, tiles, st);
     if (e != cudaSuccess)
         return e;
     if (c.dx) {
-        const ExpandArgs x = {c.w.p, c.w.pair, half_words(c.A), c.scale, half_words(c.base), c.ldb,
+        const ExpandArgs x = {c.w.p, c.w.mid, kLifted<T> && !c.dA ? nullptr : parts, half_words(c.A), c.scale, half_words(c.base), c.ldb,
                               static_cast<uint16_t *>(c.dx), c.lddx, c.L, c.K, c.r,
                               c.K % 8 == 0, vec_rows(c.base, c.ldb, c.n),
                               vec_rows(c.dx, c.lddx, c.n)};
         e = launch_expand<T, true, PAD>(x, tiles, c.sms, st);
+        if (e != cudaSuccess)
+            return e;
+    }
+    if (kLifted<T> && c.dA && !c.dx) {
+        e = launch_pdl(adapter_split_kernel<T, PAD>, dim3(tiles), dim3(kThreads), 0, st, c.w.p, c.L,
+                       c.w.mid, parts);
         if (e != cudaSuccess)
             return e;
     }
@@ -1018,12 +1217,14 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
     o.splits = c.w.splits;
     o.part = c.w.outer_part;
     o.tickets = c.w.outer_tickets;
+    o.u = parts;
+    o.h = half_words(c.h);
     if (c.dA)
         o.a = {half_words(c.x), c.ldx, vec_rows(c.x, c.ldx, c.n), c.K, (c.K + kCols - 1) / kCols,
-               c.w.pair, static_cast<uint16_t *>(c.dA)};
+               static_cast<uint16_t *>(c.dA)};
     if (c.dB)
         o.b = {half_words(c.dy), c.lddy, vec_rows(c.dy, c.lddy, c.n), c.N,
-               (c.N + kCols - 1) / kCols, half_words(c.h), static_cast<uint16_t *>(c.dB)};
+               (c.N + kCols - 1) / kCols, static_cast<uint16_t *>(c.dB)};
     // Several blocks a CTA once they fill the SMs' two places eight times: few tokens each, so
     // that a CTA's start weighs.  Measured, one block a CTA against this: 64 adapters of 4096 x
     // 4096, 500 tokens (rank 16) 82 and 72 us, 8192 tokens (rank 32) 144 and 137; 256 adapters
@@ -1033,7 +1234,7 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
     o.turns = std::max(1, (int)std::min(8LL, (long long)blocks * c.L / (8 * c.sms)));
     return launch_wide(adapter_outer_kernel<T, PAD>,
                        dim3((blocks + o.turns - 1) / o.turns, c.L, o.splits),
-                       kOuterStages * kOuterStage<PAD> + kSmemSlack, st, o);
+                       kOuterStages * kOuterStage<T, PAD> + kSmemSlack, st, o);
 }
 
 template <typename T>
