@@ -531,7 +531,7 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
  * aligned; scale fp32 [n_adapters] (NULL: 1); h [n][rank] of type dtype, 16-byte
  * aligned (NULL: not kept), what moe_adapter_grad takes.  out may be base itself.
  * Sums are fp32; between the two products h is the sum of values of dtype that have 22
- * (fp16) or 16 (bf16) bits of it.  In fp16 they are relative to the token's largest h,
+ * (fp16) or 24 (bf16) bits of it.  In fp16 they are relative to the token's largest h,
  * whatever its size: h may be far below fp16's smallest number or above 65504.  out and h
  * are rounded once (an h above 65504 is kept as an infinity).  Rows on 16-byte boundaries are read by
  * wide loads, others (odd widths) value by value.  When a wait for the tensor cores

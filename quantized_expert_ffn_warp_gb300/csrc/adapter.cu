@@ -17,14 +17,17 @@
 // slices 20 and the expansion 55 (5.2 TB/s of base and out); the gradients of 8192 tokens
 // through 4096 x 4096 at rank 32 102 us: 6, 20, 35, and 34 for the weights'.  13 tokens of
 // 13 requests take 16 us, three launches of dependent loads.
-// h and u are kept in fp32 and multiplied as the sum of two values of the activations'
-// type, since the tensor cores take 16-bit operands: one would add a rounding of 2^-9
-// (bf16) to the delta and to dA, and the second product is hidden behind the copies.
-// fp16's two values hold 22 bits of what lies near their largest number only (gradients'
-// u are often below 2^-14, all of its range a subnormal's), so that they are 2^e h and 2^e u
-// with the largest next to 2^15: e of a token where the token's own result is formed, of an
-// adapter in the sums over its tokens, where the second value has 2^11 besides and sums of
-// its own.  The factors are undone in fp32.
+// h and u are fp32 sums and are multiplied as sums of values of the activations' type, since
+// the tensor cores take 16-bit operands: one would add a rounding of 2^-9 (bf16) to the
+// delta and to dA.  bf16 takes three, all 24 bits; with two, 16 bits, dA differed from fp32
+// products by 1.5e-4 of itself in place of 1.1e-4, all else the rounding of the result.
+// The third costs 4 us of 89 in the first case and 7 us of 116 in the gradients at rank 64
+// (8192 tokens, 4096 x 4096), and nothing up to rank 32.
+// fp16 takes two, 22 bits of what lies near its largest number only (gradients' u are often
+// below 2^-14, all of its range a subnormal's), so that they are 2^e h and 2^e u with the
+// largest next to 2^15: e of a token where the token's own result is formed, of an adapter
+// in the sums over its tokens, where the second value has 2^11 besides and sums of its own.
+// The factors are undone in fp32.
 #include <algorithm>
 
 #include "adapter.cuh"

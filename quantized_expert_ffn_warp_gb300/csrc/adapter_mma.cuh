@@ -74,7 +74,7 @@ struct Tensor {
     uint32_t tmem;
     volatile int *gave_up;
 };
-constexpr int kStages = 4;      // at most
+constexpr int kStages = 5;      // at most
 struct TensorSmem {
     uint64_t bar[kStages];
     uint32_t tmem;
@@ -195,9 +195,10 @@ __device__ __forceinline__ uint16_t bits(T v)
     return *reinterpret_cast<const uint16_t *>(&v);
 }
 
-// An fp32 value of h or u is multiplied as the sum of kParts values of T.
+// An fp32 value of h or u is multiplied as the sum of kParts values of T: 24 bits in bf16,
+// 22 in fp16.
 template <typename T>
-constexpr int kParts = 2;
+constexpr int kParts = std::is_same_v<T, __nv_bfloat16> ? 3 : 2;
 // The type's own exponents do not reach all fp32 values: 2^e of them are split.
 template <typename T>
 constexpr bool kLifted = std::is_same_v<T, __half>;
@@ -534,8 +535,11 @@ template <int PAD>
 constexpr int kAhead = PAD <= 64 ? 2 : 1;
 template <int PAD>
 constexpr int kRowBuffers = kAhead<PAD> + 1;
+// One block ahead, a block's matrix is copied when the last product is done with its own.
+template <int PAD>
+constexpr int kMatrices = kAhead<PAD>;
 template <typename T, bool BY_ROW, int PAD>
-constexpr int kExpandSmem = 128 * kTile * kPartBlocks<T, PAD> + 2 * kMatrix<BY_ROW, PAD> +
+constexpr int kExpandSmem = 128 * kTile * kPartBlocks<T, PAD> + kMatrices<PAD> * kMatrix<BY_ROW, PAD> +
                             kRowBuffers<PAD> * kRowsBytes + kSmemSlack;
 
 // Tiles of tokens (the product's rows) times blocks of columns: a CTA takes an equal share
@@ -582,7 +586,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
     constexpr int parts = kParts<T>, matrix = kMatrix<BY_ROW, PAD>;
     constexpr int ahead = kAhead<PAD>, buffers = kRowBuffers<PAD>;
     const uint32_t hs = smem_base(), mats = hs + 128 * kTile * kPartBlocks<T, PAD>;
-    const uint32_t rows = mats + 2 * matrix;
+    const uint32_t rows = mats + kMatrices<PAD> * matrix;
     // the matrix: rows of ranks (0 behind the last), or (BY_ROW) of columns for each rank
     using W = std::conditional_t<BY_ROW, Rows<kCols / 8, PAD, kExpandThreads>,
                                  Rows<PAD / 8, kCols, kExpandThreads>>;
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             from[j] = a.base + (long long)toks[base_row + kBasePass * j] * a.ldb + 8 * base_chunk;
         const auto fetch = [&](int step) {
             const int c0 = (first + step) * kCols;
-            const uint32_t ws = mats + (step & 1) * matrix + wr.at;
+            const uint32_t ws = mats + step % kMatrices<PAD> * matrix + wr.at;
             const bool whole = c0 + kCols <= a.N;
             if (step >= steps) {
                 commit_copies();
@@ -743,7 +747,7 @@ __global__ void __launch_bounds__(kExpandThreads, 1) adapter_expand_kernel(Expan
             if (warp == 0 && step < steps) {
                 tc_fence_after();
                 if (elect_one()) {
-                    const uint32_t mat = mats + (step & 1) * matrix;
+                    const uint32_t mat = mats + step % kMatrices<PAD> * matrix;
                     const int buffer = (done + step) & 1;
 #pragma unroll
                     for (int part = 0; part < parts; part++)
@@ -893,9 +897,15 @@ struct OuterArgs {
     float *part;            // [splits][L][blocks of both][kCols][PAD]
     unsigned *tickets;      // [L][blocks of both]
 };
-constexpr int kOuterStages = 3, kOuterList = 16;    // steps whose tokens are at hand
+constexpr int kOuterList = 16;      // steps whose tokens are at hand
+// Tokens of a step, and steps: two CTAs an SM, each with two steps of 64 tokens on their way,
+// or four of 32 where three parts of 64 ranks leave no room for three stages of 64.
 template <typename T, int PAD>
-constexpr int kOuterStage = 128 * kBlk * (kCols / kBlk + kPartBlocks<T, PAD>);
+constexpr int kOuterTokens = PAD == 64 && kParts<T> == 3 ? 32 : 64;
+template <typename T, int PAD>
+constexpr int kOuterStage = 128 * kOuterTokens<T, PAD> * (kCols / kBlk + kPartBlocks<T, PAD>);
+template <typename T, int PAD>
+constexpr int kOuterStages = kOuterTokens<T, PAD> == 32 ? 5 : 3;
 
 // Sixteen ranks of a column from rank k on, at the end of a sum over tokens.
 template <typename T>
@@ -926,14 +936,15 @@ template <typename T, int PAD>
 __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_kernel(OuterArgs a)
 {
     __shared__ TensorSmem ts;
-    __shared__ int toks[kOuterList * kBlk];
+    constexpr int tokens = kOuterTokens<T, PAD>;
+    __shared__ int toks[kOuterList * tokens];
     __shared__ int last;
     pdl_wait();
     const int adapter = blockIdx.y, split = blockIdx.z, all_blocks = a.a.blocks + a.b.blocks;
     const int first = blockIdx.x * a.turns, stop = min(first + a.turns, all_blocks);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lo = a.p.off[adapter], count = a.p.off[adapter + 1] - lo;
-    const int all = (count + kBlk - 1) / kBlk;
+    const int all = (count + tokens - 1) / tokens;
     const int begin = (int)((long long)all * split / a.splits);
     const int steps = (int)((long long)all * (split + 1) / a.splits) - begin;
     const int c = 32 * warp + lane;
@@ -953,10 +964,10 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
     const Tensor t = tensor_begin(ts, cols);
     const uint32_t smem = smem_base();
     constexpr int stage_bytes = kOuterStage<T, PAD>;
-    using X = Rows<kCols / 8, kBlk>;
-    using V = Rows<PAD / 8, kBlk>;
-    const X xr(128 * kBlk);
-    const V vr(128 * kBlk);
+    using X = Rows<kCols / 8, tokens>;
+    using V = Rows<PAD / 8, tokens>;
+    const X xr(128 * tokens);
+    const V vr(128 * tokens);
     const float2 lift =
         kLifted<T> ? lift_of(__uint_as_float(a.p.most[adapter])) : make_float2(1.f, 1.f);
     for (int blk = first; blk < stop; blk++) {
@@ -968,16 +979,16 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
         const int rank_bytes = 8 * vr.chunk < a.r ? 16 : 0;     // 0 for the ranks behind the last
         const uint16_t *ranks = rank_bytes ? a.h + 8 * vr.chunk : a.h;
         const auto fetch = [&](int i, int stage) {
-            const int s0 = (begin + i) * kBlk;
+            const int s0 = (begin + i) * tokens;
             if (i % kOuterList == 0) {      // the list that the next steps take their tokens from
-                for (int j = threadIdx.x; j < kOuterList * kBlk; j += kThreads)
+                for (int j = threadIdx.x; j < kOuterList * tokens; j += kThreads)
                     toks[j] = s0 + j < count ? a.p.perm[lo + s0 + j] : -1;
                 __syncthreads();
             }
-            const int *list = toks + i % kOuterList * kBlk;
+            const int *list = toks + i % kOuterList * tokens;
             const uint32_t xs = smem + stage * stage_bytes + xr.at;
-            const uint32_t vs = smem + stage * stage_bytes + 128 * kBlk * (kCols / kBlk);
-            if (whole && s0 + kBlk <= count) {
+            const uint32_t vs = smem + stage * stage_bytes + 128 * tokens * (kCols / kBlk);
+            if (whole && s0 + tokens <= count) {
 #pragma unroll
                 for (int j = 0; j < X::kPasses; j++)
                     copy16(xs + X::kNext * j, src + list[xr.row + X::kPass * j] * o.ld, 16);
@@ -999,7 +1010,7 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
 #pragma unroll
                     for (int p = 0; p < parts; p++) {
                         const int chunk = p * (PAD / 8) + vr.chunk;
-                        copy16(vs + (chunk >> 3) * (128 * kBlk) +
+                        copy16(vs + (chunk >> 3) * (128 * tokens) +
                                    sw128_at(vr.row + V::kPass * j, chunk & 7),
                                in ? from + (V::kPass * j * parts + p) * PAD : a.u, in ? 16 : 0);
                     }
@@ -1015,21 +1026,21 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
         };
         // the parts' sums lie side by side too, at most 256 columns an instruction
         const auto multiply = [&](int stage, bool first) {
-            const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * kBlk * (kCols / kBlk);
-            const uint64_t da = sw128_desc_mn(at, 128 * kBlk);
+            const uint32_t at = smem + stage * stage_bytes, vs = at + 128 * tokens * (kCols / kBlk);
+            const uint64_t da = sw128_desc_mn(at, 128 * tokens);
             for (int n0 = 0, all = of_a ? parts * PAD : PAD; n0 < all; n0 += 256) {
                 const uint32_t idesc =
                     (1u << 4) | (std::is_same_v<T, __nv_bfloat16> ? (1u << 7 | 1u << 10) : 0u) |
                     ((uint32_t)(min(all - n0, 256) >> 3) << 17) | (8u << 24) | kMnMajorA | kMnMajorB;
-                const uint64_t db = sw128_desc_mn(vs + n0 / kBlk * (128 * kBlk), 128 * kBlk);
+                const uint64_t db = sw128_desc_mn(vs + n0 / kBlk * (128 * tokens), 128 * tokens);
 #pragma unroll
-                for (int k = 0; k < kBlk / 16; k++)
+                for (int k = 0; k < tokens / 16; k++)
                     umma_ss(t.tmem + n0, da + 128 * k, db + 128 * k, idesc, !first || k);
             }
         };
         if (blk > first)
             __syncthreads();        // the list of tokens is taken again
-        contract<kOuterStages>(t, steps, blk - first, fetch, multiply);
+        contract<kOuterStages<T, PAD>>(t, steps, blk - first, fetch, multiply);
         const bool failed = *t.gave_up;
         const int block = adapter * all_blocks + blk;
         const long long slots = (long long)a.L * all_blocks;
@@ -1234,7 +1245,7 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
     o.turns = std::max(1, (int)std::min(8LL, (long long)blocks * c.L / (8 * c.sms)));
     return launch_wide(adapter_outer_kernel<T, PAD>,
                        dim3((blocks + o.turns - 1) / o.turns, c.L, o.splits),
-                       kOuterStages * kOuterStage<T, PAD> + kSmemSlack, st, o);
+                       kOuterStages<T, PAD> * kOuterStage<T, PAD> + kSmemSlack, st, o);
 }
 
 template <typename T>

@@ -171,7 +171,8 @@ def _parts(dtype, n):
 TOL = 6 * 2.0 ** -21
 
 
-@pytest.mark.parametrize("dtype,size", [("fp16", 1.0), ("fp16", 2.0 ** -9)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 1.0), ("bf16", 2.0 ** -30), ("fp16", 1.0),
+                                        ("fp16", 2.0 ** -9)])
 @pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
 def test_h_and_u_keep_their_bits(dtype, size, rank):
     moe, n = _moe(), 700
@@ -201,7 +202,7 @@ def test_h_and_u_keep_their_bits(dtype, size, rank):
     assert ((got["dx"][:, 0].double() - want).abs() <= TOL + half_step(want, dt)).all()
 
 
-@pytest.mark.parametrize("dtype,size", [("fp16", 1.0), ("fp16", 2.0 ** -9)])
+@pytest.mark.parametrize("dtype,size", [("bf16", 1.0), ("fp16", 1.0), ("fp16", 2.0 ** -9)])
 @pytest.mark.parametrize("rank", [8, 24, 64, 128])
 def test_sums_over_tokens_keep_the_bits_of_u(dtype, size, rank):
     """Two tokens an adapter, whose u differ in the last part alone, and x = 1, -1."""
