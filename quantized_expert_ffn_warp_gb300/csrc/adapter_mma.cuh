@@ -124,12 +124,16 @@ __host__ __device__ constexpr int row_blocks(int r) { return (r + kBlk - 1) / kB
 // A multi-stage contraction: fetch(i, stage) starts the copies of step i, multiply(stage,
 // first) issues its products in one elected thread.  Copies of the steps ahead are under
 // way while a step is multiplied; a stage is filled again when its products are done.
-// `turn` contractions of as many steps went before it in the CTA.
+// Bit s of `uses` counts the waits for stage s over the CTA's contractions, by their parity:
+// none is left out if the CTA goes on to `another`.
 template <int S, typename F, typename M>
-__device__ __forceinline__ void contract(const Tensor &t, int steps, int turn, F fetch, M multiply)
+__device__ __forceinline__ void contract(const Tensor &t, int steps, uint32_t &uses, bool another,
+                                         F fetch, M multiply)
 {
-    // uses of a stage's barrier in front of step i
-    const auto use = [&](int i) { return turn * ((steps - i % S + S - 1) / S) + i / S; };
+    const auto wait = [&](int s) {
+        tensor_wait(t, s, uses >> s);
+        uses ^= 1u << s;
+    };
 #pragma unroll
     for (int i = 0; i < S - 1; i++) {
         if (i < steps)
@@ -152,16 +156,37 @@ __device__ __forceinline__ void contract(const Tensor &t, int steps, int turn, F
         const int before = stage == 0 ? S - 1 : stage - 1;
         if (i + S - 1 < steps) {
             if (i > 0)
-                tensor_wait(t, before, use(i - 1));
+                wait(before);
             fetch(i + S - 1, before);
         }
         commit_copies();
         stage = stage + 1 == S ? 0 : stage + 1;
     }
     wait_copies<0>();
-    if (steps > 0)
-        tensor_wait(t, (steps - 1) % S, use(steps - 1));
+    // the last step first: those in front of it are done then, and cost no wait
+    for (int i = another ? min(steps, S) : min(steps, 1); i > 0; i--) {
+        stage = stage == 0 ? S - 1 : stage - 1;
+        wait(stage);
+    }
     tc_fence_after();
+}
+// A LONG contraction, of more than kOneChain terms, is cut into chains of kChain, whose sums are
+// added in fp32: the tensor cores cut what a chain adds to a step of its sum, always towards 0
+// (0.4% of a sum of 2^20 terms of one sign in one chain).  kOneChain terms are 1024 sums of 16,
+// off by 2^-13 of the terms at most.  A variant of its own, since the code for chains costs
+// every CTA 0.3 us although it is not run (8192 tokens of 64 adapters 138 to 142 us).
+constexpr int kChain = 4096, kOneChain = 16384;
+
+// Sixteen sums, with those that an earlier chain left at `kept`.
+__device__ __forceinline__ void add_kept(float (&v)[16], uint32_t kept, bool any)
+{
+    if (!any)
+        return;
+    float w[16];
+    tmem_ld16(kept, w);
+#pragma unroll
+    for (int e = 0; e < 16; e++)
+        v[e] += w[e];
 }
 
 // A call's dynamic shared memory from a 1024-byte boundary on, as the swizzle needs.
@@ -304,7 +329,7 @@ constexpr int kShrinkStage = 128 * kTile + (BY_ROW ? 128 * kBlk * row_blocks(PAD
 
 // A tile's tokens (the product's rows) times all ranks.  The slices' sums are added by
 // whichever CTA of a tile arrives last, in the slices' order.
-template <typename T, bool BY_ROW, int PAD>
+template <typename T, bool BY_ROW, int PAD, bool LONG>
 __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_shrink_kernel(ShrinkArgs a)
 {
     __shared__ TensorSmem ts;
@@ -320,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_shrink_ke
                 a.h[(long long)a.p.perm[tile.y + i / a.r] * a.r + i % a.r] = 0;
         return;
     }
-    constexpr uint32_t cols = tmem_cols(PAD);
+    constexpr uint32_t cols = tmem_cols(LONG ? 2 * PAD : PAD);
     const Tensor t = tensor_begin(ts, cols);
     const int blocks = (a.K + kBlk - 1) / kBlk;
     const int begin = (int)((long long)blocks * slice / a.slices);
@@ -393,36 +418,50 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_shrink_ke
         for (int k = 0; k < 4; k++)
             umma_ss(t.tmem, da + 2 * k, db + (BY_ROW ? 128 : 2) * k, idesc, !first || k);
     };
-    contract<kShrinkStages>(t, end - begin, 0, fetch, multiply);
-    const bool failed = *t.gave_up;
+    const uint32_t sums = t.tmem + ((uint32_t)(32 * (warp & 3)) << 16), kept = sums + PAD;
     const int at = 32 * warp + lane, place = tile.y + at;
+    const int token = at < tile.z ? a.p.perm[place] : 0;
+    uint32_t uses = 0;
     float most = 0.f;
-    if (warp < 4) {
-        const int token = at < tile.z ? a.p.perm[place] : 0;
+    constexpr int chain = kChain / kBlk;
+    int s0 = begin;
+    do {
+        const bool more = LONG && s0 + chain < end;
+        const auto fetch_from = [&](int i, int stage) { fetch(s0 - begin + i, stage); };
+        contract<kShrinkStages>(t, more ? chain : end - s0, uses, more, fetch_from, multiply);
+        const bool failed = *t.gave_up;
+        if (warp < 4)
 #pragma unroll 1
-        for (int c = 0; c < PAD; c += 16) {
-            float v[16];
-            tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + c, v);
-            if (at < tile.z) {
-#pragma unroll
-                for (int q = 0; q < 4; q++) {
-                    float d[4];
-#pragma unroll
-                    for (int e = 0; e < 4; e++)
-                        d[e] = failed ? NAN : v[4 * q + e];
-                    if (a.slices == 1)
-                        put_results<T, PAD>(a, place, token, c + 4 * q, d, most);
-                    else
-                        *reinterpret_cast<float4 *>(
-                            a.part + ((long long)slice * a.n + place) * PAD + c + 4 * q) =
-                            make_float4(d[0], d[1], d[2], d[3]);
+            for (int c = 0; c < PAD; c += 16) {
+                float v[16];
+                tmem_ld16(sums + c, v);
+                add_kept(v, kept + c, LONG && s0 > begin);
+                if (more) {
+                    tmem_st16(kept + c, v);
+                    continue;
                 }
+                if (at < tile.z) {
+#pragma unroll
+                    for (int q = 0; q < 4; q++) {
+                        float d[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++)
+                            d[e] = failed ? NAN : v[4 * q + e];
+                        if (a.slices == 1)
+                            put_results<T, PAD>(a, place, token, c + 4 * q, d, most);
+                        else
+                            *reinterpret_cast<float4 *>(
+                                a.part + ((long long)slice * a.n + place) * PAD + c + 4 * q) =
+                                make_float4(d[0], d[1], d[2], d[3]);
+                    }
+                }
+                __syncwarp();       // the next load is the whole warp's
             }
-            __syncwarp();       // the next load is the whole warp's
-        }
-        if (a.most && a.slices == 1)
-            put_most(a, tile.x, most);
-    }
+        tc_fence_before();          // the next chain's products write where this one's were read
+        s0 += chain;
+    } while (LONG && s0 < end);
+    if (a.most && a.slices == 1 && warp < 4)
+        put_most(a, tile.x, most);
     tensor_end(t, cols);
     if (a.slices == 1)
         return;
@@ -932,7 +971,7 @@ __device__ __forceinline__ void put_outer(const OuterArgs &a, const OuterSide &o
 
 // The sum over an adapter's tokens of kCols columns (the product's rows) times all ranks.
 // Both operands are read along their rows: the tokens are the contraction.
-template <typename T, int PAD>
+template <typename T, int PAD, bool LONG>
 __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_kernel(OuterArgs a)
 {
     __shared__ TensorSmem ts;
@@ -960,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
         return;
     }
     constexpr int parts = kParts<T>;
-    constexpr uint32_t cols = tmem_cols(parts * PAD);
+    constexpr uint32_t cols = tmem_cols((LONG ? parts + 1 : parts) * PAD);
     const Tensor t = tensor_begin(ts, cols);
     const uint32_t smem = smem_base();
     constexpr int stage_bytes = kOuterStage<T, PAD>;
@@ -968,6 +1007,7 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
     using V = Rows<PAD / 8, tokens>;
     const X xr(128 * tokens);
     const V vr(128 * tokens);
+    uint32_t uses = 0;
     const float2 lift =
         kLifted<T> ? lift_of(__uint_as_float(a.p.most[adapter])) : make_float2(1.f, 1.f);
     for (int blk = first; blk < stop; blk++) {
@@ -1040,47 +1080,65 @@ __global__ void __launch_bounds__(kThreads, PAD <= 64 ? 2 : 1) adapter_outer_ker
         };
         if (blk > first)
             __syncthreads();        // the list of tokens is taken again
-        contract<kOuterStages<T, PAD>>(t, steps, blk - first, fetch, multiply);
-        const bool failed = *t.gave_up;
+        const uint32_t sums = t.tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+        const uint32_t kept = sums + parts * PAD;
         const int block = adapter * all_blocks + blk;
         const long long slots = (long long)a.L * all_blocks;
-        if (warp < 4)
+        constexpr int chain = kChain / tokens;
+        int s0 = 0;
+        do {                        // once without steps: 0
+            if (LONG && s0 > 0)
+                __syncthreads();    // the list of tokens is taken again
+            const bool more = LONG && s0 + chain < steps;
+            const auto fetch_from = [&](int i, int stage) { fetch(s0 + i, stage); };
+            contract<kOuterStages<T, PAD>>(t, more ? chain : steps - s0, uses,
+                                           more || blk + 1 < stop, fetch_from, multiply);
+            const bool failed = *t.gave_up;
+            if (warp < 4)
 #pragma unroll 1
-            for (int k = 0; k < PAD; k += 16) {
-                float v[16];
-                tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + k, v);
-                if (of_a) {
-                    float weight = lift.y;
-#pragma unroll
-                    for (int e = 0; e < 16; e++)
-                        v[e] *= weight;
-#pragma unroll
-                    for (int p = 1; p < parts; p++) {
-                        float rest[16];
-                        tmem_ld16(t.tmem + ((uint32_t)(32 * warp) << 16) + p * PAD + k, rest);
-                        weight /= kNext<T>;
+                for (int k = 0; k < PAD; k += 16) {
+                    float v[16];
+                    tmem_ld16(sums + k, v);
+                    if (of_a) {
+                        float weight = lift.y;
 #pragma unroll
                         for (int e = 0; e < 16; e++)
-                            v[e] = fmaf(rest[e], weight, v[e]);
-                    }
-                }
+                            v[e] *= weight;
 #pragma unroll
-                for (int e = 0; e < 16; e++)
-                    v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
-                if (a.splits == 1) {
+                        for (int p = 1; p < parts; p++) {
+                            float rest[16];
+                            tmem_ld16(sums + p * PAD + k, rest);
+                            weight /= kNext<T>;
+#pragma unroll
+                            for (int e = 0; e < 16; e++)
+                                v[e] = fmaf(rest[e], weight, v[e]);
+                        }
+                    }
+                    add_kept(v, kept + k, LONG && s0 > 0);
+                    if (more) {
+                        tmem_st16(kept + k, v);
+                        continue;
+                    }
 #pragma unroll
                     for (int e = 0; e < 16; e++)
-                        v[e] *= scale;
-                    put_outer<T>(a, o, of_a, adapter, c0 + c, k, v);
-                    continue;
-                }
-                float4 *p = reinterpret_cast<float4 *>(
-                    a.part + ((split * slots + block) * kCols + c) * PAD + k);
+                        v[e] = failed ? NAN : steps > 0 ? v[e] : 0.f;
+                    if (a.splits == 1) {
 #pragma unroll
-                for (int q = 0; q < 4; q++)
-                    p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-            }
-        tc_fence_before();          // the next block's products write where this one's were read
+                        for (int e = 0; e < 16; e++)
+                            v[e] *= scale;
+                        put_outer<T>(a, o, of_a, adapter, c0 + c, k, v);
+                        __syncwarp();       // the next load is the whole warp's
+                        continue;
+                    }
+                    float4 *p = reinterpret_cast<float4 *>(
+                        a.part + ((split * slots + block) * kCols + c) * PAD + k);
+#pragma unroll
+                    for (int q = 0; q < 4; q++)
+                        p[q] = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                }
+            tc_fence_before();      // the next chain's products write where this one's were read
+            s0 += chain;
+        } while (LONG && s0 < steps);
         if (a.splits == 1)
             continue;
         __threadfence();
@@ -1148,7 +1206,10 @@ cudaError_t launch_wide(void (*kernel)(P...), dim3 grid, int smem, cudaStream_t 
 template <typename T, bool BY_ROW, int PAD>
 cudaError_t launch_shrink(const ShrinkArgs &a, int tiles, cudaStream_t st)
 {
-    return launch_wide(adapter_shrink_kernel<T, BY_ROW, PAD>, dim3(tiles, a.slices),
+    const bool chains = a.K > (long long)kOneChain * a.slices;
+    return launch_wide(chains ? adapter_shrink_kernel<T, BY_ROW, PAD, true>
+                              : adapter_shrink_kernel<T, BY_ROW, PAD, false>,
+                       dim3(tiles, a.slices),
                        kShrinkStages * kShrinkStage<BY_ROW, PAD> + kSmemSlack, st, a);
 }
 
@@ -1243,7 +1304,8 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
     // adapters end apart: the second takes 148.
     const int blocks = o.a.blocks + o.b.blocks;
     o.turns = std::max(1, (int)std::min(8LL, (long long)blocks * c.L / (8 * c.sms)));
-    return launch_wide(adapter_outer_kernel<T, PAD>,
+    return launch_wide(c.n > kOneChain * o.splits ? adapter_outer_kernel<T, PAD, true>
+                                                  : adapter_outer_kernel<T, PAD, false>,
                        dim3((blocks + o.turns - 1) / o.turns, c.L, o.splits),
                        kOuterStages<T, PAD> * kOuterStage<T, PAD> + kSmemSlack, st, o);
 }

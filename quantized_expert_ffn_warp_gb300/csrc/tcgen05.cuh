@@ -165,8 +165,25 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&v)[32
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
 
-// The same of an operand whose rows of 128 bytes hold 64 of its M or N index, one row for
-// each K: 8 rows of K are 1024 bytes, the next 64 of M or N lie `next` bytes on.  Its
+// Into 16 consecutive fp32 columns of this warp's 32 tensor-memory lanes.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&f)[16])
+{
+    uint32_t v[16];
+#pragma unroll
+    for (int i = 0; i < 16; i++)
+        v[i] = __float_as_uint(f[i]);
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16};"
+        ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]),
+          "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]),
+          "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// A shared-memory operand whose rows of 128 bytes hold 64 of its M or N index, one row for
+// each K, swizzled: 8 rows of K are 1024 bytes, the next 64 of M or N lie `next` bytes on.  Its
 // instruction descriptor has kMnMajorA or kMnMajorB; the start address advances by 2048
 // bytes per 16-K step.
 __device__ __forceinline__ uint64_t sw128_desc_mn(uint32_t addr, uint32_t next)

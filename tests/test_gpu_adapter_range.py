@@ -1,5 +1,5 @@
 """Adapters where h and u, the products between the two matrices, are far from 1 in
-size, not finite, or have more bits than the activations' type."""
+size, have more bits than the activations' type, or are summed over very many tokens."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -224,3 +224,50 @@ def test_sums_over_tokens_keep_the_bits_of_u(dtype, size, rank):
     want = (v[:, last].double() * s ** last)[:, None].expand(n, 16)
     assert ((got["dA"][:, rank - 1].double() - want).abs() <= TOL + half_step(want, dt)).all()
     assert (got["dA"][:, :rank - 1] == 0).all()
+
+
+# ---------------------------------------------------------------- long sums
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+@pytest.mark.parametrize("n,rank", [(1 << 20, 8), (300001, 64), (150000, 128), (16385, 64), (16384, 24)])
+def test_sums_over_very_many_tokens_of_one_sign(n, rank, dtype):
+    """One of many loaded adapters has all tokens.  16384 tokens at most are one chain, 1024
+    accumulations of 16 terms off by a step 2 H each; more are chains of 4096, 256 such
+    accumulations each, and at most 257 sums of those, H each.  The lower parts of u are
+    2^-8 and less of the first and so are their sums' errors."""
+    moe, count = _moe(), 304
+    g = torch.Generator(device="cuda").manual_seed(n)
+
+    def part(*shape, top=1.0):
+        return ((torch.rand(shape, device="cuda", generator=g) / 2 + 0.5) * top).to(DT[dtype])
+    x, dy, h = part(n, 16), part(n, 24, top=2.0 ** -8), part(n, rank)
+    A, B = part(count, rank, 16), part(count, 24, rank, top=0.25)
+    ids = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    got = moe.adapter_grad(dy, x, h, ids, A, B, input_grad=False)
+    u = dy.double() @ B[5].double()
+    for name, want in (("dA", u.t() @ x.double()), ("dB", dy.double().t() @ h.double())):
+        v = got[name][5].double()
+        err = (1024 * 2 * 1.01 + 32) * H * want
+        assert ((v - want).abs() <= err + half_step(want, x.dtype)).all(), name
+        got[name][5] = 0
+        assert (got[name] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_long_contractions_of_one_sign(dtype):
+    """A x over 2^20 columns in one piece, as many loaded adapters and some tokens have
+    them.  Chains of 16384 columns are 1024 accumulations of 16 terms, off by a step 2 H
+    each; 64 sums of those, H each."""
+    moe, n, cols, count = _moe(), 160, 1 << 20, 304
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.rand((n, cols), device="cuda", generator=g) / 2 + 0.5).to(DT[dtype])
+    A = torch.zeros((count, 8, cols), dtype=DT[dtype], device="cuda")
+    A[7] = (torch.rand((8, cols), device="cuda", generator=g) / 2 + 0.5) * 2.0 ** -10
+    B = torch.zeros((count, 8, 8), dtype=DT[dtype], device="cuda")
+    B[7] = torch.eye(8, device="cuda")
+    ids = torch.full((n,), 7, dtype=torch.int32, device="cuda")
+    out, h = moe.adapter(x, ids, A, B)
+    want = x.double() @ A[7].double().t()
+    err = (1024 * 2 + 64 + 32) * H * want
+    for got in (out, h):
+        assert ((got.double() - want).abs() <= err + half_step(want, x.dtype)).all()
