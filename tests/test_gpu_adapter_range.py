@@ -271,3 +271,45 @@ def test_long_contractions_of_one_sign(dtype):
     err = (1024 * 2 + 64 + 32) * H * want
     for got in (out, h):
         assert ((got.double() - want).abs() <= err + half_step(want, x.dtype)).all()
+
+
+# ---------------------------------------------------------------- the same bits
+
+@pytest.mark.parametrize("n", [5, 900])
+def test_fp16_same_bits_on_streams_in_graphs_and_in_any_order(n):
+    """Each token's and each adapter's power of two is found anew in every call."""
+    moe = _moe()
+    cols, rows, rank, count = 512, 768, 24, 5
+    randn, ids = operands(n, cols, rows, rank, count, "fp16")
+    A, B = randn(count, rank, cols, scale=0.05), randn(count, rows, rank, scale=1e-3)
+    dy = randn(n, rows, scale=1e-4)
+
+    def both(x, stream=None):
+        out, h = moe.adapter(x, ids, A, B, stream=stream)
+        g = moe.adapter_grad(dy, x, h, ids, A, B, stream=stream)
+        only = moe.adapter_grad(dy, x, h, ids, A, B, input_grad=False, stream=stream)
+        assert set(only) == {"dA", "dB"}
+        return [out, h, g["dx"], g["dA"], g["dB"], only["dA"], only["dB"]]
+    x = randn(n, cols)
+    first = both(x)
+    torch.cuda.synchronize()
+    assert torch.equal(first[3], first[5]) and torch.equal(first[4], first[6])
+    side = torch.cuda.Stream()
+    again = both(x, side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(first, again))
+    p = torch.randperm(n, device="cuda")
+    out, h = moe.adapter(x[p].contiguous(), ids[p].contiguous(), A, B)
+    assert torch.equal(out, first[0][p]) and torch.equal(h, first[1][p])
+    static, pool, graphs = x.clone(), torch.cuda.graph_pool_handle(), []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, pool=pool):
+            res = both(static)
+        graphs.append((g, res))
+    for turn in range(4):       # sizes that differ from call to call
+        static.copy_(randn(n, cols, scale=(1.0, 1e-3, 100.0, 1e-5)[turn]))
+        g, res = graphs[turn % 2]
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(res, both(static)))
