@@ -13,10 +13,10 @@
 // layout, and the descriptors take either side of a matrix as the contraction's, so that
 // nothing is transposed.
 // Measured in a replayed graph: 4001 tokens of 9 requests through 4096 x 14336 at rank 64
-// (bf16, with base) 85 us, of which the plan takes 5, the shrink and the join of its
-// slices 20 and the expansion 55 (5.2 TB/s of base and out); the gradients of 8192 tokens
-// through 4096 x 4096 at rank 32 102 us: 6, 20, 35, and 34 for the weights'.  13 tokens of
-// 13 requests take 16 us, three launches of dependent loads.
+// (bf16, with base) 89 us, of which the plan takes 5, the shrink and the join of its
+// slices 20 and the expansion 59 (229 MB of base and out at 3.9 TB/s); the gradients of 8192
+// tokens through 4096 x 4096 at rank 32 103 us: 6, 20, 35, and 34 for the weights'.  13
+// tokens of 13 requests take 16.5 us, three launches of dependent loads.
 // h and u are fp32 sums and are multiplied as sums of values of the activations' type, since
 // the tensor cores take 16-bit operands: one would add a rounding of 2^-9 (bf16) to the
 // delta and to dA.  bf16 takes three, all 24 bits; with two, 16 bits, dA differed from fp32
@@ -163,8 +163,8 @@ __global__ void __launch_bounds__(1024) adapter_plan_kernel(const int32_t *__res
 
 // ---------------------------------------------------------------- host
 
-// CTAs that share the contraction of a tile: two for each SM in all, each with two steps
-// at least.  Asks no device, since the workspace depends on it.
+// CTAs that share the contraction of a tile: two for each SM in all (above rank 64 the shared
+// memory of one fits an SM, and they make two waves), each with two steps at least.  Asks no device, since the workspace depends on it.
 int shrink_slices(int n, int L, int K)
 {
     const int most = std::max(1, (K + kAdapterStep - 1) / kAdapterStep / 2);

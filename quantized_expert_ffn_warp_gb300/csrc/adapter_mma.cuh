@@ -1299,9 +1299,9 @@ cudaError_t run_adapter_grad(const AdapterGradCall &c, cudaStream_t st)
                (c.N + kCols - 1) / kCols, static_cast<uint16_t *>(c.dB)};
     // Several blocks a CTA once they fill the SMs' two places eight times: few tokens each, so
     // that a CTA's start weighs.  Measured, one block a CTA against this: 64 adapters of 4096 x
-    // 4096, 500 tokens (rank 16) 82 and 72 us, 8192 tokens (rank 32) 144 and 137; 256 adapters
-    // of 2048 x 2048, 9000 tokens (rank 16) 166 and 137.  With fewer than eight, unequal
-    // adapters end apart: the second takes 148.
+    // 4096, 500 tokens (rank 16) 85 and 74 us, 8192 tokens (rank 32) 147 and 140; 256 adapters
+    // of 2048 x 2048, 9000 tokens (rank 16) 170 and 141.  With fewer than eight, unequal
+    // adapters end apart: the second took 148 where it took 137 with eight.
     const int blocks = o.a.blocks + o.b.blocks;
     o.turns = std::max(1, (int)std::min(8LL, (long long)blocks * c.L / (8 * c.sms)));
     return launch_wide(c.n > kOneChain * o.splits ? adapter_outer_kernel<T, PAD, true>

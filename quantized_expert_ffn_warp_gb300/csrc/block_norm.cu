@@ -17,7 +17,7 @@
 // thread's part by itself (no barriers).  The column sums stay in registers and leave as
 // one partial row per kRun rows and CTA, added by a second kernel in a fixed order.
 // Measured: 16001 x 4096 bf16 with a gate per token 84 us (92% of the measured copy rate),
-// its gradients for 16384 x 4096 137 us (87%, half of the issue slots used); 4000 x 16384
+// its gradients for 16384 x 4096 139 us (86%, half of the issue slots used); 4000 x 16384
 // 82 and 163 us (94% and 71%).  More than 8192 columns of the gradient take a cluster of two
 // CTAs.  One CTA of four words a thread, its sums in shared memory and no row ahead: 269 us.
 // Every thread adding all warps' sums: 97 and 184 us; and with a cluster's barrier in place
