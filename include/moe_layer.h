@@ -533,7 +533,8 @@ int moe_balance_loss_grad(const void *logits, int dtype, long long ld, int n_tok
  * Sums are fp32; between the two products h is the sum of values of dtype that have 22
  * (fp16) or 24 (bf16) bits of it.  In fp16 they are relative to the token's largest h,
  * whatever its size: h may be far below fp16's smallest number or above 65504.  out and h
- * are rounded once (an h above 65504 is kept as an infinity).  Rows on 16-byte boundaries are read by
+ * are rounded once (an h above 65504 is kept as an infinity).  An infinity in x or A gives
+ * what fp32 sums give, one in B may give NaN, as a value of h can be 0.  Rows on 16-byte boundaries are read by
  * wide loads, others (odd widths) value by value.  When a wait for the tensor cores
  * gives up (after 2 s), the outputs that it concerns are NaN.
  * rank a multiple of 8 in 8 .. 128; n_adapters 1 .. 1024; n_tokens, cols and rows 1 ..
@@ -565,7 +566,8 @@ int moe_adapter(const void *x, long long ldx, int dtype, int n_tokens, int cols,
  * there.  dx, dA and dB may be NULL and are left out then; x is read for dA, h for dB.
  * dx may be base itself.  Sums are fp32 in a fixed order, u is held as h is in moe_adapter
  * (in the fp16 sums over tokens relative to the adapter's largest u: 22 bits of a token's u
- * down to 2^-28 of that), the results are rounded once.  The workspace is that of
+ * down to 2^-28 of that), the results are rounded once.  An infinity in dy, B or h gives what
+ * fp32 sums give, one in A (for dx) or x (for dA) may give NaN.  The workspace is that of
  * moe_adapter.
  * Errors: those of moe_adapter.
  */
